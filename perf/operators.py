@@ -10,9 +10,9 @@ The definitions.
 - Rotary: token (t, y, x) turns channel pair i of axis a by position_a * theta^(-2 i / dim_a).
 - Cache: per token and head, groups of 32 channels; the step s is the smallest number with 5
   exponent and 3 mantissa bits (the top byte of an fp16 below its sign) with Q s >= max|x|, Q = 127
-  or 7; the code is rint(x / s), stored plus 128 or 8; the cache stands for s times the code.  Four-bit
-  codes: channel 8 j + 2 k + t is nibble k + 4 t of 32-bit word j.  Keys are turned and rounded to
-  bf16 before they are quantised.  Token p lives in slot p while p < sink, else in slot
+  or 7, at most 56 (8 bits) or 896 (4 bits); the code is rint(x / s), stored plus 128 or 8; the cache
+  stands for s times the code.  Four-bit codes: channel 8 j + 2 k + t is nibble k + 4 t of 32-bit word
+  j.  Keys are turned and rounded to bf16 before they are quantised.  Token p lives in slot p while p < sink, else in slot
   sink + (p - sink) % ring.
 - Attention: Query row i stands at position q_start + i, in frame position // tpf.  It sees a key j
   that is still held when frame(j) <= frame(i) and (frame(i) - frame(j) < frames or j < sink).  The
@@ -236,9 +236,9 @@ def _turn(x, case, start):
 
 
 def _grid(bits):
-    """The steps (fp32) in the order of their bytes, up to the largest whose largest multiple is an fp16."""
+    """The steps (fp32) in the order of their bytes, up to the largest."""
     table = (torch.arange(248, dtype=torch.int16) << 7).view(torch.float16).float()
-    return table[table * (127 if bits == 8 else 7) <= 65504.0].cuda()
+    return table[table <= (56.0 if bits == 8 else 896.0)].cuda()
 
 
 def _quantise(x, bits):
@@ -395,7 +395,7 @@ def _rounded64(x, bits):
     top = 127.0 if bits == 8 else 7.0
     e, f = torch.meshgrid(torch.arange(31, dtype=torch.float64), torch.arange(8, dtype=torch.float64), indexing="ij")
     steps = torch.where(e > 0, (1 + f / 8) * 2 ** (e - 15), f / 8 * 2.0 ** -14).reshape(-1).to(x.device)
-    steps = steps[steps * top <= 65504]
+    steps = steps[steps <= (56 if bits == 8 else 896)]
     g = x.reshape(-1, D // GROUP, GROUP)
     amax = g.abs().amax(-1)
     s = steps[torch.bucketize(amax / top, steps).clamp(max=steps.numel() - 1)][..., None]
