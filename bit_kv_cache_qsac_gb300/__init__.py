@@ -35,7 +35,10 @@ EXPORTED = ("qwm_status_string", "qwm_workspace_bytes", "qwm_create", "qwm_destr
             "qwm_dequantize", "qwm_sync_status", "qwm_update_query_stats_noalloc", "qwm_quantize_kv_full",
             "qwm_dequantize_chunks", "qwm_select_rank", "qwm_psac_kept", "qwm_psac_plan", "qwm_psac_pack",
             # comparison baselines (include/qwm_baselines.h)
-            "qwm_kivi_quantize", "qwm_kivi_dequantize", "qwm_prq_residual", "qwm_prq_dequantize")
+            "qwm_kivi_quantize", "qwm_kivi_dequantize", "qwm_prq_residual", "qwm_prq_dequantize",
+            # the recent window (include/qwm_window.h)
+            "qwm_rope_plan", "qwm_rope", "qwm_window_bytes", "qwm_window_write", "qwm_window_read", "qwm_window_attend",
+            "qwm_window_attend_workspace")
 
 
 class QwmError(RuntimeError):
@@ -159,8 +162,10 @@ class Context:
         self.cfg = qwm_config(heads, head_dim, n_centroids, group, top_m, rank, bits, kmeans_iters, 0, storage,
                               psac_gate, test_flags)
         h = C.c_void_p()
+        self.handle = None
         _check(_lib.qwm_create(C.byref(self.cfg), C.byref(h)), "qwm_create")
         self.handle = h
+        self.device = torch.device("cuda", torch.cuda.current_device())
 
     @property
     def heads(self):
@@ -574,3 +579,10 @@ def qwm_quantize_kv_full(ctx: Context, k, v, n: int, S, n_seen, u_r, out: Chunk,
                                    C.byref(s), C.byref(dbg) if dbg is not None else None, _stream(stream))
     _check(st, "qwm_quantize_kv_full")
     out.rank_eff = s.rank_eff
+
+
+# ---------------------------------------------------------------- the recent window (qwm_window.h)
+
+from .window import (QWM_ROPE_HALF, QWM_ROPE_INTERLEAVED, RopeSpec, Window, qwm_rope, qwm_rope_plan,  # noqa: E402
+                     qwm_rope_spec, qwm_strides, qwm_window, qwm_window_attend, qwm_window_attend_workspace,
+                     qwm_window_bytes, qwm_window_read, qwm_window_write)

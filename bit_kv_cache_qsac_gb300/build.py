@@ -27,7 +27,8 @@ def _needs(obj: str, deps: list[str]) -> bool:
 def build(verbose: bool = False, ptxas_info: bool = False) -> str:
     os.makedirs(OBJ_DIR, exist_ok=True)
     sources = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
-    headers = sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + [os.path.join(HERE, "..", "include", "qwm.h")]
+    headers = (sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) +
+               sorted(glob.glob(os.path.join(HERE, "..", "include", "*.h"))))
     jobs = []
     for src in sources:
         obj = os.path.join(OBJ_DIR, os.path.basename(src)[:-3] + ".o")

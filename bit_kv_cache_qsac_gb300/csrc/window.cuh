@@ -1,0 +1,316 @@
+// Device code shared by the recent-window kernels: rotary angles, the window cache's codes and
+// steps, and which keys a Query row sees.
+#pragma once
+
+#include "../../include/qwm_window.h"
+#include "qwm_internal.cuh"
+#include "tc.cuh"
+
+namespace win {
+
+constexpr int D = QWM_D;
+constexpr int kGroup = 32;              // channels that share a step
+constexpr int kSteps = D / kGroup;      // step bytes of a row: one 32-bit word
+
+// ------------------------------------------------------------------ rotary positions
+
+// Cosine and sine of an angle given as pos * turn / 2^64 turns, each as an unevaluated sum hi + lo.
+// The product is taken modulo 2^64, i.e. modulo a whole turn, in integers: no position is too far.
+// The remainder to the nearest quarter turn, |x| <= pi/4, goes through the Taylor series of sine and
+// cosine with the leading terms kept in two floats; hi + lo is within about 2^-27 of the value, so a
+// rotated channel is rounded to bf16 as the exact one is but for one in some 10^5.
+__device__ __forceinline__ void rope_sincos(int64_t pos, uint64_t turn, float &ch, float &cl, float &sh, float &sl) {
+  const uint64_t a = (uint64_t)pos * turn;
+  const uint32_t quarter = (uint32_t)((a + (1ull << 61)) >> 62);
+  const int64_t r = (int64_t)(a - ((uint64_t)quarter << 62));
+  const int32_t hi = (int32_t)(r >> 32);
+  const float fh = (float)hi;
+  const float fl = (float)(hi - (int32_t)fh) + (float)(uint32_t)r * 0x1p-32f;
+  // 2 pi 2^-32 as a sum of two floats
+  constexpr double kTau = 6.283185307179586476925286766559 * 0x1p-32;
+  constexpr float kTauHi = (float)kTau, kTauLo = (float)(kTau - (double)kTauHi);
+  const float x = fh * kTauHi;
+  const float xl = fmaf(fh, kTauLo, fmaf(fl, kTauHi, fmaf(fh, kTauHi, -x)));
+  const float z = x * x;
+  const float zl = fmaf(2.f * x, xl, fmaf(x, x, -z));
+  float pc = fmaf(z, 1.f / 479001600.f, -1.f / 3628800.f);
+  pc = fmaf(pc, z, 1.f / 40320.f);
+  pc = fmaf(pc, z, -1.f / 720.f);
+  pc = fmaf(pc, z, 1.f / 24.f);
+  const float c0 = 1.f - 0.5f * z;
+  const float c1 = fmaf(z * z, pc, fmaf(-0.5f, zl, (1.f - c0) - 0.5f * z));
+  const float c = c0 + c1, cr = c1 - (c - c0);
+  float ps = fmaf(z, 1.f / 6227020800.f, -1.f / 39916800.f);
+  ps = fmaf(ps, z, 1.f / 362880.f);
+  ps = fmaf(ps, z, -1.f / 5040.f);
+  ps = fmaf(ps, z, 1.f / 120.f);
+  ps = fmaf(ps, z, -1.f / 6.f);
+  const float s1 = fmaf(xl, c, x * z * ps);
+  const float s = x + s1, sr = s1 - (s - x);
+  const bool swap = quarter & 1u;
+  const float sgc = ((quarter + 1u) & 2u) ? -1.f : 1.f, sgs = (quarter & 2u) ? -1.f : 1.f;
+  ch = sgc * (swap ? s : c);
+  cl = sgc * (swap ? sr : cr);
+  sh = sgs * (swap ? c : s);
+  sl = sgs * (swap ? cr : sr);
+}
+
+// a c - b s and a s + b c with c = ch + cl, s = sh + sl: the products' rounding errors are carried, so
+// each result is within a little over half a unit of fp32.
+__device__ __forceinline__ float rope_cos(float a, float b, float ch, float cl, float sh, float sl) {
+  const float t = b * sh, e = fmaf(b, sh, -t);
+  return fmaf(a, ch, -t) + fmaf(a, cl, -fmaf(b, sl, e));
+}
+__device__ __forceinline__ float rope_sin(float a, float b, float ch, float cl, float sh, float sl) {
+  const float t = b * ch, e = fmaf(b, ch, -t);
+  return fmaf(a, sh, t) + fmaf(a, sl, fmaf(b, cl, e));
+}
+
+// The coordinate of position p (>= 0) on one axis of the spec's grid.
+__device__ __forceinline__ int64_t rope_coord(const qwm_rope_spec &sp, int64_t p, int axis) {
+  if (p < ((int64_t)1 << 31)) {
+    const uint32_t q = (uint32_t)p, row = q / (uint32_t)sp.grid_w;
+    if (axis == 2) return q - row * (uint32_t)sp.grid_w;
+    const uint32_t t = row / (uint32_t)sp.grid_h;
+    return axis == 0 ? t : row - t * (uint32_t)sp.grid_h;
+  }
+  const int64_t row = p / sp.grid_w;
+  if (axis == 2) return p - row * sp.grid_w;
+  const int64_t t = row / sp.grid_h;
+  return axis == 0 ? t : row - t * sp.grid_h;
+}
+
+// The angles of one token for the 8 channels 8 v .. 8 v + 7 of a row (v = 0..15).  INTERLEAVED: the four
+// pairs inside them; HALF: the eight pairs they are the first or the second half of.
+template <int PAIRING>
+struct RopeVec {
+  static constexpr int kPairs = PAIRING == QWM_ROPE_INTERLEAVED ? 4 : 8;
+  float ch[kPairs], cl[kPairs], sh[kPairs], sl[kPairs];
+  int active;   // INTERLEAVED: pairs turned; HALF: 1 first half, 2 second half, 0 neither
+
+  // pos3: (t, y, x) of the token, or NULL to take them from position p and the grid
+  __device__ __forceinline__ void init(const qwm_rope_spec &sp, int v, int64_t p, const int32_t *pos3) {
+    int64_t c[3];
+#pragma unroll
+    for (int a = 0; a < 3; a++) c[a] = pos3 ? (int64_t)pos3[a] : rope_coord(sp, p, a);
+    const int half = sp.rot >> 1;
+    int i0;
+    if (PAIRING == QWM_ROPE_INTERLEAVED) {
+      i0 = 4 * v;
+      active = half - i0 < 0 ? 0 : (half - i0 < 4 ? half - i0 : 4);
+    } else {
+      i0 = 8 * v < half ? 8 * v : 8 * v - half;
+      active = 8 * v < half ? 1 : (8 * v < sp.rot ? 2 : 0);
+    }
+#pragma unroll
+    for (int i = 0; i < kPairs; i++) {
+      ch[i] = 1.f;
+      cl[i] = sh[i] = sl[i] = 0.f;
+      if (active && (PAIRING == QWM_ROPE_HALF || i < active)) {
+        const int ax = sp.axis[i0 + i];
+        rope_sincos(ax == 0 ? c[0] : (ax == 1 ? c[1] : c[2]), sp.turn[i0 + i], ch[i], cl[i], sh[i], sl[i]);
+      }
+    }
+  }
+  // Turn the 8 bf16 channels in w (4 words).  HALF: every lane of the 16-lane row takes part.
+  __device__ __forceinline__ void turn(const qwm_rope_spec &sp, uint32_t (&w)[4]) const {
+    if (PAIRING == QWM_ROPE_INTERLEAVED) {
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const float a = __uint_as_float(w[i] << 16), b = __uint_as_float(w[i] & 0xFFFF0000u);
+        const uint32_t t = tc::pack_bf16x2(rope_cos(a, b, ch[i], cl[i], sh[i], sl[i]),
+                                           rope_sin(a, b, ch[i], cl[i], sh[i], sl[i]));
+        if (i < active) w[i] = t;
+      }
+    } else {
+      const int lane = threadIdx.x & 31, off = sp.rot >> 4;
+      const int partner = active == 1 ? lane + off : (active == 2 ? lane - off : lane);
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const uint32_t q = __shfl_sync(0xffffffffu, w[i], partner & 31);
+        float o[2];
+#pragma unroll
+        for (int j = 0; j < 2; j++) {
+          const int k = 2 * i + j;
+          const float mine = __uint_as_float(j ? (w[i] & 0xFFFF0000u) : (w[i] << 16));
+          const float other = __uint_as_float(j ? (q & 0xFFFF0000u) : (q << 16));
+          o[j] = active == 1 ? rope_cos(mine, other, ch[k % kPairs], cl[k % kPairs], sh[k % kPairs], sl[k % kPairs])
+                             : rope_sin(other, mine, ch[k % kPairs], cl[k % kPairs], sh[k % kPairs], sl[k % kPairs]);
+        }
+        if (active) w[i] = tc::pack_bf16x2(o[0], o[1]);
+      }
+    }
+  }
+};
+
+// ------------------------------------------------------------------ codes and steps
+
+__host__ __device__ constexpr float code_max(int bits) { return bits == 8 ? 127.f : 7.f; }
+__host__ __device__ constexpr uint32_t step_max(int bits) { return bits == 8 ? 0xA6u : 0xC6u; }  // 56, 896
+
+__device__ __forceinline__ float step_value(uint32_t b) { return __half2float(__ushort_as_half((uint16_t)(b << 7))); }
+
+// The smallest step (as its byte) with Q s >= amax, at most step_max.  Q s has 11 significant bits at
+// most, so the comparisons are exact; the first guess is off by one at most.
+template <int BITS>
+__device__ __forceinline__ uint32_t step_for(float amax) {
+  constexpr float Q = code_max(BITS);
+  const uint32_t h = __half_as_ushort(__float2half_ru(amax * (1.f / Q)));
+  uint32_t b = (h + 0x7Fu) >> 7;
+  b = b < step_max(BITS) ? b : step_max(BITS);
+  if (b > 0u && step_value(b - 1u) * Q >= amax) b--;
+  if (b < step_max(BITS) && step_value(b) * Q < amax) b++;
+  return b;
+}
+
+// rint(x / s) plus the code width's bias, in the low byte.  The quotient is first rounded to a grid of
+// 2^-11: x has 8 significant bits and s has 4, so a quotient that is not halfway between integers is
+// at least 2^-9.9 away from halfway and stays on its side, while one that is lands exactly on it.
+__device__ __forceinline__ uint32_t code_of(float x, float inv, float bias) {
+  const float snap = __fsub_rn(__fmaf_rn(x, inv, 0x1.8p12f), 0x1.8p12f);
+  return __float_as_uint(__fadd_rn(snap, 0x1.8p23f + bias)) & 0xFFu;
+}
+
+// Decode constants of a step byte: s and -bias' s in both halves, where bias' is the integer that the
+// code's fp16 bit pattern below stands above the signed code (1152 or 72; 1152 s and 72 s are exact and
+// finite for every step up to step_max).  (pattern) s - bias' s in one fp16 FMA is then exactly code * s.
+template <int BITS>
+__device__ __forceinline__ void step_consts(uint32_t byte, uint32_t &s2, uint32_t &n2) {
+  const uint32_t s = byte << 7;
+  s2 = s | (s << 16);
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(n2) : "r"(s2), "r"(BITS == 8 ? 0xE480E480u : 0xD480D480u));
+}
+
+// 8 bits: four codes (one word) -> fp16 pairs of channels (0, 1) and (2, 3).
+__device__ __forceinline__ void decode8(uint32_t x, uint32_t s2, uint32_t n2, uint32_t &p0, uint32_t &p1) {
+  p0 = tc::hfma2(__byte_perm(x, 0x64646464u, 0x4140), s2, n2);   // fp16 bits 0x64cc = 1024 + c
+  p1 = tc::hfma2(__byte_perm(x, 0x64646464u, 0x4342), s2, n2);
+}
+// 4 bits: eight codes (one word) -> fp16 pairs of channels (0, 1), (2, 3), (4, 5), (6, 7).
+__device__ __forceinline__ void decode4(uint32_t x, uint32_t s2, uint32_t n2, uint32_t (&p)[4]) {
+  p[0] = tc::hfma2(((x << 4) & 0x00F000F0u) | 0x54005400u, s2, n2);   // fp16 bits 0x54c0 = 64 + c
+  p[1] = tc::hfma2((x & 0x00F000F0u) | 0x54005400u, s2, n2);
+  p[2] = tc::hfma2(((x >> 4) & 0x00F000F0u) | 0x54005400u, s2, n2);
+  p[3] = tc::hfma2(((x >> 8) & 0x00F000F0u) | 0x54005400u, s2, n2);
+}
+
+// ------------------------------------------------------------------ which keys a row sees
+
+// Sequence and window of an attention call, for one sequence.
+struct Seq {
+  int64_t len, sink, ring, tpf, frames;
+  // first and past-the-last position of the recent keys of frame f (f = -1: none), and sinks seen
+  __device__ __forceinline__ int64_t hi(int64_t f) const {
+    const int64_t e = (f + 1) * tpf;
+    return e < len ? e : len;
+  }
+  __device__ __forceinline__ int64_t lo(int64_t f) const {
+    int64_t l = f + 1 > frames ? (f + 1 - frames) * tpf : 0;
+    l = l > len - ring ? l : len - ring;
+    return l > sink ? l : sink;
+  }
+  __device__ __forceinline__ int64_t sinks(int64_t f) const {
+    const int64_t e = hi(f);
+    return e < sink ? e : sink;
+  }
+  __device__ __forceinline__ int64_t frame(int64_t p) const { return p < 0 ? -1 : (tpf == 1 ? p : p / tpf); }
+};
+
+// The keys that the rows of positions p0 .. p1 (p0 <= p1) see between them, numbered 0 .. total - 1: the
+// sinks first, then the recent ones.  Key v lives in slot v (v < ns) or sink + (base + v - ns) mod ring.
+struct Keys {
+  int ns, total;
+  int64_t lo;
+  uint32_t base;
+  __device__ __forceinline__ void init(const Seq &s, int64_t f0, int64_t f1) {
+    ns = (int)s.sinks(f1);
+    lo = s.lo(f0);
+    const int64_t n = s.hi(f1) - lo;
+    total = ns + (n > 0 ? (int)n : 0);
+    base = (uint32_t)((lo - s.sink) % s.ring);
+  }
+  __device__ __forceinline__ uint32_t slot(int v, uint32_t sink, uint32_t ring) const {
+    if (v < ns) return (uint32_t)v;
+    uint32_t r = base + (uint32_t)(v - ns);
+    r = r >= ring ? r - ring : r;
+    return sink + r;
+  }
+};
+
+// The keys of `Keys` that one row sees: 0 .. c0 - 1 and c1 .. c2 - 1.
+struct Row {
+  int c0, c1, c2;
+  __device__ __forceinline__ void init(const Seq &s, const Keys &k, int64_t f) {
+    c0 = c1 = c2 = 0;
+    if (f < 0) return;
+    c0 = (int)s.sinks(f);
+    const int64_t l = s.lo(f), h = s.hi(f);
+    if (h > l) {
+      c1 = k.ns + (int)(l - k.lo);
+      c2 = k.ns + (int)(h - k.lo);
+    }
+  }
+  __device__ __forceinline__ bool sees(int v) const { return v < c0 || (v >= c1 && v < c2); }
+};
+
+// The keys that every row of frames f0 .. f1 sees: 0 .. e0 - 1 and e1 .. e2 - 1 (both ends of a row's
+// recent keys grow with its frame, and where the first and the last row see some, all do).
+struct Everyone {
+  int e0, e1, e2;
+  __device__ __forceinline__ void init(const Seq &s, const Keys &k, int64_t f0, int64_t f1) {
+    e0 = (int)s.sinks(f0);
+    const int64_t l = s.lo(f1), h = s.hi(f0);
+    e1 = e2 = 0;
+    if (h > l && h > s.lo(f0) && s.hi(f1) > l) {
+      e1 = k.ns + (int)(l - k.lo);
+      e2 = k.ns + (int)(h - k.lo);
+      if (e1 <= e0) e1 = 0;   // no gap after the sinks
+    }
+  }
+  __device__ __forceinline__ bool see(int v0, int v1) const { return v1 <= e0 || (v0 >= e1 && v1 <= e2); }
+};
+
+}  // namespace win
+
+// Launchers of the recent-window calls (each returns the launch's error).
+cudaError_t launch_rope(const qwm_rope_spec &spec, const uint16_t *x, const qwm_strides &xs, int batch, int heads,
+                        int64_t n, const int64_t *start, const int32_t *pos, uint16_t *out, const qwm_strides &os,
+                        int num_sms, cudaStream_t st);
+cudaError_t launch_window_write(const qwm_window &w, const uint16_t *k, const qwm_strides &ks, const uint16_t *v,
+                                const qwm_strides &vs, int64_t n, const int64_t *start, const int32_t *count,
+                                const qwm_rope_spec *rope, const int32_t *pos, int num_sms, int32_t *status,
+                                cudaStream_t st);
+cudaError_t launch_window_read(const qwm_window &w, const int64_t *start, const int64_t *length, const int32_t *count,
+                               int64_t n, uint16_t *k_hat, uint16_t *v_hat, int num_sms, cudaStream_t st);
+
+// An attention call over the window cache, as its kernels take it.
+struct WindowAttend {
+  qwm_window w;
+  const uint16_t *q;
+  qwm_strides qs;
+  int64_t nq;
+  const int64_t *q_start, *length;
+  const int32_t *q_count;
+  int64_t tpf, frames;
+  float scale_log2;      // softmax_scale * log2(e)
+  void *out;
+  qwm_strides os;
+  int out_f32, merge;
+  float *lse;
+  int32_t *status;
+  int H, group;          // Query heads; Query heads per Key head
+  int64_t rows;          // group * nq: Query rows of one Key head, row r = (Query i = r / group, head r % group)
+  int splits;            // parts the keys are split into
+  float *part;           // splits > 1: [batch * kv_heads][splits][rows][128] outputs of the parts,
+  float *part_lse;       //             [batch * kv_heads][splits][rows] their log-sum-exps
+};
+// How a call is run: with tensor-memory tiles of 256 Query rows per CTA, or with warp tiles of 8 or 16
+// rows; and into how many parts its keys are split.
+struct WindowPlan {
+  bool tiles;
+  int splits;
+};
+WindowPlan window_plan(int64_t batch, int64_t kv_heads, int64_t rows, int64_t keys, int num_sms);
+cudaError_t launch_window_decode(const WindowAttend &a, cudaStream_t st);
+cudaError_t launch_window_tiles(const WindowAttend &a, cudaStream_t st);
+cudaError_t launch_window_combine(const WindowAttend &a, cudaStream_t st);
