@@ -198,7 +198,7 @@ static qwm_status check_attend(const qwm_ctx *ctx, const qwm_window *win, int64_
   if (ctx->cfg.heads % win->kv_heads != 0) return QWM_ERR_SHAPE;
   if (tpf < 1 || frames < 1) return QWM_ERR_ARG;
   if (nq > kMaxTokens || tpf > ((int64_t)1 << 31) || frames > ((int64_t)1 << 31)) return QWM_ERR_SHAPE;
-  if (nq * ctx->cfg.heads / win->kv_heads > ((int64_t)1 << 30)) return QWM_ERR_SHAPE;
+  if ((int64_t)win->batch * ctx->cfg.heads * nq > ((int64_t)1 << 36)) return QWM_ERR_SHAPE;   // Query rows
   return QWM_OK;
 }
 

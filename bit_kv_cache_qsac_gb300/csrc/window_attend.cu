@@ -8,17 +8,21 @@
 // Work split: a pair of CTAs (a cluster of two, cta_group::2 MMAs) takes one Key head x 512 Query rows
 // (row r = Query r / group, head r % group) and one part of the keys those rows see between them; CTA c
 // holds rows 256 x + 128 c .. + 127 of its two tiles x = 0, 1.  The B operand of an M = 256 MMA is
-// split by N, so CTA c decodes only keys 64 c .. 64 c + 63 of a 128-key tile for Q K^T and only channels
-// 64 c .. 64 c + 63 for P V: half of every tile.  Keys are numbered along what the rows see (the sinks,
+// split by N, so CTA c decodes only keys 32 c .. 32 c + 31 of every 64 for Q K^T and only channels
+// 64 c .. 64 c + 63 for P V: half of everything.  Keys are numbered along what the rows see (the sinks,
 // then the window), so a tile has no gaps whatever the ring's offset; each producer thread looks its
 // rows' slots up.
-// Warp roles of each CTA (17 warps):
-//   warps 0-3, 4-7  softmax of Query tile 0 / 1: thread = Query row = TMEM lane;
-//   warp 8          allocates TMEM; in the even CTA one thread issues every MMA of the pair;
-//   warps 9-12      Key producers, warps 13-16 Value producers: codes two tiles ahead in registers,
-//                   decoded (one permute and one fp16 FMA per pair at 8 bits) into swizzled stages.
-// TMEM (512 columns): S0 | S1 | O0 | O1, P_x over S_x.  MMA order per tile: S0(j), PV1(j-1), S1(j),
-// PV0(j); the commit after S_x(j) also certifies PV_x(j-1), so softmax x may then rescale O_x.
+// Warp roles of each CTA (13 warps, so that a thread may hold 128 registers):
+//   warps 0-3, 4-7  softmax of Query tile 0 / 1: thread = Query row = TMEM lane, 64 logits at a time;
+//   warps 8-11      producers: codes two stages ahead in registers, decoded (one permute and one fp16
+//                   FMA per pair at 8 bits) into swizzled stages;
+//   warp 12         allocates TMEM; in the even CTA it issues every MMA of the pair.
+// TMEM (512 columns): S_x as two buffers of 64 keys, P_x over them, O_x.  Keys arrive in stages of 128
+// and are multiplied 64 at a time: as soon as PV_x(t) has been issued its buffer takes S_x(t + 2), so
+// the softmax warps find the next step's logits ready and the tensor pipe always holds work: per step
+// and tile 8 MMAs of 256 x 64 x 16 (43 cycles each, bound by reading Q from shared memory) and 4 of
+// 256 x 128 x 16 (64 cycles).  MMAs execute in issue order, so a buffer is written after the PV that
+// read it.
 // Every wait is bounded (about one second); on expiry QWM_ERR_DEVICE_TIMEOUT is recorded, every role
 // stops, outstanding MMAs are drained and TMEM is freed.
 #include "window.cuh"
@@ -26,9 +30,10 @@
 namespace {
 
 constexpr int D = win::D;
-constexpr int BM = 128, BN = 128, NQT = 2;
-constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kKWarp0 = 9, kVWarp0 = 13, kProdWarps = 4;
-constexpr int kThreads = 32 * (kSoftmaxWarps + 1 + 2 * kProdWarps);
+constexpr int BM = 128, BN = 128, NQT = 2;  // Query rows of a CTA tile, keys of a stage, CTA tiles
+constexpr int BS = 64;                      // keys of a step
+constexpr int kSoftmaxWarps = 8, kProdWarp0 = 8, kProdWarps = 4, kMmaWarp = 12;
+constexpr int kThreads = 32 * (kSoftmaxWarps + kProdWarps + 1);
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units the maximum may lag behind
 constexpr int kStages = 4;
@@ -45,7 +50,7 @@ constexpr int kSmemAlloc = kSmemBytes + 1024;
 
 struct Bars {
   uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
-  uint64_t s_full[2], p_ready[2], o_done, drain;
+  uint64_t s_full[2][2], p_ready[2][2], pv_done[2][2], o_done, drain;
 };
 
 __device__ __forceinline__ void fail(int *abort_flag, int32_t *status) {
@@ -109,65 +114,79 @@ struct RowOut {
   }
 };
 
-// A producer thread's share of a 128-key tile: four pieces of 16 channels.
+// A producer thread's share of a 128-key stage: four pieces of 16 channels.
 template <int BITS>
 struct Pieces {
   uint32_t c[4][BITS / 2];
-  uint32_t step;   // one byte per piece
+  uint32_t step[4];
 };
 
-// Producer thread of a pair CTA (rank cr): Keys: key rows 64 cr + 16 w + 4 i + lane / 8 (i = 0..3),
-// channels 16 (lane % 8); Values: key rows 32 w + 8 i + lane / 4, channels 64 cr + 16 (lane % 4).
+// One producer thread's side of Keys or Values in CTA cr of a pair.  Keys: rows r = 16 w + 4 i + lane / 4 % 4
+// (i = 0..3) of the CTA's half, key 64 (r / 32) + 32 cr + r % 32, channels 16 (lane % 4 + 4 (lane / 16));
+// Values: key rows 32 w + 8 i + lane / 4, channels 64 cr + 16 (lane % 4).  A quarter warp's 16-byte stores
+// take two rows, one of even and one of odd number, so the swizzle puts them into eight bank groups.
 template <int BITS, bool VAL>
-__device__ __forceinline__ void producer(const WindowAttend &a, unsigned char *sm, Bars &bars, int *abort_flag,
-                                         const win::Keys &keys, int64_t y, int j0, int J, int cr, int pr) {
-  volatile int *abort_v = abort_flag;
-  const int lane = pr & 31, w = pr >> 5;
-  const int row0 = VAL ? 32 * w + (lane >> 2) : 16 * w + (lane >> 3);   // row in the block of piece 0
-  constexpr int kRowStep = VAL ? 8 : 4;
-  const int piece = VAL ? (lane & 3) : (lane & 7);
-  const int ch = VAL ? 64 * cr + 16 * piece : 16 * piece;
-  const int key0 = VAL ? row0 : 64 * cr + row0;
-  const int64_t head_row = y * (a.w.sink + a.w.ring);
-  const uint8_t *codes = (VAL ? a.w.v_codes : a.w.k_codes) + head_row * (D * BITS / 8) + ch * BITS / 8;
-  const uint8_t *steps = (VAL ? a.w.v_step : a.w.k_step) + head_row * win::kSteps + ch / win::kGroup;
-  const uint32_t sink = (uint32_t)a.w.sink, ring = (uint32_t)a.w.ring;
-  uint64_t *empty = VAL ? bars.v_empty : bars.k_empty;
-  const uint32_t full_base = tc::mapa(tc::smem_u32(VAL ? &bars.v_full[0] : &bars.k_full[0]), 0);
-  const uint32_t block0 = tc::smem_u32(sm + (VAL ? OFF_V : OFF_K)) + (VAL ? 0u : (uint32_t)(piece >> 2) * kBlkH);
-  constexpr uint32_t kStage = VAL ? (uint32_t)kBlk : 2u * kBlkH;
-  const uint32_t chunk = 2u * (uint32_t)(piece & 3);
-  // Keys: the upper four lanes of a row store their second chunk first, so that a quarter warp's eight
-  // 16-byte stores fall into eight different bank groups
-  const uint32_t flip = (!VAL && (piece >> 2)) ? 1u : 0u;
+struct Producer {
+  static constexpr int kRowStep = VAL ? 8 : 4;
+  static constexpr uint32_t kStage = VAL ? (uint32_t)kBlk : 2u * kBlkH;
+  static constexpr int kRowBytes = D * BITS / 8;
+  const uint8_t *codes, *steps;   // of slot key0
+  int key0;
+  uint32_t dst[2][2];             // shared addresses of the piece's two chunks in even and odd rows i
 
-  auto load = [&](int j, Pieces<BITS> &p) {
-    p.step = 0u;
+  __device__ __forceinline__ Producer(const WindowAttend &a, unsigned char *sm, int64_t y, int cr, int w, int lane) {
+    const int row0 = VAL ? 32 * w + (lane >> 2) : 16 * w + ((lane >> 2) & 3);
+    const int piece = VAL ? (lane & 3) : (lane & 3) + 4 * (lane >> 4);
+    const int ch = VAL ? 64 * cr + 16 * piece : 16 * piece;
+    key0 = VAL ? row0 : BS * (w >> 1) + 32 * cr + (row0 & 31);
+    const int64_t head_row = y * (a.w.sink + a.w.ring) + key0;
+    codes = (VAL ? a.w.v_codes : a.w.k_codes) + head_row * kRowBytes + ch * BITS / 8;
+    steps = (VAL ? a.w.v_step : a.w.k_step) + head_row * win::kSteps + ch / win::kGroup;
+    const uint32_t block = tc::smem_u32(sm + (VAL ? OFF_V : OFF_K)) + (VAL ? 0u : (uint32_t)(piece >> 2) * kBlkH);
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const int v = (j0 + j) * BN + key0 + kRowStep * i;
-      if (v < keys.total) {
-        const uint64_t s = keys.slot(v, sink, ring);
-        if (BITS == 8) {
-          const uint4 x = __ldg((const uint4 *)(codes + s * (D * BITS / 8)));
-          p.c[i][0] = x.x; p.c[i][1] = x.y; p.c[i][2 % (BITS / 2)] = x.z; p.c[i][3 % (BITS / 2)] = x.w;
-        } else {
-          const uint2 x = __ldg((const uint2 *)(codes + s * (D * BITS / 8)));
-          p.c[i][0] = x.x; p.c[i][1] = x.y;
-        }
-        p.step |= (uint32_t)__ldg(steps + s * win::kSteps) << (8 * i);
-      } else {   // past the last key: a zero row
+    for (int i = 0; i < 2; i++)
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        const uint32_t row = (uint32_t)(row0 + kRowStep * i), chunk = 2u * (uint32_t)(piece & 3) + h;
+        dst[i][h] = block + row * 128u + ((chunk ^ (row & 7u)) << 4);
+      }
+  }
+  __device__ __forceinline__ void load1(const uint8_t *c, const uint8_t *s, Pieces<BITS> &p, int i) const {
+    if (BITS == 8) {
+      const uint4 x = __ldg((const uint4 *)c);
+      p.c[i][0] = x.x; p.c[i][1] = x.y; p.c[i][2 % (BITS / 2)] = x.z; p.c[i][3 % (BITS / 2)] = x.w;
+    } else {
+      const uint2 x = __ldg((const uint2 *)c);
+      p.c[i][0] = x.x; p.c[i][1] = x.y;
+    }
+    p.step[i] = __ldg(s);
+  }
+  // The codes of the stage of keys v0 .. v0 + 127; `slot0` >= 0: they lie in consecutive slots from there.
+  __device__ __forceinline__ void load(const win::Keys &keys, int v0, int64_t slot0, uint32_t sink, uint32_t ring,
+                                       Pieces<BITS> &p) const {
+    if (slot0 >= 0) {
+      const uint8_t *c = codes + slot0 * kRowBytes, *s = steps + slot0 * win::kSteps;
+#pragma unroll
+      for (int i = 0; i < 4; i++) load1(c + i * kRowStep * kRowBytes, s + i * kRowStep * win::kSteps, p, i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const int v = v0 + key0 + kRowStep * i;
+        p.step[i] = 0u;   // past the last key: a zero row
 #pragma unroll
         for (int u = 0; u < BITS / 2; u++) p.c[i][u] = 0u;
+        if (v < keys.total) {
+          const int64_t d = (int64_t)keys.slot(v, sink, ring) - key0;
+          load1(codes + d * kRowBytes, steps + d * win::kSteps, p, i);
+        }
       }
     }
-  };
-  auto store = [&](int stage, const Pieces<BITS> &p) {
-    const uint32_t block = block0 + (uint32_t)stage * kStage;
+  }
+  __device__ __forceinline__ void store(uint32_t stage, const Pieces<BITS> &p) const {
 #pragma unroll
     for (int i = 0; i < 4; i++) {
       uint32_t s2, n2, d[8];
-      win::step_consts<BITS>((p.step >> (8 * i)) & 0xFFu, s2, n2);
+      win::step_consts<BITS>(p.step[i], s2, n2);
       if (BITS == 8) {
 #pragma unroll
         for (int u = 0; u < 4; u++) win::decode8(p.c[i][u % (BITS / 2)], s2, n2, d[2 * u], d[2 * u + 1]);
@@ -178,32 +197,12 @@ __device__ __forceinline__ void producer(const WindowAttend &a, unsigned char *s
         win::decode4(p.c[i][1], s2, n2, q);
         d[4] = q[0]; d[5] = q[1]; d[6] = q[2]; d[7] = q[3];
       }
-      const uint32_t row = (uint32_t)(row0 + kRowStep * i), rb = block + row * 128u, rx = row & 7u;
-      const uint4 lo = make_uint4(d[0], d[1], d[2], d[3]), hi = make_uint4(d[4], d[5], d[6], d[7]);
-      tc::sts128(rb + (((chunk + flip) ^ rx) << 4), flip ? hi : lo);
-      tc::sts128(rb + (((chunk + 1u - flip) ^ rx) << 4), flip ? lo : hi);
+      const uint32_t at = stage * kStage + (uint32_t)(i >> 1) * (2u * kRowStep * 128u);
+      tc::sts128(dst[i & 1][0] + at, make_uint4(d[0], d[1], d[2], d[3]));
+      tc::sts128(dst[i & 1][1] + at, make_uint4(d[4], d[5], d[6], d[7]));
     }
-  };
-
-  Pieces<BITS> A, B;
-  load(0, A);
-  if (J > 1) load(1, B);
-  auto step = [&](int j, Pieces<BITS> &cur) -> bool {
-    const int s = j % kStages;
-    if (j >= kStages && !tc::mbar_wait(&empty[s], (j / kStages - 1) & 1, kWaitNs)) fail(abort_flag, a.status);
-    if (__any_sync(0xffffffffu, *abort_v != 0)) return false;  // warp-uniform exit
-    store(s, cur);
-    tc::fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) tc::mbar_arrive_remote(full_base + 8u * (uint32_t)s);
-    if (j + 2 < J) load(j + 2, cur);
-    return true;
-  };
-  for (int j = 0; j < J; j += 2) {
-    if (!step(j, A)) break;
-    if (j + 1 < J && !step(j + 1, B)) break;
   }
-}
+};
 
 template <int BITS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
@@ -213,16 +212,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __shared__ Bars bars;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_flag;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int64_t y = blockIdx.y, b = y / a.w.kv_heads;
-  const int kvh = (int)(y - b * a.w.kv_heads), split = (int)blockIdx.z;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  // pairs in launch order: every Key head's full items, head by head (its cache stays in L2), then every
+  // head's last item, whose second Query tile may be empty: the short ones fill the last wave's gaps
+  const int64_t pair = blockIdx.x >> 1, heads = (int64_t)a.w.batch * a.w.kv_heads;
+  const int64_t items = (a.rows + kPairRows - 1) / kPairRows, early = heads * (items - 1);
+  const int64_t y = pair < early ? pair / (items - 1) : pair - early, b = y / a.w.kv_heads;
+  const int64_t item = pair < early ? pair - y * (items - 1) : items - 1;
+  const int kvh = (int)(y - b * a.w.kv_heads), split = (int)blockIdx.y;
   const int cr = (int)tc::cluster_ctarank();
   volatile int *abort_v = &abort_flag;
 
   const int64_t q0 = a.q_start[b];
   int64_t nq = a.q_count ? (int64_t)a.q_count[b] : a.nq;
   nq = nq < a.nq ? nq : a.nq;
-  const int64_t pair0 = (int64_t)(blockIdx.x >> 1) * kPairRows;
+  const int64_t pair0 = item * kPairRows;
   const int64_t rows = nq * a.group;              // live rows of this Key head
   if (q0 < 0 || pair0 >= rows) return;            // the same in both CTAs
   const win::Seq seq{a.length[b], a.w.sink, a.w.ring, a.tpf, a.frames};
@@ -280,8 +284,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       tc::mbar_init(&bars.v_empty[i], 1);
     }
     for (int i = 0; i < 2; i++) {
-      tc::mbar_init(&bars.s_full[i], 1);
-      tc::mbar_init(&bars.p_ready[i], 8);              // both CTAs' 4 softmax warps of tile i
+      tc::mbar_init(&bars.s_full[i][0], 1);
+      tc::mbar_init(&bars.s_full[i][1], 1);
+      // both CTAs' 4 softmax warps of tile i; one barrier per buffer, as a warp may finish its next step
+      // before another has finished this one
+      tc::mbar_init(&bars.p_ready[i][0], 8);
+      tc::mbar_init(&bars.p_ready[i][1], 8);
+      tc::mbar_init(&bars.pv_done[i][0], 1);
+      tc::mbar_init(&bars.pv_done[i][1], 1);
     }
     tc::mbar_init(&bars.o_done, 1);
     tc::mbar_init(&bars.drain, 1);
@@ -298,14 +308,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc::cluster_sync();  // both CTAs' barriers exist before the first arrival from the peer
   tc::fence_after_sync();
   const uint32_t tmem = tmem_base_sh;
+  const int key_end = keys.total < (j0 + J) * BN ? keys.total : (j0 + J) * BN;
+  const int steps = (key_end - j0 * BN + BS - 1) / BS;   // 2 J, or one less when the last stage is half empty
 
   if (warp < kSoftmaxWarps) {
     // ======================= softmax (Query tile x, row = TMEM lane) =======================
     const int x = warp / 4, sub = warp % 4;
-    const int Jx = (x == 1 && skip1) ? 0 : J;
+    const int Tx = (x == 1 && skip1) ? 0 : steps;
     const uint32_t lane_addr = (uint32_t)(32 * sub) << 16;
-    const uint32_t tS = tmem + lane_addr + 128u * x, tO = tmem + lane_addr + 256u + 128u * x;
-    const uint32_t p_ready0 = tc::mapa(tc::smem_u32(&bars.p_ready[x]), 0);
+    const uint32_t tS0 = tmem + lane_addr + 128u * x, tO = tmem + lane_addr + 256u + 128u * x;
+    const uint32_t p_ready0 = tc::mapa(tc::smem_u32(&bars.p_ready[x][0]), 0);
     const float sl2 = a.scale_log2;
     const uint64_t sc2 = pk64(sl2, sl2);
     const int64_t w0 = row_base + (int64_t)x * 2 * BM + 32 * sub;   // this warp's first row
@@ -319,87 +331,79 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     float m_used = -INFINITY;
     uint64_t acc0 = 0ull, acc1 = 0ull;
     bool ok = true;
-    for (int j = 0; j < Jx; j++) {
-      const int v0 = (j0 + j) * BN;
-      const bool full = every.see(v0, v0 + BN);
-      if (!tc::mbar_wait(&bars.s_full[x], j & 1, kWaitNs)) fail(&abort_flag, a.status);
+    for (int t = 0; t < Tx; t++) {
+      const int v0 = j0 * BN + t * BS;
+      const bool full = every.see(v0, v0 + BS);
+      const uint32_t tS = tS0 + (uint32_t)(t & 1) * BS;
+      if (!tc::mbar_wait(&bars.s_full[x][t & 1], (t >> 1) & 1, kWaitNs)) fail(&abort_flag, a.status);
       if (*abort_v) { ok = false; break; }
       tc::fence_after_sync();
-      // one pass over the tile, 32 columns at a time: their maximum, then their exponentials with the
-      // running maximum m_used; when it grows by more than 2^8 (rare after the first columns) the sum,
-      // O and the P columns already stored for this tile are first rescaled
-      uint32_t s[32];
-#pragma unroll 1
-      for (int cq = 0; cq < 4; cq++) {
-        tc::tmem_ld16(tS + 32u * cq, s);
-        tc::tmem_ld16(tS + 32u * cq + 16u, s + 16);
-        tc::tmem_ld_wait();
-        if (!full) {
-          const int v = v0 + 32 * cq;
+      // the step's logits at once: their maximum, then their exponentials with the running maximum
+      // m_used; when it grows by more than 2^8 (rare after the first step) the sum and O are rescaled
+      uint32_t s[BS];
+#pragma unroll
+      for (int i = 0; i < BS; i += 16) tc::tmem_ld16(tS + (uint32_t)i, s + i);
+      tc::tmem_ld_wait();
+      if (!full) {
+#pragma unroll
+        for (int h = 0; h < BS / 32; h++) {
+          const int v = v0 + 32 * h;
           const uint32_t seen = low_bits(mine.c0 - v) | (low_bits(mine.c2 - v) & ~low_bits(mine.c1 - v));
 #pragma unroll
           for (int i = 0; i < 32; i++)
-            if (!((seen >> i) & 1u)) s[i] = 0xFF800000u;  // -inf: weight exactly 0
+            if (!((seen >> i) & 1u)) s[32 * h + i] = 0xFF800000u;  // -inf: weight exactly 0
         }
-        float mx0 = -INFINITY, mx1 = -INFINITY;
+      }
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-          mx0 = tc::max3(mx0, __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
-          mx1 = tc::max3(mx1, __uint_as_float(s[i + 2]), __uint_as_float(s[i + 3]));
-        }
-        const float m_new = fmaxf(m_used, fmaxf(mx0, mx1) * sl2);
-        if (__any_sync(0xffffffffu, m_new > m_used + kRescaleThreshold)) {
-          const float alpha = m_new == -INFINITY ? 1.f : tc::ex2_approx(m_used - m_new);
-          const uint64_t a2 = pk64(alpha, alpha);
-          acc0 = tc::fma2(acc0, a2, 0ull);
-          acc1 = tc::fma2(acc1, a2, 0ull);
-          if (j > 0) {  // O of the earlier tiles (complete: S_x(j) finished after PV_x(j-1))
-#pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-              uint32_t o[32];
-              tc::tmem_ld32(tO + c, o);
-              tc::tmem_ld_wait();
+      for (int i = 0; i < BS; i += 8)
 #pragma unroll
-              for (int i = 0; i < 32; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-              tc::tmem_st32(tO + c, o);
-            }
-          }
-          tc::tmem_st_wait();
+        for (int u = 0; u < 4; u++)
+          mx[u] = tc::max3(mx[u], __uint_as_float(s[i + 2 * u]), __uint_as_float(s[i + 2 * u + 1]));
+      const float m_new = fmaxf(m_used, tc::max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * sl2);
+      if (__any_sync(0xffffffffu, m_new > m_used + kRescaleThreshold)) {
+        const float alpha = m_new == -INFINITY ? 1.f : tc::ex2_approx(m_used - m_new);
+        const uint64_t a2 = pk64(alpha, alpha);
+        acc0 = tc::fma2(acc0, a2, 0ull);
+        acc1 = tc::fma2(acc1, a2, 0ull);
+        if (t > 0) {  // O of the earlier steps, once PV_x(t-1) has been added (PV_x(t) waits for this warp)
+          if (!tc::mbar_wait(&bars.pv_done[x][(t - 1) & 1], ((t - 1) >> 1) & 1, kWaitNs)) fail(&abort_flag, a.status);
+          tc::fence_after_sync();
 #pragma unroll 1
-          for (int pc = 0; pc < cq; pc++) {  // P columns of this tile already written
-            uint32_t pw[16];
-            tc::tmem_ld16(tS + 16u * pc, pw);
+          for (int c = 0; c < D; c += 16) {
+            uint32_t o[16];
+            tc::tmem_ld16(tO + c, o);
             tc::tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 16; i++) {
-              const float2 v = __half22float2(*(const __half2 *)&pw[i]);
-              pw[i] = tc::pack_f16x2(v.x * alpha, v.y * alpha);
-            }
-            tc::tmem_st16(tS + 16u * pc, pw);
+            for (int i = 0; i < 16; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+            tc::tmem_st16(tO + c, o);
           }
-          m_used = m_new;
         }
-        const float mneg = m_used == -INFINITY ? 0.f : -m_used;  // a row that has seen no key yet
-        const uint64_t nm2 = pk64(mneg, mneg);
+        m_used = m_new;
+      }
+      const float mneg = m_used == -INFINITY ? 0.f : -m_used;  // a row that has seen no key yet
+      const uint64_t nm2 = pk64(mneg, mneg);
+#pragma unroll
+      for (int h = 0; h < BS / 32; h++) {
         uint32_t pw[16];
 #pragma unroll
         for (int i = 0; i < 16; i++) {  // packed fp32 pairs: S * scale - m, then 2^x
-          const uint64_t x2 = tc::fma2(pk64(s[2 * i], s[2 * i + 1]), sc2, nm2);
+          const uint64_t x2 = tc::fma2(pk64(s[32 * h + 2 * i], s[32 * h + 2 * i + 1]), sc2, nm2);
           const float e0 = tc::ex2_approx(tc::f2lo(x2)), e1 = tc::ex2_approx(tc::f2hi(x2));
           const uint64_t e2 = pk64(e0, e1);
           if (i & 1) acc1 = tc::add2(acc1, e2);
           else acc0 = tc::add2(acc0, e2);
           pw[i] = tc::pack_f16x2(e0, e1);
         }
-        tc::tmem_st16(tS + 16u * cq, pw);  // P (fp16 pairs) overlays logits already read
+        tc::tmem_st16(tS + 16u * h, pw);  // P (fp16 pairs) over the logits
       }
       tc::tmem_st_wait();
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive_remote(p_ready0);
+      if (lane == 0) tc::mbar_arrive_remote(p_ready0 + 8u * (uint32_t)(t & 1));
     }
-    if (ok && Jx > 0 && !tc::mbar_wait(&bars.o_done, 0, kWaitNs)) fail(&abort_flag, a.status);
-    if (ok && Jx > 0 && !*abort_v) {
+    if (ok && Tx > 0 && !tc::mbar_wait(&bars.o_done, 0, kWaitNs)) fail(&abort_flag, a.status);
+    if (ok && Tx > 0 && !*abort_v) {
       tc::fence_after_sync();
       const uint64_t lsum = tc::add2(acc0, acc1);
       const float l = tc::f2lo(lsum) + tc::f2hi(lsum);
@@ -431,76 +435,127 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == kMmaWarp) {
-    // ======================= MMA issue: one thread of the even CTA, for the pair =======================
-    if (cr == 0 && lane == 0) {
-      const uint32_t idesc = tc::idesc_f16_f32(2 * BM, BN);
-      const uint32_t idesc_pv = tc::idesc_f16_f32_bmn(2 * BM, D);
-      const uint32_t tS[2] = {tmem, tmem + 128u}, tO[2] = {tmem + 256u, tmem + 384u};
-      const uint32_t sQ = tc::smem_u32(sm + OFF_Q), sK = tc::smem_u32(sm + OFF_K), sV = tc::smem_u32(sm + OFF_V);
+    // ======================= MMA issue: the even CTA's warp 8, for the pair =======================
+    if (cr == 0) {
+      constexpr uint32_t idesc = tc::idesc_f16_f32(2 * BM, BS), idesc_pv = tc::idesc_f16_f32_bmn(2 * BM, D);
       constexpr uint16_t kBoth = 3;
-      int prev_stage = 0;
+      // broadcast, so that everything derived from them is the warp's and not a lane's
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), s0 = __shfl_sync(0xffffffffu, tc::smem_u32(sm), 0);
+      const int n = __shfl_sync(0xffffffffu, steps, 0);
+      const bool one = __shfl_sync(0xffffffffu, (int)skip1, 0) != 0;
+      const uint64_t dq = tc::desc_sw128(s0 + OFF_Q), dk = tc::desc_sw128(s0 + OFF_K);
+      const uint64_t dv = tc::desc_sw128_mn(s0 + OFF_V, kBlk, 1024);
       bool ok = true;
-      auto qk = [&](int x, int s) {
-#pragma unroll
-        for (int kk = 0; kk < D / 16; kk++) {
-          const uint32_t qo = (uint32_t)((kk / 4) * kBlk + 32 * (kk % 4));
-          const uint32_t ko = (uint32_t)((kk / 4) * kBlkH + 32 * (kk % 4));
-          tc::mma2_ss(tS[x], tc::desc_sw128(sQ + (x * 2) * kBlk + qo), tc::desc_sw128(sK + s * 2 * kBlkH + ko), idesc,
-                      kk > 0);
-        }
+      auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {   // the warp's common answer
+        return __all_sync(0xffffffffu, tc::mbar_wait_cluster(bar, parity, kWaitNs) && !*abort_v);
       };
-      auto pv = [&](int x, int s, bool first) {
+      auto qk = [&](int x, int t) {
+        const uint32_t ko = (uint32_t)((t >> 1) % kStages) * 2 * kBlkH + (uint32_t)(t & 1) * 32 * 128;
+        const uint64_t da = dq + (uint64_t)(x * 2 * kBlk / 16), db = dk + (uint64_t)(ko / 16);
+        const uint32_t d = tm + 128u * x + (uint32_t)(t & 1) * BS;
 #pragma unroll
-        for (int kk = 0; kk < BN / 16; kk++)
-          tc::mma2_ts(tO[x], tS[x] + 8u * kk, tc::desc_sw128_mn(sV + s * kBlk + 2048u * kk, kBlk, 1024), idesc_pv,
-                      (!first || kk > 0));
+        for (int kk = 0; kk < D / 16; kk++)
+          tc::mma2_ss_warp(d, da + (uint64_t)(((kk / 4) * kBlk + 32 * (kk % 4)) / 16),
+                           db + (uint64_t)(((kk / 4) * kBlkH + 32 * (kk % 4)) / 16), idesc, kk > 0);
+        tc::mma2_commit_warp(&bars.s_full[x][t & 1], kBoth);
       };
-      for (int j = 0; ok && j < J; j++) {
-        const int s = j % kStages;
-        const uint32_t ph = (uint32_t)(j / kStages) & 1u;
-        ok = tc::mbar_wait_cluster(&bars.k_full[s], ph, kWaitNs) && !*abort_v;
+      auto pv = [&](int x, int t) {
+        const uint32_t vo = (uint32_t)((t >> 1) % kStages) * kBlk + (uint32_t)(t & 1) * BS * 128;
+        const uint64_t db = dv + (uint64_t)(vo / 16);
+        const uint32_t p = tm + 128u * x + (uint32_t)(t & 1) * BS;
+#pragma unroll
+        for (int kk = 0; kk < BS / 16; kk++)
+          tc::mma2_ts_warp(tm + 256u + 128u * x, p + 8u * kk, db + (uint64_t)(2048 * kk / 16), idesc_pv,
+                           (t > 0 || kk > 0));
+        tc::mma2_commit_warp(&bars.pv_done[x][t & 1], kBoth);
+      };
+      auto stage_ends = [&](int t) { return (t & 1) || t + 1 == n; };
+      auto keys_there = [&](int t) {   // the Keys of step t (a stage's first step waits for it)
+        return (t & 1) || wait(&bars.k_full[(t >> 1) % kStages], ((t >> 1) / kStages) & 1);
+      };
+      for (int t = 0; ok && t < 2 && t < n; t++) {
+        ok = keys_there(t);
         if (!ok) break;
         tc::fence_after_sync();
-        qk(0, s);
-        tc::mma2_commit(&bars.s_full[0], kBoth);
-        if (j > 0 && !skip1) {
-          ok = tc::mbar_wait_cluster(&bars.p_ready[1], (j - 1) & 1, kWaitNs) && !*abort_v;
+        qk(0, t);
+        if (!one) qk(1, t);
+        if (stage_ends(t)) tc::mma2_commit_warp(&bars.k_empty[(t >> 1) % kStages], kBoth);
+      }
+      for (int t = 0; ok && t < n; t++) {
+        if (!(t & 1)) ok = wait(&bars.v_full[(t >> 1) % kStages], ((t >> 1) / kStages) & 1);
+        ok = ok && wait(&bars.p_ready[0][t & 1], (t >> 1) & 1);
+        if (!ok) break;
+        tc::fence_after_sync();
+        pv(0, t);
+        if (t + 2 < n) {
+          ok = keys_there(t + 2);
           if (!ok) break;
           tc::fence_after_sync();
-          pv(1, prev_stage, j - 1 == 0);
-          tc::mma2_commit(&bars.v_empty[prev_stage], kBoth);
+          qk(0, t + 2);
         }
-        if (!skip1) {
-          qk(1, s);
-          tc::mma2_commit(&bars.s_full[1], kBoth);
+        if (!one) {
+          ok = wait(&bars.p_ready[1][t & 1], (t >> 1) & 1);
+          if (!ok) break;
+          tc::fence_after_sync();
+          pv(1, t);
+          if (t + 2 < n) qk(1, t + 2);
         }
-        tc::mma2_commit(&bars.k_empty[s], kBoth);
-        ok = tc::mbar_wait_cluster(&bars.v_full[s], ph, kWaitNs) &&
-             tc::mbar_wait_cluster(&bars.p_ready[0], j & 1, kWaitNs) && !*abort_v;
-        if (!ok) break;
-        tc::fence_after_sync();
-        pv(0, s, j == 0);
-        if (skip1) tc::mma2_commit(&bars.v_empty[s], kBoth);  // no second tile reads this stage
-        prev_stage = s;
+        if (stage_ends(t)) tc::mma2_commit_warp(&bars.v_empty[(t >> 1) % kStages], kBoth);
+        if (t + 2 < n && stage_ends(t + 2)) tc::mma2_commit_warp(&bars.k_empty[((t + 2) >> 1) % kStages], kBoth);
       }
-      if (ok) {
-        if (!skip1) {
-          ok = tc::mbar_wait_cluster(&bars.p_ready[1], (J - 1) & 1, kWaitNs) && !*abort_v;
-          if (ok) {
-            tc::fence_after_sync();
-            pv(1, prev_stage, J - 1 == 0);
-          }
-        }
-        if (ok) tc::mma2_commit(&bars.o_done, kBoth);
-      }
+      if (ok) tc::mma2_commit_warp(&bars.o_done, kBoth);
       if (!ok) fail(&abort_flag, a.status);
-      tc::mma2_commit(&bars.drain, 1);  // every MMA issued above completes before TMEM is released
+      tc::mma2_commit_warp(&bars.drain, 1);  // every MMA issued above completes before TMEM is released
       if (!tc::mbar_wait(&bars.drain, 0, kWaitNs)) qwm_dev_error(a.status, QWM_ERR_DEVICE_TIMEOUT);
     }
-  } else if (warp < kVWarp0) {
-    producer<BITS, false>(a, sm, bars, &abort_flag, keys, y, j0, J, cr, tid - 32 * kKWarp0);
   } else {
-    producer<BITS, true>(a, sm, bars, &abort_flag, keys, y, j0, J, cr, tid - 32 * kVWarp0);
+    // ======================= producers: Keys, then Values, of every stage =======================
+    const int w = warp - kProdWarp0;
+    const Producer<BITS, false> pk(a, sm, y, cr, w, lane);
+    const Producer<BITS, true> pv(a, sm, y, cr, w, lane);
+    const uint32_t sink = (uint32_t)a.w.sink, ring = (uint32_t)a.w.ring;
+    auto slot0_of = [&](int v0) -> int64_t {   // the slot of key v0 when the stage's slots are consecutive
+      const uint32_t s = keys.slot(v0, sink, ring);
+      return v0 + BN <= keys.total && keys.slot(v0 + BN - 1, sink, ring) == s + BN - 1 ? (int64_t)s : -1;
+    };
+    // the even CTA's full barriers (consecutive 8-byte words), as shared::cluster addresses
+    const uint32_t k_full = tc::mapa(tc::smem_u32(&bars.k_full[0]), 0), v_full = tc::mapa(tc::smem_u32(&bars.v_full[0]), 0);
+    auto hand_over = [&](uint32_t full) {
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive_remote(full);
+    };
+    auto free_again = [&](uint64_t *empty, int j) -> bool {   // the stage's previous contents are consumed
+      if (j >= kStages && !tc::mbar_wait(empty, (j / kStages - 1) & 1, kWaitNs)) fail(&abort_flag, a.status);
+      return !__any_sync(0xffffffffu, *abort_v != 0);         // warp-uniform exit
+    };
+    Pieces<BITS> k0, v0, k1, v1;
+    int64_t at = slot0_of(j0 * BN);
+    pk.load(keys, j0 * BN, at, sink, ring, k0);
+    pv.load(keys, j0 * BN, at, sink, ring, v0);
+    if (J > 1) {
+      at = slot0_of((j0 + 1) * BN);
+      pk.load(keys, (j0 + 1) * BN, at, sink, ring, k1);
+      pv.load(keys, (j0 + 1) * BN, at, sink, ring, v1);
+    }
+    auto stage = [&](int j, Pieces<BITS> &k, Pieces<BITS> &v) -> bool {
+      const int s = j % kStages;
+      if (!free_again(&bars.k_empty[s], j)) return false;
+      pk.store((uint32_t)s, k);
+      hand_over(k_full + 8u * (uint32_t)s);
+      const int next = (j0 + j + 2) * BN;
+      const int64_t slot0 = j + 2 < J ? slot0_of(next) : 0;
+      if (j + 2 < J) pk.load(keys, next, slot0, sink, ring, k);
+      if (!free_again(&bars.v_empty[s], j)) return false;
+      pv.store((uint32_t)s, v);
+      hand_over(v_full + 8u * (uint32_t)s);
+      if (j + 2 < J) pv.load(keys, next, slot0, sink, ring, v);
+      return true;
+    };
+    for (int j = 0; j < J; j += 2) {
+      if (!stage(j, k0, v0)) break;
+      if (j + 1 < J && !stage(j + 1, k1, v1)) break;
+    }
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -516,8 +571,9 @@ cudaError_t launch_bits(const WindowAttend &a, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(window_attend_kernel<BITS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        kSmemAlloc);
   if (e != cudaSuccess) return e;
-  const dim3 grid((unsigned)(2 * ((a.rows + kPairRows - 1) / kPairRows)), (unsigned)(a.w.batch * a.w.kv_heads),
-                  (unsigned)a.splits);
+  const int64_t pairs = (int64_t)a.w.batch * a.w.kv_heads * ((a.rows + kPairRows - 1) / kPairRows);
+  if (2 * pairs > INT32_MAX) return cudaErrorInvalidValue;
+  const dim3 grid((unsigned)(2 * pairs), (unsigned)a.splits);
   window_attend_kernel<BITS><<<grid, kThreads, kSmemAlloc, st>>>(a);
   return cudaGetLastError();
 }
