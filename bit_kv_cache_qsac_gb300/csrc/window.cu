@@ -110,7 +110,7 @@ template <int BITS>
 __global__ void __launch_bounds__(kThreads)
     window_read_kernel(qwm_window w, const int64_t *__restrict__ start, const int64_t *__restrict__ length,
                        const int32_t *__restrict__ count, int64_t n, uint16_t *__restrict__ k_hat,
-                       uint16_t *__restrict__ v_hat, int heads_per_block) {
+                       uint16_t *__restrict__ v_hat, int heads_per_block, win::Bases bases) {
   const int v = threadIdx.x & 15, row = threadIdx.x >> 4;
   const int64_t tok = (int64_t)blockIdx.x * kRows + row;
   if (tok >= (int64_t)w.batch * n) return;
@@ -136,10 +136,10 @@ __global__ void __launch_bounds__(kThreads)
         win::step_consts<BITS>(steps[r * win::kSteps + (v >> 2)], s2, n2);
         if (BITS == 8) {
           const uint2 x = *(const uint2 *)(codes + r * win::D + 8 * v);
-          win::decode8(x.x, s2, n2, pr[0], pr[1]);
-          win::decode8(x.y, s2, n2, pr[2], pr[3]);
+          win::decode8(x.x, s2, n2, bases, pr[0], pr[1]);
+          win::decode8(x.y, s2, n2, bases, pr[2], pr[3]);
         } else {
-          win::decode4(*(const uint32_t *)(codes + r * (win::D / 2) + 4 * v), s2, n2, pr);
+          win::decode4(*(const uint32_t *)(codes + r * (win::D / 2) + 4 * v), s2, n2, bases, pr);
         }
 #pragma unroll
         for (int u = 0; u < 4; u++) {
@@ -192,8 +192,8 @@ cudaError_t launch_window_read(const qwm_window &w, const int64_t *start, const 
   const int hpb = heads_per_block(tiles, w.kv_heads, num_sms);
   const dim3 grid((unsigned)tiles, (unsigned)((w.kv_heads + hpb - 1) / hpb));
   if (w.bits == 8)
-    window_read_kernel<8><<<grid, kThreads, 0, st>>>(w, start, length, count, n, k_hat, v_hat, hpb);
+    window_read_kernel<8><<<grid, kThreads, 0, st>>>(w, start, length, count, n, k_hat, v_hat, hpb, win::kBases);
   else
-    window_read_kernel<4><<<grid, kThreads, 0, st>>>(w, start, length, count, n, k_hat, v_hat, hpb);
+    window_read_kernel<4><<<grid, kThreads, 0, st>>>(w, start, length, count, n, k_hat, v_hat, hpb, win::kBases);
   return cudaGetLastError();
 }

@@ -171,27 +171,53 @@ __device__ __forceinline__ uint32_t code_of(float x, float inv, float bias) {
   return __float_as_uint(__fadd_rn(snap, 0x1.8p23f + bias)) & 0xFFu;
 }
 
-// Decode constants of a step byte: s and -bias' s in both halves, where bias' is the integer that the
-// code's fp16 bit pattern below stands above the signed code (1152 or 72; 1152 s and 72 s are exact and
-// finite for every step up to step_max).  (pattern) s - bias' s in one fp16 FMA is then exactly code * s.
+// Decode constants of a step: s and -bias' s in both halves, where bias' is the integer that a code's fp16
+// bit pattern below stands above the signed code (1152, or 72; 1152 s and 72 s are exact and finite for
+// every step up to step_max).  (pattern) s - bias' s in one fp16 FMA is then exactly code * s.
+template <int BITS>
+__device__ __forceinline__ void step_consts2(uint32_t s2, uint32_t &n2) {
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(n2) : "r"(s2), "r"(BITS == 8 ? 0xE480E480u : 0xD480D480u));
+}
 template <int BITS>
 __device__ __forceinline__ void step_consts(uint32_t byte, uint32_t &s2, uint32_t &n2) {
-  const uint32_t s = byte << 7;
-  s2 = s | (s << 16);
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(n2) : "r"(s2), "r"(BITS == 8 ? 0xE480E480u : 0xD480D480u));
+  s2 = byte * 0x00800080u;   // byte << 7 in both halves
+  step_consts2<BITS>(s2, n2);
+}
+
+// fp16 bit patterns that codes are placed into: 0x6400 = 1024 (ulp 1) and 0x5400 = 64 (ulp 1/16), in both
+// halves.  They are kernel arguments, not literals: a three-input logic instruction holds one literal,
+// so (x & mask) | base is one instruction when `base` is in a register and two when it is not.
+struct Bases {
+  uint32_t k1024, k64;
+};
+constexpr Bases kBases = {0x64006400u, 0x54005400u};
+template <uint32_t MASK>
+__device__ __forceinline__ uint32_t place(uint32_t x, uint32_t base) {   // (x & MASK) | base
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(x), "n"(MASK), "r"(base));
+  return d;
 }
 
 // 8 bits: four codes (one word) -> fp16 pairs of channels (0, 1) and (2, 3).
-__device__ __forceinline__ void decode8(uint32_t x, uint32_t s2, uint32_t n2, uint32_t &p0, uint32_t &p1) {
-  p0 = tc::hfma2(__byte_perm(x, 0x64646464u, 0x4140), s2, n2);   // fp16 bits 0x64cc = 1024 + c
-  p1 = tc::hfma2(__byte_perm(x, 0x64646464u, 0x4342), s2, n2);
+__device__ __forceinline__ void decode8(uint32_t x, uint32_t s2, uint32_t n2, const Bases &c, uint32_t &p0, uint32_t &p1) {
+  p0 = tc::hfma2(__byte_perm(x, c.k1024, 0x5150), s2, n2);   // fp16 bits 0x64cc = 1024 + c
+  p1 = tc::hfma2(__byte_perm(x, c.k1024, 0x5352), s2, n2);
 }
-// 4 bits: eight codes (one word) -> fp16 pairs of channels (0, 1), (2, 3), (4, 5), (6, 7).
-__device__ __forceinline__ void decode4(uint32_t x, uint32_t s2, uint32_t n2, uint32_t (&p)[4]) {
-  p[0] = tc::hfma2(((x << 4) & 0x00F000F0u) | 0x54005400u, s2, n2);   // fp16 bits 0x54c0 = 64 + c
-  p[1] = tc::hfma2((x & 0x00F000F0u) | 0x54005400u, s2, n2);
-  p[2] = tc::hfma2(((x >> 4) & 0x00F000F0u) | 0x54005400u, s2, n2);
-  p[3] = tc::hfma2(((x >> 8) & 0x00F000F0u) | 0x54005400u, s2, n2);
+// 4 bits: eight codes (one word) -> fp16 pairs of channels (0, 1), (2, 3), (4, 5), (6, 7).  Nibbles at bits
+// 4-7 of a half read as 64 + c (0x54c0), those at bits 0-3 as 1024 + c (0x640c): the latter's 1032 s is
+// not exact, so they take an addition and a product, which costs less than the shift it saves (logic
+// and shifts run at half the rate of the fp16 pipe).
+__device__ __forceinline__ void decode4(uint32_t x, uint32_t s2, uint32_t n2, const Bases &c, uint32_t (&p)[4]) {
+  const uint32_t y = x >> 8;
+  auto low = [&](uint32_t v) {
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(tc::hadd2(place<0x000F000Fu>(v, c.k1024), 0xE408E408u)), "r"(s2));
+    return d;
+  };
+  p[0] = low(x);
+  p[1] = tc::hfma2(place<0x00F000F0u>(x, c.k64), s2, n2);
+  p[2] = low(y);
+  p[3] = tc::hfma2(place<0x00F000F0u>(y, c.k64), s2, n2);
 }
 
 // ------------------------------------------------------------------ which keys a row sees
@@ -213,7 +239,11 @@ struct Seq {
     const int64_t e = hi(f);
     return e < sink ? e : sink;
   }
-  __device__ __forceinline__ int64_t frame(int64_t p) const { return p < 0 ? -1 : (tpf == 1 ? p : p / tpf); }
+  __device__ __forceinline__ int64_t frame(int64_t p) const {
+    if (p < 0) return -1;
+    if (tpf == 1) return p;
+    return ((p | tpf) >> 32) == 0 ? (int64_t)((uint32_t)p / (uint32_t)tpf) : p / tpf;
+  }
 };
 
 // The keys that the rows of positions p0 .. p1 (p0 <= p1) see between them, numbered 0 .. total - 1: the
@@ -227,7 +257,8 @@ struct Keys {
     lo = s.lo(f0);
     const int64_t n = s.hi(f1) - lo;
     total = ns + (n > 0 ? (int)n : 0);
-    base = (uint32_t)((lo - s.sink) % s.ring);
+    const int64_t d = lo - s.sink;   // >= 0
+    base = (d >> 32) == 0 ? (uint32_t)d % (uint32_t)s.ring : (uint32_t)(d % s.ring);
   }
   __device__ __forceinline__ uint32_t slot(int v, uint32_t sink, uint32_t ring) const {
     if (v < ns) return (uint32_t)v;
@@ -303,12 +334,15 @@ struct WindowAttend {
   int splits;            // parts the keys are split into
   float *part;           // splits > 1: [batch * kv_heads][splits][rows][128] outputs of the parts,
   float *part_lse;       //             [batch * kv_heads][splits][rows] their log-sum-exps
+  win::Bases bases;      // win::kBases
 };
 // How a call is run: with tensor-memory tiles of 256 Query rows per CTA, or with warp tiles of 8 or 16
 // rows; and into how many parts its keys are split.
+constexpr int kWindowCluster = 8;   // parts of the warp tiles that are joined inside a thread-block cluster
 struct WindowPlan {
   bool tiles;
   int splits;
+  bool joins() const { return splits > 1 && (tiles || splits > kWindowCluster); }   // by a second kernel
 };
 WindowPlan window_plan(int64_t batch, int64_t kv_heads, int64_t rows, int64_t keys, int num_sms);
 cudaError_t launch_window_decode(const WindowAttend &a, cudaStream_t st);

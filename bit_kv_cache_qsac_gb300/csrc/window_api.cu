@@ -210,7 +210,7 @@ static WindowPlan plan_of(const qwm_ctx *ctx, const qwm_window *win, int64_t nq,
 size_t qwm_window_attend_workspace(const qwm_ctx *ctx, const qwm_window *win, int64_t nq, int64_t tpf, int64_t frames) {
   if (check_attend(ctx, win, nq, tpf, frames) != QWM_OK || nq == 0) return 0;
   const WindowPlan p = plan_of(ctx, win, nq, tpf, frames);
-  if (p.splits == 1) return 0;
+  if (!p.joins()) return 0;
   const size_t rows = (size_t)win->batch * ctx->cfg.heads * (size_t)nq;
   return rows * (size_t)p.splits * (QWM_D + 1) * sizeof(float);
 }
@@ -248,11 +248,12 @@ qwm_status qwm_window_attend(qwm_ctx *ctx, const qwm_window *win, const uint16_t
   a.status = ctx->status;
   a.H = H; a.group = H / win->kv_heads; a.rows = nq * a.group;
   a.splits = p.splits;
-  a.part = p.splits > 1 ? (float *)ws : nullptr;
-  a.part_lse = p.splits > 1 ? a.part + (size_t)win->batch * H * (size_t)nq * p.splits * QWM_D : nullptr;
+  a.bases = win::kBases;
+  a.part = p.joins() ? (float *)ws : nullptr;
+  a.part_lse = p.joins() ? a.part + (size_t)win->batch * H * (size_t)nq * p.splits * QWM_D : nullptr;
   const cudaStream_t st = (cudaStream_t)stream;
   cudaError_t e = p.tiles ? launch_window_tiles(a, st) : launch_window_decode(a, st);
-  if (e == cudaSuccess && p.splits > 1) e = launch_window_combine(a, st);
+  if (e == cudaSuccess && p.joins()) e = launch_window_combine(a, st);
   return cuda_status(e);
 }
 

@@ -182,19 +182,19 @@ struct Producer {
       }
     }
   }
-  __device__ __forceinline__ void store(uint32_t stage, const Pieces<BITS> &p) const {
+  __device__ __forceinline__ void store(uint32_t stage, const Pieces<BITS> &p, const win::Bases &bases) const {
 #pragma unroll
     for (int i = 0; i < 4; i++) {
       uint32_t s2, n2, d[8];
       win::step_consts<BITS>(p.step[i], s2, n2);
       if (BITS == 8) {
 #pragma unroll
-        for (int u = 0; u < 4; u++) win::decode8(p.c[i][u % (BITS / 2)], s2, n2, d[2 * u], d[2 * u + 1]);
+        for (int u = 0; u < 4; u++) win::decode8(p.c[i][u % (BITS / 2)], s2, n2, bases, d[2 * u], d[2 * u + 1]);
       } else {
         uint32_t q[4];
-        win::decode4(p.c[i][0], s2, n2, q);
+        win::decode4(p.c[i][0], s2, n2, bases, q);
         d[0] = q[0]; d[1] = q[1]; d[2] = q[2]; d[3] = q[3];
-        win::decode4(p.c[i][1], s2, n2, q);
+        win::decode4(p.c[i][1], s2, n2, bases, q);
         d[4] = q[0]; d[5] = q[1]; d[6] = q[2]; d[7] = q[3];
       }
       const uint32_t at = stage * kStage + (uint32_t)(i >> 1) * (2u * kRowStep * 128u);
@@ -541,13 +541,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     auto stage = [&](int j, Pieces<BITS> &k, Pieces<BITS> &v) -> bool {
       const int s = j % kStages;
       if (!free_again(&bars.k_empty[s], j)) return false;
-      pk.store((uint32_t)s, k);
+      pk.store((uint32_t)s, k, a.bases);
       hand_over(k_full + 8u * (uint32_t)s);
       const int next = (j0 + j + 2) * BN;
       const int64_t slot0 = j + 2 < J ? slot0_of(next) : 0;
       if (j + 2 < J) pk.load(keys, next, slot0, sink, ring, k);
       if (!free_again(&bars.v_empty[s], j)) return false;
-      pv.store((uint32_t)s, v);
+      pv.store((uint32_t)s, v, a.bases);
       hand_over(v_full + 8u * (uint32_t)s);
       if (j + 2 < J) pv.load(keys, next, slot0, sink, ring, v);
       return true;
@@ -585,14 +585,22 @@ cudaError_t launch_window_tiles(const WindowAttend &a, cudaStream_t st) {
 }
 
 // Few rows run on warp tiles, which read the cache once per 16 rows at most; more run on tensor-memory
-// tiles.  Keys are split until the parts fill the SMs, while a part keeps a few steps of work.
+// tiles.  Keys are split until the parts fill the SMs, while a part keeps a few steps of work.  Warp tiles
+// are first split into a cluster's CTAs (clusters of 7 or 8 leave SMs of a GPC over: a tenth of the
+// slots is counted off), further only where 8 parts would leave long parts to few SMs.
 WindowPlan window_plan(int64_t batch, int64_t kv_heads, int64_t rows, int64_t keys, int num_sms) {
   WindowPlan p;
   p.tiles = rows > 16;
-  const int64_t items = batch * kv_heads * (p.tiles ? 2 * ((rows + kPairRows - 1) / kPairRows) : 1);
-  const int64_t want = (p.tiles ? 1 : (rows <= 8 ? 2 : 1)) * (int64_t)num_sms / items;
   const int64_t most = (keys + 255) / 256;
-  int64_t s = want < most ? want : most;
+  int64_t s;
+  if (p.tiles) {
+    s = (int64_t)num_sms / (batch * kv_heads * 2 * ((rows + kPairRows - 1) / kPairRows));
+  } else {
+    const int64_t slots = (rows <= 8 ? 2 : 1) * (int64_t)num_sms;
+    s = slots * 9 / 10 / (batch * kv_heads);
+    if (s > kWindowCluster && keys <= 1024 * kWindowCluster) s = kWindowCluster;
+  }
+  s = s < most ? s : most;
   p.splits = (int)(s < 1 ? 1 : (s > 64 ? 64 : s));
   return p;
 }
