@@ -13,34 +13,43 @@ constexpr int kThreads = 256, kRows = kThreads / 16;
 constexpr int kUnroll = 4;   // heads whose loads are in flight together
 
 template <int PAIRING>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 3)
     rope_kernel(const __grid_constant__ qwm_rope_spec sp, const uint16_t *__restrict__ x, qwm_strides xs, int batch,
                 int heads, int64_t n, const int64_t *__restrict__ start, const int32_t *__restrict__ pos,
                 uint16_t *out, qwm_strides os, int heads_per_block) {
+  __shared__ win::RopeTable tab;
   const int v = threadIdx.x & 15, row = threadIdx.x >> 4;
   const int64_t tok = (int64_t)blockIdx.x * kRows + row;   // over [batch][n]
   const bool in = tok < (int64_t)batch * n;
-  const int64_t b = in ? tok / n : 0, i = in ? tok - b * n : 0;
-  const int64_t s0 = start[b];
-  const bool live = in && s0 >= 0;
-  if (!__any_sync(0xffffffffu, live)) return;
-  win::RopeVec<PAIRING> rv;
-  rv.init(sp, v, live ? s0 + i : 0, pos ? pos + (b * n + i) * 3 : nullptr);
+  const int64_t b = in ? win::quotient(tok, n) : 0, i = in ? tok - b * n : 0;
   const int h0 = blockIdx.y * heads_per_block;
   const int h1 = h0 + heads_per_block < heads ? h0 + heads_per_block : heads;
   const uint16_t *src = x + b * xs.batch + i * xs.token + 8 * v;
   uint16_t *dst = out + b * os.batch + i * os.token + 8 * v;
-  for (int h = h0; h < h1; h += kUnroll) {
-    uint4 r[kUnroll] = {};
+  uint4 r[kUnroll];
+  auto load = [&](int h) {
 #pragma unroll
     for (int u = 0; u < kUnroll; u++)
-      if (live && h + u < h1) r[u] = *(const uint4 *)(src + (int64_t)(h + u) * xs.head);
+      r[u] = h + u < h1 ? *(const uint4 *)(src + (int64_t)(h + u) * xs.head) : make_uint4(0, 0, 0, 0);
+  };
+  load(h0);   // in flight while the angles are formed
+  const int64_t s0 = start[b];
+  const bool live = in && s0 >= 0;
+  tab.fill(sp);
+  win::RopeVec<PAIRING> rv;
+  rv.init(sp, tab, v, live ? s0 + i : 0, pos ? pos + (b * n + i) * 3 : nullptr);
+  for (int h = h0; h < h1; h += kUnroll) {
+    uint32_t w[kUnroll][4];
 #pragma unroll
     for (int u = 0; u < kUnroll; u++) {
-      uint32_t w[4] = {r[u].x, r[u].y, r[u].z, r[u].w};
-      if (h + u < h1) rv.turn(sp, w);   // the same for every lane of the block
+      w[u][0] = r[u].x; w[u][1] = r[u].y; w[u][2] = r[u].z; w[u][3] = r[u].w;
+    }
+    if (h + kUnroll < h1) load(h + kUnroll);   // other rows than the ones written below
+#pragma unroll
+    for (int u = 0; u < kUnroll; u++) {
+      rv.turn(sp, w[u]);
       if (live && h + u < h1)
-        *(uint4 *)(dst + (int64_t)(h + u) * os.head) = make_uint4(w[0], w[1], w[2], w[3]);
+        *(uint4 *)(dst + (int64_t)(h + u) * os.head) = make_uint4(w[u][0], w[u][1], w[u][2], w[u][3]);
     }
   }
 }
@@ -51,14 +60,12 @@ cudaError_t launch_rope(const qwm_rope_spec &spec, const uint16_t *x, const qwm_
                         int64_t n, const int64_t *start, const int32_t *pos, uint16_t *out, const qwm_strides &os,
                         int num_sms, cudaStream_t st) {
   const int64_t tiles = ((int64_t)batch * n + kRows - 1) / kRows;
-  // few tokens: one head per block, to fill the SMs; many: up to 8 heads share a token's angles
-  int64_t hpb = tiles * heads / (8 * (int64_t)num_sms);
-  hpb = hpb < 1 ? 1 : (hpb > 8 ? 8 : hpb);
+  const int hpb = heads_per_block(tiles, heads, num_sms, 9);
   const dim3 grid((unsigned)tiles, (unsigned)((heads + hpb - 1) / hpb));
   if (spec.pairing == QWM_ROPE_INTERLEAVED)
     rope_kernel<QWM_ROPE_INTERLEAVED><<<grid, kThreads, 0, st>>>(spec, x, xs, batch, heads, n, start, pos, out, os,
-                                                                 (int)hpb);
+                                                                 hpb);
   else
-    rope_kernel<QWM_ROPE_HALF><<<grid, kThreads, 0, st>>>(spec, x, xs, batch, heads, n, start, pos, out, os, (int)hpb);
+    rope_kernel<QWM_ROPE_HALF><<<grid, kThreads, 0, st>>>(spec, x, xs, batch, heads, n, start, pos, out, os, hpb);
   return cudaGetLastError();
 }

@@ -8,10 +8,12 @@
 
 namespace {
 
-constexpr int kThreads = 256, kRows = kThreads / 16;
+constexpr int kThreads = 256, kRows = kThreads / 16, kReadRows = kThreads / 8;
 
-__device__ __forceinline__ bool bf16x2_nonfinite(uint32_t w) {
-  return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {   // a NaN stays one
+  uint32_t d;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
 }
 
 // Eight bf16 channels of a row (4 words) -> this lane's code bytes (8 bits: c0, c1; 4 bits: c0) and the
@@ -19,36 +21,52 @@ __device__ __forceinline__ bool bf16x2_nonfinite(uint32_t w) {
 template <int BITS>
 __device__ __forceinline__ void quantise(const uint32_t (&w)[4], uint32_t &c0, uint32_t &c1, uint32_t &step,
                                          bool &bad) {
-  constexpr float Q = win::code_max(BITS);
-  float f[8], amax = 0.f;
+  constexpr float kTop = win::code_max(BITS) * (BITS == 8 ? 56.f : 896.f);
+  uint32_t m = max_bf16x2(max_bf16x2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
+                          max_bf16x2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+  m = max_bf16x2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = max_bf16x2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  const float mlo = __uint_as_float(m << 16), mhi = __uint_as_float(m & 0xFFFF0000u);
+  float amax = fmaxf(mlo, mhi), f[8];
 #pragma unroll
   for (int i = 0; i < 4; i++) {
     f[2 * i] = __uint_as_float(w[i] << 16);
     f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
   }
+  const bool out = !(mlo <= kTop && mhi <= kTop);   // out of range or NaN, somewhere in the group
+  if (__any_sync(0xffffffffu, out)) {   // cut to the range, NaN to 0
+    if (out) {
+      bad = true;
+      amax = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; i++) amax = fmaxf(amax, fabsf(f[i]));   // fmaxf passes over a NaN
-  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-  constexpr float kTop = Q * (BITS == 8 ? 56.f : 896.f);
-  bool out = amax > kTop;
-#pragma unroll
-  for (int i = 0; i < 4; i++) out |= bf16x2_nonfinite(w[i]);
-  if (out) {   // cut to the range, NaN to 0
-    bad = true;
-#pragma unroll
-    for (int i = 0; i < 8; i++) f[i] = isnan(f[i]) ? 0.f : fminf(fmaxf(f[i], -kTop), kTop);
+      for (int i = 0; i < 8; i++) {
+        f[i] = isnan(f[i]) ? 0.f : fminf(fmaxf(f[i], -kTop), kTop);
+        amax = fmaxf(amax, fabsf(f[i]));
+      }
+    }
+    float a = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
+    amax = out ? a : amax;
   }
-  step = win::step_for<BITS>(amax);
-  const float s = win::step_value(step), inv = s > 0.f ? __frcp_rn(s) : 0.f;
-  uint32_t c[8];
+  float s, inv;
+  step = win::step_for<BITS>(amax, s);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+  inv = s > 0.f ? inv : 0.f;
+  const uint64_t inv2 = tc::f2(inv, inv);
+  uint32_t c[8];   // 0x4B400000 + code
 #pragma unroll
-  for (int i = 0; i < 8; i++) c[i] = win::code_of(f[i], inv, BITS == 8 ? 128.f : 8.f);
-  if (BITS == 8) {
-    c0 = c[0] | (c[1] << 8) | (c[2] << 16) | (c[3] << 24);
-    c1 = c[4] | (c[5] << 8) | (c[6] << 16) | (c[7] << 24);
-  } else {   // channel 2 k + t in nibble k + 4 t
-    c0 = c[0] | (c[2] << 4) | (c[4] << 8) | (c[6] << 12) | (c[1] << 16) | (c[3] << 20) | (c[5] << 24) | (c[7] << 28);
+  for (int i = 0; i < 4; i++) {
+    const uint64_t v = win::codes_of(tc::f2(f[2 * i], f[2 * i + 1]), inv2);
+    c[2 * i] = (uint32_t)v;
+    c[2 * i + 1] = (uint32_t)(v >> 32);
+  }
+  if (BITS == 8) {   // low bytes, biased by 128: the sign bit flips
+    c0 = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410) ^ 0x80808080u;
+    c1 = __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410) ^ 0x80808080u;
+  } else {   // channel 2 k + t in nibble k + 4 t: the sum of (0x4B400000 + code) 16^n, less that of the
+             // constants (modulo 2^32) and with 8 added in every nibble
+    c0 = ((((((c[7] * 16u + c[5]) * 16u + c[3]) * 16u + c[1]) * 16u + c[6]) * 16u + c[4]) * 16u + c[2]) * 16u + c[0] +
+         (0x88888888u - 0x3F400000u);
     c1 = 0u;
   }
 }
@@ -68,93 +86,121 @@ __global__ void __launch_bounds__(kThreads)
                         qwm_strides ks, const uint16_t *__restrict__ vv, qwm_strides vs, int64_t n,
                         const int64_t *__restrict__ start, const int32_t *__restrict__ count,
                         const int32_t *__restrict__ pos, int heads_per_block, int32_t *status) {
+  __shared__ win::RopeTable tab;
   const int v = threadIdx.x & 15, row = threadIdx.x >> 4;
   const int64_t tok = (int64_t)blockIdx.x * kRows + row;
   const bool in = tok < (int64_t)w.batch * n;
-  const int64_t b = in ? tok / n : 0, i = in ? tok - b * n : 0;
+  const int64_t b = in ? win::quotient(tok, n) : 0, i = in ? tok - b * n : 0;
+  const int h0 = blockIdx.y * heads_per_block;
+  const int h1 = h0 + heads_per_block < w.kv_heads ? h0 + heads_per_block : w.kv_heads;
+  const uint16_t *kp = k + b * ks.batch + i * ks.token + h0 * ks.head + 8 * v;
+  const uint16_t *vp = vv + b * vs.batch + i * vs.token + h0 * vs.head + 8 * v;
+  uint4 a = *(const uint4 *)kp, c = *(const uint4 *)vp;   // in flight while the angles are formed
   const int64_t s0 = start[b];
   int64_t cnt = count ? (int64_t)count[b] : n;
   cnt = cnt < n ? cnt : n;
   const int64_t p = s0 + i, end = s0 + cnt;
   // of tokens that share a slot the last of the call is kept
   const bool live = in && s0 >= 0 && i < cnt && (p < w.sink || p >= end - w.ring);
-  if (!__any_sync(0xffffffffu, live)) return;
   win::RopeVec<TURN == QWM_ROPE_HALF ? QWM_ROPE_HALF : QWM_ROPE_INTERLEAVED> rv;
-  if (TURN >= 0) rv.init(sp, v, live ? p : 0, pos ? pos + (b * n + i) * 3 : nullptr);
+  if (TURN >= 0) {
+    tab.fill(sp);
+    rv.init(sp, tab, v, live ? p : 0, pos ? pos + (b * n + i) * 3 : nullptr);
+  }
+  if (!__any_sync(0xffffffffu, live)) return;
   const int64_t slots = w.sink + w.ring;
-  const int64_t slot = live ? (p < w.sink ? p : w.sink + (p - w.sink) % w.ring) : 0;
-  const int h0 = blockIdx.y * heads_per_block;
-  const int h1 = h0 + heads_per_block < w.kv_heads ? h0 + heads_per_block : w.kv_heads;
-  const uint16_t *kp = k + b * ks.batch + i * ks.token + 8 * v, *vp = vv + b * vs.batch + i * vs.token + 8 * v;
+  const int64_t slot = live ? (p < w.sink ? p : w.sink + win::remainder(p - w.sink, w.ring)) : 0;
+  int64_t slot_row = (b * w.kv_heads + h0) * slots + slot;
   bool bad = false;
-#pragma unroll 2
   for (int h = h0; h < h1; h++) {
-    uint4 a = make_uint4(0, 0, 0, 0), c = a;
-    if (live) {
-      a = *(const uint4 *)(kp + (int64_t)h * ks.head);
-      c = *(const uint4 *)(vp + (int64_t)h * vs.head);
-    }
     uint32_t kw[4] = {a.x, a.y, a.z, a.w}, vw[4] = {c.x, c.y, c.z, c.w};
+    if (h + 1 < h1) {   // the next head's rows
+      kp += ks.head;
+      vp += vs.head;
+      a = *(const uint4 *)kp;
+      c = *(const uint4 *)vp;
+    }
+    if (!live) kw[0] = kw[1] = kw[2] = kw[3] = vw[0] = vw[1] = vw[2] = vw[3] = 0u;   // padding is not looked at
     if (TURN >= 0) rv.turn(sp, kw);
     uint32_t c0, c1, step;
-    const int64_t slot_row = (b * w.kv_heads + h) * slots + slot;
     quantise<BITS>(kw, c0, c1, step, bad);
     if (live) store_row<BITS>(w.k_codes, w.k_step, slot_row, v, c0, c1, step);
     quantise<BITS>(vw, c0, c1, step, bad);
     if (live) store_row<BITS>(w.v_codes, w.v_step, slot_row, v, c0, c1, step);
+    slot_row += slots;
   }
   if (bad && live) qwm_dev_error(status, QWM_ERR_RANGE);
 }
 
+// Eight channels of a cached row -> bf16 (4 words).
+template <int BITS>
+__device__ __forceinline__ uint4 restore(uint2 x, uint32_t step, const win::Bases &bases) {
+  uint32_t s2, n2, pr[4], o[4];
+  win::step_consts<BITS>(step, s2, n2);
+  if (BITS == 8) {
+    win::decode8(x.x, s2, n2, bases, pr[0], pr[1]);
+    win::decode8(x.y, s2, n2, bases, pr[2], pr[3]);
+  } else {
+    win::decode4(x.x, s2, n2, bases, pr);
+  }
+#pragma unroll
+  for (int u = 0; u < 4; u++) {
+    const float2 f = __half22float2(*(const __half2 *)&pr[u]);
+    o[u] = tc::pack_bf16x2(f.x, f.y);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// Eight lanes take a row, vectors v and v + 8 of it each, so that every store instruction writes whole
+// 128-byte lines; the loads of a head's Keys and Values are in flight together.
 template <int BITS>
 __global__ void __launch_bounds__(kThreads)
     window_read_kernel(qwm_window w, const int64_t *__restrict__ start, const int64_t *__restrict__ length,
                        const int32_t *__restrict__ count, int64_t n, uint16_t *__restrict__ k_hat,
                        uint16_t *__restrict__ v_hat, int heads_per_block, win::Bases bases) {
-  const int v = threadIdx.x & 15, row = threadIdx.x >> 4;
-  const int64_t tok = (int64_t)blockIdx.x * kRows + row;
+  const int v = threadIdx.x & 7, row = threadIdx.x >> 3;
+  const int64_t tok = (int64_t)blockIdx.x * kReadRows + row;
   if (tok >= (int64_t)w.batch * n) return;
-  const int64_t b = tok / n, i = tok - b * n;
+  const int64_t b = win::quotient(tok, n), i = tok - b * n;
   const int64_t s0 = start[b], len = length[b], p = s0 + i;
   if (s0 < 0 || (count && i >= count[b])) return;
   const bool held = p < len && (p < w.sink || p >= len - w.ring);
   const int64_t slots = w.sink + w.ring;
-  const int64_t slot = held ? (p < w.sink ? p : w.sink + (p - w.sink) % w.ring) : 0;
+  const int64_t slot = held ? (p < w.sink ? p : w.sink + win::remainder(p - w.sink, w.ring)) : 0;
   const int h0 = blockIdx.y * heads_per_block;
   const int h1 = h0 + heads_per_block < w.kv_heads ? h0 + heads_per_block : w.kv_heads;
+  constexpr int kVec = BITS;   // bytes of a vector's codes
+  const int64_t r0 = (b * w.kv_heads + h0) * slots + slot, o0 = ((b * w.kv_heads + h0) * n + i) * win::D + 8 * v;
+  const uint8_t *codes[2] = {w.k_codes + r0 * (win::D * BITS / 8) + kVec * v, w.v_codes + r0 * (win::D * BITS / 8) + kVec * v};
+  const uint8_t *steps[2] = {w.k_step + r0 * win::kSteps, w.v_step + r0 * win::kSteps};
+  uint16_t *dst[2] = {k_hat ? k_hat + o0 : nullptr, v_hat ? v_hat + o0 : nullptr};
 #pragma unroll 2
   for (int h = h0; h < h1; h++) {
-    const int64_t bh = b * w.kv_heads + h, r = bh * slots + slot;
+    uint2 x[2][2];
+    uint32_t st[2] = {0u, 0u};
 #pragma unroll
     for (int t = 0; t < 2; t++) {
-      uint16_t *dst = t ? v_hat : k_hat;
-      const uint8_t *codes = t ? w.v_codes : w.k_codes, *steps = t ? w.v_step : w.k_step;
-      if (!dst) continue;
-      uint32_t o[4] = {0u, 0u, 0u, 0u};
-      if (held) {
-        uint32_t s2, n2, pr[4];
-        win::step_consts<BITS>(steps[r * win::kSteps + (v >> 2)], s2, n2);
-        if (BITS == 8) {
-          const uint2 x = *(const uint2 *)(codes + r * win::D + 8 * v);
-          win::decode8(x.x, s2, n2, bases, pr[0], pr[1]);
-          win::decode8(x.y, s2, n2, bases, pr[2], pr[3]);
-        } else {
-          win::decode4(*(const uint32_t *)(codes + r * (win::D / 2) + 4 * v), s2, n2, bases, pr);
-        }
+      x[t][0] = x[t][1] = BITS == 8 ? make_uint2(0x80808080u, 0x80808080u) : make_uint2(0x88888888u, 0u);   // codes of 0
+      if (held && dst[t]) {
+        st[t] = *(const uint32_t *)steps[t];
 #pragma unroll
-        for (int u = 0; u < 4; u++) {
-          const float2 f = __half22float2(*(const __half2 *)&pr[u]);
-          o[u] = tc::pack_bf16x2(f.x, f.y);
+        for (int e = 0; e < 2; e++) {
+          const uint8_t *c = codes[t] + 8 * kVec * e;
+          if (BITS == 8) x[t][e] = *(const uint2 *)c;
+          else x[t][e].x = *(const uint32_t *)c;
         }
       }
-      *(uint4 *)(dst + (bh * n + i) * win::D + 8 * v) = make_uint4(o[0], o[1], o[2], o[3]);
+      codes[t] += slots * (win::D * BITS / 8);
+      steps[t] += slots * win::kSteps;
+    }
+#pragma unroll
+    for (int t = 0; t < 2; t++) {
+      if (!dst[t]) continue;
+      *(uint4 *)dst[t] = restore<BITS>(x[t][0], (st[t] >> (8 * (v >> 2))) & 0xFFu, bases);
+      *(uint4 *)(dst[t] + 64) = restore<BITS>(x[t][1], (st[t] >> (8 * (2 + (v >> 2)))) & 0xFFu, bases);
+      dst[t] += n * win::D;
     }
   }
-}
-
-int heads_per_block(int64_t tiles, int heads, int num_sms) {
-  const int64_t h = tiles * heads / (8 * (int64_t)num_sms);
-  return (int)(h < 1 ? 1 : (h > 8 ? 8 : h));
 }
 
 template <int BITS>
@@ -162,7 +208,7 @@ cudaError_t write_bits(const qwm_window &w, const uint16_t *k, const qwm_strides
                        const qwm_strides &vs, int64_t n, const int64_t *start, const int32_t *count,
                        const qwm_rope_spec *rope, const int32_t *pos, int num_sms, int32_t *status, cudaStream_t st) {
   const int64_t tiles = ((int64_t)w.batch * n + kRows - 1) / kRows;
-  const int hpb = heads_per_block(tiles, w.kv_heads, num_sms);
+  const int hpb = heads_per_block(tiles, w.kv_heads, num_sms, rope ? 9 : 20);
   const dim3 grid((unsigned)tiles, (unsigned)((w.kv_heads + hpb - 1) / hpb));
   const qwm_rope_spec none = {};
   if (!rope)
@@ -188,8 +234,8 @@ cudaError_t launch_window_write(const qwm_window &w, const uint16_t *k, const qw
 
 cudaError_t launch_window_read(const qwm_window &w, const int64_t *start, const int64_t *length, const int32_t *count,
                                int64_t n, uint16_t *k_hat, uint16_t *v_hat, int num_sms, cudaStream_t st) {
-  const int64_t tiles = ((int64_t)w.batch * n + kRows - 1) / kRows;
-  const int hpb = heads_per_block(tiles, w.kv_heads, num_sms);
+  const int64_t tiles = ((int64_t)w.batch * n + kReadRows - 1) / kReadRows;
+  const int hpb = heads_per_block(tiles, w.kv_heads, num_sms, 40);
   const dim3 grid((unsigned)tiles, (unsigned)((w.kv_heads + hpb - 1) / hpb));
   if (w.bits == 8)
     window_read_kernel<8><<<grid, kThreads, 0, st>>>(w, start, length, count, n, k_hat, v_hat, hpb, win::kBases);

@@ -55,15 +55,12 @@ __device__ __forceinline__ void rope_sincos(int64_t pos, uint64_t turn, float &c
   sl = sgs * (swap ? cr : sr);
 }
 
-// a c - b s and a s + b c with c = ch + cl, s = sh + sl: the products' rounding errors are carried, so
-// each result is within a little over half a unit of fp32.
-__device__ __forceinline__ float rope_cos(float a, float b, float ch, float cl, float sh, float sl) {
-  const float t = b * sh, e = fmaf(b, sh, -t);
-  return fmaf(a, ch, -t) + fmaf(a, cl, -fmaf(b, sl, e));
-}
-__device__ __forceinline__ float rope_sin(float a, float b, float ch, float cl, float sh, float sl) {
-  const float t = b * ch, e = fmaf(b, ch, -t);
-  return fmaf(a, sh, t) + fmaf(a, sl, fmaf(b, cl, e));
+// p x + q y for two channels at a time, with x = xh + xl and y = yh + yl: the error of the rounded product
+// q yh is carried (ny = -yh), so each result is within a little over half a unit of fp32.
+__device__ __forceinline__ uint64_t rope_pair(uint64_t p, uint64_t q, uint64_t xh, uint64_t xl, uint64_t yh,
+                                              uint64_t yl, uint64_t ny) {
+  const uint64_t t = tc::mul2(q, yh), e = tc::fma2(q, yh, tc::mul2(q, ny));
+  return tc::add2(tc::fma2(p, xh, t), tc::fma2(p, xl, tc::fma2(q, yl, e)));
 }
 
 // The coordinate of position p (>= 0) on one axis of the spec's grid.
@@ -80,64 +77,94 @@ __device__ __forceinline__ int64_t rope_coord(const qwm_rope_spec &sp, int64_t p
   return axis == 0 ? t : row - t * sp.grid_h;
 }
 
-// The angles of one token for the 8 channels 8 v .. 8 v + 7 of a row (v = 0..15).  INTERLEAVED: the four
-// pairs inside them; HALF: the eight pairs they are the first or the second half of.
+// The spec's table in shared memory: lanes read different pairs, which constant memory would serve one
+// address at a time.  Every thread of the block takes part.
+struct RopeTable {
+  uint64_t turn[64];
+  uint8_t axis[64];
+  __device__ __forceinline__ void fill(const qwm_rope_spec &sp) {
+    if (threadIdx.x < 64) {
+      turn[threadIdx.x] = sp.turn[threadIdx.x];
+      axis[threadIdx.x] = sp.axis[threadIdx.x];
+    }
+    __syncthreads();
+  }
+};
+
+// The angles of one token for the 8 channels 8 v .. 8 v + 7 of a row (v = 0..15), two at a time.
+// INTERLEAVED: pairs (a, b) inside the vector, out_a = a c - b s, out_b = b c + a s; the packed lanes are
+// pairs 2 i and 2 i + 1.  HALF: the vector is the first or the second half of eight pairs and its partner
+// is another lane's: out = mine c -+ other s; the packed lanes are channels 2 i and 2 i + 1.
 template <int PAIRING>
 struct RopeVec {
-  static constexpr int kPairs = PAIRING == QWM_ROPE_INTERLEAVED ? 4 : 8;
-  float ch[kPairs], cl[kPairs], sh[kPairs], sl[kPairs];
+  static constexpr int kN = PAIRING == QWM_ROPE_INTERLEAVED ? 2 : 4;
+  uint64_t ch[kN], cl[kN], sh[kN], sl[kN], nch[kN], nsh[kN], nsl[kN];   // HALF: s signed for this half
   int active;   // INTERLEAVED: pairs turned; HALF: 1 first half, 2 second half, 0 neither
 
   // pos3: (t, y, x) of the token, or NULL to take them from position p and the grid
-  __device__ __forceinline__ void init(const qwm_rope_spec &sp, int v, int64_t p, const int32_t *pos3) {
+  __device__ __forceinline__ void init(const qwm_rope_spec &sp, const RopeTable &tab, int v, int64_t p,
+                                       const int32_t *pos3) {
     int64_t c[3];
 #pragma unroll
     for (int a = 0; a < 3; a++) c[a] = pos3 ? (int64_t)pos3[a] : rope_coord(sp, p, a);
     const int half = sp.rot >> 1;
-    int i0;
+    int i0, n;   // first pair, pairs turned
     if (PAIRING == QWM_ROPE_INTERLEAVED) {
       i0 = 4 * v;
-      active = half - i0 < 0 ? 0 : (half - i0 < 4 ? half - i0 : 4);
+      n = half - i0 < 0 ? 0 : (half - i0 < 4 ? half - i0 : 4);
+      active = n;
     } else {
-      i0 = 8 * v < half ? 8 * v : 8 * v - half;
       active = 8 * v < half ? 1 : (8 * v < sp.rot ? 2 : 0);
+      i0 = active == 2 ? 8 * v - half : 8 * v;
+      n = active ? 8 : 0;
     }
 #pragma unroll
-    for (int i = 0; i < kPairs; i++) {
-      ch[i] = 1.f;
-      cl[i] = sh[i] = sl[i] = 0.f;
-      if (active && (PAIRING == QWM_ROPE_HALF || i < active)) {
-        const int ax = sp.axis[i0 + i];
-        rope_sincos(ax == 0 ? c[0] : (ax == 1 ? c[1] : c[2]), sp.turn[i0 + i], ch[i], cl[i], sh[i], sl[i]);
+    for (int i = 0; i < kN; i++) {
+      float f[2][4];
+#pragma unroll
+      for (int e = 0; e < 2; e++) {
+        f[e][0] = 1.f;
+        f[e][1] = f[e][2] = f[e][3] = 0.f;
+        if (2 * i + e < n) {
+          const int k = i0 + 2 * i + e, ax = tab.axis[k];
+          rope_sincos(ax == 0 ? c[0] : (ax == 1 ? c[1] : c[2]), tab.turn[k], f[e][0], f[e][1], f[e][2], f[e][3]);
+        }
+        if (PAIRING == QWM_ROPE_HALF && active == 1) {
+          f[e][2] = -f[e][2];
+          f[e][3] = -f[e][3];
+        }
       }
+      ch[i] = tc::f2(f[0][0], f[1][0]);
+      cl[i] = tc::f2(f[0][1], f[1][1]);
+      sh[i] = tc::f2(f[0][2], f[1][2]);
+      sl[i] = tc::f2(f[0][3], f[1][3]);
+      nch[i] = tc::f2(-f[0][0], -f[1][0]);
+      nsh[i] = tc::f2(-f[0][2], -f[1][2]);
+      nsl[i] = tc::f2(-f[0][3], -f[1][3]);
     }
   }
   // Turn the 8 bf16 channels in w (4 words).  HALF: every lane of the 16-lane row takes part.
   __device__ __forceinline__ void turn(const qwm_rope_spec &sp, uint32_t (&w)[4]) const {
+    auto lo = [](uint32_t x) { return __uint_as_float(x << 16); };
+    auto hi = [](uint32_t x) { return __uint_as_float(x & 0xFFFF0000u); };
     if (PAIRING == QWM_ROPE_INTERLEAVED) {
 #pragma unroll
-      for (int i = 0; i < 4; i++) {
-        const float a = __uint_as_float(w[i] << 16), b = __uint_as_float(w[i] & 0xFFFF0000u);
-        const uint32_t t = tc::pack_bf16x2(rope_cos(a, b, ch[i], cl[i], sh[i], sl[i]),
-                                           rope_sin(a, b, ch[i], cl[i], sh[i], sl[i]));
-        if (i < active) w[i] = t;
+      for (int i = 0; i < 2; i++) {
+        const uint64_t a = tc::f2(lo(w[2 * i]), lo(w[2 * i + 1])), b = tc::f2(hi(w[2 * i]), hi(w[2 * i + 1]));
+        const uint64_t x = rope_pair(a, b, ch[i], cl[i], nsh[i], nsl[i], sh[i]);   // a c - b s
+        const uint64_t y = rope_pair(a, b, sh[i], sl[i], ch[i], cl[i], nch[i]);    // a s + b c
+        if (2 * i < active) w[2 * i] = tc::pack_bf16x2(tc::f2lo(x), tc::f2lo(y));
+        if (2 * i + 1 < active) w[2 * i + 1] = tc::pack_bf16x2(tc::f2hi(x), tc::f2hi(y));
       }
     } else {
       const int lane = threadIdx.x & 31, off = sp.rot >> 4;
-      const int partner = active == 1 ? lane + off : (active == 2 ? lane - off : lane);
+      const int partner = (active == 1 ? lane + off : (active == 2 ? lane - off : lane)) & 31;
 #pragma unroll
       for (int i = 0; i < 4; i++) {
-        const uint32_t q = __shfl_sync(0xffffffffu, w[i], partner & 31);
-        float o[2];
-#pragma unroll
-        for (int j = 0; j < 2; j++) {
-          const int k = 2 * i + j;
-          const float mine = __uint_as_float(j ? (w[i] & 0xFFFF0000u) : (w[i] << 16));
-          const float other = __uint_as_float(j ? (q & 0xFFFF0000u) : (q << 16));
-          o[j] = active == 1 ? rope_cos(mine, other, ch[k % kPairs], cl[k % kPairs], sh[k % kPairs], sl[k % kPairs])
-                             : rope_sin(other, mine, ch[k % kPairs], cl[k % kPairs], sh[k % kPairs], sl[k % kPairs]);
-        }
-        if (active) w[i] = tc::pack_bf16x2(o[0], o[1]);
+        const uint32_t q = __shfl_sync(0xffffffffu, w[i], partner);
+        const uint64_t mine = tc::f2(lo(w[i]), hi(w[i])), other = tc::f2(lo(q), hi(q));
+        const uint64_t x = rope_pair(mine, other, ch[i % kN], cl[i % kN], sh[i % kN], sl[i % kN], nsh[i % kN]);
+        if (active) w[i] = tc::pack_bf16x2(tc::f2lo(x), tc::f2hi(x));
       }
     }
   }
@@ -150,25 +177,33 @@ __host__ __device__ constexpr uint32_t step_max(int bits) { return bits == 8 ? 0
 
 __device__ __forceinline__ float step_value(uint32_t b) { return __half2float(__ushort_as_half((uint16_t)(b << 7))); }
 
-// The smallest step (as its byte) with Q s >= amax, at most step_max.  Q s has 11 significant bits at
-// most, so the comparisons are exact; the first guess is off by one at most.
+// The smallest step with Q s >= amax (amax a bf16 value), at most step_max: its byte, and s itself.
+// amax has 8 significant bits and a step 4, so the quotient is a step exactly or at least 2^-11 (relative)
+// away from every step: rounding up to 3 mantissa bits after taking 16 units off (the multiplication's
+// error is below 2) finds it.  Below 2^-14 steps are multiples of 2^-17.
 template <int BITS>
-__device__ __forceinline__ uint32_t step_for(float amax) {
+__device__ __forceinline__ uint32_t step_for(float amax, float &s) {
   constexpr float Q = code_max(BITS);
-  const uint32_t h = __half_as_ushort(__float2half_ru(amax * (1.f / Q)));
-  uint32_t b = (h + 0x7Fu) >> 7;
-  b = b < step_max(BITS) ? b : step_max(BITS);
-  if (b > 0u && step_value(b - 1u) * Q >= amax) b--;
-  if (b < step_max(BITS) && step_value(b) * Q < amax) b++;
-  return b;
+  const float t = amax * (1.f / Q);
+  if (t < 0x1p-14f * (1.f - 0x1p-20f)) {
+    const float m = ceilf(t * 0x1p17f * (1.f - 0x1p-20f));
+    s = m * 0x1p-17f;
+    return (uint32_t)m;
+  }
+  constexpr uint32_t kTop = (step_max(BITS) << 20) + ((127u - 15u) << 23);
+  uint32_t b = (__float_as_uint(t) + (0xFFFFFu - 16u)) & 0xFFF00000u;
+  b = b < kTop ? b : kTop;
+  s = __uint_as_float(b);
+  return (b >> 20) - ((127u - 15u) << 3);
 }
 
-// rint(x / s) plus the code width's bias, in the low byte.  The quotient is first rounded to a grid of
-// 2^-11: x has 8 significant bits and s has 4, so a quotient that is not halfway between integers is
-// at least 2^-9.9 away from halfway and stays on its side, while one that is lands exactly on it.
-__device__ __forceinline__ uint32_t code_of(float x, float inv, float bias) {
-  const float snap = __fsub_rn(__fmaf_rn(x, inv, 0x1.8p12f), 0x1.8p12f);
-  return __float_as_uint(__fadd_rn(snap, 0x1.8p23f + bias)) & 0xFFu;
+// Two codes: rint(x / s) in the low bits of each result's pattern (0x4B400000 + code).  The quotient is
+// first rounded to a grid of 2^-11: x has 8 significant bits and s has 4, so a quotient that is not
+// halfway between integers is at least 2^-9.9 away from halfway and stays on its side, while one that
+// is lands exactly on it (and then ties to even).
+__device__ __forceinline__ uint64_t codes_of(uint64_t x2, uint64_t inv2) {
+  const uint64_t grid = tc::f2(0x1.8p12f, 0x1.8p12f), ungrid = tc::f2(-0x1.8p12f, -0x1.8p12f);
+  return tc::add2(tc::add2(tc::fma2(x2, inv2, grid), ungrid), tc::f2(0x1.8p23f, 0x1.8p23f));
 }
 
 // Decode constants of a step: s and -bias' s in both halves, where bias' is the integer that a code's fp16
@@ -222,6 +257,14 @@ __device__ __forceinline__ void decode4(uint32_t x, uint32_t s2, uint32_t n2, co
 
 // ------------------------------------------------------------------ which keys a row sees
 
+// a / b of non-negative numbers, in 32 bits where they fit (a 64-bit division takes some 100 instructions).
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+__device__ __forceinline__ int64_t remainder(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a % (uint32_t)b) : a % b;
+}
+
 // Sequence and window of an attention call, for one sequence.
 struct Seq {
   int64_t len, sink, ring, tpf, frames;
@@ -240,9 +283,7 @@ struct Seq {
     return e < sink ? e : sink;
   }
   __device__ __forceinline__ int64_t frame(int64_t p) const {
-    if (p < 0) return -1;
-    if (tpf == 1) return p;
-    return ((p | tpf) >> 32) == 0 ? (int64_t)((uint32_t)p / (uint32_t)tpf) : p / tpf;
+    return p < 0 ? -1 : (tpf == 1 ? p : quotient(p, tpf));
   }
 };
 
@@ -257,8 +298,7 @@ struct Keys {
     lo = s.lo(f0);
     const int64_t n = s.hi(f1) - lo;
     total = ns + (n > 0 ? (int)n : 0);
-    const int64_t d = lo - s.sink;   // >= 0
-    base = (d >> 32) == 0 ? (uint32_t)d % (uint32_t)s.ring : (uint32_t)(d % s.ring);
+    base = (uint32_t)remainder(lo - s.sink, s.ring);   // lo >= sink
   }
   __device__ __forceinline__ uint32_t slot(int v, uint32_t sink, uint32_t ring) const {
     if (v < ns) return (uint32_t)v;
@@ -302,6 +342,17 @@ struct Everyone {
 };
 
 }  // namespace win
+
+// Heads that a block of the elementwise calls walks over: few enough for about `per_sm` blocks per SM, in
+// equal shares.  What a block forms once per token (angles, slots) costs about 2 us of latency, so the
+// fewer blocks the better while they still fill the SMs in whole waves: a 720p chunk of 40 heads turns in
+// 37 us with 9 blocks per SM (20 heads each), 43 us with 20, 59 us with 45; without angles 20 (writing)
+// and 40 (reading back) measure best.
+inline int heads_per_block(int64_t tiles, int64_t heads, int num_sms, int per_sm) {
+  int64_t parts = ((int64_t)num_sms * per_sm + tiles / 2) / tiles;
+  parts = parts < 1 ? 1 : (parts > heads ? heads : parts);
+  return (int)((heads + parts - 1) / parts);
+}
 
 // Launchers of the recent-window calls (each returns the launch's error).
 cudaError_t launch_rope(const qwm_rope_spec &spec, const uint16_t *x, const qwm_strides &xs, int batch, int heads,

@@ -79,7 +79,7 @@ struct RowOut {
       lse = a.part_lse + pr;
       return;
     }
-    const int64_t i = r / a.group;
+    const int64_t i = win::quotient(r, a.group);
     const int h = kvh * a.group + (int)(r - i * a.group);
     const int64_t at = b * a.os.batch + h * a.os.head + i * a.os.token;
     if (a.out_f32) f32 = (float *)a.out + at;
@@ -217,7 +217,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // head's last item, whose second Query tile may be empty: the short ones fill the last wave's gaps
   const int64_t pair = blockIdx.x >> 1, heads = (int64_t)a.w.batch * a.w.kv_heads;
   const int64_t items = (a.rows + kPairRows - 1) / kPairRows, early = heads * (items - 1);
-  const int64_t y = pair < early ? pair / (items - 1) : pair - early, b = y / a.w.kv_heads;
+  const int64_t y = pair < early ? win::quotient(pair, items - 1) : pair - early, b = win::quotient(y, a.w.kv_heads);
   const int64_t item = pair < early ? pair - y * (items - 1) : items - 1;
   const int kvh = (int)(y - b * a.w.kv_heads), split = (int)blockIdx.y;
   const int cr = (int)tc::cluster_ctarank();
@@ -230,7 +230,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int64_t rows = nq * a.group;              // live rows of this Key head
   if (q0 < 0 || pair0 >= rows) return;            // the same in both CTAs
   const win::Seq seq{a.length[b], a.w.sink, a.w.ring, a.tpf, a.frames};
-  auto frame_of = [&](int64_t r) { return seq.frame(q0 + r / a.group); };
+  auto frame_of = [&](int64_t r) { return seq.frame(q0 + win::quotient(r, a.group)); };
   const int64_t pair1 = pair0 + kPairRows < rows ? pair0 + kPairRows : rows;
   win::Keys keys;
   keys.init(seq, frame_of(pair0), frame_of(pair1 - 1));
@@ -260,7 +260,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int64_t r = row_base + (int64_t)x * 2 * BM + rr;
     uint4 v = make_uint4(0, 0, 0, 0);
     if (r < rows) {
-      const int64_t i = r / a.group;
+      const int64_t i = win::quotient(r, a.group);
       v = *(const uint4 *)(a.q + b * a.qs.batch + (kvh * a.group + (r - i * a.group)) * a.qs.head + i * a.qs.token +
                            8 * ci);
     }

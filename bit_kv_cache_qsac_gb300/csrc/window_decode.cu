@@ -41,7 +41,7 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 // Where a row's output goes, and the final step of every path: write, or merge into what is there.
 __device__ __forceinline__ void finish4(const WindowAttend &a, int64_t b, int kvh, int64_t r, int ch, float4 o,
                                         float L) {
-  const int64_t i = (r >> 31) == 0 ? (int64_t)((uint32_t)r / (uint32_t)a.group) : r / a.group;
+  const int64_t i = win::quotient(r, a.group);
   const int h = kvh * a.group + (int)(r - i * a.group);
   const int64_t at = b * a.os.batch + h * a.os.head + i * a.os.token + ch;
   if (a.out_f32) {
@@ -63,7 +63,7 @@ __device__ __forceinline__ void finish4(const WindowAttend &a, int64_t b, int kv
 }
 __device__ __forceinline__ void finish_lse(const WindowAttend &a, int64_t b, int kvh, int64_t r, float L) {
   if (!a.lse) return;
-  const int64_t i = r / a.group;
+  const int64_t i = win::quotient(r, a.group);
   float *p = a.lse + (b * a.H + kvh * a.group + (int)(r - i * a.group)) * a.nq + i;
   if (a.merge) {
     const float Lp = *p, Lm = fmaxf(Lp, L);
@@ -526,9 +526,9 @@ __global__ void __launch_bounds__(256) window_combine_kernel(const __grid_consta
   const int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int64_t heads = (int64_t)a.w.batch * a.w.kv_heads;
   if (item >= heads * a.rows) return;
-  const int64_t y = item / a.rows, r = item - y * a.rows, b = y / a.w.kv_heads;
+  const int64_t y = win::quotient(item, a.rows), r = item - y * a.rows, b = win::quotient(y, a.w.kv_heads);
   const int kvh = (int)(y - b * a.w.kv_heads);
-  if (a.q_start[b] < 0 || (a.q_count && r / a.group >= a.q_count[b])) return;
+  if (a.q_start[b] < 0 || (a.q_count && win::quotient(r, a.group) >= a.q_count[b])) return;
   const float *pl = a.part_lse + y * a.splits * a.rows + r;
   float M = -INFINITY;
   for (int s = 0; s < a.splits; s++) M = fmaxf(M, pl[s * a.rows]);
