@@ -12,7 +12,7 @@ namespace {
 constexpr int kThreads = 256, kRows = kThreads / 16;
 constexpr int kUnroll = 4;   // heads whose loads are in flight together
 
-template <int PAIRING>
+template <int PAIRING, bool WHOLE>
 __global__ void __launch_bounds__(kThreads, 3)
     rope_kernel(const __grid_constant__ qwm_rope_spec sp, const uint16_t *__restrict__ x, qwm_strides xs, int batch,
                 int heads, int64_t n, const int64_t *__restrict__ start, const int32_t *__restrict__ pos,
@@ -36,7 +36,7 @@ __global__ void __launch_bounds__(kThreads, 3)
   const int64_t s0 = start[b];
   const bool live = in && s0 >= 0;
   tab.fill(sp);
-  win::RopeVec<PAIRING> rv;
+  win::RopeVec<PAIRING, WHOLE> rv;
   rv.init(sp, tab, v, live ? s0 + i : 0, pos ? pos + (b * n + i) * 3 : nullptr);
   for (int h = h0; h < h1; h += kUnroll) {
     uint32_t w[kUnroll][4];
@@ -62,10 +62,9 @@ cudaError_t launch_rope(const qwm_rope_spec &spec, const uint16_t *x, const qwm_
   const int64_t tiles = ((int64_t)batch * n + kRows - 1) / kRows;
   const int hpb = heads_per_block(tiles, heads, num_sms, 9);
   const dim3 grid((unsigned)tiles, (unsigned)((heads + hpb - 1) / hpb));
-  if (spec.pairing == QWM_ROPE_INTERLEAVED)
-    rope_kernel<QWM_ROPE_INTERLEAVED><<<grid, kThreads, 0, st>>>(spec, x, xs, batch, heads, n, start, pos, out, os,
-                                                                 hpb);
-  else
-    rope_kernel<QWM_ROPE_HALF><<<grid, kThreads, 0, st>>>(spec, x, xs, batch, heads, n, start, pos, out, os, hpb);
+  auto kernel = spec.pairing == QWM_ROPE_INTERLEAVED
+                    ? (spec.rot == win::D ? rope_kernel<QWM_ROPE_INTERLEAVED, true> : rope_kernel<QWM_ROPE_INTERLEAVED, false>)
+                    : (spec.rot == win::D ? rope_kernel<QWM_ROPE_HALF, true> : rope_kernel<QWM_ROPE_HALF, false>);
+  kernel<<<grid, kThreads, 0, st>>>(spec, x, xs, batch, heads, n, start, pos, out, os, hpb);
   return cudaGetLastError();
 }

@@ -52,13 +52,13 @@ __device__ __forceinline__ void quantise(const uint32_t (&w)[4], uint32_t &c0, u
   step = win::step_for<BITS>(amax, s);
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
   inv = s > 0.f ? inv : 0.f;
-  const uint64_t inv2 = tc::f2(inv, inv);
+  const uint64_t inv2 = win::pair2(inv, inv);
   uint32_t c[8];   // 0x4B400000 + code
 #pragma unroll
   for (int i = 0; i < 4; i++) {
-    const uint64_t v = win::codes_of(tc::f2(f[2 * i], f[2 * i + 1]), inv2);
-    c[2 * i] = (uint32_t)v;
-    c[2 * i + 1] = (uint32_t)(v >> 32);
+    const float2 v = win::split2(win::codes_of(win::pair2(f[2 * i], f[2 * i + 1]), inv2));
+    c[2 * i] = __float_as_uint(v.x);
+    c[2 * i + 1] = __float_as_uint(v.y);
   }
   if (BITS == 8) {   // low bytes, biased by 128: the sign bit flips
     c0 = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410) ^ 0x80808080u;
@@ -79,8 +79,8 @@ __device__ __forceinline__ void store_row(uint8_t *codes, uint8_t *steps, int64_
   if ((v & 3) == 0) steps[slot_row * win::kSteps + (v >> 2)] = (uint8_t)step;
 }
 
-// TURN: -1 Keys are stored as they come, else the pairing they are turned by.
-template <int BITS, int TURN>
+// TURN: -1 Keys are stored as they come, else the pairing they are turned by (WHOLE: all channels).
+template <int BITS, int TURN, bool WHOLE>
 __global__ void __launch_bounds__(kThreads)
     window_write_kernel(const __grid_constant__ qwm_rope_spec sp, qwm_window w, const uint16_t *__restrict__ k,
                         qwm_strides ks, const uint16_t *__restrict__ vv, qwm_strides vs, int64_t n,
@@ -102,12 +102,13 @@ __global__ void __launch_bounds__(kThreads)
   const int64_t p = s0 + i, end = s0 + cnt;
   // of tokens that share a slot the last of the call is kept
   const bool live = in && s0 >= 0 && i < cnt && (p < w.sink || p >= end - w.ring);
-  win::RopeVec<TURN == QWM_ROPE_HALF ? QWM_ROPE_HALF : QWM_ROPE_INTERLEAVED> rv;
+  win::RopeVec<TURN == QWM_ROPE_HALF ? QWM_ROPE_HALF : QWM_ROPE_INTERLEAVED, WHOLE> rv;
   if (TURN >= 0) {
     tab.fill(sp);
     rv.init(sp, tab, v, live ? p : 0, pos ? pos + (b * n + i) * 3 : nullptr);
   }
   if (!__any_sync(0xffffffffu, live)) return;
+  const bool all = __all_sync(0xffffffffu, live);
   const int64_t slots = w.sink + w.ring;
   const int64_t slot = live ? (p < w.sink ? p : w.sink + win::remainder(p - w.sink, w.ring)) : 0;
   int64_t slot_row = (b * w.kv_heads + h0) * slots + slot;
@@ -120,7 +121,9 @@ __global__ void __launch_bounds__(kThreads)
       a = *(const uint4 *)kp;
       c = *(const uint4 *)vp;
     }
-    if (!live) kw[0] = kw[1] = kw[2] = kw[3] = vw[0] = vw[1] = vw[2] = vw[3] = 0u;   // padding is not looked at
+    if (!all) {   // padding is not looked at
+      if (!live) kw[0] = kw[1] = kw[2] = kw[3] = vw[0] = vw[1] = vw[2] = vw[3] = 0u;
+    }
     if (TURN >= 0) rv.turn(sp, kw);
     uint32_t c0, c1, step;
     quantise<BITS>(kw, c0, c1, step, bad);
@@ -211,14 +214,14 @@ cudaError_t write_bits(const qwm_window &w, const uint16_t *k, const qwm_strides
   const int hpb = heads_per_block(tiles, w.kv_heads, num_sms, rope ? 9 : 20);
   const dim3 grid((unsigned)tiles, (unsigned)((w.kv_heads + hpb - 1) / hpb));
   const qwm_rope_spec none = {};
-  if (!rope)
-    window_write_kernel<BITS, -1><<<grid, kThreads, 0, st>>>(none, w, k, ks, v, vs, n, start, count, pos, hpb, status);
-  else if (rope->pairing == QWM_ROPE_INTERLEAVED)
-    window_write_kernel<BITS, QWM_ROPE_INTERLEAVED>
-        <<<grid, kThreads, 0, st>>>(*rope, w, k, ks, v, vs, n, start, count, pos, hpb, status);
-  else
-    window_write_kernel<BITS, QWM_ROPE_HALF>
-        <<<grid, kThreads, 0, st>>>(*rope, w, k, ks, v, vs, n, start, count, pos, hpb, status);
+  auto kernel = window_write_kernel<BITS, -1, false>;
+  if (rope && rope->pairing == QWM_ROPE_INTERLEAVED)
+    kernel = rope->rot == win::D ? window_write_kernel<BITS, QWM_ROPE_INTERLEAVED, true>
+                                 : window_write_kernel<BITS, QWM_ROPE_INTERLEAVED, false>;
+  else if (rope)
+    kernel = rope->rot == win::D ? window_write_kernel<BITS, QWM_ROPE_HALF, true>
+                                 : window_write_kernel<BITS, QWM_ROPE_HALF, false>;
+  kernel<<<grid, kThreads, 0, st>>>(rope ? *rope : none, w, k, ks, v, vs, n, start, count, pos, hpb, status);
   return cudaGetLastError();
 }
 

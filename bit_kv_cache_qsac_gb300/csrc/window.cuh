@@ -12,6 +12,18 @@ constexpr int D = QWM_D;
 constexpr int kGroup = 32;              // channels that share a step
 constexpr int kSteps = D / kGroup;      // step bytes of a row: one 32-bit word
 
+// Two floats as one operand of the packed fp32 instructions, and back.
+__device__ __forceinline__ uint64_t pair2(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ float2 split2(uint64_t v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+
 // ------------------------------------------------------------------ rotary positions
 
 // Cosine and sine of an angle given as pos * turn / 2^64 turns, each as an unevaluated sum hi + lo.
@@ -95,7 +107,8 @@ struct RopeTable {
 // INTERLEAVED: pairs (a, b) inside the vector, out_a = a c - b s, out_b = b c + a s; the packed lanes are
 // pairs 2 i and 2 i + 1.  HALF: the vector is the first or the second half of eight pairs and its partner
 // is another lane's: out = mine c -+ other s; the packed lanes are channels 2 i and 2 i + 1.
-template <int PAIRING>
+// WHOLE: all 128 channels are turned (every vector is active).
+template <int PAIRING, bool WHOLE>
 struct RopeVec {
   static constexpr int kN = PAIRING == QWM_ROPE_INTERLEAVED ? 2 : 4;
   uint64_t ch[kN], cl[kN], sh[kN], sl[kN], nch[kN], nsh[kN], nsl[kN];   // HALF: s signed for this half
@@ -134,13 +147,13 @@ struct RopeVec {
           f[e][3] = -f[e][3];
         }
       }
-      ch[i] = tc::f2(f[0][0], f[1][0]);
-      cl[i] = tc::f2(f[0][1], f[1][1]);
-      sh[i] = tc::f2(f[0][2], f[1][2]);
-      sl[i] = tc::f2(f[0][3], f[1][3]);
-      nch[i] = tc::f2(-f[0][0], -f[1][0]);
-      nsh[i] = tc::f2(-f[0][2], -f[1][2]);
-      nsl[i] = tc::f2(-f[0][3], -f[1][3]);
+      ch[i] = pair2(f[0][0], f[1][0]);
+      cl[i] = pair2(f[0][1], f[1][1]);
+      sh[i] = pair2(f[0][2], f[1][2]);
+      sl[i] = pair2(f[0][3], f[1][3]);
+      nch[i] = pair2(-f[0][0], -f[1][0]);
+      nsh[i] = pair2(-f[0][2], -f[1][2]);
+      nsl[i] = pair2(-f[0][3], -f[1][3]);
     }
   }
   // Turn the 8 bf16 channels in w (4 words).  HALF: every lane of the 16-lane row takes part.
@@ -150,21 +163,21 @@ struct RopeVec {
     if (PAIRING == QWM_ROPE_INTERLEAVED) {
 #pragma unroll
       for (int i = 0; i < 2; i++) {
-        const uint64_t a = tc::f2(lo(w[2 * i]), lo(w[2 * i + 1])), b = tc::f2(hi(w[2 * i]), hi(w[2 * i + 1]));
+        const uint64_t a = pair2(lo(w[2 * i]), lo(w[2 * i + 1])), b = pair2(hi(w[2 * i]), hi(w[2 * i + 1]));
         const uint64_t x = rope_pair(a, b, ch[i], cl[i], nsh[i], nsl[i], sh[i]);   // a c - b s
         const uint64_t y = rope_pair(a, b, sh[i], sl[i], ch[i], cl[i], nch[i]);    // a s + b c
-        if (2 * i < active) w[2 * i] = tc::pack_bf16x2(tc::f2lo(x), tc::f2lo(y));
-        if (2 * i + 1 < active) w[2 * i + 1] = tc::pack_bf16x2(tc::f2hi(x), tc::f2hi(y));
+        if (WHOLE || 2 * i < active) w[2 * i] = tc::pack_bf16x2(split2(x).x, split2(y).x);
+        if (WHOLE || 2 * i + 1 < active) w[2 * i + 1] = tc::pack_bf16x2(split2(x).y, split2(y).y);
       }
     } else {
-      const int lane = threadIdx.x & 31, off = sp.rot >> 4;
+      const int lane = threadIdx.x & 31, off = WHOLE ? 8 : sp.rot >> 4;
       const int partner = (active == 1 ? lane + off : (active == 2 ? lane - off : lane)) & 31;
 #pragma unroll
       for (int i = 0; i < 4; i++) {
         const uint32_t q = __shfl_sync(0xffffffffu, w[i], partner);
-        const uint64_t mine = tc::f2(lo(w[i]), hi(w[i])), other = tc::f2(lo(q), hi(q));
+        const uint64_t mine = pair2(lo(w[i]), hi(w[i])), other = pair2(lo(q), hi(q));
         const uint64_t x = rope_pair(mine, other, ch[i % kN], cl[i % kN], sh[i % kN], sl[i % kN], nsh[i % kN]);
-        if (active) w[i] = tc::pack_bf16x2(tc::f2lo(x), tc::f2hi(x));
+        if (WHOLE || active) w[i] = tc::pack_bf16x2(split2(x).x, split2(x).y);
       }
     }
   }
@@ -202,8 +215,8 @@ __device__ __forceinline__ uint32_t step_for(float amax, float &s) {
 // halfway between integers is at least 2^-9.9 away from halfway and stays on its side, while one that
 // is lands exactly on it (and then ties to even).
 __device__ __forceinline__ uint64_t codes_of(uint64_t x2, uint64_t inv2) {
-  const uint64_t grid = tc::f2(0x1.8p12f, 0x1.8p12f), ungrid = tc::f2(-0x1.8p12f, -0x1.8p12f);
-  return tc::add2(tc::add2(tc::fma2(x2, inv2, grid), ungrid), tc::f2(0x1.8p23f, 0x1.8p23f));
+  const uint64_t grid = pair2(0x1.8p12f, 0x1.8p12f), ungrid = pair2(-0x1.8p12f, -0x1.8p12f);
+  return tc::add2(tc::add2(tc::fma2(x2, inv2, grid), ungrid), pair2(0x1.8p23f, 0x1.8p23f));
 }
 
 // Decode constants of a step: s and -bias' s in both halves, where bias' is the integer that a code's fp16
