@@ -166,6 +166,7 @@ class Context:
         _check(_lib.qwm_create(C.byref(self.cfg), C.byref(h)), "qwm_create")
         self.handle = h
         self.device = torch.device("cuda", torch.cuda.current_device())
+        self.window_workspace = {}   # qwm_window_attend: workspace bytes by shape
 
     @property
     def heads(self):

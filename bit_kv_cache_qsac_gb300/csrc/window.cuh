@@ -2,6 +2,8 @@
 // steps, and which keys a Query row sees.
 #pragma once
 
+#include <atomic>
+
 #include "../../include/qwm_window.h"
 #include "qwm_internal.cuh"
 #include "tc.cuh"
@@ -131,30 +133,52 @@ struct RopeVec {
       i0 = active == 2 ? 8 * v - half : 8 * v;
       n = active ? 8 : 0;
     }
+    // HALF: a lane and its partner turn the same eight pairs; each forms the angles of four
+    constexpr int kMine = 4;
+    float f[2 * kN][4], g[kMine][4];
+#pragma unroll
+    for (int k = 0; k < kMine; k++) {
+      const int j = k + (PAIRING == QWM_ROPE_HALF && active == 2 ? 4 : 0);
+      g[k][0] = 1.f;
+      g[k][1] = g[k][2] = g[k][3] = 0.f;
+      if (j < n) {
+        const int ax = tab.axis[i0 + j];
+        rope_sincos(ax == 0 ? c[0] : (ax == 1 ? c[1] : c[2]), tab.turn[i0 + j], g[k][0], g[k][1], g[k][2], g[k][3]);
+      }
+    }
+    if (PAIRING == QWM_ROPE_INTERLEAVED) {
+#pragma unroll
+      for (int k = 0; k < kMine; k++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) f[k][e] = g[k][e];
+    } else {
+      const int other = partner(sp);
+#pragma unroll
+      for (int k = 0; k < kMine; k++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+          const float o = __shfl_sync(0xffffffffu, g[k][e], other);
+          const float a0 = active == 2 ? o : g[k][e], a1 = active == 2 ? g[k][e] : o;
+          const float sign = e >= 2 && active == 1 ? -1.f : 1.f;
+          f[k][e] = sign * a0;
+          f[(k + kMine) % (2 * kN)][e] = sign * a1;
+        }
+    }
 #pragma unroll
     for (int i = 0; i < kN; i++) {
-      float f[2][4];
-#pragma unroll
-      for (int e = 0; e < 2; e++) {
-        f[e][0] = 1.f;
-        f[e][1] = f[e][2] = f[e][3] = 0.f;
-        if (2 * i + e < n) {
-          const int k = i0 + 2 * i + e, ax = tab.axis[k];
-          rope_sincos(ax == 0 ? c[0] : (ax == 1 ? c[1] : c[2]), tab.turn[k], f[e][0], f[e][1], f[e][2], f[e][3]);
-        }
-        if (PAIRING == QWM_ROPE_HALF && active == 1) {
-          f[e][2] = -f[e][2];
-          f[e][3] = -f[e][3];
-        }
-      }
-      ch[i] = pair2(f[0][0], f[1][0]);
-      cl[i] = pair2(f[0][1], f[1][1]);
-      sh[i] = pair2(f[0][2], f[1][2]);
-      sl[i] = pair2(f[0][3], f[1][3]);
-      nch[i] = pair2(-f[0][0], -f[1][0]);
-      nsh[i] = pair2(-f[0][2], -f[1][2]);
-      nsl[i] = pair2(-f[0][3], -f[1][3]);
+      ch[i] = pair2(f[2 * i][0], f[2 * i + 1][0]);
+      cl[i] = pair2(f[2 * i][1], f[2 * i + 1][1]);
+      sh[i] = pair2(f[2 * i][2], f[2 * i + 1][2]);
+      sl[i] = pair2(f[2 * i][3], f[2 * i + 1][3]);
+      nch[i] = pair2(-f[2 * i][0], -f[2 * i + 1][0]);
+      nsh[i] = pair2(-f[2 * i][2], -f[2 * i + 1][2]);
+      nsl[i] = pair2(-f[2 * i][3], -f[2 * i + 1][3]);
     }
+  }
+  // HALF: the lane that holds the other half of this lane's pairs (itself where nothing is turned).
+  __device__ __forceinline__ int partner(const qwm_rope_spec &sp) const {
+    const int lane = threadIdx.x & 31, off = WHOLE ? 8 : sp.rot >> 4;
+    return (active == 1 ? lane + off : (active == 2 ? lane - off : lane)) & 31;
   }
   // Turn the 8 bf16 channels in w (4 words).  HALF: every lane of the 16-lane row takes part.
   __device__ __forceinline__ void turn(const qwm_rope_spec &sp, uint32_t (&w)[4]) const {
@@ -170,11 +194,10 @@ struct RopeVec {
         if (WHOLE || 2 * i + 1 < active) w[2 * i + 1] = tc::pack_bf16x2(split2(x).y, split2(y).y);
       }
     } else {
-      const int lane = threadIdx.x & 31, off = WHOLE ? 8 : sp.rot >> 4;
-      const int partner = (active == 1 ? lane + off : (active == 2 ? lane - off : lane)) & 31;
+      const int from = partner(sp);
 #pragma unroll
       for (int i = 0; i < 4; i++) {
-        const uint32_t q = __shfl_sync(0xffffffffu, w[i], partner);
+        const uint32_t q = __shfl_sync(0xffffffffu, w[i], from);
         const uint64_t mine = pair2(lo(w[i]), hi(w[i])), other = pair2(lo(q), hi(q));
         const uint64_t x = rope_pair(mine, other, ch[i % kN], cl[i % kN], sh[i % kN], sl[i % kN], nsh[i % kN]);
         if (WHOLE || active) w[i] = tc::pack_bf16x2(split2(x).x, split2(x).y);
@@ -355,6 +378,20 @@ struct Everyone {
 };
 
 }  // namespace win
+
+// Allow a kernel its dynamic shared memory, once per device (the attribute stays; setting it again on
+// every launch would cost more than the launch).  `done` is the kernel's own; a race sets it twice.
+template <typename Kernel>
+cudaError_t allow_shared(Kernel kernel, int bytes, std::atomic<uint64_t> &done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 // Heads that a block of the elementwise calls walks over: few enough for about `per_sm` blocks per SM, in
 // equal shares.  What a block forms once per token (angles, slots) costs about 2 us of latency, so the

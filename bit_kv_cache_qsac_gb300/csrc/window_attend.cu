@@ -87,31 +87,6 @@ struct RowOut {
     if (a.lse) lse = a.lse + (b * a.H + h) * a.nq + i;
     merge = a.merge;
   }
-  // 32 channels from channel c: (keep) out + o inv
-  __device__ __forceinline__ void store32(int c, const uint32_t (&o)[32], float inv, float keep) const {
-    if (bf16) {
-#pragma unroll
-      for (int v = 0; v < 4; v++) {
-        uint32_t w[4];
-#pragma unroll
-        for (int u = 0; u < 4; u++)
-          w[u] = tc::pack_bf16x2(__uint_as_float(o[8 * v + 2 * u]) * inv, __uint_as_float(o[8 * v + 2 * u + 1]) * inv);
-        *(uint4 *)(bf16 + c + 8 * v) = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-      return;
-    }
-#pragma unroll
-    for (int v = 0; v < 8; v++) {
-      float4 *dst = (float4 *)(f32 + c + 4 * v);
-      float4 x = make_float4(__uint_as_float(o[4 * v]) * inv, __uint_as_float(o[4 * v + 1]) * inv,
-                             __uint_as_float(o[4 * v + 2]) * inv, __uint_as_float(o[4 * v + 3]) * inv);
-      if (keep > 0.f) {
-        const float4 p = *dst;
-        x = make_float4(fmaf(keep, p.x, x.x), fmaf(keep, p.y, x.y), fmaf(keep, p.z, x.z), fmaf(keep, p.w, x.w));
-      }
-      *dst = x;
-    }
-  }
 };
 
 // A producer thread's share of a 128-key stage: four pieces of 16 channels.
@@ -238,45 +213,73 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int j0 = (int)((int64_t)tiles * split / a.splits);
   const int J = (int)((int64_t)tiles * (split + 1) / a.splits) - j0;
   const int64_t row_base = pair0 + (int64_t)cr * BM;   // this CTA's row 0 of tile 0
-  if (J == 0) {   // these rows see no key (in this part)
-    for (int e = tid; e < NQT * BM; e += kThreads) {
-      const int64_t r = row_base + (int64_t)(e / BM) * 2 * BM + e % BM;
+  if (J == 0) {   // these rows see no key (in this part): 16 lanes write a row's zeros
+    for (int e = tid; e < NQT * BM * 16; e += kThreads) {
+      const int64_t r = row_base + (int64_t)(e / 16 / BM) * 2 * BM + e / 16 % BM;
       if (r >= rows) continue;
       RowOut out;
       out.init(a, y, b, kvh, split, r);
       if (out.merge) continue;
-      const uint32_t zero[32] = {};
-      for (int c = 0; c < D; c += 32) out.store32(c, zero, 0.f, 0.f);
-      if (out.lse) *out.lse = -INFINITY;
+      const int c = 8 * (e & 15);
+      if (out.bf16) {
+        *(uint4 *)(out.bf16 + c) = make_uint4(0, 0, 0, 0);
+      } else {
+        *(float4 *)(out.f32 + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+        *(float4 *)(out.f32 + c + 4) = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      if (out.lse && c == 0) *out.lse = -INFINITY;
     }
     return;
   }
   const bool skip1 = pair0 + 2 * BM >= rows;   // the second 256-row tile is empty
 
-  // ---- this CTA's two Query tiles -> shared memory as fp16 ----
-  for (int e = tid; e < NQT * BM * (D / 8); e += kThreads) {
-    const int row = e / (D / 8), ci = e % (D / 8);
-    const int x = row / BM, rr = row % BM;
-    const int64_t r = row_base + (int64_t)x * 2 * BM + rr;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (r < rows) {
-      const int64_t i = win::quotient(r, a.group);
-      v = *(const uint4 *)(a.q + b * a.qs.batch + (kvh * a.group + (r - i * a.group)) * a.qs.head + i * a.qs.token +
-                           8 * ci);
+  // ---- this CTA's two Query tiles -> shared memory, by the softmax warps: all rows' copies in flight at
+  // once, then bf16 -> fp16 in place (loops kept rolled: code that runs once per CTA is fetched once) ----
+  if (warp < kSoftmaxWarps) {
+    const int ci = tid & 15, rr0 = tid >> 4;   // 16-byte piece of a row; rows rr0, rr0 + 16, ...
+    const uint16_t *qb = a.q + b * a.qs.batch + (int64_t)kvh * a.group * a.qs.head + 8 * ci;
+    // piece ci of row rr0 of tile 0; 16 rows on is 2 KB further, the next tile 2 blocks
+    const uint32_t dst = tc::smem_u32(sm) + OFF_Q + (uint32_t)(ci / 8) * kBlk + tc::sw128_offset((uint32_t)rr0, 8u * (ci % 8));
+    const int step_i = 16 / a.group, step_h = 16 - step_i * a.group;
+    int64_t r = row_base + rr0, i = win::quotient(r, a.group);
+    int h = (int)(r - i * a.group);
+#pragma unroll 1
+    for (int k = 0; k < NQT * BM / 16; k++) {
+      const bool in = r < rows;
+      tc::cp_async16_zfill(dst + (uint32_t)(k >> 3) * 2u * kBlk + (uint32_t)(k & 7) * 2048u,
+                           in ? qb + h * a.qs.head + i * a.qs.token : qb, in ? 16u : 0u);
+      r += 16;   // 16 rows on: 16 / group Queries and 16 % group heads
+      i += step_i;
+      h += step_h;
+      if (h >= a.group) {
+        h -= a.group;
+        i++;
+      }
+      if (k == 7) {   // the second tile starts 256 rows after the first
+        r = row_base + 2 * BM + rr0;
+        i = win::quotient(r, a.group);
+        h = (int)(r - i * a.group);
+      }
     }
-    const uint32_t bw[4] = {v.x, v.y, v.z, v.w};
-    uint32_t hw[4];
+    tc::cp_async_commit();
+    tc::cp_async_wait<0>();
     bool bad = false;
+#pragma unroll 2
+    for (int k = 0; k < NQT * BM / 16; k++) {
+      const uint32_t at = dst + (uint32_t)(k >> 3) * 2u * kBlk + (uint32_t)(k & 7) * 2048u;
+      const uint4 v = tc::lds128(at);
+      const uint32_t bw[4] = {v.x, v.y, v.z, v.w};
+      uint32_t hw[4];
 #pragma unroll
-    for (int u = 0; u < 4; u++) {
-      hw[u] = tc::pack_f16x2(__uint_as_float(bw[u] << 16), __uint_as_float(bw[u] & 0xFFFF0000u));
-      bad |= (hw[u] & 0x7C00u) == 0x7C00u || (hw[u] & 0x7C000000u) == 0x7C000000u;
+      for (int u = 0; u < 4; u++) {
+        hw[u] = tc::pack_f16x2(__uint_as_float(bw[u] << 16), __uint_as_float(bw[u] & 0xFFFF0000u));
+        bad |= (hw[u] & 0x7C00u) == 0x7C00u || (hw[u] & 0x7C000000u) == 0x7C000000u;
+      }
+      tc::sts128(at, make_uint4(hw[0], hw[1], hw[2], hw[3]));
     }
     if (bad) qwm_dev_error(a.status, QWM_ERR_RANGE);
-    *(uint4 *)(sm + OFF_Q + (x * 2 + ci / 8) * kBlk + tc::sw128_offset(rr, 8 * (ci % 8))) =
-        make_uint4(hw[0], hw[1], hw[2], hw[3]);
   }
-  if (tid == 0) {
+  if (tid == 32 * kMmaWarp) {
     for (int i = 0; i < kStages; i++) {
       tc::mbar_init(&bars.k_full[i], 2 * kProdWarps);  // both CTAs' producer warps (even CTA's copy used)
       tc::mbar_init(&bars.v_full[i], 2 * kProdWarps);
@@ -426,12 +429,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         if (write && out.lse) *out.lse = L;
       }
-      uint32_t o[32];
+      // through shared memory (every operand has been read), so that the stores write whole rows: a
+      // 16 KB buffer per warp, 16-byte pieces permuted by the row's low bits against bank conflicts
+      const uint32_t buf = tc::smem_u32(sm) + (uint32_t)warp * 16384u, rx = (uint32_t)lane & 7u;
+      const bool half = a.splits == 1 && !a.out_f32;   // bf16 rows
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
+        uint32_t o[32];
         tc::tmem_ld32(tO + c, o);
         tc::tmem_ld_wait();
-        if (write) out.store32(c, o, inv, keep);
+#pragma unroll
+        for (int i = 0; i < 32; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
+        if (half) {
+#pragma unroll
+          for (int v = 0; v < 4; v++) {
+            uint32_t w[4];
+#pragma unroll
+            for (int u = 0; u < 4; u++)
+              w[u] = tc::pack_bf16x2(__uint_as_float(o[8 * v + 2 * u]), __uint_as_float(o[8 * v + 2 * u + 1]));
+            tc::sts128(buf + (uint32_t)lane * 256u + ((((uint32_t)(c / 8 + v)) ^ rx) << 4), make_uint4(w[0], w[1], w[2], w[3]));
+          }
+        } else {
+#pragma unroll
+          for (int v = 0; v < 8; v++)
+            tc::sts128(buf + (uint32_t)lane * 512u + ((((uint32_t)(c / 4 + v)) ^ rx) << 4),
+                       make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]));
+        }
+      }
+      __syncwarp();
+      const uint32_t writes = __ballot_sync(0xffffffffu, write);
+      const uint64_t mine_out = half ? (uint64_t)out.bf16 : (uint64_t)out.f32;
+      if (half) {
+#pragma unroll 4
+        for (int i = 0; i < 16; i++) {
+          const int rw = 2 * i + (lane >> 4), c = lane & 15;
+          uint16_t *dst = (uint16_t *)__shfl_sync(0xffffffffu, mine_out, rw);
+          const uint4 v = tc::lds128(buf + (uint32_t)rw * 256u + ((uint32_t)(c ^ (rw & 7)) << 4));
+          if ((writes >> rw) & 1u) *(uint4 *)(dst + 8 * c) = v;
+        }
+      } else {
+#pragma unroll 4
+        for (int rw = 0; rw < 32; rw++) {
+          float *dst = (float *)__shfl_sync(0xffffffffu, mine_out, rw);
+          const float k = __shfl_sync(0xffffffffu, keep, rw);
+          const uint4 v = tc::lds128(buf + (uint32_t)rw * 512u + ((uint32_t)(lane ^ (rw & 7)) << 4));
+          if ((writes >> rw) & 1u) {
+            float4 x = make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+            if (k > 0.f) {
+              const float4 p = *(const float4 *)(dst + 4 * lane);
+              x = make_float4(fmaf(k, p.x, x.x), fmaf(k, p.y, x.y), fmaf(k, p.z, x.z), fmaf(k, p.w, x.w));
+            }
+            *(float4 *)(dst + 4 * lane) = x;
+          }
+        }
       }
     }
   } else if (warp == kMmaWarp) {
@@ -518,6 +568,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t s = keys.slot(v0, sink, ring);
       return v0 + BN <= keys.total && keys.slot(v0 + BN - 1, sink, ring) == s + BN - 1 ? (int64_t)s : -1;
     };
+    Pieces<BITS> k0, v0, k1, v1;
+    int64_t at = slot0_of(j0 * BN);
+    pk.load(keys, j0 * BN, at, sink, ring, k0);
+    pv.load(keys, j0 * BN, at, sink, ring, v0);
+    if (J > 1) {
+      at = slot0_of((j0 + 1) * BN);
+      pk.load(keys, (j0 + 1) * BN, at, sink, ring, k1);
+      pv.load(keys, (j0 + 1) * BN, at, sink, ring, v1);
+    }
     // the even CTA's full barriers (consecutive 8-byte words), as shared::cluster addresses
     const uint32_t k_full = tc::mapa(tc::smem_u32(&bars.k_full[0]), 0), v_full = tc::mapa(tc::smem_u32(&bars.v_full[0]), 0);
     auto hand_over = [&](uint32_t full) {
@@ -529,15 +588,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (j >= kStages && !tc::mbar_wait(empty, (j / kStages - 1) & 1, kWaitNs)) fail(&abort_flag, a.status);
       return !__any_sync(0xffffffffu, *abort_v != 0);         // warp-uniform exit
     };
-    Pieces<BITS> k0, v0, k1, v1;
-    int64_t at = slot0_of(j0 * BN);
-    pk.load(keys, j0 * BN, at, sink, ring, k0);
-    pv.load(keys, j0 * BN, at, sink, ring, v0);
-    if (J > 1) {
-      at = slot0_of((j0 + 1) * BN);
-      pk.load(keys, (j0 + 1) * BN, at, sink, ring, k1);
-      pv.load(keys, (j0 + 1) * BN, at, sink, ring, v1);
-    }
     auto stage = [&](int j, Pieces<BITS> &k, Pieces<BITS> &v) -> bool {
       const int s = j % kStages;
       if (!free_again(&bars.k_empty[s], j)) return false;
@@ -568,8 +618,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 template <int BITS>
 cudaError_t launch_bits(const WindowAttend &a, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(window_attend_kernel<BITS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       kSmemAlloc);
+  static std::atomic<uint64_t> allowed{0};
+  const cudaError_t e = allow_shared(window_attend_kernel<BITS>, kSmemAlloc, allowed);
   if (e != cudaSuccess) return e;
   const int64_t pairs = (int64_t)a.w.batch * a.w.kv_heads * ((a.rows + kPairRows - 1) / kPairRows);
   if (2 * pairs > INT32_MAX) return cudaErrorInvalidValue;

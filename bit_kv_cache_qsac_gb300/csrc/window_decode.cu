@@ -558,7 +558,8 @@ __global__ void __launch_bounds__(256) window_combine_kernel(const __grid_consta
 template <int BITS, int NT, bool CLUSTER>
 cudaError_t decode_launch(const WindowAttend &a, cudaStream_t st) {
   auto kernel = window_decode_kernel<BITS, NT, CLUSTER>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Ring<BITS>::kBytes);
+  static std::atomic<uint64_t> allowed{0};
+  const cudaError_t e = allow_shared(kernel, Ring<BITS>::kBytes, allowed);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.splits, (unsigned)(a.w.batch * a.w.kv_heads));

@@ -14,9 +14,10 @@ import math
 
 import torch
 
-from . import (ActiveChunk, Chunk, Context, pack_psac_layout, qwm_attend, qwm_attend_merge, qwm_dequantize,
+from . import (ActiveChunk, Chunk, Context, Window, pack_psac_layout, qwm_attend, qwm_attend_merge, qwm_dequantize,
                qwm_fit_centroids_kv,
-               qwm_quantize_kv, qwm_quantize_kv_full, qwm_select_rank, qwm_sync_status, qwm_update_query_stats)
+               qwm_quantize_kv, qwm_quantize_kv_full, qwm_rope, qwm_select_rank, qwm_sync_status,
+               qwm_update_query_stats, qwm_window_attend, qwm_window_read, qwm_window_write)
 
 
 class CompressedLayer:
@@ -181,3 +182,67 @@ class CompressedLayer:
 
     def nbytes(self) -> int:
         return sum(c.nbytes() for c in self.chunks)
+
+
+class WindowedLayer:
+    """One layer's cache with its newest chunks in a window at 8 or 4 bits and everything older packed to
+    2 bits.
+
+    The 2-bit packing is made for history; the newest frames, which the next ones lean on most, stay at 8
+    or 4 bits.  A step writes its chunk into the window (Keys turned by `rope`), attends over the packed
+    history and the window in one softmax, and folds its Queries into the statistics; when the window is
+    full, its oldest chunk is first read back and packed with the statistics gathered so far."""
+
+    def __init__(self, ctx: Context, chunk_tokens: int, window_chunks: int, bits: int = 8, tpf: int | None = None,
+                 rope=None, device=None, **layer_options):
+        """chunk_tokens: tokens of every chunk; window_chunks: chunks the window holds; tpf: tokens of a
+        frame, for the block-causal mask inside the window (default: a chunk, i.e. a chunk sees itself
+        whole); rope: a RopeSpec by which Queries and Keys are turned at their positions, or None;
+        layer_options: CompressedLayer's."""
+        if chunk_tokens < 1 or window_chunks < 1:
+            raise ValueError("chunk_tokens and window_chunks must be at least 1")
+        self.ctx = ctx
+        self.rope = rope
+        self.chunk_tokens = chunk_tokens
+        self.tpf = chunk_tokens if tpf is None else tpf
+        self.packed = CompressedLayer(ctx, device, **layer_options)
+        self.window = Window.empty(bits, 1, ctx.heads, 0, window_chunks * chunk_tokens, self.packed.device)
+        self.length = 0                                                        # tokens seen
+        self._length = torch.zeros(1, dtype=torch.int64, device=self.packed.device)   # the same, on the device
+
+    def step(self, k: torch.Tensor, v: torch.Tensor, q: torch.Tensor, stream=None) -> torch.Tensor:
+        """Add the chunk k, v [H][chunk_tokens][d] and attend with its Queries q [H][nq][d] (row i is token
+        i of the chunk): fp32 [H][nq][d]."""
+        n, ring = self.chunk_tokens, self.window.ring
+        H, nq, d = q.shape
+        if k.shape[1] != n or v.shape[1] != n or nq > n:
+            raise ValueError(f"expected a chunk of {n} tokens and at most as many Queries, got {k.shape[1]} and {nq}")
+        ctx, main = self.ctx, stream if stream is not None else torch.cuda.current_stream(self.packed.device)
+        with torch.cuda.stream(main):
+            if self.length >= ring:   # the oldest chunk makes room: read back and packed
+                old = [torch.empty(1, H, n, d, dtype=torch.bfloat16, device=k.device) for _ in range(2)]
+                qwm_window_read(ctx, self.window, self._length - ring, self._length, *old, stream=main)
+                self.packed.append_chunk(old[0][0], old[1][0], stream=main)
+            begin, self._length = self._length, self._length + n
+            qwm_window_write(ctx, self.window, k[None], v[None], begin, rope=self.rope, stream=main)
+            if self.rope is not None:
+                turned = torch.empty(H, nq, d, dtype=torch.bfloat16, device=q.device)
+                qwm_rope(ctx, self.rope, q[None], begin, turned[None], stream=main)
+                q = turned
+            out = torch.empty(H, nq, d, dtype=torch.float32, device=q.device)
+            lse = torch.empty(H, nq, dtype=torch.float32, device=q.device)
+            scale = 1.0 / math.sqrt(d)
+            if self.packed.chunks:
+                qwm_attend_merge(ctx, q, nq, self.packed.chunks, scale, out, lse, False, main)
+            # the window holds exactly the chunks that are not packed: every frame of it is recent
+            qwm_window_attend(ctx, self.window, q[None], begin, self._length, self.tpf, ring // self.tpf + 2, scale,
+                              out[None], lse=lse[None], merge=bool(self.packed.chunks), stream=main)
+            self.packed.fold_queries(q, main)
+            self.length += n
+        return out
+
+    def check(self, stream=None) -> int:
+        return self.packed.check(stream)
+
+    def nbytes(self) -> int:
+        return self.packed.nbytes() + self.window.nbytes()

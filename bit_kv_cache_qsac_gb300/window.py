@@ -78,43 +78,45 @@ class RopeSpec(qwm_rope_spec):
                       int(bool(inverse)), self)
 
 
-def _on(ctx, t: torch.Tensor, name: str) -> None:
+def _refuse(ctx, t, name: str, dtypes, shape) -> None:
+    """Raise what is wrong with a tensor (the checks that failed together in the callers)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name}: expected a CUDA tensor")
     if t.device != ctx.device:
         raise ValueError(f"{name}: on {t.device}, the context is on {ctx.device}")
-
-
-def _rows(ctx, t: torch.Tensor, name: str, shape, dtypes) -> tuple[int, qwm_strides]:
-    """Pointer and strides of an activation."""
-    _on(ctx, t, name)
     if t.dtype not in dtypes:
-        raise TypeError(f"{name}: expected one of {[str(d) for d in dtypes]}, got {t.dtype}")
+        raise TypeError(f"{name}: expected {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    st = t.stride()
-    if st[3] != 1:
+    raise ValueError(f"{name}: tensor must be contiguous")
+
+
+def _rows(ctx, t, name: str, shape, dtypes):
+    """Pointer and strides of an activation."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.shape != shape or t.device != ctx.device:
+        _refuse(ctx, t, name, dtypes, shape)
+    b, h, n, one = t.stride()
+    if one != 1:
         raise ValueError(f"{name}: channels must be contiguous")
-    return t.data_ptr(), qwm_strides(*(st[i] if shape[i] > 1 else 0 for i in range(3)))
+    return t.data_ptr(), qwm_strides(b if shape[0] > 1 else 0, h if shape[1] > 1 else 0, n if shape[2] > 1 else 0)
 
 
 def _array(ctx, t, name: str, dtype, shape) -> int | None:
     """Pointer of a dense device array (or None)."""
     if t is None:
         return None
-    _on(ctx, t, name)
-    if t.dtype != dtype:
-        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: tensor must be contiguous")
+    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.device != ctx.device or
+            not t.is_contiguous()):
+        _refuse(ctx, t, name, (dtype,), shape)
     return t.data_ptr()
+
+
+_current_stream = torch._C._cuda_getCurrentRawStream   # the handle itself: a tenth of torch.cuda.current_stream's time
 
 
 def _stream_of(ctx, stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream(ctx.device).cuda_stream
+        return _current_stream(ctx.device.index)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -236,7 +238,12 @@ def qwm_window_attend(ctx, win: Window, q, q_start, length, tpf: int, frames: in
     shape = (w.batch, H, nq, _D)
     qp, qs = _rows(ctx, q, "q", shape, _BF16)
     op, os_ = _rows(ctx, out, "out", shape, _BF16 + (torch.float32,))
-    need = _lib.qwm_window_attend_workspace(ctx.handle, C.byref(w), nq, tpf, frames)
+    key = (w.batch, w.kv_heads, w.sink, w.ring, nq, tpf, frames)   # all the size depends on, beside the context
+    need = ctx.window_workspace.get(key)
+    if need is None:
+        need = ctx.window_workspace[key] = _lib.qwm_window_attend_workspace(ctx.handle, C.byref(w), nq, tpf, frames)
+        if len(ctx.window_workspace) > 1000:
+            ctx.window_workspace.clear()
     if need and ws is None:
         if stream is None:
             ws = torch.empty(need, dtype=torch.uint8, device=ctx.device)
@@ -245,7 +252,7 @@ def qwm_window_attend(ctx, win: Window, q, q_start, length, tpf: int, frames: in
             with torch.cuda.stream(s):
                 ws = torch.empty(need, dtype=torch.uint8, device=ctx.device)
     if ws is not None:
-        _array(ctx, ws, "ws", torch.uint8, tuple(ws.shape))
+        _array(ctx, ws, "ws", torch.uint8, (ws.numel(),))
     _check(_lib.qwm_window_attend(ctx.handle, C.byref(w), qp, C.byref(qs), nq,
                                   _array(ctx, q_start, "q_start", torch.int64, (w.batch,)),
                                   _array(ctx, length, "length", torch.int64, (w.batch,)),

@@ -530,3 +530,44 @@ def test_two_calls_at_once(qwm):
     torch.cuda.synchronize()
     for w, g in zip(want, got):
         assert all(torch.equal(w, o) for o in g)
+
+
+@pytest.mark.parametrize("bits,tpf,rope", [(8, None, True), (4, 64, False)])
+def test_windowed_layer_over_a_packed_history(qwm, bits, tpf, rope):
+    """A stream of chunks: the newest two in the window, older ones read back and packed to 2 bits.  The
+    output equals 64-bit attention over the packed chunks (the oracle's) and the window's values joined by
+    their log-sum-exps, within the attention's bar of 2e-2 x RMS(O)."""
+    import oracle
+    import synth
+    from bit_kv_cache_qsac_gb300 import stream
+    from helpers import chunk_head, from_u16, to_u16
+    H, n = 2, 256
+    ctx = qwm.Context(heads=H, n_centroids=64)
+    spec = qwm.RopeSpec((44, 42, 42), grid=(16, 16)) if rope else None
+    layer = stream.WindowedLayer(ctx, n, 2, bits=bits, tpf=tpf, rope=spec)
+    keys, vals = synth.keys(synth.TINY), synth.values(synth.TINY)
+    for t in range(4):
+        k, v = (from_u16(np.ascontiguousarray(x[:, t * n:(t + 1) * n]), torch.bfloat16) for x in (keys, vals))
+        q = from_u16(synth.queries(synth.TINY, t, n), torch.bfloat16)
+        out = layer.step(k, v, q)
+        assert layer.check() == 0
+        assert len(layer.packed.chunks) == max(0, t - 1)
+        if rope:
+            turned = torch.empty(1, H, n, 128, dtype=torch.bfloat16, device="cuda")
+            qwm.qwm_rope(ctx, spec, q[None], ints([t * n]), turned)
+            q = turned[0]
+        length = (t + 1) * n
+        for h in range(H):
+            pos, kw, vw = decoded(layer.window, 0, h, length)
+            assert pos[0] == max(0, length - 2 * n)
+            want, lse, _, _ = ref.attend(f64(q[h]), kw, vw, pos, t * n, tpf or n, 10 ** 6, 0, SCALE)
+            if layer.packed.chunks:
+                heads = [chunk_head(c, h) for c in layer.packed.chunks]
+                far, far_lse = oracle.attend_rows(to_u16(q[h]), np.arange(n), heads, SCALE, with_lse=True)
+                top = np.maximum(lse, far_lse)
+                a, b = np.exp2(lse - top)[:, None], np.exp2(far_lse - top)[:, None]
+                want = (a * want + b * far) / (a + b)
+            err = np.abs(f64(out[h]) - want).max() / np.sqrt(np.mean(want ** 2))
+            assert err <= 2e-2, (t, h, err)
+    with pytest.raises(ValueError):
+        layer.step(k[:, :10], v[:, :10], q[:, :10])
