@@ -210,8 +210,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   win::Keys keys;
   keys.init(seq, frame_of(pair0), frame_of(pair1 - 1));
   const int tiles = (keys.total + BN - 1) / BN;
-  const int j0 = (int)((int64_t)tiles * split / a.splits);
-  const int J = (int)((int64_t)tiles * (split + 1) / a.splits) - j0;
+  // (tiles < 2^24 and splits <= 64: 32 bits)
+  const int j0 = a.splits == 1 ? 0 : (int)((uint32_t)tiles * (uint32_t)split / (uint32_t)a.splits);
+  const int J = (a.splits == 1 ? tiles : (int)((uint32_t)tiles * (uint32_t)(split + 1) / (uint32_t)a.splits)) - j0;
   const int64_t row_base = pair0 + (int64_t)cr * BM;   // this CTA's row 0 of tile 0
   if (J == 0) {   // these rows see no key (in this part): 16 lanes write a row's zeros
     for (int e = tid; e < NQT * BM * 16; e += kThreads) {
@@ -240,31 +241,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint16_t *qb = a.q + b * a.qs.batch + (int64_t)kvh * a.group * a.qs.head + 8 * ci;
     // piece ci of row rr0 of tile 0; 16 rows on is 2 KB further, the next tile 2 blocks
     const uint32_t dst = tc::smem_u32(sm) + OFF_Q + (uint32_t)(ci / 8) * kBlk + tc::sw128_offset((uint32_t)rr0, 8u * (ci % 8));
+    // 16 rows on: 16 / group Queries and 16 % group heads, a Query more where the heads run over
     const int step_i = 16 / a.group, step_h = 16 - step_i * a.group;
-    int64_t r = row_base + rr0, i = win::quotient(r, a.group);
-    int h = (int)(r - i * a.group);
+    const int64_t ahead = step_i * a.qs.token + step_h * a.qs.head, wrap = a.qs.token - a.group * a.qs.head;
 #pragma unroll 1
-    for (int k = 0; k < NQT * BM / 16; k++) {
-      const bool in = r < rows;
-      tc::cp_async16_zfill(dst + (uint32_t)(k >> 3) * 2u * kBlk + (uint32_t)(k & 7) * 2048u,
-                           in ? qb + h * a.qs.head + i * a.qs.token : qb, in ? 16u : 0u);
-      r += 16;   // 16 rows on: 16 / group Queries and 16 % group heads
-      i += step_i;
-      h += step_h;
-      if (h >= a.group) {
-        h -= a.group;
-        i++;
-      }
-      if (k == 7) {   // the second tile starts 256 rows after the first
-        r = row_base + 2 * BM + rr0;
-        i = win::quotient(r, a.group);
-        h = (int)(r - i * a.group);
+    for (int x = 0; x < NQT; x++) {
+      int64_t r = row_base + (int64_t)x * 2 * BM + rr0;
+      const int64_t i = win::quotient(r, a.group);
+      int h = (int)(r - i * a.group);
+      const uint16_t *src = qb + h * a.qs.head + i * a.qs.token;
+#pragma unroll
+      for (int k = 0; k < BM / 16; k++) {
+        const bool in = r < rows;
+        tc::cp_async16_zfill(dst + (uint32_t)x * 2u * kBlk + (uint32_t)k * 2048u, in ? src : qb, in ? 16u : 0u);
+        r += 16;
+        h += step_h;
+        src += ahead + (h >= a.group ? wrap : 0);
+        h -= h >= a.group ? a.group : 0;
       }
     }
     tc::cp_async_commit();
     tc::cp_async_wait<0>();
     bool bad = false;
-#pragma unroll 2
+#pragma unroll 8
     for (int k = 0; k < NQT * BM / 16; k++) {
       const uint32_t at = dst + (uint32_t)(k >> 3) * 2u * kBlk + (uint32_t)(k & 7) * 2048u;
       const uint4 v = tc::lds128(at);
@@ -300,6 +299,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc::mbar_init(&bars.drain, 1);
     abort_flag = 0;
     tc::fence_mbar_init();
+  }
+  // producers: their sides, and the codes of the first stage, fetched while the Queries are
+  const int pw = warp >= kProdWarp0 && warp < kProdWarp0 + kProdWarps ? warp - kProdWarp0 : 0;
+  const Producer<BITS, false> pk(a, sm, y, cr, pw, lane);
+  const Producer<BITS, true> pv(a, sm, y, cr, pw, lane);
+  const uint32_t sink = (uint32_t)a.w.sink, ring = (uint32_t)a.w.ring;
+  auto slot0_of = [&](int v0) -> int64_t {   // the slot of key v0 when the stage's slots are consecutive
+    const uint32_t s = keys.slot(v0, sink, ring);
+    return v0 + BN <= keys.total && keys.slot(v0 + BN - 1, sink, ring) == s + BN - 1 ? (int64_t)s : -1;
+  };
+  Pieces<BITS> k0, v0, k1, v1;
+  int64_t at = 0;
+  if (warp >= kProdWarp0 && warp < kProdWarp0 + kProdWarps) {
+    at = slot0_of(j0 * BN);
+    pk.load(keys, j0 * BN, at, sink, ring, k0);
+    pv.load(keys, j0 * BN, at, sink, ring, v0);
   }
   if (warp == kMmaWarp) {
     tc::tmem_alloc2(&tmem_base_sh, 512);
@@ -560,18 +575,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else {
     // ======================= producers: Keys, then Values, of every stage =======================
-    const int w = warp - kProdWarp0;
-    const Producer<BITS, false> pk(a, sm, y, cr, w, lane);
-    const Producer<BITS, true> pv(a, sm, y, cr, w, lane);
-    const uint32_t sink = (uint32_t)a.w.sink, ring = (uint32_t)a.w.ring;
-    auto slot0_of = [&](int v0) -> int64_t {   // the slot of key v0 when the stage's slots are consecutive
-      const uint32_t s = keys.slot(v0, sink, ring);
-      return v0 + BN <= keys.total && keys.slot(v0 + BN - 1, sink, ring) == s + BN - 1 ? (int64_t)s : -1;
-    };
-    Pieces<BITS> k0, v0, k1, v1;
-    int64_t at = slot0_of(j0 * BN);
-    pk.load(keys, j0 * BN, at, sink, ring, k0);
-    pv.load(keys, j0 * BN, at, sink, ring, v0);
     if (J > 1) {
       at = slot0_of((j0 + 1) * BN);
       pk.load(keys, (j0 + 1) * BN, at, sink, ring, k1);

@@ -142,7 +142,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) window_decode_kerne
   const int rows = (int)nq * a.group;
   const int64_t head_row = (int64_t)blockIdx.y * (a.w.sink + a.w.ring);
   const int steps_all = (keys.total + kKeys - 1) / kKeys;
-  const int j0 = (int)((int64_t)steps_all * blockIdx.x / a.splits), j1 = (int)((int64_t)steps_all * (blockIdx.x + 1) / a.splits);
+  int j0 = 0, j1 = steps_all;   // (steps_all < 2^28 and splits <= 64: the products can pass 32 bits)
+  if (a.splits > 1) {
+    const uint32_t q = (uint32_t)steps_all / (uint32_t)a.splits, rem = (uint32_t)steps_all - q * (uint32_t)a.splits, k = blockIdx.x;
+    j0 = (int)(k * q + (k < rem ? k : rem));
+    j1 = j0 + (int)(q + (k < rem ? 1u : 0u));
+  }
 
   // ---- copies of step j's 16 keys into a stage of the warp's ring (one group) ----
   const uint32_t ring0 = tc::smem_u32(dyn) + (uint32_t)(warp * R::kStages * R::kStage);
