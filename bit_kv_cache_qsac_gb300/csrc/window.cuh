@@ -433,17 +433,19 @@ struct WindowAttend {
   int H, group;          // Query heads; Query heads per Key head
   int64_t rows;          // group * nq: Query rows of one Key head, row r = (Query i = r / group, head r % group)
   int splits;            // parts the keys are split into
+  int cluster;           // warp tiles: the parts are the CTAs of a cluster
   float *part;           // splits > 1: [batch * kv_heads][splits][rows][128] outputs of the parts,
   float *part_lse;       //             [batch * kv_heads][splits][rows] their log-sum-exps
   win::Bases bases;      // win::kBases
 };
 // How a call is run: with tensor-memory tiles of 256 Query rows per CTA, or with warp tiles of 8 or 16
 // rows; and into how many parts its keys are split.
-constexpr int kWindowCluster = 8;   // parts of the warp tiles that are joined inside a thread-block cluster
+constexpr int kWindowCluster = 8;   // parts of the warp tiles that are joined inside a thread-block cluster, at most
 struct WindowPlan {
   bool tiles;
   int splits;
-  bool joins() const { return splits > 1 && (tiles || splits > kWindowCluster); }   // by a second kernel
+  bool cluster;   // the parts are a cluster's CTAs; else (splits > 1) a second kernel joins them
+  bool joins() const { return splits > 1 && !cluster; }
 };
 WindowPlan window_plan(int64_t batch, int64_t kv_heads, int64_t rows, int64_t keys, int num_sms);
 cudaError_t launch_window_decode(const WindowAttend &a, cudaStream_t st);

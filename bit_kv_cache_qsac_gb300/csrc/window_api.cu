@@ -248,6 +248,7 @@ qwm_status qwm_window_attend(qwm_ctx *ctx, const qwm_window *win, const uint16_t
   a.status = ctx->status;
   a.H = H; a.group = H / win->kv_heads; a.rows = nq * a.group;
   a.splits = p.splits;
+  a.cluster = p.cluster;
   a.bases = win::kBases;
   a.part = p.joins() ? (float *)ws : nullptr;
   a.part_lse = p.joins() ? a.part + (size_t)win->batch * H * (size_t)nq * p.splits * QWM_D : nullptr;

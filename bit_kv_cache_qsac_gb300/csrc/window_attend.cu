@@ -198,12 +198,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int cr = (int)tc::cluster_ctarank();
   volatile int *abort_v = &abort_flag;
 
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the joining kernel, if any, may line up
+  // ---- this CTA's two Query tiles -> shared memory, by the softmax warps: all rows' copies in flight while
+  // the rest is worked out, whatever turns out to be padding ----
+  const int64_t pair0 = item * kPairRows, row_base = pair0 + (int64_t)cr * BM;   // row_base: this CTA's row 0 of tile 0
+  // this thread's piece of row tid / 16 of tile 0; 16 rows on is 2 KB further, the next tile 2 blocks
+  const uint32_t q_dst = tc::smem_u32(sm) + OFF_Q + (uint32_t)((tid & 15) / 8) * kBlk +
+                         tc::sw128_offset((uint32_t)tid >> 4, 8u * (tid & 7));
+  if (warp < kSoftmaxWarps) {
+    const int ci = tid & 15, rr0 = tid >> 4;   // 16-byte piece of a row; rows rr0, rr0 + 16, ...
+    const uint16_t *qb = a.q + b * a.qs.batch + (int64_t)kvh * a.group * a.qs.head + 8 * ci;
+    // 16 rows on: 16 / group Queries and 16 % group heads, a Query more where the heads run over
+    const int step_i = 16 / a.group, step_h = 16 - step_i * a.group;
+    const int64_t ahead = step_i * a.qs.token + step_h * a.qs.head, wrap = a.qs.token - a.group * a.qs.head;
+#pragma unroll 1
+    for (int x = 0; x < NQT; x++) {
+      int64_t r = row_base + (int64_t)x * 2 * BM + rr0;
+      const int64_t i = win::quotient(r, a.group);
+      int h = (int)(r - i * a.group);
+      const uint16_t *src = qb + h * a.qs.head + i * a.qs.token;
+#pragma unroll
+      for (int k = 0; k < BM / 16; k++) {
+        const bool in = r < a.rows;
+        tc::cp_async16_zfill(q_dst + (uint32_t)x * 2u * kBlk + (uint32_t)k * 2048u, in ? src : qb, in ? 16u : 0u);
+        r += 16;
+        h += step_h;
+        src += ahead + (h >= a.group ? wrap : 0);
+        h -= h >= a.group ? a.group : 0;
+      }
+    }
+    tc::cp_async_commit();
+  }
+
   const int64_t q0 = a.q_start[b];
   int64_t nq = a.q_count ? (int64_t)a.q_count[b] : a.nq;
   nq = nq < a.nq ? nq : a.nq;
-  const int64_t pair0 = item * kPairRows;
   const int64_t rows = nq * a.group;              // live rows of this Key head
-  if (q0 < 0 || pair0 >= rows) return;            // the same in both CTAs
+  if (q0 < 0 || pair0 >= rows) {                  // the same in both CTAs
+    tc::cp_async_wait<0>();
+    return;
+  }
   const win::Seq seq{a.length[b], a.w.sink, a.w.ring, a.tpf, a.frames};
   auto frame_of = [&](int64_t r) { return seq.frame(q0 + win::quotient(r, a.group)); };
   const int64_t pair1 = pair0 + kPairRows < rows ? pair0 + kPairRows : rows;
@@ -213,7 +247,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // (tiles < 2^24 and splits <= 64: 32 bits)
   const int j0 = a.splits == 1 ? 0 : (int)((uint32_t)tiles * (uint32_t)split / (uint32_t)a.splits);
   const int J = (a.splits == 1 ? tiles : (int)((uint32_t)tiles * (uint32_t)(split + 1) / (uint32_t)a.splits)) - j0;
-  const int64_t row_base = pair0 + (int64_t)cr * BM;   // this CTA's row 0 of tile 0
   if (J == 0) {   // these rows see no key (in this part): 16 lanes write a row's zeros
     for (int e = tid; e < NQT * BM * 16; e += kThreads) {
       const int64_t r = row_base + (int64_t)(e / 16 / BM) * 2 * BM + e / 16 % BM;
@@ -230,48 +263,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       if (out.lse && c == 0) *out.lse = -INFINITY;
     }
+    tc::cp_async_wait<0>();
     return;
   }
   const bool skip1 = pair0 + 2 * BM >= rows;   // the second 256-row tile is empty
 
-  // ---- this CTA's two Query tiles -> shared memory, by the softmax warps: all rows' copies in flight at
-  // once, then bf16 -> fp16 in place (loops kept rolled: code that runs once per CTA is fetched once) ----
+  // ---- the Queries, which have arrived by now: bf16 -> fp16 in place, padding rows 0 ----
   if (warp < kSoftmaxWarps) {
-    const int ci = tid & 15, rr0 = tid >> 4;   // 16-byte piece of a row; rows rr0, rr0 + 16, ...
-    const uint16_t *qb = a.q + b * a.qs.batch + (int64_t)kvh * a.group * a.qs.head + 8 * ci;
-    // piece ci of row rr0 of tile 0; 16 rows on is 2 KB further, the next tile 2 blocks
-    const uint32_t dst = tc::smem_u32(sm) + OFF_Q + (uint32_t)(ci / 8) * kBlk + tc::sw128_offset((uint32_t)rr0, 8u * (ci % 8));
-    // 16 rows on: 16 / group Queries and 16 % group heads, a Query more where the heads run over
-    const int step_i = 16 / a.group, step_h = 16 - step_i * a.group;
-    const int64_t ahead = step_i * a.qs.token + step_h * a.qs.head, wrap = a.qs.token - a.group * a.qs.head;
-#pragma unroll 1
-    for (int x = 0; x < NQT; x++) {
-      int64_t r = row_base + (int64_t)x * 2 * BM + rr0;
-      const int64_t i = win::quotient(r, a.group);
-      int h = (int)(r - i * a.group);
-      const uint16_t *src = qb + h * a.qs.head + i * a.qs.token;
-#pragma unroll
-      for (int k = 0; k < BM / 16; k++) {
-        const bool in = r < rows;
-        tc::cp_async16_zfill(dst + (uint32_t)x * 2u * kBlk + (uint32_t)k * 2048u, in ? src : qb, in ? 16u : 0u);
-        r += 16;
-        h += step_h;
-        src += ahead + (h >= a.group ? wrap : 0);
-        h -= h >= a.group ? a.group : 0;
-      }
-    }
-    tc::cp_async_commit();
     tc::cp_async_wait<0>();
     bool bad = false;
 #pragma unroll 8
     for (int k = 0; k < NQT * BM / 16; k++) {
-      const uint32_t at = dst + (uint32_t)(k >> 3) * 2u * kBlk + (uint32_t)(k & 7) * 2048u;
+      const uint32_t at = q_dst + (uint32_t)(k >> 3) * 2u * kBlk + (uint32_t)(k & 7) * 2048u;
+      const bool in = row_base + (k >> 3) * 2 * BM + (k & 7) * 16 + (tid >> 4) < rows;
       const uint4 v = tc::lds128(at);
       const uint32_t bw[4] = {v.x, v.y, v.z, v.w};
       uint32_t hw[4];
 #pragma unroll
       for (int u = 0; u < 4; u++) {
-        hw[u] = tc::pack_f16x2(__uint_as_float(bw[u] << 16), __uint_as_float(bw[u] & 0xFFFF0000u));
+        hw[u] = in ? tc::pack_f16x2(__uint_as_float(bw[u] << 16), __uint_as_float(bw[u] & 0xFFFF0000u)) : 0u;
         bad |= (hw[u] & 0x7C00u) == 0x7C00u || (hw[u] & 0x7C000000u) == 0x7C000000u;
       }
       tc::sts128(at, make_uint4(hw[0], hw[1], hw[2], hw[3]));
@@ -638,22 +648,24 @@ cudaError_t launch_window_tiles(const WindowAttend &a, cudaStream_t st) {
 }
 
 // Few rows run on warp tiles, which read the cache once per 16 rows at most; more run on tensor-memory
-// tiles.  Keys are split until the parts fill the SMs, while a part keeps a few steps of work.  Warp tiles
-// are first split into a cluster's CTAs (clusters of 7 or 8 leave SMs of a GPC over: a tenth of the
-// slots is counted off), further only where 8 parts would leave long parts to few SMs.
+// tiles.  Keys are split until the parts fill the SMs, while a part keeps a few steps of work.
+// Warp tiles: up to 8 parts are the CTAs of a cluster (clusters do not fill every slot of a GPC: a tenth of
+// the slots is counted off); a second kernel that joins more parts costs about 3 us, some 500 keys of a
+// CTA's time, so it is taken where the parts get that much shorter.
 WindowPlan window_plan(int64_t batch, int64_t kv_heads, int64_t rows, int64_t keys, int num_sms) {
   WindowPlan p;
   p.tiles = rows > 16;
-  const int64_t most = (keys + 255) / 256;
-  int64_t s;
+  const int64_t heads = batch * kv_heads, most = (keys + 255) / 256;
+  auto clamp = [&](int64_t s, int64_t top) { return s < 1 ? 1 : (s < most ? (s < top ? s : top) : (most < top ? most : top)); };
   if (p.tiles) {
-    s = (int64_t)num_sms / (batch * kv_heads * 2 * ((rows + kPairRows - 1) / kPairRows));
-  } else {
-    const int64_t slots = (rows <= 8 ? 2 : 1) * (int64_t)num_sms;
-    s = slots * 9 / 10 / (batch * kv_heads);
-    if (s > kWindowCluster && keys <= 1024 * kWindowCluster) s = kWindowCluster;
+    p.cluster = false;
+    p.splits = (int)clamp((int64_t)num_sms / (heads * 2 * ((rows + kPairRows - 1) / kPairRows)), 64);
+    return p;
   }
-  s = s < most ? s : most;
-  p.splits = (int)(s < 1 ? 1 : (s > 64 ? 64 : s));
+  const int64_t slots = (rows <= 8 ? 2 : 1) * (int64_t)num_sms;
+  const int64_t near = clamp(slots * 9 / 10 / heads, kWindowCluster), far = clamp(slots / heads, 64);
+  p.cluster = keys / near - keys / far < 512;
+  p.splits = (int)(p.cluster ? near : far);
+  if (p.splits == 1) p.cluster = false;
   return p;
 }

@@ -130,6 +130,22 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) window_decode_kerne
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const uint32_t b = blockIdx.y / (uint32_t)a.w.kv_heads;
   const int kvh = (int)(blockIdx.y - b * (uint32_t)a.w.kv_heads);
+  if (!CLUSTER) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the joining kernel may line up
+  // ---- Queries as the first product's B fragments (row g of every 8), bf16 for now; on their way while
+  // the rest is worked out, and whatever they are: rows that turn out to be padding are dropped below ----
+  uint32_t qf[NT][8][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; nt++) {
+    const int r = 8 * nt + g, i = (int)((uint32_t)r / (uint32_t)a.group);
+    const uint16_t *qp = a.q + b * a.qs.batch + (kvh * a.group + (r - i * a.group)) * a.qs.head + i * a.qs.token;
+#pragma unroll
+    for (int ks = 0; ks < 8; ks++) {
+      const int ch = BITS == 8 ? 16 * (t + 4 * (ks >> 2)) + 4 * (ks & 3) : 32 * t + 4 * ks;
+      const uint2 w = r < a.rows ? *(const uint2 *)(qp + ch) : make_uint2(0, 0);
+      qf[nt][ks][0] = w.x;
+      qf[nt][ks][1] = w.y;
+    }
+  }
   const int64_t q0 = a.q_start[b], len = a.length[b];
   int64_t nq = a.q_count ? (int64_t)a.q_count[b] : a.nq;
   nq = nq < a.nq ? nq : a.nq;
@@ -195,36 +211,19 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) window_decode_kerne
   copy(j0 + warp, 0);
   copy(j0 + warp + kWarps, 1);
 
-  // ---- the rows this thread masks (columns 2 t, 2 t + 1 of every 8), and what all rows see ----
-  win::Row mask[NT][2];
+  win::Everyone every;
+  every.init(seq, keys, f0, f1);
+  bool bad = false;
 #pragma unroll
   for (int nt = 0; nt < NT; nt++)
 #pragma unroll
-    for (int e = 0; e < 2; e++) {
-      const int r = 8 * nt + 2 * t + e;
-      mask[nt][e].init(seq, keys, r < rows ? seq.frame(q0 + r / a.group) : -1);
-    }
-  win::Everyone every;
-  every.init(seq, keys, f0, f1);
-
-  // ---- Queries as the first product's B fragments (row g of every 8), fp16 ----
-  uint32_t qf[NT][8][2];
-  bool bad = false;
+    for (int ks = 0; ks < 8; ks++)
 #pragma unroll
-  for (int nt = 0; nt < NT; nt++) {
-    const int r = 8 * nt + g, i = r / a.group;
-    const uint16_t *qp = a.q + b * a.qs.batch + (kvh * a.group + (r - i * a.group)) * a.qs.head + i * a.qs.token;
-#pragma unroll
-    for (int ks = 0; ks < 8; ks++) {
-      const int ch = BITS == 8 ? 16 * (t + 4 * (ks >> 2)) + 4 * (ks & 3) : 32 * t + 4 * ks;
-      const uint2 w = r < rows ? *(const uint2 *)(qp + ch) : make_uint2(0, 0);
-      qf[nt][ks][0] = tc::pack_f16x2(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u));
-      qf[nt][ks][1] = tc::pack_f16x2(__uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u));
-#pragma unroll
-      for (int e = 0; e < 2; e++)
+      for (int e = 0; e < 2; e++) {
+        const uint32_t w = 8 * nt + g < rows ? qf[nt][ks][e] : 0u;
+        qf[nt][ks][e] = tc::pack_f16x2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
         bad |= (qf[nt][ks][e] & 0x7C00u) == 0x7C00u || (qf[nt][ks][e] & 0x7C000000u) == 0x7C000000u;
-    }
-  }
+      }
   if (bad) qwm_dev_error(a.status, QWM_ERR_RANGE);
 
   float o[NT][8][4], m[NT][2], mneg[NT][2], l[NT][2];
@@ -316,14 +315,20 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) window_decode_kerne
         for (int e = 0; e < 4; e++) s[u16][nt][e] += s_[nt][e];
     }
     // ---- masked; the running maximum (log2 units); P ----
-    if (!every.see(v0, v0 + kKeys)) {
+    if (!every.see(v0, v0 + kKeys)) {   // a few steps of a call: what each of the thread's rows sees is worked out here
 #pragma unroll
-      for (int u16 = 0; u16 < kSub; u16++)
+      for (int nt = 0; nt < NT; nt++)
 #pragma unroll
-        for (int nt = 0; nt < NT; nt++)
+        for (int e = 0; e < 2; e++) {
+          const int r = 8 * nt + 2 * t + e;
+          win::Row mask;
+          mask.init(seq, keys, r < rows ? seq.frame(q0 + (uint32_t)r / (uint32_t)a.group) : -1);
 #pragma unroll
-          for (int e = 0; e < 4; e++)
-            if (!mask[nt][e & 1].sees(v0 + 16 * u16 + krow + (e & 2))) s[u16][nt][e] = -INFINITY;
+          for (int u16 = 0; u16 < kSub; u16++)
+#pragma unroll
+            for (int k = 0; k < 2; k++)
+              if (!mask.sees(v0 + 16 * u16 + krow + 2 * k)) s[u16][nt][e + 2 * k] = -INFINITY;
+        }
     }
     uint32_t pb[kSub][NT][2];
 #pragma unroll
@@ -527,6 +532,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) window_decode_kerne
 // Parts of a row joined: the weighted mean of the parts' outputs, each weighted by its share of the
 // exponential sum.  One warp per row.
 __global__ void __launch_bounds__(256) window_combine_kernel(const __grid_constant__ WindowAttend a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // launched while the parts are computed: wait for them
   const int lane = threadIdx.x & 31;
   const int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int64_t heads = (int64_t)a.w.batch * a.w.kv_heads;
@@ -582,9 +588,8 @@ cudaError_t decode_launch(const WindowAttend &a, cudaStream_t st) {
 
 template <int BITS>
 cudaError_t decode_bits(const WindowAttend &a, cudaStream_t st) {
-  const bool cluster = a.splits > 1 && a.splits <= kWindowCluster;
-  if (a.rows <= 8) return cluster ? decode_launch<BITS, 1, true>(a, st) : decode_launch<BITS, 1, false>(a, st);
-  return cluster ? decode_launch<BITS, 2, true>(a, st) : decode_launch<BITS, 2, false>(a, st);
+  if (a.rows <= 8) return a.cluster ? decode_launch<BITS, 1, true>(a, st) : decode_launch<BITS, 1, false>(a, st);
+  return a.cluster ? decode_launch<BITS, 2, true>(a, st) : decode_launch<BITS, 2, false>(a, st);
 }
 
 }  // namespace
@@ -593,8 +598,17 @@ cudaError_t launch_window_decode(const WindowAttend &a, cudaStream_t st) {
   return a.w.bits == 8 ? decode_bits<8>(a, st) : decode_bits<4>(a, st);
 }
 
+// Launched as a dependent of the parts' kernel, so that its start-up overlaps their work.
 cudaError_t launch_window_combine(const WindowAttend &a, cudaStream_t st) {
   const int64_t items = (int64_t)a.w.batch * a.w.kv_heads * a.rows;
-  window_combine_kernel<<<(unsigned)((items + 7) / 8), 256, 0, st>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((items + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, window_combine_kernel, a);
 }
