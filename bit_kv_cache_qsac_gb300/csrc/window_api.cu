@@ -207,12 +207,14 @@ static WindowPlan plan_of(const qwm_ctx *ctx, const qwm_window *win, int64_t nq,
                      ctx->num_sms);
 }
 
+// The parts' outputs and log-sum-exps, when a second kernel joins them.
+static size_t workspace_of(const qwm_ctx *ctx, const qwm_window *win, int64_t nq, const WindowPlan &p) {
+  return p.joins() ? (size_t)win->batch * ctx->cfg.heads * (size_t)nq * p.splits * (QWM_D + 1) * sizeof(float) : 0;
+}
+
 size_t qwm_window_attend_workspace(const qwm_ctx *ctx, const qwm_window *win, int64_t nq, int64_t tpf, int64_t frames) {
   if (check_attend(ctx, win, nq, tpf, frames) != QWM_OK || nq == 0) return 0;
-  const WindowPlan p = plan_of(ctx, win, nq, tpf, frames);
-  if (!p.joins()) return 0;
-  const size_t rows = (size_t)win->batch * ctx->cfg.heads * (size_t)nq;
-  return rows * (size_t)p.splits * (QWM_D + 1) * sizeof(float);
+  return workspace_of(ctx, win, nq, plan_of(ctx, win, nq, tpf, frames));
 }
 
 qwm_status qwm_window_attend(qwm_ctx *ctx, const qwm_window *win, const uint16_t *q, const qwm_strides *qs, int64_t nq,
@@ -233,7 +235,7 @@ qwm_status qwm_window_attend(qwm_ctx *ctx, const qwm_window *win, const uint16_t
   if (!aligned_to(q_start, 8) || !aligned_to(length, 8) || !aligned_to(q_count, 4) || !aligned_to(lse, 4))
     return QWM_ERR_ALIGN;
   const WindowPlan p = plan_of(ctx, win, nq, tpf, frames);
-  const size_t need = qwm_window_attend_workspace(ctx, win, nq, tpf, frames);
+  const size_t need = workspace_of(ctx, win, nq, p);
   if (need > 0 && (!ws || ws_bytes < need)) return QWM_ERR_ARG;
   if (need > 0 && !aligned16(ws)) return QWM_ERR_ALIGN;
   DeviceGuard dev(ctx->device);

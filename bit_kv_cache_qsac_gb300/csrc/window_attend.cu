@@ -647,25 +647,40 @@ cudaError_t launch_window_tiles(const WindowAttend &a, cudaStream_t st) {
   return a.w.bits == 8 ? launch_bits<8>(a, st) : launch_bits<4>(a, st);
 }
 
-// Few rows run on warp tiles, which read the cache once per 16 rows at most; more run on tensor-memory
-// tiles.  Keys are split until the parts fill the SMs, while a part keeps a few steps of work.
-// Warp tiles: up to 8 parts are the CTAs of a cluster (clusters do not fill every slot of a GPC: a tenth of
-// the slots is counted off); a second kernel that joins more parts costs about 3 us, some 500 keys of a
-// CTA's time, so it is taken where the parts get that much shorter.
+// Few rows run on warp tiles, which read the cache once per 16 rows; more than 32 on tensor-memory tiles (at
+// 39,000 tokens of 40 heads, 8 bits: 16 rows take 90 us, up to 256 rows on tensor-memory tiles 235).
+// The keys are split into the number of parts for which whole waves of CTAs end soonest, by what a part
+// costs in cycles, as measured: on warp tiles 12 per key (a CTA of 8 warps, whatever the code width) and
+// 10,000 for starting and ending, 6,000 more for a second kernel that joins the parts; up to 8 parts may be
+// a cluster's CTAs instead, which fill nine tenths of the slots.  On tensor-memory tiles 20 per key, 20,000
+// and 7,000; calls that fill the SMs are left whole.
 WindowPlan window_plan(int64_t batch, int64_t kv_heads, int64_t rows, int64_t keys, int num_sms) {
   WindowPlan p;
-  p.tiles = rows > 16;
-  const int64_t heads = batch * kv_heads, most = (keys + 255) / 256;
-  auto clamp = [&](int64_t s, int64_t top) { return s < 1 ? 1 : (s < most ? (s < top ? s : top) : (most < top ? most : top)); };
-  if (p.tiles) {
-    p.cluster = false;
-    p.splits = (int)clamp((int64_t)num_sms / (heads * 2 * ((rows + kPairRows - 1) / kPairRows)), 64);
-    return p;
+  p.tiles = rows > 32;
+  p.splits = 1;
+  p.cluster = false;
+  const int64_t heads = batch * kv_heads, most = keys / 256 < 64 ? keys / 256 : 64;   // 256 keys a part at least
+  const int64_t work = p.tiles ? heads * ((rows + kPairRows - 1) / kPairRows) : heads * (rows <= 8 ? 1 : (rows + 15) / 16);
+  const int64_t slots = p.tiles ? num_sms / 2 : (rows <= 8 ? 2 : 1) * (int64_t)num_sms;
+  if (work >= slots) return p;
+  const int64_t per_key = p.tiles ? 20 : 12, fixed = p.tiles ? 20000 : 10000, join = p.tiles ? 7000 : 6000;
+  int64_t best = keys * per_key + fixed;
+  for (int64_t s = 2; s <= most && work * s <= 4 * slots; s++) {
+    const int64_t part = keys * per_key / s + fixed;
+    const int64_t joined = (work * s + slots - 1) / slots * part + join;
+    if (joined < best) {
+      best = joined;
+      p.splits = (int)s;
+      p.cluster = false;
+    }
+    if (!p.tiles && s <= kWindowCluster) {
+      const int64_t near = slots * 9 / 10, clustered = (work * s + near - 1) / near * part;
+      if (clustered < best) {
+        best = clustered;
+        p.splits = (int)s;
+        p.cluster = true;
+      }
+    }
   }
-  const int64_t slots = (rows <= 8 ? 2 : 1) * (int64_t)num_sms;
-  const int64_t near = clamp(slots * 9 / 10 / heads, kWindowCluster), far = clamp(slots / heads, 64);
-  p.cluster = keys / near - keys / far < 512;
-  p.splits = (int)(p.cluster ? near : far);
-  if (p.splits == 1) p.cluster = false;
   return p;
 }

@@ -131,12 +131,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) window_decode_kerne
   const uint32_t b = blockIdx.y / (uint32_t)a.w.kv_heads;
   const int kvh = (int)(blockIdx.y - b * (uint32_t)a.w.kv_heads);
   if (!CLUSTER) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the joining kernel may line up
+  const int row0 = 8 * NT * (int)blockIdx.z;   // this CTA's block of rows
   // ---- Queries as the first product's B fragments (row g of every 8), bf16 for now; on their way while
   // the rest is worked out, and whatever they are: rows that turn out to be padding are dropped below ----
   uint32_t qf[NT][8][2];
 #pragma unroll
   for (int nt = 0; nt < NT; nt++) {
-    const int r = 8 * nt + g, i = (int)((uint32_t)r / (uint32_t)a.group);
+    const int r = row0 + 8 * nt + g, i = (int)((uint32_t)r / (uint32_t)a.group);
     const uint16_t *qp = a.q + b * a.qs.batch + (kvh * a.group + (r - i * a.group)) * a.qs.head + i * a.qs.token;
 #pragma unroll
     for (int ks = 0; ks < 8; ks++) {
@@ -149,13 +150,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) window_decode_kerne
   const int64_t q0 = a.q_start[b], len = a.length[b];
   int64_t nq = a.q_count ? (int64_t)a.q_count[b] : a.nq;
   nq = nq < a.nq ? nq : a.nq;
-  if (q0 < 0 || nq <= 0) return;   // the whole cluster
+  if (q0 < 0 || nq <= 0 || nq * a.group <= row0) return;   // the whole cluster
   const win::Seq seq{len, a.w.sink, a.w.ring, a.tpf, a.frames};
-  const int64_t f0 = seq.frame(q0), f1 = seq.frame(q0 + nq - 1);
+  const int rows_all = (int)nq * a.group, rows = rows_all - row0 < 8 * NT ? rows_all - row0 : 8 * NT;   // live rows: of all, here
+  const int64_t f0 = seq.frame(q0 + (uint32_t)row0 / (uint32_t)a.group);
+  const int64_t f1 = seq.frame(q0 + (uint32_t)(row0 + rows - 1) / (uint32_t)a.group);
   win::Keys keys;
   keys.init(seq, f0, f1);
   const uint32_t sink = (uint32_t)a.w.sink, ring = (uint32_t)a.w.ring;
-  const int rows = (int)nq * a.group;
   const int64_t head_row = (int64_t)blockIdx.y * (a.w.sink + a.w.ring);
   const int steps_all = (keys.total + kKeys - 1) / kKeys;
   int j0 = 0, j1 = steps_all;   // (steps_all < 2^28 and splits <= 64: the products can pass 32 bits)
@@ -322,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) window_decode_kerne
         for (int e = 0; e < 2; e++) {
           const int r = 8 * nt + 2 * t + e;
           win::Row mask;
-          mask.init(seq, keys, r < rows ? seq.frame(q0 + (uint32_t)r / (uint32_t)a.group) : -1);
+          mask.init(seq, keys, r < rows ? seq.frame(q0 + (uint32_t)(row0 + r) / (uint32_t)a.group) : -1);
 #pragma unroll
           for (int u16 = 0; u16 < kSub; u16++)
 #pragma unroll
@@ -484,11 +486,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) window_decode_kerne
         const float inv = L > 0.f ? 1.f / L : 0.f, lse = L > 0.f ? M + log2f(L) : -INFINITY;
         acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
         if (a.splits == 1) {
-          finish4(a, b, kvh, r, ch, acc, lse);
+          finish4(a, b, kvh, row0 + r, ch, acc, lse);
           __syncwarp();   // merging lanes have read the earlier log-sum-exp
-          if (lane == 0) finish_lse(a, b, kvh, r, lse);
+          if (lane == 0) finish_lse(a, b, kvh, row0 + r, lse);
         } else {
-          const int64_t pr = ((int64_t)blockIdx.y * a.splits + blockIdx.x) * a.rows + r;
+          const int64_t pr = ((int64_t)blockIdx.y * a.splits + blockIdx.x) * a.rows + row0 + r;
           *(float4 *)(a.part + pr * D + ch) = acc;
           if (lane == 0) a.part_lse[pr] = lse;
         }
@@ -521,9 +523,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) window_decode_kerne
           acc.w = fmaf(x.w, wt, acc.w);
         }
       const float inv = L > 0.f ? 1.f / L : 0.f, lse = L > 0.f ? M + log2f(L) : -INFINITY;
-      finish4(a, b, kvh, r, 4 * lane, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv), lse);
+      finish4(a, b, kvh, row0 + r, 4 * lane, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv), lse);
       __syncwarp();
-      if (lane == 0) finish_lse(a, b, kvh, r, lse);
+      if (lane == 0) finish_lse(a, b, kvh, row0 + r, lse);
     }
     tc::cluster_sync();   // no CTA leaves while its part is read
   }
@@ -573,7 +575,7 @@ cudaError_t decode_launch(const WindowAttend &a, cudaStream_t st) {
   const cudaError_t e = allow_shared(kernel, Ring<BITS>::kBytes, allowed);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)a.splits, (unsigned)(a.w.batch * a.w.kv_heads));
+  cfg.gridDim = dim3((unsigned)a.splits, (unsigned)(a.w.batch * a.w.kv_heads), (unsigned)((a.rows + 8 * NT - 1) / (8 * NT)));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = Ring<BITS>::kBytes;
   cfg.stream = st;

@@ -316,11 +316,12 @@ def check_attention(win, q, q_starts, lengths, tpf, frames, scale, out, lse, cou
 FEW = [(8, [1], 1, 1, 1, 0, 1, 1, 1), (4, [1], 1, 1, 1, 1, 1, 1, 5), (8, [200], 8, 2, 1, 4, 100, 1, 100),
        (4, [300, 0, 17, 150], 6, 2, 5, 3, 150, 1, 120), (8, [40, 41], 4, 4, 7, 8, 33, 1, 10),
        (4, [500], 16, 1, 1, 0, 500, 1, 500), (8, [500], 15, 1, 1, 7, 400, 1, 77), (4, [260], 2, 2, 16, 16, 200, 8, 3),
-       (8, [5000], 2, 1, 3, 64, 4000, 1, 3500), (4, [9000], 3, 3, 1, 100, 7000, 390, 12), (8, [31], 2, 2, 2, 50, 9, 1, 3)]
+       (8, [5000], 2, 1, 3, 64, 4000, 1, 3500), (4, [9000], 3, 3, 1, 100, 7000, 390, 12), (8, [31], 2, 2, 2, 50, 9, 1, 3),
+       (8, [400, 30], 3, 3, 17, 5, 300, 1, 90), (4, [5000], 8, 1, 4, 0, 4800, 1, 4000), (8, [300], 5, 1, 5, 9, 200, 16, 5)]
 MANY = [(8, [300], 2, 2, 300, 0, 300, 1, 300), (4, [300], 2, 2, 300, 5, 290, 1, 64), (8, [700, 650], 4, 1, 130, 3, 700, 1, 500),
         (4, [513, 0, 1], 2, 1, 17, 16, 256, 1, 200), (8, [1000], 1, 1, 520, 100, 600, 100, 4), (4, [1024], 2, 2, 128, 128, 896, 128, 3),
         (8, [640], 3, 3, 33, 0, 640, 1, 1), (4, [2000], 2, 2, 257, 7, 1500, 50, 9), (8, [90], 2, 2, 200, 20, 60, 1, 30),
-        (8, [6000], 1, 1, 40, 33, 5000, 1, 4500)]
+        (8, [6000], 1, 1, 40, 33, 5000, 1, 4500), (4, [700], 11, 1, 3, 2, 600, 1, 333)]
 
 
 @pytest.mark.parametrize("case", FEW + MANY)
