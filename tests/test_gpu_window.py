@@ -572,3 +572,63 @@ def test_windowed_layer_over_a_packed_history(qwm, bits, tpf, rope):
             assert err <= 2e-2, (t, h, err)
     with pytest.raises(ValueError):
         layer.step(k[:, :10], v[:, :10], q[:, :10])
+
+
+# (bits, batch, H, kv, nq, counts, sink, ring, length, tpf, frames): more units of 512 rows than the GPU holds at
+# once, so that a pair of CTAs walks over several, of one and of two Query tiles, with and without live rows
+UNITS = [(4, 2, 48, 48, 530, None, 5, 600, 700, 1, 300), (4, 7, 24, 12, 300, [300, 0, 10, 131, 300, 256, 257], 0, 900, 900, 64, 4),
+         (4, 40, 8, 4, 40, None, 3, 200, 190, 1, 60), (4, 1, 90, 90, 1100, None, 0, 64, 1500, 1, 20)]
+
+
+@pytest.mark.parametrize("case", UNITS)
+def test_attend_many_units(qwm, case):
+    bits, b, H, kv, nq, counts, sink, ring, length, tpf, frames = case
+    rng = np.random.default_rng(nq)
+    ctx = ctx_of(qwm, H)
+    win = fill(qwm, ctx, rng, bits, kv, sink, ring, [length - 3 * i for i in range(b)])
+    lengths = [length - 3 * i for i in range(b)]
+    starts = [max(0, n - nq) for n in lengths]
+    q = rows(rng, b, H, nq)
+    out = torch.full((b, H, nq, 128), 5.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((b, H, nq), 5.0, dtype=torch.float32, device="cuda")
+    for _ in range(2):
+        qwm.qwm_window_attend(ctx, win, q, ints(starts), ints(lengths), tpf, frames, SCALE, out, lse=lse,
+                              q_count=ints(counts, torch.int32) if counts else None)
+    assert qwm.qwm_sync_status(ctx) == 0
+    slots = sink + ring
+    values = torch.empty(2, b, kv, slots, 128, dtype=torch.bfloat16, device="cuda")   # 4-bit values are exact in bf16
+    ahead = torch.full((b, slots), -1, dtype=torch.int64)
+    for i, n in enumerate(lengths):
+        pos = ref.held(n, sink, ring)
+        ahead[i, :len(pos)] = torch.tensor(pos)
+    for i in range(b):   # held tokens: the sinks, then the last ring ones
+        m = int((ahead[i] >= 0).sum())
+        head = min(sink, m)
+        one = qwm.Window(bits, sink, ring, *(t[i:i + 1] for t in (win.k_codes, win.k_step, win.v_codes, win.v_step)))
+        for at, cnt in ((0, head), (head, m - head)):
+            if cnt:
+                kh, vh = (torch.empty(1, kv, cnt, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+                qwm.qwm_window_read(ctx, one, ints([int(ahead[i, at])]), ints([lengths[i]]), kh, vh)
+                values[0, i, :, at:at + cnt], values[1, i, :, at:at + cnt] = kh[0], vh[0]
+    for i in range(b):
+        live = counts[i] if counts else nq
+        assert bool((out[i][:, live:] == 5).all()) and bool((lse[i][:, live:] == 5).all())
+        if not live:
+            continue
+        pos = ahead[i][ahead[i] >= 0].cuda()
+        k, v = (values[e, i, :, :pos.numel()].double().repeat_interleave(H // kv, 0) for e in range(2))
+        fq = (torch.arange(live, device="cuda") + starts[i]) // tpf
+        see = (pos // tpf <= fq[:, None]) & ((fq[:, None] - pos // tpf < frames) | (pos < sink))
+        qq = q[i, :, :live].double()
+        x = (qq @ k.transpose(1, 2) * (SCALE * math.log2(math.e))).masked_fill(~see, -math.inf)
+        wl = torch.logsumexp(x * math.log(2.0), -1) / math.log(2.0)
+        w = torch.exp2(x - wl[..., None])
+        want, spread = w @ v, w @ v.abs()
+        mag = (qq.abs() @ k.abs().transpose(1, 2)).amax(-1) * SCALE * math.log2(math.e)
+        eps = (2.0 ** -11 + 2.0 ** -16 * mag + 2.0 ** -20)[..., None]
+        bound = 2 * eps * spread + pos.numel() * 2.0 ** -25 * v.abs().max() + 2.0 ** -8 * want.abs()
+        some = see.any(1)
+        assert bool((out[i][:, :live][:, ~some] == 0).all()) and bool(torch.isneginf(lse[i][:, :live][:, ~some]).all())
+        assert bool(((out[i, :, :live].double() - want).abs() <= bound)[:, some].all()), i
+        off = (lse[i, :, :live].double() - wl).abs() <= 2.0 ** -16 * mag + 2.0 ** -20 + 2.0 ** -22 * wl.abs()
+        assert bool(off[:, some].all()), i
