@@ -14,7 +14,7 @@ constexpr int kUnroll = 4;   // heads whose loads are in flight together
 
 template <int PAIRING, bool WHOLE>
 __global__ void __launch_bounds__(kThreads, 3)
-    rope_kernel(const __grid_constant__ qwm_rope_spec sp, const uint16_t *__restrict__ x, qwm_strides xs, int batch,
+    rope_kernel(const __grid_constant__ qwm_rope_spec sp, const uint16_t *x, qwm_strides xs, int batch,
                 int heads, int64_t n, const int64_t *__restrict__ start, const int32_t *__restrict__ pos,
                 uint16_t *out, qwm_strides os, int heads_per_block) {
   __shared__ win::RopeTable tab;
@@ -34,7 +34,7 @@ __global__ void __launch_bounds__(kThreads, 3)
   };
   load(h0);   // in flight while the angles are formed
   const int64_t s0 = start[b];
-  const bool live = in && s0 >= 0;
+  const bool live = in && win::starts(s0);
   tab.fill(sp);
   win::RopeVec<PAIRING, WHOLE> rv;
   rv.init(sp, tab, v, live ? s0 + i : 0, pos ? pos + (b * n + i) * 3 : nullptr);

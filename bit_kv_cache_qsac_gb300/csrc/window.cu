@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kThreads)
   cnt = cnt < n ? cnt : n;
   const int64_t p = s0 + i, end = s0 + cnt;
   // of tokens that share a slot the last of the call is kept
-  const bool live = in && s0 >= 0 && i < cnt && (p < w.sink || p >= end - w.ring);
+  const bool live = in && win::starts(s0) && i < cnt && (p < w.sink || p >= end - w.ring);
   win::RopeVec<TURN == QWM_ROPE_HALF ? QWM_ROPE_HALF : QWM_ROPE_INTERLEAVED, WHOLE> rv;
   if (TURN >= 0) {
     tab.fill(sp);
@@ -165,8 +165,8 @@ __global__ void __launch_bounds__(kThreads)
   const int64_t tok = (int64_t)blockIdx.x * kReadRows + row;
   if (tok >= (int64_t)w.batch * n) return;
   const int64_t b = win::quotient(tok, n), i = tok - b * n;
-  const int64_t s0 = start[b], len = length[b], p = s0 + i;
-  if (s0 < 0 || (count && i >= count[b])) return;
+  const int64_t s0 = start[b], len = win::tokens_of(length[b]), p = s0 + i;
+  if (!win::starts(s0) || (count && i >= count[b])) return;
   const bool held = p < len && (p < w.sink || p >= len - w.ring);
   const int64_t slots = w.sink + w.ring;
   const int64_t slot = held ? (p < w.sink ? p : w.sink + win::remainder(p - w.sink, w.ring)) : 0;

@@ -301,6 +301,13 @@ __device__ __forceinline__ int64_t remainder(int64_t a, int64_t b) {
   return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a % (uint32_t)b) : a % b;
 }
 
+// Positions end here, so that sums of a position, a count and a frame stay inside 64 bits.
+constexpr int64_t kMaxPosition = (int64_t)1 << 62;
+// A sequence that starts outside 0 .. kMaxPosition is left out.
+__device__ __forceinline__ bool starts(int64_t p) { return p >= 0 && p <= kMaxPosition; }
+// Tokens of a sequence as the kernels count with them.
+__device__ __forceinline__ int64_t tokens_of(int64_t len) { return len > 0 ? len : 0; }
+
 // Sequence and window of an attention call, for one sequence.
 struct Seq {
   int64_t len, sink, ring, tpf, frames;

@@ -25,6 +25,7 @@ struct DeviceGuard {
 };
 
 constexpr int64_t kMaxTokens = (int64_t)1 << 24;   // tokens of one call and sequence
+constexpr int64_t kMaxSlots = (int64_t)1 << 30;    // of a cache and sequence: key numbers are 32 bits in the kernels
 constexpr int64_t kMaxGridY = 65535;
 
 // An activation [batch][heads][n][128] by strides; `written`: its rows must not overlap.
@@ -33,7 +34,7 @@ qwm_status check_rows(const void *p, const qwm_strides *s, int64_t batch, int64_
   if (!aligned16(p)) return QWM_ERR_ALIGN;
   const int64_t st[3] = {s->batch, s->head, s->token}, ex[3] = {batch, heads, n};
   for (int i = 0; i < 3; i++) {
-    if (st[i] < 0 || st[i] > ((int64_t)1 << 40)) return QWM_ERR_ARG;
+    if (st[i] < 0 || st[i] > ((int64_t)1 << 38)) return QWM_ERR_ARG;
     if (st[i] & 7) return QWM_ERR_ALIGN;
   }
   if (!written) return QWM_OK;
@@ -66,8 +67,7 @@ qwm_status check_shape(const qwm_window *w) {
   if (!w) return QWM_ERR_ARG;
   if (w->bits != 8 && w->bits != 4) return QWM_ERR_UNSUPPORTED;
   if (w->batch < 1 || w->kv_heads < 1 || w->reserved != 0 || w->sink < 0 || w->ring < 1) return QWM_ERR_ARG;
-  if (w->sink >= ((int64_t)1 << 31) || w->ring >= ((int64_t)1 << 31) || w->sink + w->ring >= ((int64_t)1 << 31))
-    return QWM_ERR_SHAPE;
+  if (w->sink > kMaxSlots || w->ring > kMaxSlots || w->sink + w->ring > kMaxSlots) return QWM_ERR_SHAPE;
   if ((int64_t)w->batch * w->kv_heads > kMaxGridY) return QWM_ERR_SHAPE;
   return QWM_OK;
 }

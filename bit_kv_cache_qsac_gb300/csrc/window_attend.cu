@@ -234,11 +234,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   int64_t nq = a.q_count ? (int64_t)a.q_count[b] : a.nq;
   nq = nq < a.nq ? nq : a.nq;
   const int64_t rows = nq * a.group;              // live rows of this Key head
-  if (q0 < 0 || pair0 >= rows) {                  // the same in both CTAs
+  if (!win::starts(q0) || pair0 >= rows) {        // the same in both CTAs
     tc::cp_async_wait<0>();
     return;
   }
-  const win::Seq seq{a.length[b], a.w.sink, a.w.ring, a.tpf, a.frames};
+  const win::Seq seq{win::tokens_of(a.length[b]), a.w.sink, a.w.ring, a.tpf, a.frames};
   auto frame_of = [&](int64_t r) { return seq.frame(q0 + win::quotient(r, a.group)); };
   const int64_t pair1 = pair0 + kPairRows < rows ? pair0 + kPairRows : rows;
   win::Keys keys;
@@ -510,7 +510,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == kMmaWarp) {
-    // ======================= MMA issue: the even CTA's warp 8, for the pair =======================
+    // ======================= MMA issue: the even CTA's, for the pair =======================
     if (cr == 0) {
       constexpr uint32_t idesc = tc::idesc_f16_f32(2 * BM, BS), idesc_pv = tc::idesc_f16_f32_bmn(2 * BM, D);
       constexpr uint16_t kBoth = 3;

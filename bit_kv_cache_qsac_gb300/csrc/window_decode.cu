@@ -147,10 +147,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) window_decode_kerne
       qf[nt][ks][1] = w.y;
     }
   }
-  const int64_t q0 = a.q_start[b], len = a.length[b];
+  const int64_t q0 = a.q_start[b], len = win::tokens_of(a.length[b]);
   int64_t nq = a.q_count ? (int64_t)a.q_count[b] : a.nq;
   nq = nq < a.nq ? nq : a.nq;
-  if (q0 < 0 || nq <= 0 || nq * a.group <= row0) return;   // the whole cluster
+  if (!win::starts(q0) || nq <= 0 || nq * a.group <= row0) return;   // the whole cluster
   const win::Seq seq{len, a.w.sink, a.w.ring, a.tpf, a.frames};
   const int rows_all = (int)nq * a.group, rows = rows_all - row0 < 8 * NT ? rows_all - row0 : 8 * NT;   // live rows: of all, here
   const int64_t f0 = seq.frame(q0 + (uint32_t)row0 / (uint32_t)a.group);
@@ -541,7 +541,7 @@ __global__ void __launch_bounds__(256) window_combine_kernel(const __grid_consta
   if (item >= heads * a.rows) return;
   const int64_t y = win::quotient(item, a.rows), r = item - y * a.rows, b = win::quotient(y, a.w.kv_heads);
   const int kvh = (int)(y - b * a.w.kv_heads);
-  if (a.q_start[b] < 0 || (a.q_count && win::quotient(r, a.group) >= a.q_count[b])) return;
+  if (!win::starts(a.q_start[b]) || (a.q_count && win::quotient(r, a.group) >= a.q_count[b])) return;
   const float *pl = a.part_lse + y * a.splits * a.rows + r;
   float M = -INFINITY;
   for (int s = 0; s < a.splits; s++) M = fmaxf(M, pl[s * a.rows]);

@@ -14,12 +14,12 @@
  * Conventions as in qwm.h (device pointers, caller-owned, 16-byte aligned, bf16 as uint16_t bit
  * patterns, asynchronous on the stream, a qwm_status return), and further:
  *  - Activations have shape [batch][heads][tokens][128] with the channels contiguous and the other
- *    three strides given (qwm_strides, in elements, multiples of 8), so that a projection's
+ *    three strides given (qwm_strides, in elements, multiples of 8, at most 2^38), so that a projection's
  *    token-major output needs no transposition.  Rows that a call writes must not overlap.
  *  - What changes from step to step is read on the device (start, count, length: one entry per
  *    sequence), so a captured CUDA graph of a step can be replayed with new values in the same
- *    buffers.  A sequence whose start (q_start) is negative, or whose count is 0, is skipped: its rows
- *    are left as they were.  With count, rows from count[b] on are padding and left as they were.
+ *    buffers.  A sequence whose start (q_start) is negative or above 2^62, or whose count is 0 or less,
+ *    is skipped: its rows are left as they were.  A negative length counts as 0.  With count, rows from count[b] on are padding and left as they were.
  *  - Errors only the device sees (QWM_ERR_RANGE, QWM_ERR_DEVICE_TIMEOUT) go to the context's status
  *    word (qwm_sync_status).
  *  - The calls use no memory of the context but the status word: calls on different streams need
@@ -91,7 +91,7 @@ typedef struct {
   int32_t kv_heads;  /* >= 1 */
   int32_t reserved;  /* 0 */
   int64_t sink;      /* >= 0 */
-  int64_t ring;      /* >= 1; sink + ring < 2^31 */
+  int64_t ring;      /* >= 1; sink + ring <= 2^30 */
   uint8_t *k_codes, *v_codes; /* [batch][kv_heads][sink + ring][128 * bits / 8] */
   uint8_t *k_step, *v_step;   /* [batch][kv_heads][sink + ring][4] */
 } qwm_window;

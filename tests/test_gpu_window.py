@@ -632,3 +632,50 @@ def test_attend_many_units(qwm, case):
         assert bool(((out[i, :, :live].double() - want).abs() <= bound)[:, some].all()), i
         off = (lse[i, :, :live].double() - wl).abs() <= 2.0 ** -16 * mag + 2.0 ** -20 + 2.0 ** -22 * wl.abs()
         assert bool(off[:, some].all()), i
+
+
+# ------------------------------------------------------------------ values only the device sees
+
+FAR = [2 ** 63 - 1, 2 ** 62 + 1, -2 ** 63, -1]   # no position of a token: the sequence is skipped
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+def test_positions_outside_the_range_leave_everything_as_it_was(qwm, bits):
+    rng = np.random.default_rng(21)
+    b, n, ctx = len(FAR), 9, ctx_of(qwm, 2)
+    x = rows(rng, b, 2, n)
+    five = torch.full_like(x, 5.0)
+    out = five.clone()
+    qwm.qwm_rope(ctx, qwm.RopeSpec((64, 32, 32)), x, ints(FAR), out)
+    assert torch.equal(out, five)
+    win = qwm.Window.empty(bits, b, 2, 4, 60)
+    for spec in (None, qwm.RopeSpec((64, 32, 32)), qwm.RopeSpec((128, 0, 0), pairing="half")):
+        qwm.qwm_window_write(ctx, win, x, x, ints(FAR), rope=spec)
+    assert not any(bool(t.any()) for t in (win.k_codes, win.k_step, win.v_codes, win.v_step))
+    kh, vh = torch.full((b, 2, n, 128), 5.0, dtype=torch.bfloat16, device="cuda"), torch.full((b, 2, n, 128), 5.0, dtype=torch.bfloat16, device="cuda")
+    qwm.qwm_window_read(ctx, win, ints(FAR), ints([64] * b), kh, vh)
+    assert bool((kh == 5).all()) and bool((vh == 5).all())
+    for nq in (1, 40):
+        q = rows(rng, b, 2, nq)
+        o = torch.full((b, 2, nq, 128), 5.0, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((b, 2, nq), 5.0, dtype=torch.float32, device="cuda")
+        qwm.qwm_window_attend(ctx, win, q, ints(FAR), ints([64] * b), 1, 60, SCALE, o, lse=lse)
+        assert bool((o == 5).all()) and bool((lse == 5).all())
+
+
+@pytest.mark.parametrize("nq", [1, 12, 40, 300])
+@pytest.mark.parametrize("ring", [60, 9000])   # 9000: the keys are split
+def test_negative_lengths_hold_no_token(qwm, nq, ring):
+    rng = np.random.default_rng(22)
+    lengths, ctx = [-1, -5000, -2 ** 40, -2 ** 63], ctx_of(qwm, 2)
+    b, win = len(lengths), qwm.Window.empty(8, len(lengths), 1, 4, ring)
+    win.k_codes.fill_(200), win.v_codes.fill_(200), win.k_step.fill_(0x78), win.v_step.fill_(0x78)
+    q = rows(rng, b, 2, nq)
+    out = torch.full((b, 2, nq, 128), 5.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((b, 2, nq), 5.0, dtype=torch.float32, device="cuda")
+    qwm.qwm_window_attend(ctx, win, q, ints([100] * b), ints(lengths), 1, ring, SCALE, out, lse=lse)
+    assert qwm.qwm_sync_status(ctx) == 0
+    assert bool((out == 0).all()) and bool(torch.isneginf(lse).all())
+    kh = torch.full((b, 1, 7, 128), 5.0, dtype=torch.bfloat16, device="cuda")
+    qwm.qwm_window_read(ctx, win, ints([0, 2, 3, 4]), ints(lengths), kh, None)
+    assert bool((kh == 0).all())

@@ -189,3 +189,13 @@ def test_binding_refuses_host_tensors_and_shapes(qwm):
         qwm.qwm_window_write(Ctx, qwm.Window.empty(8, 1, 8, 0, 4, device="cpu"), x, x, torch.zeros(1, dtype=torch.int64))
     with pytest.raises(ValueError):
         qwm.Window.empty(2, 1, 8, 0, 4, device="cpu")
+
+
+def test_sizes_beyond_the_kernels_index_range_are_refused(qwm):
+    for sink, ring in ((0, (1 << 30) + 1), (1 << 29, (1 << 29) + 1), ((1 << 63) - 1, (1 << 63) - 1)):
+        with pytest.raises(qwm.QwmError):
+            qwm.qwm_window_bytes(8, 1, 1, sink, ring)
+    assert qwm.qwm_window_bytes(4, 1, 1, 1 << 29, 1 << 29) == (64 << 30, 4 << 30)
+    lib, ctx, w = qwm.raw_library(), _ctx(qwm), _win(qwm)
+    for far in (dict(batch=(1 << 38) + 8), dict(head=1 << 62), dict(token=(1 << 63) - 8)):
+        assert lib.qwm_window_write(ctx, w, OK, _st(qwm, **far), OK, _st(qwm), 3, OK, None, None, None, None) == qwm.QWM_ERR_ARG
