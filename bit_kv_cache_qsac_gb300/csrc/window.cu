@@ -4,6 +4,9 @@
 // A step has 4 significant bits, so code * s has at most 11 and is exact in fp16, whatever reads it.
 // Bound: memory (write: 512 B of bf16 read and 264 or 136 B written per token and head; read: the
 // reverse).  16 lanes take one row, 8 channels each; four of them share a step, found by two shuffles.
+// Measured, 40 heads x 10,800 tokens at 4 bits: written (Keys turned by three axes) in 64.6 us = 4.3 TB/s,
+// held by instruction issue (74%: two rows are quantised per 512 bytes read); read back in 43 us = 6.5
+// TB/s.  8 bits, 40 heads x 4,680: read back in 24.8 us = 5.8 TB/s.
 #include "window.cuh"
 
 namespace {
