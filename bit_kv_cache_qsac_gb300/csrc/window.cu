@@ -141,18 +141,18 @@ __global__ void __launch_bounds__(kThreads)
 // Eight channels of a cached row -> bf16 (4 words).
 template <int BITS>
 __device__ __forceinline__ uint4 restore(uint2 x, uint32_t step, const win::Bases &bases) {
-  uint32_t s2, n2, pr[4], o[4];
-  win::step_consts<BITS>(step, s2, n2);
+  uint32_t pr[4], o[4];
+  const win::Step st = win::step_of_byte<BITS>(step);
   if (BITS == 8) {
-    win::decode8(x.x, s2, n2, bases, pr[0], pr[1]);
-    win::decode8(x.y, s2, n2, bases, pr[2], pr[3]);
+    win::decode8(x.x, st, bases, pr[0], pr[1]);
+    win::decode8(x.y, st, bases, pr[2], pr[3]);
   } else {
-    win::decode4(x.x, s2, n2, bases, pr);
+    win::decode4(x.x, st, bases, pr);
   }
 #pragma unroll
   for (int u = 0; u < 4; u++) {
     const float2 f = __half22float2(*(const __half2 *)&pr[u]);
-    o[u] = tc::pack_bf16x2(f.x, f.y);
+    o[u] = tc::pack_bf16x2(f.x * win::kUnit<BITS>, f.y * win::kUnit<BITS>);
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }

@@ -242,17 +242,31 @@ __device__ __forceinline__ uint64_t codes_of(uint64_t x2, uint64_t inv2) {
   return tc::add2(tc::add2(tc::fma2(x2, inv2, grid), ungrid), pair2(0x1.8p23f, 0x1.8p23f));
 }
 
-// Decode constants of a step: s and -bias' s in both halves, where bias' is the integer that a code's fp16
-// bit pattern below stands above the signed code (1152, or 72; 1152 s and 72 s are exact and finite for
-// every step up to step_max).  (pattern) s - bias' s in one fp16 FMA is then exactly code * s.
+// What the decoders below give is the value over kUnit: at 4 bits a sixteenth, so that every constant of
+// every step stays finite in fp16.  Whoever multiplies by decoded values has a scale to fold it into.
 template <int BITS>
-__device__ __forceinline__ void step_consts2(uint32_t s2, uint32_t &n2) {
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(n2) : "r"(s2), "r"(BITS == 8 ? 0xE480E480u : 0xD480D480u));
+constexpr float kUnit = BITS == 8 ? 1.f : 16.f;
+// Decode constants of a step, in both halves: s / unit and minus that times what a code's fp16 bit pattern
+// below stands above the signed code: 1152 (8 bits); 72 (4 bits, pattern from 64) and 1032 (nl: pattern
+// from 1024).  (pattern) s - bias s in one fp16 FMA is then exactly code * s: a step has 4 significant bits,
+// 9 * s and 129 * s at most 11, and 1152 * 56 and 1032 / 16 * 896 are below 65504; the smallest step, 2^-17,
+// over 16 is still on fp16's grid.
+struct Step {
+  uint32_t s, n, nl;
+};
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
 }
 template <int BITS>
-__device__ __forceinline__ void step_consts(uint32_t byte, uint32_t &s2, uint32_t &n2) {
-  s2 = byte * 0x00800080u;   // byte << 7 in both halves
-  step_consts2<BITS>(s2, n2);
+__device__ __forceinline__ Step step_of(uint32_t s2) {   // two steps as fp16 pairs
+  if (BITS == 8) return {s2, hmul2(s2, 0xE480E480u), 0u};
+  return {hmul2(s2, 0x2C002C00u), hmul2(s2, 0xC480C480u), hmul2(s2, 0xD408D408u)};   // 1/16, -72/16, -1032/16
+}
+template <int BITS>
+__device__ __forceinline__ Step step_of_byte(uint32_t byte) {
+  return step_of<BITS>(byte * 0x00800080u);   // byte << 7 in both halves
 }
 
 // fp16 bit patterns that codes are placed into: 0x6400 = 1024 (ulp 1) and 0x5400 = 64 (ulp 1/16), in both
@@ -270,25 +284,18 @@ __device__ __forceinline__ uint32_t place(uint32_t x, uint32_t base) {   // (x &
 }
 
 // 8 bits: four codes (one word) -> fp16 pairs of channels (0, 1) and (2, 3).
-__device__ __forceinline__ void decode8(uint32_t x, uint32_t s2, uint32_t n2, const Bases &c, uint32_t &p0, uint32_t &p1) {
-  p0 = tc::hfma2(__byte_perm(x, c.k1024, 0x5150), s2, n2);   // fp16 bits 0x64cc = 1024 + c
-  p1 = tc::hfma2(__byte_perm(x, c.k1024, 0x5352), s2, n2);
+__device__ __forceinline__ void decode8(uint32_t x, const Step &st, const Bases &c, uint32_t &p0, uint32_t &p1) {
+  p0 = tc::hfma2(__byte_perm(x, c.k1024, 0x5150), st.s, st.n);   // fp16 bits 0x64cc = 1024 + c
+  p1 = tc::hfma2(__byte_perm(x, c.k1024, 0x5352), st.s, st.n);
 }
 // 4 bits: eight codes (one word) -> fp16 pairs of channels (0, 1), (2, 3), (4, 5), (6, 7).  Nibbles at bits
-// 4-7 of a half read as 64 + c (0x54c0), those at bits 0-3 as 1024 + c (0x640c): the latter's 1032 s is
-// not exact, so they take an addition and a product, which costs less than the shift it saves (logic
-// and shifts run at half the rate of the fp16 pipe).
-__device__ __forceinline__ void decode4(uint32_t x, uint32_t s2, uint32_t n2, const Bases &c, uint32_t (&p)[4]) {
+// 4-7 of a half read as 64 + c (0x54c0), those at bits 0-3 as 1024 + c (0x640c).
+__device__ __forceinline__ void decode4(uint32_t x, const Step &st, const Bases &c, uint32_t (&p)[4]) {
   const uint32_t y = x >> 8;
-  auto low = [&](uint32_t v) {
-    uint32_t d;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(tc::hadd2(place<0x000F000Fu>(v, c.k1024), 0xE408E408u)), "r"(s2));
-    return d;
-  };
-  p[0] = low(x);
-  p[1] = tc::hfma2(place<0x00F000F0u>(x, c.k64), s2, n2);
-  p[2] = low(y);
-  p[3] = tc::hfma2(place<0x00F000F0u>(y, c.k64), s2, n2);
+  p[0] = tc::hfma2(place<0x000F000Fu>(x, c.k1024), st.s, st.nl);
+  p[1] = tc::hfma2(place<0x00F000F0u>(x, c.k64), st.s, st.n);
+  p[2] = tc::hfma2(place<0x000F000Fu>(y, c.k1024), st.s, st.nl);
+  p[3] = tc::hfma2(place<0x00F000F0u>(y, c.k64), st.s, st.n);
 }
 
 // ------------------------------------------------------------------ which keys a row sees

@@ -165,16 +165,16 @@ struct Producer {
   __device__ __forceinline__ void store(uint32_t stage, const Pieces<BITS> &p, const win::Bases &bases) const {
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-      uint32_t s2, n2, d[8];
-      win::step_consts<BITS>(p.step[i], s2, n2);
+      uint32_t d[8];
+      const win::Step st = win::step_of_byte<BITS>(p.step[i]);
       if (BITS == 8) {
 #pragma unroll
-        for (int u = 0; u < 4; u++) win::decode8(p.c[i][u % (BITS / 2)], s2, n2, bases, d[2 * u], d[2 * u + 1]);
+        for (int u = 0; u < 4; u++) win::decode8(p.c[i][u % (BITS / 2)], st, bases, d[2 * u], d[2 * u + 1]);
       } else {
         uint32_t q[4];
-        win::decode4(p.c[i][0], s2, n2, bases, q);
+        win::decode4(p.c[i][0], st, bases, q);
         d[0] = q[0]; d[1] = q[1]; d[2] = q[2]; d[3] = q[3];
-        win::decode4(p.c[i][1], s2, n2, bases, q);
+        win::decode4(p.c[i][1], st, bases, q);
         d[4] = q[0]; d[5] = q[1]; d[6] = q[2]; d[7] = q[3];
       }
       const uint32_t at = stage * kStage + (uint32_t)(i >> 1) * (2u * kRowStep * 128u);
@@ -351,7 +351,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t lane_addr = (uint32_t)(32 * sub) << 16;
     const uint32_t tS0 = tmem + lane_addr + 128u * x, tO = tmem + lane_addr + 256u + 128u * x;
     const uint32_t p_ready0 = tc::mapa(tc::smem_u32(&bars.p_ready[x][0]), 0);
-    const float sl2 = a.scale_log2;
+    const float sl2 = a.scale_log2 * win::kUnit<BITS>;
     const uint64_t sc2 = pk64(sl2, sl2);
     const int64_t w0 = row_base + (int64_t)x * 2 * BM + 32 * sub;   // this warp's first row
     const int64_t r = w0 + lane;
@@ -440,7 +440,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       tc::fence_after_sync();
       const uint64_t lsum = tc::add2(acc0, acc1);
       const float l = tc::f2lo(lsum) + tc::f2hi(lsum);
-      float inv = l > 0.f ? 1.f / l : 0.f, keep = 0.f;
+      float inv = l > 0.f ? win::kUnit<BITS> / l : 0.f, keep = 0.f;
       float L = l > 0.f ? m_used + log2f(l) : -INFINITY;
       bool write = r < rows;
       RowOut out;

@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) window_decode_kerne
     l[nt][0] = l[nt][1] = 0.f;
   }
   const int krow = 4 * (g >> 1) + (g & 1);   // the key of MMA row g; row g + 8 is two further on
-  const float sl2 = a.scale_log2;
+  const float sl2 = a.scale_log2 * win::kUnit<BITS>;
   // the step byte of the thread's group, of one row or of two
   const uint32_t ksel = BITS == 8 ? (uint32_t)(t >> 1) * 0x1111u : (uint32_t)t * 0x1111u;
   const uint32_t vsel = (uint32_t)(g >> 1) * 0x1111u + 0x4400u;
@@ -275,39 +275,33 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) window_decode_kerne
       if (BITS == 8) {
 #pragma unroll
         for (int pc = 0; pc < 2; pc++) {   // pieces t and t + 4: step groups t / 2 and 2 + t / 2
-          uint32_t s2[2], n2[2];
+          win::Step ks[2];
 #pragma unroll
-          for (int e = 0; e < 2; e++) {
-            s2[e] = step_pair(kst[e], kst[e], ksel + (pc ? 0x2222u : 0u));
-            win::step_consts2<8>(s2[e], n2[e]);
-          }
+          for (int e = 0; e < 2; e++) ks[e] = win::step_of<8>(step_pair(kst[e], kst[e], ksel + (pc ? 0x2222u : 0u)));
           const uint32_t ka = kb ^ (pc ? 64u : 0u);
           const uint4 xa = tc::lds128(ka), xb = tc::lds128(ka + 256u);
           const uint32_t x[2][4] = {{xa.x, xa.y, xa.z, xa.w}, {xb.x, xb.y, xb.z, xb.w}};
 #pragma unroll
           for (int u = 0; u < 4; u++) {
             uint32_t a0, a1, a2, a3;
-            win::decode8(x[0][u], s2[0], n2[0], a.bases, a0, a2);
-            win::decode8(x[1][u], s2[1], n2[1], a.bases, a1, a3);
+            win::decode8(x[0][u], ks[0], a.bases, a0, a2);
+            win::decode8(x[1][u], ks[1], a.bases, a1, a3);
 #pragma unroll
             for (int nt = 0; nt < NT; nt++)
               mma16816((u & 1) ? s_[nt] : s[u16][nt], a0, a1, a2, a3, qf[nt][4 * pc + u][0], qf[nt][4 * pc + u][1]);
           }
         }
       } else {
-        uint32_t s2[2], n2[2];
+        win::Step ks[2];
 #pragma unroll
-        for (int e = 0; e < 2; e++) {
-          s2[e] = step_pair(kst[e], kst[e], ksel);
-          win::step_consts2<4>(s2[e], n2[e]);
-        }
+        for (int e = 0; e < 2; e++) ks[e] = win::step_of<4>(step_pair(kst[e], kst[e], ksel));
         const uint4 xa = tc::lds128(kb), xb = tc::lds128(kb + 128u);
         const uint32_t x[2][4] = {{xa.x, xa.y, xa.z, xa.w}, {xb.x, xb.y, xb.z, xb.w}};
 #pragma unroll
         for (int u = 0; u < 4; u++) {
           uint32_t p[4], r[4];
-          win::decode4(x[0][u], s2[0], n2[0], a.bases, p);
-          win::decode4(x[1][u], s2[1], n2[1], a.bases, r);
+          win::decode4(x[0][u], ks[0], a.bases, p);
+          win::decode4(x[1][u], ks[1], a.bases, r);
 #pragma unroll
           for (int nt = 0; nt < NT; nt++) {
             mma16816(s[u16][nt], p[0], r[0], p[1], r[1], qf[nt][2 * u][0], qf[nt][2 * u][1]);
@@ -389,11 +383,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) window_decode_kerne
     for (int u16 = 0; u16 < kSub; u16++) {
       const uint32_t vb = st + voff + (uint32_t)(u16 * 16 * R::kRow);
       const uint4 vs = tc::lds128(st + vsoff + 64u * u16);   // the steps of keys 4 t .. 4 t + 3
-      uint32_t s2[2], n2[2];
-      s2[0] = step_pair(vs.x, vs.y, vsel);
-      s2[1] = step_pair(vs.z, vs.w, vsel);
-      win::step_consts2<BITS>(s2[0], n2[0]);
-      win::step_consts2<BITS>(s2[1], n2[1]);
+      const win::Step vt[2] = {win::step_of<BITS>(step_pair(vs.x, vs.y, vsel)), win::step_of<BITS>(step_pair(vs.z, vs.w, vsel))};
       if (BITS == 8) {
         uint4 x[4];
 #pragma unroll
@@ -408,10 +398,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) window_decode_kerne
           for (int h = 0; h < 2; h++) {
             const uint32_t sel = h ? 0x7632u : 0x5410u;
             const uint32_t ka = __byte_perm(q[0], q[1], sel), kb = __byte_perm(q[2], q[3], sel);
-            const uint32_t a0 = tc::hfma2(win::place<0x00FF00FFu>(ka, a.bases.k1024), s2[0], n2[0]);
-            const uint32_t a1 = tc::hfma2(win::place<0x00FF00FFu>(ka >> 8, a.bases.k1024), s2[0], n2[0]);
-            const uint32_t a2 = tc::hfma2(win::place<0x00FF00FFu>(kb, a.bases.k1024), s2[1], n2[1]);
-            const uint32_t a3 = tc::hfma2(win::place<0x00FF00FFu>(kb >> 8, a.bases.k1024), s2[1], n2[1]);
+            const uint32_t a0 = tc::hfma2(win::place<0x00FF00FFu>(ka, a.bases.k1024), vt[0].s, vt[0].n);
+            const uint32_t a1 = tc::hfma2(win::place<0x00FF00FFu>(ka >> 8, a.bases.k1024), vt[0].s, vt[0].n);
+            const uint32_t a2 = tc::hfma2(win::place<0x00FF00FFu>(kb, a.bases.k1024), vt[1].s, vt[1].n);
+            const uint32_t a3 = tc::hfma2(win::place<0x00FF00FFu>(kb >> 8, a.bases.k1024), vt[1].s, vt[1].n);
 #pragma unroll
             for (int nt = 0; nt < NT; nt++) mma16816(o[nt][2 * w + h], a0, a1, a2, a3, pb[u16][nt][0], pb[u16][nt][1]);
           }
@@ -426,8 +416,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) window_decode_kerne
 #pragma unroll
           for (int e = 0; e < 2; e++) {   // low halves: nibbles 0-3 (even channels), high halves: odd
             const uint32_t qa = w ? x[2 * e].y : x[2 * e].x, qb = w ? x[2 * e + 1].y : x[2 * e + 1].x;
-            win::decode4(__byte_perm(qa, qb, 0x5410), s2[e], n2[e], a.bases, ev[e]);
-            win::decode4(__byte_perm(qa, qb, 0x7632), s2[e], n2[e], a.bases, od[e]);
+            win::decode4(__byte_perm(qa, qb, 0x5410), vt[e], a.bases, ev[e]);
+            win::decode4(__byte_perm(qa, qb, 0x7632), vt[e], a.bases, od[e]);
           }
 #pragma unroll
           for (int k = 0; k < 4; k++)
@@ -487,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) window_decode_kerne
         *(float4 *)&part_o[r][ch] = acc;
         if (lane == 0) part_ml[r] = make_float2(M, L);
       } else {
-        const float inv = L > 0.f ? 1.f / L : 0.f, lse = L > 0.f ? M + log2f(L) : -INFINITY;
+        const float inv = L > 0.f ? win::kUnit<BITS> / L : 0.f, lse = L > 0.f ? M + log2f(L) : -INFINITY;
         acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
         if (a.splits == 1) {
           finish4(a, b, kvh, row0 + r, ch, acc, lse);
@@ -526,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) window_decode_kerne
           acc.z = fmaf(x.z, wt, acc.z);
           acc.w = fmaf(x.w, wt, acc.w);
         }
-      const float inv = L > 0.f ? 1.f / L : 0.f, lse = L > 0.f ? M + log2f(L) : -INFINITY;
+      const float inv = L > 0.f ? win::kUnit<BITS> / L : 0.f, lse = L > 0.f ? M + log2f(L) : -INFINITY;
       finish4(a, b, kvh, row0 + r, 4 * lane, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv), lse);
       __syncwarp();
       if (lane == 0) finish_lse(a, b, kvh, row0 + r, lse);
