@@ -41,7 +41,7 @@ constexpr int kSoftmaxWarps = 8, kProdWarp0 = 8, kProdWarps = 4, kMmaWarp = 12;
 constexpr int kThreads = 32 * (kSoftmaxWarps + kProdWarps + 1);
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units the maximum may lag behind
-constexpr int kStages = 4;
+constexpr int kStages = 4;                  // (a power of two)
 constexpr int kPairRows = 2 * NQT * BM;
 
 // shared-memory map of one CTA (bytes from a 1024-aligned base)
@@ -55,7 +55,7 @@ constexpr int kSmemAlloc = kSmemBytes + 1024;
 
 struct Bars {
   uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
-  uint64_t s_full[2][2], p_ready[2][2], pv_done[2][2], o_done, drain;
+  uint64_t s_full[2][2], p_ready[2][2], pv_done[2][2], q_full, o_done, drain;
 };
 
 __device__ __forceinline__ void fail(int *abort_flag, int32_t *status) {
@@ -68,6 +68,11 @@ __device__ __forceinline__ uint64_t pk64(uint32_t lo, uint32_t hi) {
   return d;
 }
 __device__ __forceinline__ uint64_t pk64(float lo, float hi) { return pk64(__float_as_uint(lo), __float_as_uint(hi)); }
+__device__ __forceinline__ uint32_t max_f16x2(uint32_t a, uint32_t b) {   // a NaN stays one
+  uint32_t d;
+  asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
 // The lowest n bits set (n clamped to 0..32).
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u); }
 
@@ -204,8 +209,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   volatile int *abort_v = &abort_flag;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the joining kernel, if any, may line up
+  if (warp == kMmaWarp) {
+    if (lane == 0) {
+      for (int i = 0; i < kStages; i++) {
+        tc::mbar_init(&bars.k_full[i], 2 * kProdWarps);  // both CTAs' producer warps (even CTA's copy used)
+        tc::mbar_init(&bars.v_full[i], 2 * kProdWarps);
+        tc::mbar_init(&bars.k_empty[i], 1);
+        tc::mbar_init(&bars.v_empty[i], 1);
+      }
+      for (int i = 0; i < 2; i++) {
+        tc::mbar_init(&bars.s_full[i][0], 1);
+        tc::mbar_init(&bars.s_full[i][1], 1);
+        // both CTAs' 4 softmax warps of tile i; one barrier per buffer, as a warp may finish its next step
+        // before another has finished this one
+        tc::mbar_init(&bars.p_ready[i][0], 8);
+        tc::mbar_init(&bars.p_ready[i][1], 8);
+        tc::mbar_init(&bars.pv_done[i][0], 1);
+        tc::mbar_init(&bars.pv_done[i][1], 1);
+      }
+      tc::mbar_init(&bars.q_full, 2 * kSoftmaxWarps);    // both CTAs' softmax warps (even CTA's copy used)
+      tc::mbar_init(&bars.o_done, 1);
+      tc::mbar_init(&bars.drain, 1);
+      abort_flag = 0;
+      tc::fence_mbar_init();
+    }
+    __syncwarp();
+    tc::tmem_alloc2(&tmem_base_sh, 512);
+    tc::tmem_relinquish2();
+    tc::fence_before_sync();
+  }
+  // Nothing of the peer's is touched before the other half of this barrier, which every way out passes
+  // too.  (This half waits for the warp's memory operations, so it stands before the Queries'.)
+  tc::cluster_arrive();
+  // the sequence's numbers, on their way while the rest is set up
+  const int64_t q0 = a.q_start[b], len = win::tokens_of(a.length[b]);
+  int64_t nq = a.q_count ? (int64_t)a.q_count[b] : a.nq;
   // ---- this CTA's two Query tiles -> shared memory, by the softmax warps: all rows' copies in flight while
-  // the rest is worked out, whatever turns out to be padding ----
+  // the keys are worked out, whatever turns out to be padding.  (Loops stay rolled here and below: a CTA's
+  // first pass through its code is paced by instruction fetches.) ----
   const int64_t pair0 = item * kPairRows, row_base = pair0 + (int64_t)cr * BM;   // row_base: this CTA's row 0 of tile 0
   // this thread's piece of row tid / 16 of tile 0; 16 rows on is 2 KB further, the next tile 2 blocks
   const uint32_t q_dst = tc::smem_u32(sm) + OFF_Q + (uint32_t)((tid & 15) / 8) * kBlk +
@@ -218,15 +259,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int64_t ahead = step_i * a.qs.token + step_h * a.qs.head, wrap = a.qs.token - a.group * a.qs.head;
 #pragma unroll 1
     for (int x = 0; x < NQT; x++) {
-      int64_t r = row_base + (int64_t)x * 2 * BM + rr0;
-      const int64_t i = win::quotient(r, a.group);
-      int h = (int)(r - i * a.group);
+      const int64_t r = row_base + (int64_t)x * 2 * BM + rr0, i = win::quotient(r, a.group);
+      int h = (int)(r - i * a.group), left = a.rows - r < BM ? (int)(a.rows - r) : BM;   // (may be negative)
       const uint16_t *src = qb + h * a.qs.head + i * a.qs.token;
-#pragma unroll
+      uint32_t dst = q_dst + (uint32_t)x * 2u * kBlk;
+#pragma unroll 2
       for (int k = 0; k < BM / 16; k++) {
-        const bool in = r < a.rows;
-        tc::cp_async16_zfill(q_dst + (uint32_t)x * 2u * kBlk + (uint32_t)k * 2048u, in ? src : qb, in ? 16u : 0u);
-        r += 16;
+        tc::cp_async16_zfill(dst, left > 0 ? src : qb, left > 0 ? 16u : 0u);
+        dst += 2048u;
+        left -= 16;
         h += step_h;
         src += ahead + (h >= a.group ? wrap : 0);
         h -= h >= a.group ? a.group : 0;
@@ -234,16 +275,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     tc::cp_async_commit();
   }
+  auto leave = [&]() {   // without having multiplied anything
+    tc::cp_async_wait<0>();
+    __syncwarp();
+    tc::cluster_wait();
+    if (warp == kMmaWarp) {
+      tc::fence_after_sync();
+      tc::tmem_dealloc2(tmem_base_sh, 512);
+    }
+  };
 
-  const int64_t q0 = a.q_start[b];
-  int64_t nq = a.q_count ? (int64_t)a.q_count[b] : a.nq;
   nq = nq < a.nq ? nq : a.nq;
   const int64_t rows = nq * a.group;              // live rows of this Key head
   if (!win::starts(q0) || pair0 >= rows) {        // the same in both CTAs
-    tc::cp_async_wait<0>();
+    leave();
     return;
   }
-  const win::Seq seq{win::tokens_of(a.length[b]), a.w.sink, a.w.ring, a.tpf, a.frames};
+  const win::Seq seq{len, a.w.sink, a.w.ring, a.tpf, a.frames};
   auto frame_of = [&](int64_t r) { return seq.frame(q0 + win::quotient(r, a.group)); };
   const int64_t pair1 = pair0 + kPairRows < rows ? pair0 + kPairRows : rows;
   win::Keys keys;
@@ -268,7 +316,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       if (out.lse && c == 0) *out.lse = -INFINITY;
     }
-    tc::cp_async_wait<0>();
+    leave();
     return;
   }
   const bool skip1 = pair0 + 2 * BM >= rows;   // the second 256-row tile is empty
@@ -276,78 +324,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // ---- the Queries, which have arrived by now: bf16 -> fp16 in place, padding rows 0 ----
   if (warp < kSoftmaxWarps) {
     tc::cp_async_wait<0>();
-    bool bad = false;
-#pragma unroll 8
-    for (int k = 0; k < NQT * BM / 16; k++) {
-      const uint32_t at = q_dst + (uint32_t)(k >> 3) * 2u * kBlk + (uint32_t)(k & 7) * 2048u;
-      const bool in = row_base + (k >> 3) * 2 * BM + (k & 7) * 16 + (tid >> 4) < rows;
-      const uint4 v = tc::lds128(at);
-      const uint32_t bw[4] = {v.x, v.y, v.z, v.w};
-      uint32_t hw[4];
+    uint32_t top = 0u;   // the largest magnitudes, a NaN above all
+#pragma unroll 1
+    for (int x = 0; x < NQT; x++) {
+      const int64_t r = row_base + (int64_t)x * 2 * BM + (tid >> 4);
+      const int left = rows - r < BM ? (int)(rows - r) : BM;
+      const uint32_t at = q_dst + (uint32_t)x * 2u * kBlk;
+#pragma unroll 4
+      for (int k = 0; k < BM / 16; k++) {
+        const uint4 v = tc::lds128(at + (uint32_t)k * 2048u);
+        const uint32_t bw[4] = {v.x, v.y, v.z, v.w};
+        uint32_t hw[4];
 #pragma unroll
-      for (int u = 0; u < 4; u++) {
-        hw[u] = in ? tc::pack_f16x2(__uint_as_float(bw[u] << 16), __uint_as_float(bw[u] & 0xFFFF0000u)) : 0u;
-        bad |= (hw[u] & 0x7C00u) == 0x7C00u || (hw[u] & 0x7C000000u) == 0x7C000000u;
+        for (int u = 0; u < 4; u++) {
+          hw[u] = 16 * k < left ? tc::pack_f16x2(__uint_as_float(bw[u] << 16), __uint_as_float(bw[u] & 0xFFFF0000u)) : 0u;
+          top = max_f16x2(top, hw[u] & 0x7FFF7FFFu);
+        }
+        tc::sts128(at + (uint32_t)k * 2048u, make_uint4(hw[0], hw[1], hw[2], hw[3]));
       }
-      tc::sts128(at, make_uint4(hw[0], hw[1], hw[2], hw[3]));
     }
-    if (bad) qwm_dev_error(a.status, QWM_ERR_RANGE);
+    if ((top & 0x7C00u) == 0x7C00u || (top & 0x7C000000u) == 0x7C000000u) qwm_dev_error(a.status, QWM_ERR_RANGE);
+    tc::fence_proxy_async_smem();
   }
-  if (tid == 32 * kMmaWarp) {
-    for (int i = 0; i < kStages; i++) {
-      tc::mbar_init(&bars.k_full[i], 2 * kProdWarps);  // both CTAs' producer warps (even CTA's copy used)
-      tc::mbar_init(&bars.v_full[i], 2 * kProdWarps);
-      tc::mbar_init(&bars.k_empty[i], 1);
-      tc::mbar_init(&bars.v_empty[i], 1);
-    }
-    for (int i = 0; i < 2; i++) {
-      tc::mbar_init(&bars.s_full[i][0], 1);
-      tc::mbar_init(&bars.s_full[i][1], 1);
-      // both CTAs' 4 softmax warps of tile i; one barrier per buffer, as a warp may finish its next step
-      // before another has finished this one
-      tc::mbar_init(&bars.p_ready[i][0], 8);
-      tc::mbar_init(&bars.p_ready[i][1], 8);
-      tc::mbar_init(&bars.pv_done[i][0], 1);
-      tc::mbar_init(&bars.pv_done[i][1], 1);
-    }
-    tc::mbar_init(&bars.o_done, 1);
-    tc::mbar_init(&bars.drain, 1);
-    abort_flag = 0;
-    tc::fence_mbar_init();
-  }
-  // producers: their sides, and the codes of the first stage, fetched while the Queries are
-  const int pw = warp >= kProdWarp0 && warp < kProdWarp0 + kProdWarps ? warp - kProdWarp0 : 0;
-  const Producer<BITS, false> pk(a, sm, y, cr, pw, lane);
-  const Producer<BITS, true> pv(a, sm, y, cr, pw, lane);
-  const uint32_t sink = (uint32_t)a.w.sink, ring = (uint32_t)a.w.ring;
-  auto slot0_of = [&](int v0) -> int64_t {   // the slot of key v0 when the stage's slots are consecutive
-    const uint32_t s = keys.slot(v0, sink, ring);
-    return v0 + BN <= keys.total && keys.slot(v0 + BN - 1, sink, ring) == s + BN - 1 ? (int64_t)s : -1;
+  // (once per role, so that the producers' first codes may be on their way before it)
+  auto joined = [&]() -> uint32_t {   // both CTAs' barriers exist, and their tensor memory: its address
+    __syncwarp();
+    tc::cluster_wait();
+    tc::fence_after_sync();
+    return tmem_base_sh;
   };
-  Pieces<BITS> k0, v0, k1, v1;
-  int64_t at = 0;
-  if (warp >= kProdWarp0 && warp < kProdWarp0 + kProdWarps) {
-    at = slot0_of(j0 * BN);
-    pk.load(keys, j0 * BN, at, sink, ring, k0);
-    pv.load(keys, j0 * BN, at, sink, ring, v0);
-  }
-  if (warp == kMmaWarp) {
-    tc::tmem_alloc2(&tmem_base_sh, 512);
-    tc::tmem_relinquish2();
-  }
-  tc::fence_proxy_async_smem();
-  tc::fence_before_sync();
-  __syncthreads();
-  tc::cluster_sync();  // both CTAs' barriers exist before the first arrival from the peer
-  tc::fence_after_sync();
-  const uint32_t tmem = tmem_base_sh;
   const int key_end = keys.total < (j0 + J) * BN ? keys.total : (j0 + J) * BN;
   const int steps = (key_end - j0 * BN + BS - 1) / BS;   // 2 J, or one less when the last stage is half empty
 
-  if (warp < kSoftmaxWarps) {
+  if (warp < (skip1 ? kSoftmaxWarps / 2 : kSoftmaxWarps)) {
     // ======================= softmax (Query tile x, row = TMEM lane) =======================
+    const uint32_t tmem = joined();
+    if (lane == 0) tc::mbar_arrive_remote(tc::mapa(tc::smem_u32(&bars.q_full), 0));
     const int x = warp / 4, sub = warp % 4;
-    const int Tx = (x == 1 && skip1) ? 0 : steps;
     const uint32_t lane_addr = (uint32_t)(32 * sub) << 16;
     const uint32_t tS0 = tmem + lane_addr + 128u * x, tO = tmem + lane_addr + 256u + 128u * x;
     const uint32_t p_ready0 = tc::mapa(tc::smem_u32(&bars.p_ready[x][0]), 0);
@@ -364,12 +377,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     float m_used = -INFINITY;
     uint64_t acc0 = 0ull, acc1 = 0ull;
     bool ok = true;
-    for (int t = 0; t < Tx; t++) {
+    for (int t = 0; t < steps; t++) {
       const int v0 = j0 * BN + t * BS;
       const bool full = every.see(v0, v0 + BS);
       const uint32_t tS = tS0 + (uint32_t)(t & 1) * BS;
-      if (!tc::mbar_wait(&bars.s_full[x][t & 1], (t >> 1) & 1, kWaitNs)) fail(&abort_flag, a.status);
-      if (*abort_v) { ok = false; break; }
+      if (!__all_sync(0xffffffffu, tc::mbar_try_wait(&bars.s_full[x][t & 1], (t >> 1) & 1))) {
+        if (!tc::mbar_wait(&bars.s_full[x][t & 1], (t >> 1) & 1, kWaitNs)) fail(&abort_flag, a.status);
+        if (__any_sync(0xffffffffu, *abort_v != 0)) { ok = false; break; }   // the whole warp
+      }
       tc::fence_after_sync();
       // the step's logits at once: their maximum, then their exponentials with the running maximum
       // m_used; when it grows by more than 2^8 (rare after the first step) the sum and O are rescaled
@@ -435,8 +450,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) tc::mbar_arrive_remote(p_ready0 + 8u * (uint32_t)(t & 1));
     }
-    if (ok && Tx > 0 && !tc::mbar_wait(&bars.o_done, 0, kWaitNs)) fail(&abort_flag, a.status);
-    if (ok && Tx > 0 && !*abort_v) {
+    if (ok && !tc::mbar_wait(&bars.o_done, 0, kWaitNs)) fail(&abort_flag, a.status);
+    if (ok && !__any_sync(0xffffffffu, *abort_v != 0)) {
       tc::fence_after_sync();
       const uint64_t lsum = tc::add2(acc0, acc1);
       const float l = tc::f2lo(lsum) + tc::f2hi(lsum);
@@ -490,7 +505,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t writes = __ballot_sync(0xffffffffu, write);
       const uint64_t mine_out = half ? (uint64_t)out.bf16 : (uint64_t)out.f32;
       if (half) {
-#pragma unroll 4
+#pragma unroll 8
         for (int i = 0; i < 16; i++) {
           const int rw = 2 * i + (lane >> 4), c = lane & 15;
           uint16_t *dst = (uint16_t *)__shfl_sync(0xffffffffu, mine_out, rw);
@@ -516,6 +531,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kMmaWarp) {
     // ======================= MMA issue: the even CTA's, for the pair =======================
+    const uint32_t tmem = joined();
     if (cr == 0) {
       constexpr uint32_t idesc = tc::idesc_f16_f32(2 * BM, BS), idesc_pv = tc::idesc_f16_f32_bmn(2 * BM, D);
       constexpr uint16_t kBoth = 3;
@@ -526,7 +542,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint64_t dq = tc::desc_sw128(s0 + OFF_Q), dk = tc::desc_sw128(s0 + OFF_K);
       const uint64_t dv = tc::desc_sw128_mn(s0 + OFF_V, kBlk, 1024);
       bool ok = true;
-      auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {   // the warp's common answer
+      // The warp's common answer.  Whether someone gave up is looked at only where there is something to
+      // wait for: the flag's read behind every barrier cost 12% of a step.
+      auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
+        if (__all_sync(0xffffffffu, tc::mbar_try_wait_cluster(bar, parity))) return true;
         return __all_sync(0xffffffffu, tc::mbar_wait_cluster(bar, parity, kWaitNs) && !*abort_v);
       };
       auto qk = [&](int x, int t) {
@@ -553,6 +572,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       auto keys_there = [&](int t) {   // the Keys of step t (a stage's first step waits for it)
         return (t & 1) || wait(&bars.k_full[(t >> 1) % kStages], ((t >> 1) / kStages) & 1);
       };
+      ok = wait(&bars.q_full, 0);
       for (int t = 0; ok && t < 2 && t < n; t++) {
         ok = keys_there(t);
         if (!ok) break;
@@ -589,12 +609,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (!tc::mbar_wait(&bars.drain, 0, kWaitNs)) qwm_dev_error(a.status, QWM_ERR_DEVICE_TIMEOUT);
     }
   } else {
-    // ======================= producers: Keys, then Values, of every stage =======================
-    if (J > 1) {
-      at = slot0_of((j0 + 1) * BN);
-      pk.load(keys, (j0 + 1) * BN, at, sink, ring, k1);
-      pv.load(keys, (j0 + 1) * BN, at, sink, ring, v1);
-    }
+    // ======================= producers: Keys, then Values, of every stage; or, where the second Query
+    // tile is empty, its softmax warps produce the Values and these only the Keys =======================
+    const bool do_k = warp >= kProdWarp0, do_v = warp < kProdWarp0 || !skip1;
+    const int pw = warp & (kProdWarps - 1);
+    const Producer<BITS, false> pk(a, sm, y, cr, pw, lane);
+    const Producer<BITS, true> pv(a, sm, y, cr, pw, lane);
+    const uint32_t sink = (uint32_t)a.w.sink, ring = (uint32_t)a.w.ring;
+    Pieces<BITS> k0, v0, k1, v1;
     // the even CTA's full barriers (consecutive 8-byte words), as shared::cluster addresses
     const uint32_t k_full = tc::mapa(tc::smem_u32(&bars.k_full[0]), 0), v_full = tc::mapa(tc::smem_u32(&bars.v_full[0]), 0);
     auto hand_over = [&](uint32_t full) {
@@ -603,26 +625,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (lane == 0) tc::mbar_arrive_remote(full);
     };
     auto free_again = [&](uint64_t *empty, int j) -> bool {   // the stage's previous contents are consumed
-      if (j >= kStages && !tc::mbar_wait(empty, (j / kStages - 1) & 1, kWaitNs)) fail(&abort_flag, a.status);
+      if (j < kStages || __all_sync(0xffffffffu, tc::mbar_try_wait(empty, (j / kStages - 1) & 1))) return true;
+      if (!tc::mbar_wait(empty, (j / kStages - 1) & 1, kWaitNs)) fail(&abort_flag, a.status);
       return !__any_sync(0xffffffffu, *abort_v != 0);         // warp-uniform exit
     };
+    // stage j is stored and the codes of stage j + 2 fetched in its place; the first round only fetches
     auto stage = [&](int j, Pieces<BITS> &k, Pieces<BITS> &v) -> bool {
-      const int s = j % kStages;
-      if (!free_again(&bars.k_empty[s], j)) return false;
-      pk.store((uint32_t)s, k, a.bases);
-      hand_over(k_full + 8u * (uint32_t)s);
-      const int next = (j0 + j + 2) * BN;
-      const int64_t slot0 = j + 2 < J ? slot0_of(next) : 0;
-      if (j + 2 < J) pk.load(keys, next, slot0, sink, ring, k);
-      if (!free_again(&bars.v_empty[s], j)) return false;
-      pv.store((uint32_t)s, v, a.bases);
-      hand_over(v_full + 8u * (uint32_t)s);
-      if (j + 2 < J) pv.load(keys, next, slot0, sink, ring, v);
+      const int s = j & (kStages - 1), next = (j0 + j + 2) * BN;
+      const bool store = j >= 0 && j < J, load = j + 2 < J;
+      int64_t slot0 = -1;   // that stage's first slot when its slots are consecutive
+      if (load) {
+        const uint32_t first = keys.slot(next, sink, ring);
+        if (next + BN <= keys.total && keys.slot(next + BN - 1, sink, ring) == first + BN - 1) slot0 = first;
+      }
+      if (do_k) {
+        if (store) {
+          if (!free_again(&bars.k_empty[s], j)) return false;
+          pk.store((uint32_t)s, k, a.bases);
+          hand_over(k_full + 8u * (uint32_t)s);
+        }
+        if (load) pk.load(keys, next, slot0, sink, ring, k);
+      }
+      if (do_v) {
+        if (store) {
+          if (!free_again(&bars.v_empty[s], j)) return false;
+          pv.store((uint32_t)s, v, a.bases);
+          hand_over(v_full + 8u * (uint32_t)s);
+        }
+        if (load) pv.load(keys, next, slot0, sink, ring, v);
+      }
       return true;
     };
-    for (int j = 0; j < J; j += 2) {
-      if (!stage(j, k0, v0)) break;
-      if (j + 1 < J && !stage(j + 1, k1, v1)) break;
+#pragma unroll 1
+    for (int j = -2; j < J; j += 2) {
+      if (!stage(j, k0, v0) || !stage(j + 1, k1, v1)) break;
+      if (j < 0) {
+        joined();
+        if (warp < kSoftmaxWarps && lane == 0) tc::mbar_arrive_remote(tc::mapa(tc::smem_u32(&bars.q_full), 0));
+      }
     }
   }
   tc::fence_before_sync();
@@ -630,7 +670,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc::cluster_sync();  // the peer has finished with this CTA's barriers, shared and tensor memory
   if (warp == kMmaWarp) {
     tc::fence_after_sync();
-    tc::tmem_dealloc2(tmem, 512);
+    tc::tmem_dealloc2(tmem_base_sh, 512);
   }
 }
 
