@@ -53,8 +53,12 @@ constexpr int OFF_V = OFF_K + kStages * 2 * kBlkH;     // stages x [128 keys][64
 constexpr int kSmemBytes = OFF_V + kStages * kBlk;
 constexpr int kSmemAlloc = kSmemBytes + 1024;
 
+template <bool B>
+struct Flag {
+  static constexpr bool value = B;
+};
 struct Bars {
-  uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+  uint64_t full[kStages], empty[kStages];
   uint64_t s_full[2][2], p_ready[2][2], pv_done[2][2], q_full, o_done, drain;
 };
 
@@ -197,6 +201,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __shared__ Bars bars;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_flag;
+  __shared__ float2 half_sums[BM];   // short items: maximum and sum of the second tile's rows
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   // pairs in launch order: every Key head's full items, head by head (its cache stays in L2), then every
   // head's last item, whose second Query tile may be empty: the short ones fill the last wave's gaps
@@ -212,10 +217,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == kMmaWarp) {
     if (lane == 0) {
       for (int i = 0; i < kStages; i++) {
-        tc::mbar_init(&bars.k_full[i], 2 * kProdWarps);  // both CTAs' producer warps (even CTA's copy used)
-        tc::mbar_init(&bars.v_full[i], 2 * kProdWarps);
-        tc::mbar_init(&bars.k_empty[i], 1);
-        tc::mbar_init(&bars.v_empty[i], 1);
+        // this CTA's producer warps; in the even CTA also the odd one's last warp, which passes on that its
+        // producers are done (a producer's own arrival in the peer would wait for its loads in flight)
+        tc::mbar_init(&bars.full[i], kProdWarps + 1 - cr);
+        tc::mbar_init(&bars.empty[i], 1);
       }
       for (int i = 0; i < 2; i++) {
         tc::mbar_init(&bars.s_full[i][0], 1);
@@ -319,7 +324,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     leave();
     return;
   }
-  const bool skip1 = pair0 + 2 * BM >= rows;   // the second 256-row tile is empty
+  // A short item: its rows fill the first Query tile at most.  Both tiles then take those rows and every
+  // other step of 64 keys each, and are joined at the end: two chains of MMA and softmax instead of one.
+  const bool brief = pair0 + 2 * BM >= rows;
 
   // ---- the Queries, which have arrived by now: bf16 -> fp16 in place, padding rows 0 ----
   if (warp < kSoftmaxWarps) {
@@ -356,7 +363,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int key_end = keys.total < (j0 + J) * BN ? keys.total : (j0 + J) * BN;
   const int steps = (key_end - j0 * BN + BS - 1) / BS;   // 2 J, or one less when the last stage is half empty
 
-  if (warp < (skip1 ? kSoftmaxWarps / 2 : kSoftmaxWarps)) {
+  if (warp < kSoftmaxWarps) {
     // ======================= softmax (Query tile x, row = TMEM lane) =======================
     const uint32_t tmem = joined();
     if (lane == 0) tc::mbar_arrive_remote(tc::mapa(tc::smem_u32(&bars.q_full), 0));
@@ -366,7 +373,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t p_ready0 = tc::mapa(tc::smem_u32(&bars.p_ready[x][0]), 0);
     const float sl2 = a.scale_log2 * win::kUnit<BITS>;
     const uint64_t sc2 = pk64(sl2, sl2);
-    const int64_t w0 = row_base + (int64_t)x * 2 * BM + 32 * sub;   // this warp's first row
+    const int64_t w0 = row_base + (brief ? 0 : (int64_t)x * 2 * BM) + 32 * sub;   // this warp's first row
+    const int mine_n = brief ? (steps + 1 - x) >> 1 : steps;   // steps of this tile
+    const int key_of = j0 * BN + (brief ? x * BS : 0), key_step = brief ? 2 * BS : BS;
     const int64_t r = w0 + lane;
     win::Row mine{0, 0, 0};
     win::Everyone every{INT32_MAX, 0, 0};   // a warp without a row masks nothing (its logits are 0)
@@ -377,8 +386,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     float m_used = -INFINITY;
     uint64_t acc0 = 0ull, acc1 = 0ull;
     bool ok = true;
-    for (int t = 0; t < steps; t++) {
-      const int v0 = j0 * BN + t * BS;
+    for (int t = 0; t < mine_n; t++) {
+      const int v0 = key_of + t * key_step;
       const bool full = every.see(v0, v0 + BS);
       const uint32_t tS = tS0 + (uint32_t)(t & 1) * BS;
       if (!__all_sync(0xffffffffu, tc::mbar_try_wait(&bars.s_full[x][t & 1], (t >> 1) & 1))) {
@@ -450,11 +459,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) tc::mbar_arrive_remote(p_ready0 + 8u * (uint32_t)(t & 1));
     }
-    if (ok && !tc::mbar_wait(&bars.o_done, 0, kWaitNs)) fail(&abort_flag, a.status);
-    if (ok && !__any_sync(0xffffffffu, *abort_v != 0)) {
+    const uint64_t lsum = tc::add2(acc0, acc1);
+    float l = tc::f2lo(lsum) + tc::f2hi(lsum), share = 1.f, share1 = 0.f;   // what O_0 and O_1 count for
+    if (brief) {   // every softmax warp comes here, whatever happened before
+      if (x == 1) half_sums[tid & (BM - 1)] = make_float2(m_used, l);
+      asm volatile("bar.sync 1, %0;" ::"n"(32 * kSoftmaxWarps) : "memory");
+      if (x == 0) {
+        const float2 o = half_sums[tid];
+        const float m = fmaxf(m_used, o.x);
+        share = m_used == -INFINITY ? 0.f : tc::ex2_approx(m_used - m);
+        share1 = o.x == -INFINITY ? 0.f : tc::ex2_approx(o.x - m);
+        l = fmaf(l, share, o.y * share1);
+        m_used = m;
+      }
+    }
+    const bool writer = !(brief && x == 1);
+    if (ok && writer && !tc::mbar_wait(&bars.o_done, 0, kWaitNs)) fail(&abort_flag, a.status);
+    if (ok && writer && !__any_sync(0xffffffffu, *abort_v != 0)) {
       tc::fence_after_sync();
-      const uint64_t lsum = tc::add2(acc0, acc1);
-      const float l = tc::f2lo(lsum) + tc::f2hi(lsum);
       float inv = l > 0.f ? win::kUnit<BITS> / l : 0.f, keep = 0.f;
       float L = l > 0.f ? m_used + log2f(l) : -INFINITY;
       bool write = r < rows;
@@ -478,13 +500,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // 16 KB buffer per warp, 16-byte pieces permuted by the row's low bits against bank conflicts
       const uint32_t buf = tc::smem_u32(sm) + (uint32_t)warp * 16384u, rx = (uint32_t)lane & 7u;
       const bool half = a.splits == 1 && !a.out_f32;   // bf16 rows
+      const float w0_out = share * inv, w1_out = share1 * inv;
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         uint32_t o[32];
         tc::tmem_ld32(tO + c, o);
         tc::tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < 32; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
+        for (int i = 0; i < 32; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * w0_out);
+        if (brief && steps > 1) {   // (a single step left O_1 unwritten)
+          uint32_t o1[32];
+          tc::tmem_ld32(tO + 128 + c, o1);
+          tc::tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; i++)
+            o[i] = __float_as_uint(fmaf(__uint_as_float(o1[i]), w1_out, __uint_as_float(o[i])));
+        }
         if (half) {
 #pragma unroll
           for (int v = 0; v < 4; v++) {
@@ -530,101 +561,111 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == kMmaWarp) {
-    // ======================= MMA issue: the even CTA's, for the pair =======================
+    // ======================= the last warps: the even CTA's issues the pair's MMAs, the odd one's passes on
+    // that its CTA's stages are full =======================
     const uint32_t tmem = joined();
-    if (cr == 0) {
+    // The warp's common answer.  Whether someone gave up is looked at only where there is something to
+    // wait for: the flag's read behind every barrier cost 12% of a step.
+    auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
+      if (__all_sync(0xffffffffu, tc::mbar_try_wait_cluster(bar, parity))) return true;
+      return __all_sync(0xffffffffu, tc::mbar_wait_cluster(bar, parity, kWaitNs) && !*abort_v);
+    };
+    if (cr == 1) {
+      const uint32_t full = tc::mapa(tc::smem_u32(&bars.full[0]), 0);
+      for (int j = 0; j < J; j++) {
+        if (!wait(&bars.full[j & (kStages - 1)], (j / kStages) & 1)) {
+          fail(&abort_flag, a.status);
+          break;
+        }
+        if (lane == 0) tc::mbar_arrive_remote(full + 8u * (uint32_t)(j & (kStages - 1)));
+      }
+    } else {
       constexpr uint32_t idesc = tc::idesc_f16_f32(2 * BM, BS), idesc_pv = tc::idesc_f16_f32_bmn(2 * BM, D);
       constexpr uint16_t kBoth = 3;
       // broadcast, so that everything derived from them is the warp's and not a lane's
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), s0 = __shfl_sync(0xffffffffu, tc::smem_u32(sm), 0);
       const int n = __shfl_sync(0xffffffffu, steps, 0);
-      const bool one = __shfl_sync(0xffffffffu, (int)skip1, 0) != 0;
       const uint64_t dq = tc::desc_sw128(s0 + OFF_Q), dk = tc::desc_sw128(s0 + OFF_K);
       const uint64_t dv = tc::desc_sw128_mn(s0 + OFF_V, kBlk, 1024);
       bool ok = true;
-      // The warp's common answer.  Whether someone gave up is looked at only where there is something to
-      // wait for: the flag's read behind every barrier cost 12% of a step.
-      auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
-        if (__all_sync(0xffffffffu, tc::mbar_try_wait_cluster(bar, parity))) return true;
-        return __all_sync(0xffffffffu, tc::mbar_wait_cluster(bar, parity, kWaitNs) && !*abort_v);
-      };
-      auto qk = [&](int x, int t) {
-        const uint32_t ko = (uint32_t)((t >> 1) % kStages) * 2 * kBlkH + (uint32_t)(t & 1) * 32 * 128;
-        const uint64_t da = dq + (uint64_t)(x * 2 * kBlk / 16), db = dk + (uint64_t)(ko / 16);
-        const uint32_t d = tm + 128u * x + (uint32_t)(t & 1) * BS;
+      // step t of tile x: both tiles take the same 64 keys, or (short items) a half each of stage t.  (The two
+      // forms are compiled apart: chosen at every step they cost a tenth of it.)
+      auto multiply = [&](auto rows_of_two) {
+        constexpr bool two = decltype(rows_of_two)::value;
+        const int T = two ? n : (n + 1) >> 1;   // steps of tile 0
+        auto stage_of = [&](int t) { return two ? t >> 1 : t; };
+        auto half_of = [&](int x, int t) { return two ? t & 1 : x; };
+        auto begins = [&](int t) { return !two || !(t & 1); };
+        auto ends = [&](int t) { return !two || (t & 1) || t + 1 == n; };
+        auto there = [&](int t) { return two || 2 * t + 1 < n; };   // tile 1 has a step t
+        auto qk = [&](int x, int t) {
+          const uint32_t ko = (uint32_t)(stage_of(t) % kStages) * 2 * kBlkH + (uint32_t)half_of(x, t) * 32 * 128;
+          const uint64_t da = dq + (uint64_t)(two ? x * 2 * kBlk / 16 : 0), db = dk + (uint64_t)(ko / 16);
+          const uint32_t d = tm + 128u * x + (uint32_t)(t & 1) * BS;
 #pragma unroll
-        for (int kk = 0; kk < D / 16; kk++)
-          tc::mma2_ss_warp(d, da + (uint64_t)(((kk / 4) * kBlk + 32 * (kk % 4)) / 16),
-                           db + (uint64_t)(((kk / 4) * kBlkH + 32 * (kk % 4)) / 16), idesc, kk > 0);
-        tc::mma2_commit_warp(&bars.s_full[x][t & 1], kBoth);
-      };
-      auto pv = [&](int x, int t) {
-        const uint32_t vo = (uint32_t)((t >> 1) % kStages) * kBlk + (uint32_t)(t & 1) * BS * 128;
-        const uint64_t db = dv + (uint64_t)(vo / 16);
-        const uint32_t p = tm + 128u * x + (uint32_t)(t & 1) * BS;
+          for (int kk = 0; kk < D / 16; kk++)
+            tc::mma2_ss_warp(d, da + (uint64_t)(((kk / 4) * kBlk + 32 * (kk % 4)) / 16),
+                             db + (uint64_t)(((kk / 4) * kBlkH + 32 * (kk % 4)) / 16), idesc, kk > 0);
+          tc::mma2_commit_warp(&bars.s_full[x][t & 1], kBoth);
+        };
+        auto pv = [&](int x, int t) {
+          const uint32_t vo = (uint32_t)(stage_of(t) % kStages) * kBlk + (uint32_t)half_of(x, t) * BS * 128;
+          const uint64_t db = dv + (uint64_t)(vo / 16);
+          const uint32_t p = tm + 128u * x + (uint32_t)(t & 1) * BS;
 #pragma unroll
-        for (int kk = 0; kk < BS / 16; kk++)
-          tc::mma2_ts_warp(tm + 256u + 128u * x, p + 8u * kk, db + (uint64_t)(2048 * kk / 16), idesc_pv,
-                           (t > 0 || kk > 0));
-        tc::mma2_commit_warp(&bars.pv_done[x][t & 1], kBoth);
-      };
-      auto stage_ends = [&](int t) { return (t & 1) || t + 1 == n; };
-      auto keys_there = [&](int t) {   // the Keys of step t (a stage's first step waits for it)
-        return (t & 1) || wait(&bars.k_full[(t >> 1) % kStages], ((t >> 1) / kStages) & 1);
+          for (int kk = 0; kk < BS / 16; kk++)
+            tc::mma2_ts_warp(tm + 256u + 128u * x, p + 8u * kk, db + (uint64_t)(2048 * kk / 16), idesc_pv,
+                             (t > 0 || kk > 0));
+          tc::mma2_commit_warp(&bars.pv_done[x][t & 1], kBoth);
+        };
+        auto keys_there = [&](int t) {   // the Keys and Values of step t (a stage's first step waits for it)
+          return !begins(t) || wait(&bars.full[stage_of(t) % kStages], (stage_of(t) / kStages) & 1);
+        };
+        for (int t = 0; ok && t < 2 && t < T; t++) {
+          ok = keys_there(t);
+          if (!ok) break;
+          tc::fence_after_sync();
+          qk(0, t);
+          if (there(t)) qk(1, t);
+        }
+        for (int t = 0; ok && t < T; t++) {
+          ok = wait(&bars.p_ready[0][t & 1], (t >> 1) & 1);
+          if (!ok) break;
+          tc::fence_after_sync();
+          pv(0, t);
+          if (t + 2 < T) {
+            ok = keys_there(t + 2);
+            if (!ok) break;
+            tc::fence_after_sync();
+            qk(0, t + 2);
+          }
+          if (there(t)) {
+            ok = wait(&bars.p_ready[1][t & 1], (t >> 1) & 1);
+            if (!ok) break;
+            tc::fence_after_sync();
+            pv(1, t);
+            if (t + 2 < T && there(t + 2)) qk(1, t + 2);
+          }
+          if (ends(t)) tc::mma2_commit_warp(&bars.empty[stage_of(t) % kStages], kBoth);   // (S precedes P V)
+        }
       };
       ok = wait(&bars.q_full, 0);
-      for (int t = 0; ok && t < 2 && t < n; t++) {
-        ok = keys_there(t);
-        if (!ok) break;
-        tc::fence_after_sync();
-        qk(0, t);
-        if (!one) qk(1, t);
-        if (stage_ends(t)) tc::mma2_commit_warp(&bars.k_empty[(t >> 1) % kStages], kBoth);
-      }
-      for (int t = 0; ok && t < n; t++) {
-        if (!(t & 1)) ok = wait(&bars.v_full[(t >> 1) % kStages], ((t >> 1) / kStages) & 1);
-        ok = ok && wait(&bars.p_ready[0][t & 1], (t >> 1) & 1);
-        if (!ok) break;
-        tc::fence_after_sync();
-        pv(0, t);
-        if (t + 2 < n) {
-          ok = keys_there(t + 2);
-          if (!ok) break;
-          tc::fence_after_sync();
-          qk(0, t + 2);
-        }
-        if (!one) {
-          ok = wait(&bars.p_ready[1][t & 1], (t >> 1) & 1);
-          if (!ok) break;
-          tc::fence_after_sync();
-          pv(1, t);
-          if (t + 2 < n) qk(1, t + 2);
-        }
-        if (stage_ends(t)) tc::mma2_commit_warp(&bars.v_empty[(t >> 1) % kStages], kBoth);
-        if (t + 2 < n && stage_ends(t + 2)) tc::mma2_commit_warp(&bars.k_empty[((t + 2) >> 1) % kStages], kBoth);
-      }
+      if (__shfl_sync(0xffffffffu, (int)brief, 0)) multiply(Flag<false>{});
+      else multiply(Flag<true>{});
       if (ok) tc::mma2_commit_warp(&bars.o_done, kBoth);
       if (!ok) fail(&abort_flag, a.status);
       tc::mma2_commit_warp(&bars.drain, 1);  // every MMA issued above completes before TMEM is released
       if (!tc::mbar_wait(&bars.drain, 0, kWaitNs)) qwm_dev_error(a.status, QWM_ERR_DEVICE_TIMEOUT);
     }
   } else {
-    // ======================= producers: Keys, then Values, of every stage; or, where the second Query
-    // tile is empty, its softmax warps produce the Values and these only the Keys =======================
-    const bool do_k = warp >= kProdWarp0, do_v = warp < kProdWarp0 || !skip1;
-    const int pw = warp & (kProdWarps - 1);
+    // ======================= producers: Keys, then Values, of every stage =======================
+    const int pw = warp - kProdWarp0;
     const Producer<BITS, false> pk(a, sm, y, cr, pw, lane);
     const Producer<BITS, true> pv(a, sm, y, cr, pw, lane);
     const uint32_t sink = (uint32_t)a.w.sink, ring = (uint32_t)a.w.ring;
     Pieces<BITS> k0, v0, k1, v1;
-    // the even CTA's full barriers (consecutive 8-byte words), as shared::cluster addresses
-    const uint32_t k_full = tc::mapa(tc::smem_u32(&bars.k_full[0]), 0), v_full = tc::mapa(tc::smem_u32(&bars.v_full[0]), 0);
-    auto hand_over = [&](uint32_t full) {
-      tc::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive_remote(full);
-    };
-    auto free_again = [&](uint64_t *empty, int j) -> bool {   // the stage's previous contents are consumed
+    auto free_again = [&](int j) -> bool {   // the previous contents of stage j's place are consumed
+      uint64_t *empty = &bars.empty[j & (kStages - 1)];
       if (j < kStages || __all_sync(0xffffffffu, tc::mbar_try_wait(empty, (j / kStages - 1) & 1))) return true;
       if (!tc::mbar_wait(empty, (j / kStages - 1) & 1, kWaitNs)) fail(&abort_flag, a.status);
       return !__any_sync(0xffffffffu, *abort_v != 0);         // warp-uniform exit
@@ -638,31 +679,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t first = keys.slot(next, sink, ring);
         if (next + BN <= keys.total && keys.slot(next + BN - 1, sink, ring) == first + BN - 1) slot0 = first;
       }
-      if (do_k) {
-        if (store) {
-          if (!free_again(&bars.k_empty[s], j)) return false;
-          pk.store((uint32_t)s, k, a.bases);
-          hand_over(k_full + 8u * (uint32_t)s);
-        }
-        if (load) pk.load(keys, next, slot0, sink, ring, k);
+      if (store) {
+        if (!free_again(j)) return false;
+        pk.store((uint32_t)s, k, a.bases);
       }
-      if (do_v) {
-        if (store) {
-          if (!free_again(&bars.v_empty[s], j)) return false;
-          pv.store((uint32_t)s, v, a.bases);
-          hand_over(v_full + 8u * (uint32_t)s);
-        }
-        if (load) pv.load(keys, next, slot0, sink, ring, v);
+      if (load) pk.load(keys, next, slot0, sink, ring, k);
+      if (store) {
+        pv.store((uint32_t)s, v, a.bases);
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bars.full[s]);
       }
+      if (load) pv.load(keys, next, slot0, sink, ring, v);
       return true;
     };
 #pragma unroll 1
     for (int j = -2; j < J; j += 2) {
       if (!stage(j, k0, v0) || !stage(j + 1, k1, v1)) break;
-      if (j < 0) {
-        joined();
-        if (warp < kSoftmaxWarps && lane == 0) tc::mbar_arrive_remote(tc::mapa(tc::smem_u32(&bars.q_full), 0));
-      }
+      if (j < 0) joined();
     }
   }
   tc::fence_before_sync();
