@@ -151,8 +151,9 @@ __device__ __forceinline__ uint4 restore(uint2 x, uint32_t step, const win::Base
   }
 #pragma unroll
   for (int u = 0; u < 4; u++) {
+    if (BITS == 4) pr[u] = win::hmul2(pr[u], 0x4C004C00u);   // times the unit, 16
     const float2 f = __half22float2(*(const __half2 *)&pr[u]);
-    o[u] = tc::pack_bf16x2(f.x * win::kUnit<BITS>, f.y * win::kUnit<BITS>);
+    o[u] = tc::pack_bf16x2(f.x, f.y);
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }

@@ -16,7 +16,10 @@
 //   warps 0-3, 4-7  softmax of Query tile 0 / 1: thread = Query row = TMEM lane, 64 logits at a time;
 //   warps 8-11      producers: codes two stages ahead in registers, decoded (one permute and one fp16
 //                   FMA per pair at 8 bits) into swizzled stages;
-//   warp 12         allocates TMEM; in the even CTA it issues every MMA of the pair.
+//   warp 12         allocates TMEM; in the even CTA it issues every MMA of the pair, in the odd one it
+//                   passes on to the even one that its producers have filled a stage.
+// An item whose rows all fit the first Query tile (a Key head's last one, or any call of up to 256 rows)
+// gives both tiles those rows and every other 64 keys each, joined at the end: 1,050 -> 700 cycles per 64 keys.
 // TMEM (512 columns): S_x as two buffers of 64 keys, P_x over them, O_x.  Keys arrive in stages of 128
 // and are multiplied 64 at a time: as soon as PV_x(t) has been issued its buffer takes S_x(t + 2), so
 // the softmax warps find the next step's logits ready and the tensor pipe always holds work: per step
@@ -24,10 +27,10 @@
 // 256 x 128 x 16 (64 cycles).  MMAs execute in issue order, so a buffer is written after the PV that
 // read it.
 // Measured (fp16 operands, 2 x 2 x 128 operations per row and visible key): 40 heads x 4,680 rows over 39,000
-// keys at 8 bits in 2.54 ms = 1,473 TFLOP/s, the tensor pipe active in 70% of all cycles and in 2,400 of
-// the loop's 2,700 per 128 keys and 512 rows; 3,600 rows over 43,200 keys at 4 bits in 2.22 ms.  Around
-// the loop an item spends about 16,000 cycles (first loads 9,000, first logits 3,000, output 4,000),
-// which a prompt under a window of 1,024 keys feels: 2 x 2,111 tokens x 32 heads in 105 us.
+// keys at 8 bits in 2.28 ms = 1,639 TFLOP/s, 3,600 rows over 43,200 keys at 4 bits in 1.92 ms = 1,657; the
+// tensor pipe is active in 81% of all cycles, and in 1,200 of about 1,260 per step of the loop.  Around the
+// loop an item spends about 15,000 cycles (first loads 7,000, first logits 2,500, output 4,000), which a
+// prompt under a window of 1,024 keys feels: 2 x 2,111 tokens x 32 heads in 96 us.
 // Every wait is bounded (about one second); on expiry QWM_ERR_DEVICE_TIMEOUT is recorded, every role
 // stops, outstanding MMAs are drained and TMEM is freed.
 #include "window.cuh"
@@ -727,7 +730,7 @@ cudaError_t launch_window_tiles(const WindowAttend &a, cudaStream_t st) {
 }
 
 // Few rows run on warp tiles, which read the cache once per 16 rows; more than 32 on tensor-memory tiles (at
-// 39,000 tokens of 40 heads, 8 bits: 16 rows take 90 us, up to 256 rows on tensor-memory tiles 235).
+// 39,000 tokens of 40 heads, 8 bits: 16 rows take 90 us, up to 256 rows on tensor-memory tiles 205).
 // The keys are split into the number of parts for which whole waves of CTAs end soonest, by what a part
 // costs in cycles, as measured: on warp tiles 12 per key (a CTA of 8 warps, whatever the code width) and
 // 10,000 for starting and ending, 6,000 more for a second kernel that joins the parts; up to 8 parts may be

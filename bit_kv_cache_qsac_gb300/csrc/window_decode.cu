@@ -15,9 +15,9 @@
 // meet in shared memory at the end, the parts of a Key head (up to 8) in the shared memory of a
 // thread-block cluster, more parts in a second kernel.
 // Measured: 16 sequences x 32 heads (8 Key heads) x 4,096 keys at 8 bits in 27.8 us = 5.0 TB/s, about 7
-// us of it before the first keys arrive and in the join; 40 heads x 39,000 keys at 4 bits in 52.6 us =
-// 4.0 TB/s, held by instruction issue (336 warp instructions per 16 keys of a head, 184 of them
-// placing, unbiasing and scaling codes).
+// us of it before the first keys arrive and in the join; 40 heads x 39,000 keys at 4 bits in 52 us = 4.1
+// TB/s, held by instruction issue (316 warp instructions per 16 keys of a head, 160 of them placing,
+// unbiasing and scaling codes, half of those on the half-rate integer pipe).
 #include "window.cuh"
 
 namespace {
