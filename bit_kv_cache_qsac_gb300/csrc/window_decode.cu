@@ -135,6 +135,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) window_decode_kerne
   const uint32_t b = blockIdx.y / (uint32_t)a.w.kv_heads;
   const int kvh = (int)(blockIdx.y - b * (uint32_t)a.w.kv_heads);
   if (!CLUSTER) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the joining kernel may line up
+  // the sequence's numbers, on their way first: the first copies wait for them
+  const int64_t q0 = a.q_start[b], len = win::tokens_of(a.length[b]);
+  int64_t nq = a.q_count ? (int64_t)a.q_count[b] : a.nq;
   const int row0 = 8 * NT * (int)blockIdx.z;   // this CTA's block of rows
   // ---- Queries as the first product's B fragments (row g of every 8), bf16 for now; on their way while
   // the rest is worked out, and whatever they are: rows that turn out to be padding are dropped below ----
@@ -151,8 +154,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) window_decode_kerne
       qf[nt][ks][1] = w.y;
     }
   }
-  const int64_t q0 = a.q_start[b], len = win::tokens_of(a.length[b]);
-  int64_t nq = a.q_count ? (int64_t)a.q_count[b] : a.nq;
   nq = nq < a.nq ? nq : a.nq;
   if (!win::starts(q0) || nq <= 0 || nq * a.group <= row0) return;   // the whole cluster
   const win::Seq seq{len, a.w.sink, a.w.ring, a.tpf, a.frames};
