@@ -13,9 +13,10 @@ namespace {
 
 constexpr int kThreads = 256, kRows = kThreads / 16, kReadRows = kThreads / 8;
 
-__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {   // a NaN stays one
+// The larger magnitude of each half (a NaN stays one); its sign means nothing.
+__device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
   uint32_t d;
-  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
 
@@ -25,20 +26,20 @@ template <int BITS>
 __device__ __forceinline__ void quantise(const uint32_t (&w)[4], uint32_t &c0, uint32_t &c1, uint32_t &step,
                                          bool &bad) {
   constexpr float kTop = win::code_max(BITS) * (BITS == 8 ? 56.f : 896.f);
-  uint32_t m = max_bf16x2(max_bf16x2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
-                          max_bf16x2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
-  m = max_bf16x2(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  m = max_bf16x2(m, __shfl_xor_sync(0xffffffffu, m, 2));
-  const float mlo = __uint_as_float(m << 16), mhi = __uint_as_float(m & 0xFFFF0000u);
-  float amax = fmaxf(mlo, mhi), f[8];
+  uint32_t m = max_abs_bf16x2(max_abs_bf16x2(w[0], w[1]), max_abs_bf16x2(w[2], w[3]));
+  m = max_abs_bf16x2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = max_abs_bf16x2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  m = max_abs_bf16x2(m, m >> 16);
+  float amax = __uint_as_float((m & 0x7FFFu) << 16), f[8], s;
 #pragma unroll
   for (int i = 0; i < 4; i++) {
     f[2 * i] = __uint_as_float(w[i] << 16);
     f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
   }
-  const bool out = !(mlo <= kTop && mhi <= kTop);   // out of range or NaN, somewhere in the group
-  if (__any_sync(0xffffffffu, out)) {   // cut to the range, NaN to 0
-    if (out) {
+  step = win::normal_step<BITS>(amax, s);
+  const bool out = !(amax <= kTop);   // out of range or NaN, somewhere in the group
+  if (__any_sync(0xffffffffu, out || win::step_is_small<BITS>(amax))) {
+    if (out) {   // cut to the range, NaN to 0
       bad = true;
       amax = 0.f;
 #pragma unroll
@@ -48,11 +49,10 @@ __device__ __forceinline__ void quantise(const uint32_t (&w)[4], uint32_t &c0, u
       }
     }
     float a = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
-    amax = out ? a : amax;
+    amax = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
+    step = win::step_is_small<BITS>(amax) ? win::small_step<BITS>(amax, s) : win::normal_step<BITS>(amax, s);
   }
-  float s, inv;
-  step = win::step_for<BITS>(amax, s);
+  float inv;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
   inv = s > 0.f ? inv : 0.f;
   const uint64_t inv2 = win::pair2(inv, inv);

@@ -216,18 +216,21 @@ __device__ __forceinline__ float step_value(uint32_t b) { return __half2float(__
 // The smallest step with Q s >= amax (amax a bf16 value), at most step_max: its byte, and s itself.
 // amax has 8 significant bits and a step 4, so the quotient is a step exactly or at least 2^-11 (relative)
 // away from every step: rounding up to 3 mantissa bits after taking 16 units off (the multiplication's
-// error is below 2) finds it.  Below 2^-14 steps are multiples of 2^-17.
+// error is below 2) finds it.  Below 2^-14 (`step_is_small`) steps are multiples of 2^-17.
 template <int BITS>
-__device__ __forceinline__ uint32_t step_for(float amax, float &s) {
-  constexpr float Q = code_max(BITS);
-  const float t = amax * (1.f / Q);
-  if (t < 0x1p-14f * (1.f - 0x1p-20f)) {
-    const float m = ceilf(t * 0x1p17f * (1.f - 0x1p-20f));
-    s = m * 0x1p-17f;
-    return (uint32_t)m;
-  }
+__device__ __forceinline__ bool step_is_small(float amax) {
+  return amax * (1.f / code_max(BITS)) < 0x1p-14f * (1.f - 0x1p-20f);
+}
+template <int BITS>
+__device__ __forceinline__ uint32_t small_step(float amax, float &s) {
+  const float m = ceilf(amax * (1.f / code_max(BITS)) * 0x1p17f * (1.f - 0x1p-20f));
+  s = m * 0x1p-17f;
+  return (uint32_t)m;
+}
+template <int BITS>
+__device__ __forceinline__ uint32_t normal_step(float amax, float &s) {
   constexpr uint32_t kTop = (step_max(BITS) << 20) + ((127u - 15u) << 23);
-  uint32_t b = (__float_as_uint(t) + (0xFFFFFu - 16u)) & 0xFFF00000u;
+  uint32_t b = (__float_as_uint(amax * (1.f / code_max(BITS))) + (0xFFFFFu - 16u)) & 0xFFF00000u;
   b = b < kTop ? b : kTop;
   s = __uint_as_float(b);
   return (b >> 20) - ((127u - 15u) << 3);
@@ -236,10 +239,11 @@ __device__ __forceinline__ uint32_t step_for(float amax, float &s) {
 // Two codes: rint(x / s) in the low bits of each result's pattern (0x4B400000 + code).  The quotient is
 // first rounded to a grid of 2^-11: x has 8 significant bits and s has 4, so a quotient that is not
 // halfway between integers is at least 2^-9.9 away from halfway and stays on its side, while one that
-// is lands exactly on it (and then ties to even).
+// is lands exactly on it (and then ties to even).  The first constant stays in the sum; the second one
+// takes it out again while it rounds to integers (both are exact).
 __device__ __forceinline__ uint64_t codes_of(uint64_t x2, uint64_t inv2) {
-  const uint64_t grid = pair2(0x1.8p12f, 0x1.8p12f), ungrid = pair2(-0x1.8p12f, -0x1.8p12f);
-  return tc::add2(tc::add2(tc::fma2(x2, inv2, grid), ungrid), pair2(0x1.8p23f, 0x1.8p23f));
+  const uint64_t grid = pair2(0x1.8p12f, 0x1.8p12f), whole = pair2(0x1.8p23f - 0x1.8p12f, 0x1.8p23f - 0x1.8p12f);
+  return tc::add2(tc::fma2(x2, inv2, grid), whole);
 }
 
 // What the decoders below give is the value over kUnit: at 4 bits a sixteenth, so that every constant of
