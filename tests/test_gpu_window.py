@@ -679,3 +679,20 @@ def test_negative_lengths_hold_no_token(qwm, nq, ring):
     kh = torch.full((b, 1, 7, 128), 5.0, dtype=torch.bfloat16, device="cuda")
     qwm.qwm_window_read(ctx, win, ints([0, 2, 3, 4]), ints(lengths), kh, None)
     assert bool((kh == 0).all())
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("length", [1, 63, 64, 65, 128, 129, 193, 700])   # halves of a stage, stages, more than the stages
+@pytest.mark.parametrize("nq", [33, 256, 257])                           # one Query tile and just past it
+def test_attend_around_one_query_tile(qwm, bits, length, nq):
+    rng = np.random.default_rng(length + nq)
+    ctx = ctx_of(qwm, 1)
+    win = fill(qwm, ctx, rng, bits, 1, 2, 800, [length])
+    q = rows(rng, 1, 1, nq)
+    out = torch.empty(1, 1, nq, 128, dtype=torch.float32, device="cuda")
+    lse = torch.empty(1, 1, nq, dtype=torch.float32, device="cuda")
+    q0 = max(0, length - nq)
+    for tpf, frames in ((1, 800), (1, 50), (100, 2)):
+        qwm.qwm_window_attend(ctx, win, q, ints([q0]), ints([length]), tpf, frames, SCALE, out, lse=lse)
+        assert qwm.qwm_sync_status(ctx) == 0
+        check_attention(win, q, [q0], [length], tpf, frames, SCALE, out, lse, out_eps=2.0 ** -22)
