@@ -14,7 +14,7 @@
 // more for V, whose pairs run along the keys).  Every warp keeps its own running maximum and sum; warps
 // meet in shared memory at the end, the parts of a Key head (up to 8) in the shared memory of a
 // thread-block cluster, more parts in a second kernel.
-// Measured: 16 sequences x 32 heads (8 Key heads) x 4,096 keys at 8 bits in 27.8 us = 5.0 TB/s, about 7
+// Measured: 16 sequences x 32 heads (8 Key heads) x 4,096 keys at 8 bits in 27.2 us = 5.1 TB/s, about 7
 // us of it before the first keys arrive and in the join; 40 heads x 39,000 keys at 4 bits in 52 us = 4.1
 // TB/s, held by instruction issue (316 warp instructions per 16 keys of a head, 160 of them placing,
 // unbiasing and scaling codes, half of those on the half-rate integer pipe).
