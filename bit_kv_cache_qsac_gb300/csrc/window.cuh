@@ -302,6 +302,14 @@ __device__ __forceinline__ void decode4(uint32_t x, const Step &st, const Bases 
   p[3] = tc::hfma2(place<0x00F000F0u>(y, c.k64), st.s, st.n);
 }
 
+// ------------------------------------------------------------------ weights
+
+// The weights 2^(l - m) of the second product are fp16, rounded to 11 bits down to 2^-14 and to multiples of
+// 2^-24 below.  So that many small ones beside a large one (a sink) are not lost from the output while the
+// sum of the weights, in fp32, has them, m stands 7 below the running maximum: the largest weight is 2^7, at
+// most 2^15 while the maximum lags by 8, and the grid is 2^-31 of it.  Output and sum share the factor.
+constexpr float kTopWeight = 7.f;
+
 // ------------------------------------------------------------------ which keys a row sees
 
 // a / b of non-negative numbers, in 32 bits where they fit (a 64-bit division takes some 100 instructions).

@@ -3,7 +3,7 @@
 //   l_ij = scale q_i . k_hat_j over the keys row i sees, o_i = softmax(l_i) V_hat, with k_hat and v_hat
 // decoded from the 8- or 4-bit cache inside the kernel.  A cached value is exact in fp16 and so is a
 // bf16 Query in the fp16 range (2^-17 to 65504), so the logits carry only fp32 rounding; the weights
-// enter the second product in fp16.
+// enter the second product in fp16, the largest as 2^7 (win::kTopWeight).
 //
 // Work split: a pair of CTAs (a cluster of two, cta_group::2 MMAs) takes one Key head x 512 Query rows
 // (row r = Query r / group, head r % group) and one part of the keys those rows see between them; CTA c
@@ -387,7 +387,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       every.init(seq, keys, frame_of(w0), frame_of(w0 + 31 < rows ? w0 + 31 : rows - 1));
     }
     float m_used = -INFINITY;
-    uint64_t acc0 = 0ull, acc1 = 0ull;
+    uint64_t acc = 0ull;   // the sum of the weights, each step's added as one: 1 / 64 of the additions to a large sum
     bool ok = true;
     for (int t = 0; t < mine_n; t++) {
       const int v0 = key_of + t * key_step;
@@ -398,8 +398,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (__any_sync(0xffffffffu, *abort_v != 0)) { ok = false; break; }   // the whole warp
       }
       tc::fence_after_sync();
-      // the step's logits at once: their maximum, then their exponentials with the running maximum
-      // m_used; when it grows by more than 2^8 (rare after the first step) the sum and O are rescaled
+      // the step's logits at once: their maximum, then their exponentials relative to m_used, which stands
+      // kTopWeight below the running maximum; when that grows by more than 2^8 (rare after the first step)
+      // the sum and O are rescaled
       uint32_t s[BS];
 #pragma unroll
       for (int i = 0; i < BS; i += 16) tc::tmem_ld16(tS + (uint32_t)i, s + i);
@@ -420,12 +421,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int u = 0; u < 4; u++)
           mx[u] = tc::max3(mx[u], __uint_as_float(s[i + 2 * u]), __uint_as_float(s[i + 2 * u + 1]));
-      const float m_new = fmaxf(m_used, tc::max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * sl2);
+      const float m_new = fmaxf(m_used, fmaf(tc::max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]), sl2, -win::kTopWeight));
       if (__any_sync(0xffffffffu, m_new > m_used + kRescaleThreshold)) {
         const float alpha = m_new == -INFINITY ? 1.f : tc::ex2_approx(m_used - m_new);
         const uint64_t a2 = pk64(alpha, alpha);
-        acc0 = tc::fma2(acc0, a2, 0ull);
-        acc1 = tc::fma2(acc1, a2, 0ull);
+        acc = tc::fma2(acc, a2, 0ull);
         if (t > 0) {  // O of the earlier steps, once PV_x(t-1) has been added (PV_x(t) waits for this warp)
           if (!tc::mbar_wait(&bars.pv_done[x][(t - 1) & 1], ((t - 1) >> 1) & 1, kWaitNs)) fail(&abort_flag, a.status);
           tc::fence_after_sync();
@@ -443,6 +443,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       const float mneg = m_used == -INFINITY ? 0.f : -m_used;  // a row that has seen no key yet
       const uint64_t nm2 = pk64(mneg, mneg);
+      uint64_t sum0 = 0ull, sum1 = 0ull;
 #pragma unroll
       for (int h = 0; h < BS / 32; h++) {
         uint32_t pw[16];
@@ -451,19 +452,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint64_t x2 = tc::fma2(pk64(s[32 * h + 2 * i], s[32 * h + 2 * i + 1]), sc2, nm2);
           const float e0 = tc::ex2_approx(tc::f2lo(x2)), e1 = tc::ex2_approx(tc::f2hi(x2));
           const uint64_t e2 = pk64(e0, e1);
-          if (i & 1) acc1 = tc::add2(acc1, e2);
-          else acc0 = tc::add2(acc0, e2);
+          if (i & 1) sum1 = h == 0 && i == 1 ? e2 : tc::add2(sum1, e2);
+          else sum0 = h == 0 && i == 0 ? e2 : tc::add2(sum0, e2);
           pw[i] = tc::pack_f16x2(e0, e1);
         }
         tc::tmem_st16(tS + 16u * h, pw);  // P (fp16 pairs) over the logits
       }
+      acc = tc::add2(acc, tc::add2(sum0, sum1));
       tc::tmem_st_wait();
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive_remote(p_ready0 + 8u * (uint32_t)(t & 1));
     }
-    const uint64_t lsum = tc::add2(acc0, acc1);
-    float l = tc::f2lo(lsum) + tc::f2hi(lsum), share = 1.f, share1 = 0.f;   // what O_0 and O_1 count for
+    float l = tc::f2lo(acc) + tc::f2hi(acc), share = 1.f, share1 = 0.f;   // what O_0 and O_1 count for
     if (brief) {   // every softmax warp comes here, whatever happened before
       if (x == 1) half_sums[tid & (BM - 1)] = make_float2(m_used, l);
       asm volatile("bar.sync 1, %0;" ::"n"(32 * kSoftmaxWarps) : "memory");

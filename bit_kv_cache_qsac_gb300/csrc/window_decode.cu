@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) window_decode_kerne
 #pragma unroll
         for (int e = 0; e < 4; e++) s[u16][nt][e] += s_[nt][e];
     }
-    // ---- masked; the running maximum (log2 units); P ----
+    // ---- masked; the running maximum (log2 units, less kTopWeight); P ----
     if (!every.see(v0, v0 + kKeys)) {   // a few steps of a call: what each of the thread's rows sees is worked out here
 #pragma unroll
       for (int nt = 0; nt < NT; nt++)
@@ -340,8 +340,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) window_decode_kerne
         x0 = tc::max3(x0, s[u16][nt][0], s[u16][nt][2]);
         x1 = tc::max3(x1, s[u16][nt][1], s[u16][nt][3]);
       }
-      x0 *= sl2;
-      x1 *= sl2;
+      x0 = fmaf(x0, sl2, -win::kTopWeight);
+      x1 = fmaf(x1, sl2, -win::kTopWeight);
       if (__any_sync(0xffffffffu, x0 > m[nt][0] + kRescale || x1 > m[nt][1] + kRescale)) {
         float n0 = x0, n1 = x1;
 #pragma unroll
