@@ -18,6 +18,7 @@ from . import (ActiveChunk, Chunk, Context, Window, pack_psac_layout, qwm_attend
                qwm_fit_centroids_kv,
                qwm_quantize_kv, qwm_quantize_kv_full, qwm_rope, qwm_select_rank, qwm_sync_status,
                qwm_update_query_stats, qwm_window_attend, qwm_window_read, qwm_window_write)
+from .window import check_rows
 
 
 class CompressedLayer:
@@ -191,7 +192,11 @@ class WindowedLayer:
     The 2-bit packing is made for history; the newest frames, which the next ones lean on most, stay at 8
     or 4 bits.  A step writes its chunk into the window (Keys turned by `rope`), attends over the packed
     history and the window in one softmax, and folds its Queries into the statistics; when the window is
-    full, its oldest chunk is first read back and packed with the statistics gathered so far."""
+    full, its oldest chunk is first read back and packed with the statistics gathered so far.
+
+    A step whose operands are refused changes nothing, and one that raises on the way (a call's error
+    status) may be made again: the layer is then `length` tokens long, as before, and the chunk that was
+    already packed to make room is not packed again."""
 
     def __init__(self, ctx: Context, chunk_tokens: int, window_chunks: int, bits: int = 8, tpf: int | None = None,
                  rope=None, device=None, **layer_options):
@@ -207,35 +212,46 @@ class WindowedLayer:
         self.tpf = chunk_tokens if tpf is None else tpf
         self.packed = CompressedLayer(ctx, device, **layer_options)
         self.window = Window.empty(bits, 1, ctx.heads, 0, window_chunks * chunk_tokens, self.packed.device)
-        self.length = 0                                                        # tokens seen
-        self._length = torch.zeros(1, dtype=torch.int64, device=self.packed.device)   # the same, on the device
+        self.length = 0    # tokens seen
+        self._packed = 0   # tokens of them that have left the window
 
     def step(self, k: torch.Tensor, v: torch.Tensor, q: torch.Tensor, stream=None) -> torch.Tensor:
         """Add the chunk k, v [H][chunk_tokens][d] and attend with its Queries q [H][nq][d] (row i is token
-        i of the chunk): fp32 [H][nq][d]."""
-        n, ring = self.chunk_tokens, self.window.ring
+        i of the chunk): fp32 [H][nq][d].  bf16 with contiguous channels and rows on 16-byte boundaries,
+        otherwise of any strides."""
+        n, ring, ctx = self.chunk_tokens, self.window.ring, self.ctx
+        for t, name in ((k, "k"), (v, "v"), (q, "q")):
+            if not isinstance(t, torch.Tensor) or t.dim() != 3:
+                raise TypeError(f"{name}: expected a tensor [heads][tokens][{ctx.cfg.head_dim}]")
         H, nq, d = q.shape
         if k.shape[1] != n or v.shape[1] != n or nq > n:
-            raise ValueError(f"expected a chunk of {n} tokens and at most as many Queries, got {k.shape[1]} and {nq}")
-        ctx, main = self.ctx, stream if stream is not None else torch.cuda.current_stream(self.packed.device)
+            raise ValueError(f"expected a chunk of {n} tokens and at most as many Queries, got {k.shape[1]}, {v.shape[1]} and {nq}")
+        for t, name, m in ((k, "k", n), (v, "v", n), (q, "q", nq)):
+            check_rows(ctx, t[None], name, (1, ctx.heads, m, ctx.cfg.head_dim))
+        main = stream if stream is not None else torch.cuda.current_stream(self.packed.device)
         with torch.cuda.stream(main):
-            if self.length >= ring:   # the oldest chunk makes room: read back and packed
+            # where the chunk that makes room began, where this one does, and the length after it
+            at = torch.arange(self.length - ring, self.length + n + 1, n, dtype=torch.int64, device=k.device)
+            oldest, begin, length = at[:1], at[-2:-1], at[-1:]
+            if self.length - self._packed >= ring:   # the oldest chunk makes room: read back and packed
                 old = [torch.empty(1, H, n, d, dtype=torch.bfloat16, device=k.device) for _ in range(2)]
-                qwm_window_read(ctx, self.window, self._length - ring, self._length, *old, stream=main)
+                qwm_window_read(ctx, self.window, oldest, begin, *old, stream=main)
                 self.packed.append_chunk(old[0][0], old[1][0], stream=main)
-            begin, self._length = self._length, self._length + n
+                self._packed += n
             qwm_window_write(ctx, self.window, k[None], v[None], begin, rope=self.rope, stream=main)
             if self.rope is not None:
                 turned = torch.empty(H, nq, d, dtype=torch.bfloat16, device=q.device)
                 qwm_rope(ctx, self.rope, q[None], begin, turned[None], stream=main)
                 q = turned
+            else:
+                q = q.contiguous()   # as the calls of the packed path take them
             out = torch.empty(H, nq, d, dtype=torch.float32, device=q.device)
             lse = torch.empty(H, nq, dtype=torch.float32, device=q.device)
             scale = 1.0 / math.sqrt(d)
             if self.packed.chunks:
                 qwm_attend_merge(ctx, q, nq, self.packed.chunks, scale, out, lse, False, main)
             # the window holds exactly the chunks that are not packed: every frame of it is recent
-            qwm_window_attend(ctx, self.window, q[None], begin, self._length, self.tpf, ring // self.tpf + 2, scale,
+            qwm_window_attend(ctx, self.window, q[None], begin, length, self.tpf, ring // self.tpf + 2, scale,
                               out[None], lse=lse[None], merge=bool(self.packed.chunks), stream=main)
             self.packed.fold_queries(q, main)
             self.length += n

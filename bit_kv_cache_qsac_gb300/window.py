@@ -101,6 +101,14 @@ def _rows(ctx, t, name: str, shape, dtypes):
     return t.data_ptr(), qwm_strides(b if shape[0] > 1 else 0, h if shape[1] > 1 else 0, n if shape[2] > 1 else 0)
 
 
+def check_rows(ctx, t, name: str, shape) -> None:
+    """Raise unless t is an activation the calls take: shape, 16-bit elements, the context's device, rows
+    that start on 16-byte boundaries."""
+    at, strides = _rows(ctx, t, name, shape, _BF16)
+    if at % 16 or any(s % 8 for s in (strides.batch, strides.head, strides.token)):
+        raise ValueError(f"{name}: rows must start on 16-byte boundaries")
+
+
 def _array(ctx, t, name: str, dtype, shape) -> int | None:
     """Pointer of a dense device array (or None)."""
     if t is None:

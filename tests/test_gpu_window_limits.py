@@ -50,3 +50,95 @@ def test_attend_counts_what_a_sink_dominates(qwm, nq, heads, bits, gap, sink, ot
     rel = 2.0 ** -11 + 2.0 ** -20 + gap * 2.0 ** -22 + n / 64 * 2.0 ** -24 + n / 16 * 2.0 ** -23
     assert float((out.double() - want).abs().max()) <= size * rel + n * 2.0 ** -32
     assert float((lse.double() - gap - math.log2(1 + share)).abs().max()) <= math.log2(math.e) * n / 64 * 2.0 ** -24 + gap * 2.0 ** -22 + 2.0 ** -20
+
+
+# ------------------------------------------------------------------ the layer
+
+def tiny_stream(n, steps, heads=2):
+    import synth
+    from helpers import from_u16
+    keys, vals = synth.keys(synth.TINY), synth.values(synth.TINY)
+    cut = lambda x, t: from_u16(np.ascontiguousarray(x[:, (t * n) % 1024:(t * n) % 1024 + n]), torch.bfloat16)
+    return [(cut(keys, t), cut(vals, t), from_u16(synth.queries(synth.TINY, t, n), torch.bfloat16)) for t in range(steps)]
+
+
+def state_of(layer):
+    """What a layer holds, without the slots of the chunk that was not added."""
+    return [layer.length, len(layer.packed.chunks), layer.packed.n_seen, layer.packed.S.clone(), layer.packed.n.clone(), layer.packed.w.clone()]
+
+
+def same_state(a, b):
+    return all(torch.equal(x, y) if isinstance(x, torch.Tensor) else x == y for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("rope", [False, True])
+def test_layer_takes_queries_of_any_strides(qwm, rope):
+    from bit_kv_cache_qsac_gb300 import stream
+    n, ctx = 256, qwm.Context(heads=2, n_centroids=64)
+    spec = qwm.RopeSpec((44, 42, 42), grid=(16, 16)) if rope else None
+    a, b = (stream.WindowedLayer(ctx, n, 2, tpf=64, rope=spec) for _ in range(2))
+    for k, v, q in tiny_stream(n, 4):
+        major = lambda t: t.transpose(0, 1).contiguous().transpose(0, 1)   # as a projection leaves it
+        assert torch.equal(a.step(k, v, q), b.step(major(k), major(v), major(q)))
+    assert same_state(state_of(a), state_of(b)) and a.check() == 0
+
+
+def refused(k, v, q):
+    """Steps that must be refused, one wrong operand each."""
+    half = lambda t: t.to(torch.float16)
+    every_other = lambda t: torch.zeros(*t.shape[:2], 256, dtype=t.dtype, device=t.device)[..., ::2]
+    odd = lambda t: torch.zeros(t.shape[0], t.shape[1], 132, dtype=t.dtype, device=t.device)[..., :128]
+    off = lambda t: torch.zeros(t.numel() + 8, dtype=t.dtype, device=t.device)[4:4 + t.numel()].view(t.shape)
+    for bad in (half, every_other, odd, off, lambda t: t.cpu(), lambda t: t[:1], lambda t: t[..., :64], lambda t: t[0], lambda t: None):
+        yield bad(k), v, q
+        yield k, bad(v), q
+        yield k, v, bad(q)
+    yield k[:, :-1], v, q
+    yield k, v[:, :-1], q
+    yield k, v, torch.cat([q, q], 1)
+
+
+@pytest.mark.parametrize("rope", [False, True])
+def test_layer_refused_steps_change_nothing(qwm, rope):
+    from bit_kv_cache_qsac_gb300 import stream
+    n, ctx = 256, qwm.Context(heads=2, n_centroids=64)
+    spec = qwm.RopeSpec((44, 42, 42), grid=(16, 16)) if rope else None
+    a, b = (stream.WindowedLayer(ctx, n, 2, tpf=64, rope=spec) for _ in range(2))
+    for k, v, q in tiny_stream(n, 4):   # with room in the window, with a full one, over a packed history
+        before = state_of(b) + [b.window.k_codes.clone(), b.window.v_codes.clone()]
+        for args in refused(k, v, q):
+            with pytest.raises((TypeError, ValueError)):
+                b.step(*args)
+        assert same_state(before, state_of(b) + [b.window.k_codes, b.window.v_codes])
+        assert torch.equal(a.step(k, v, q), b.step(k, v, q))
+    assert same_state(state_of(a), state_of(b))
+
+
+@pytest.mark.parametrize("call", ["qwm_window_read", "qwm_fit_centroids_kv", "qwm_quantize_kv", "qwm_window_write", "qwm_rope",
+                                  "qwm_attend_merge", "qwm_window_attend", "qwm_update_query_stats"])
+def test_layer_repeats_a_step_that_failed_half_way(qwm, call, monkeypatch):
+    """Whichever call of a step reports an error, the step may be made again, and the layer goes on as if
+    it had succeeded at once."""
+    from bit_kv_cache_qsac_gb300 import stream
+    n, ctx = 256, qwm.Context(heads=2, n_centroids=64)
+    spec = qwm.RopeSpec((44, 42, 42), grid=(16, 16))
+    a, b = (stream.WindowedLayer(ctx, n, 2, tpf=64, rope=spec) for _ in range(2))
+    real, failed = getattr(stream, call), 0
+    for k, v, q in tiny_stream(n, 5):
+        want = a.step(k, v, q)
+
+        def fails(*args, **kw):
+            raise qwm.QwmError(qwm.QWM_ERR_CUDA, call)
+        monkeypatch.setattr(stream, call, fails)
+        length = b.length
+        try:
+            got = b.step(k, v, q)
+        except qwm.QwmError:
+            failed += 1
+            assert b.length == length
+            monkeypatch.setattr(stream, call, real)
+            got = b.step(k, v, q)
+        monkeypatch.setattr(stream, call, real)
+        assert torch.equal(got, want)
+        assert same_state(state_of(a), state_of(b))
+    assert failed >= 3
