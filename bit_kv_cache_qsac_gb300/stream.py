@@ -214,6 +214,20 @@ class WindowedLayer:
         self.window = Window.empty(bits, 1, ctx.heads, 0, window_chunks * chunk_tokens, self.packed.device)
         self.length = 0    # tokens seen
         self._packed = 0   # tokens of them that have left the window
+        # what the layer owns was filled on this stream; a step on another one waits for the event
+        self._stream = torch.cuda.current_stream(self.packed.device)
+        self._done = self._stream.record_event()
+
+    def _follow(self, main) -> None:
+        """Let `main` take over from the stream that the layer was built or last stepped on."""
+        if main == self._stream:
+            return
+        main.wait_event(self._done)
+        for owner in (self.window, self.packed, *self.packed.chunks):
+            for t in vars(owner).values():
+                if isinstance(t, torch.Tensor):   # not handed out again before `main` is done with it
+                    t.record_stream(main)
+        self._stream = main
 
     def step(self, k: torch.Tensor, v: torch.Tensor, q: torch.Tensor, stream=None) -> torch.Tensor:
         """Add the chunk k, v [H][chunk_tokens][d] and attend with its Queries q [H][nq][d] (row i is token
@@ -230,30 +244,37 @@ class WindowedLayer:
             check_rows(ctx, t[None], name, (1, ctx.heads, m, ctx.cfg.head_dim))
         main = stream if stream is not None else torch.cuda.current_stream(self.packed.device)
         with torch.cuda.stream(main):
-            # where the chunk that makes room began, where this one does, and the length after it
-            at = torch.arange(self.length - ring, self.length + n + 1, n, dtype=torch.int64, device=k.device)
-            oldest, begin, length = at[:1], at[-2:-1], at[-1:]
-            if self.length - self._packed >= ring:   # the oldest chunk makes room: read back and packed
-                old = [torch.empty(1, H, n, d, dtype=torch.bfloat16, device=k.device) for _ in range(2)]
-                qwm_window_read(ctx, self.window, oldest, begin, *old, stream=main)
-                self.packed.append_chunk(old[0][0], old[1][0], stream=main)
-                self._packed += n
-            qwm_window_write(ctx, self.window, k[None], v[None], begin, rope=self.rope, stream=main)
-            if self.rope is not None:
-                turned = torch.empty(H, nq, d, dtype=torch.bfloat16, device=q.device)
-                qwm_rope(ctx, self.rope, q[None], begin, turned[None], stream=main)
-                q = turned
-            else:
-                q = q.contiguous()   # as the calls of the packed path take them
-            out = torch.empty(H, nq, d, dtype=torch.float32, device=q.device)
-            lse = torch.empty(H, nq, dtype=torch.float32, device=q.device)
-            scale = 1.0 / math.sqrt(d)
-            if self.packed.chunks:
-                qwm_attend_merge(ctx, q, nq, self.packed.chunks, scale, out, lse, False, main)
-            # the window holds exactly the chunks that are not packed: every frame of it is recent
-            qwm_window_attend(ctx, self.window, q[None], begin, length, self.tpf, ring // self.tpf + 2, scale,
-                              out[None], lse=lse[None], merge=bool(self.packed.chunks), stream=main)
-            self.packed.fold_queries(q, main)
+            eager = not torch.cuda.is_current_stream_capturing()   # who replays a captured step orders the replays
+            if eager:
+                self._follow(main)
+            try:
+                # where the chunk that makes room began, where this one does, and the length after it
+                at = torch.arange(self.length - ring, self.length + n + 1, n, dtype=torch.int64, device=k.device)
+                oldest, begin, length = at[:1], at[-2:-1], at[-1:]
+                if self.length - self._packed >= ring:   # the oldest chunk makes room: read back and packed
+                    old = [torch.empty(1, H, n, d, dtype=torch.bfloat16, device=k.device) for _ in range(2)]
+                    qwm_window_read(ctx, self.window, oldest, begin, *old, stream=main)
+                    self.packed.append_chunk(old[0][0], old[1][0], stream=main)
+                    self._packed += n
+                qwm_window_write(ctx, self.window, k[None], v[None], begin, rope=self.rope, stream=main)
+                if self.rope is not None:
+                    turned = torch.empty(H, nq, d, dtype=torch.bfloat16, device=q.device)
+                    qwm_rope(ctx, self.rope, q[None], begin, turned[None], stream=main)
+                    q = turned
+                else:
+                    q = q.contiguous()   # as the calls of the packed path take them
+                out = torch.empty(H, nq, d, dtype=torch.float32, device=q.device)
+                lse = torch.empty(H, nq, dtype=torch.float32, device=q.device)
+                scale = 1.0 / math.sqrt(d)
+                if self.packed.chunks:
+                    qwm_attend_merge(ctx, q, nq, self.packed.chunks, scale, out, lse, False, main)
+                # the window holds exactly the chunks that are not packed: every frame of it is recent
+                qwm_window_attend(ctx, self.window, q[None], begin, length, self.tpf, ring // self.tpf + 2, scale,
+                                  out[None], lse=lse[None], merge=bool(self.packed.chunks), stream=main)
+                self.packed.fold_queries(q, main)
+            finally:   # what was issued before an error too is waited for
+                if eager:
+                    self._done.record(main)
             self.length += n
         return out
 

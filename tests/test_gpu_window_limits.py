@@ -142,3 +142,54 @@ def test_layer_repeats_a_step_that_failed_half_way(qwm, call, monkeypatch):
         assert torch.equal(got, want)
         assert same_state(state_of(a), state_of(b))
     assert failed >= 3
+
+
+@pytest.mark.parametrize("fails", [False, True])
+def test_layer_on_other_streams_than_its_own(qwm, fails, monkeypatch):
+    """Built behind work on one stream, stepped on others in turn (after a step that failed on the one, on
+    the other): every step waits for what it needs."""
+    from bit_kv_cache_qsac_gb300 import stream
+    n, ctx = 256, qwm.Context(heads=2, n_centroids=64)
+    data = tiny_stream(n, 6)
+    plain = stream.WindowedLayer(ctx, n, 2, tpf=64)
+    want = [plain.step(*d) for d in data]
+    busy, others = torch.cuda.Stream(), [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(busy):
+        torch.cuda._sleep(20_000_000)   # about 10 ms before the layer's tensors are filled
+        layer = stream.WindowedLayer(ctx, n, 2, tpf=64)
+
+    def broken(*args, **kw):
+        raise qwm.QwmError(qwm.QWM_ERR_CUDA, "qwm_window_attend")
+    got = []
+    for i, d in enumerate(data):
+        for s in others:
+            with torch.cuda.stream(s):
+                torch.cuda._sleep(2_000_000 * (1 + i % 2))
+        if fails:
+            with monkeypatch.context() as m, pytest.raises(qwm.QwmError):
+                m.setattr(stream, "qwm_window_attend", broken)
+                layer.step(*d, stream=others[i % 2])
+        got.append(layer.step(*d, stream=others[(i + fails) % 2]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+def test_layer_step_captured_in_a_graph(qwm):
+    """A step with room in the window captured on a stream of its own and replayed with other operands."""
+    from bit_kv_cache_qsac_gb300 import stream
+    n, ctx = 256, qwm.Context(heads=2, n_centroids=64)
+    (k0, v0, q0), (k1, v1, q1) = tiny_stream(n, 2)
+    plain, layer = (stream.WindowedLayer(ctx, n, 2, tpf=64) for _ in range(2))
+    plain.step(k0, v0, q0), layer.step(k0, v0, q0)
+    want = plain.step(k1, v1, q1)
+    k, v, q = k0.clone(), v0.clone(), q0.clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = layer.step(k, v, q)
+    k.copy_(k1), v.copy_(v1), q.copy_(q1)
+    graph.replay()
+    assert torch.equal(out, want) and torch.equal(layer.window.k_codes, plain.window.k_codes)
+    torch.cuda.synchronize()
+    assert layer.length == 2 * n and torch.equal(layer.packed.S, plain.packed.S)
