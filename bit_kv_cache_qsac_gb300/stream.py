@@ -20,6 +20,8 @@ from . import (ActiveChunk, Chunk, Context, Window, pack_psac_layout, qwm_attend
                qwm_update_query_stats, qwm_window_attend, qwm_window_read, qwm_window_write)
 from .window import check_rows
 
+_MAX_CHUNKS = 128   # chunks that one call of qwm_attend or qwm_attend_merge takes
+
 
 class CompressedLayer:
     """Running state of one layer: Query statistics, basis, packed chunks, last codebooks."""
@@ -266,8 +268,8 @@ class WindowedLayer:
                 out = torch.empty(H, nq, d, dtype=torch.float32, device=q.device)
                 lse = torch.empty(H, nq, dtype=torch.float32, device=q.device)
                 scale = 1.0 / math.sqrt(d)
-                if self.packed.chunks:
-                    qwm_attend_merge(ctx, q, nq, self.packed.chunks, scale, out, lse, False, main)
+                for i in range(0, len(self.packed.chunks), _MAX_CHUNKS):
+                    qwm_attend_merge(ctx, q, nq, self.packed.chunks[i:i + _MAX_CHUNKS], scale, out, lse, i > 0, main)
                 # the window holds exactly the chunks that are not packed: every frame of it is recent
                 qwm_window_attend(ctx, self.window, q[None], begin, length, self.tpf, ring // self.tpf + 2, scale,
                                   out[None], lse=lse[None], merge=bool(self.packed.chunks), stream=main)

@@ -144,6 +144,32 @@ def test_layer_repeats_a_step_that_failed_half_way(qwm, call, monkeypatch):
     assert failed >= 3
 
 
+def test_layer_over_more_chunks_than_one_call_takes(qwm):
+    """qwm_attend_merge takes 128 chunks; the layer's history may be longer."""
+    from bit_kv_cache_qsac_gb300 import stream
+    n, H, ctx = 64, 2, qwm.Context(heads=2, n_centroids=64, kmeans_iters=1)
+    layer = stream.WindowedLayer(ctx, n, 1)
+    data = tiny_stream(n, 132)
+    for k, v, q in data:
+        out = layer.step(k, v, q)
+    assert len(layer.packed.chunks) == 131 and layer.check() == 0
+    # the same by hand: every chunk's part, joined by the log-sum-exps in 64 bits
+    parts = []
+    for c in layer.packed.chunks:
+        o, s = torch.empty(H, n, 128, device="cuda"), torch.empty(H, n, device="cuda")
+        qwm.qwm_attend_merge(ctx, q, n, [c], SCALE, o, s, False)
+        parts.append((o.double(), s.double()))
+    o, s = torch.empty(1, H, n, 128, device="cuda"), torch.empty(1, H, n, device="cuda")
+    qwm.qwm_window_attend(ctx, layer.window, q[None], ints([131 * n]), ints([132 * n]), n, 3, SCALE, o, lse=s)
+    parts.append((o[0].double(), s[0].double()))
+    top = torch.stack([s for _, s in parts]).amax(0)
+    w = [torch.exp2(s - top)[..., None] for _, s in parts]
+    want = sum(x * y for x, (y, _) in zip(w, parts)) / sum(w)
+    # the weights' fp16 rounding in every part (2^-11 each, on numerator and denominator), against |V| within
+    # the attention's bar
+    assert float((out.double() - want).abs().max() / want.pow(2).mean().sqrt()) <= 2e-2
+
+
 @pytest.mark.parametrize("fails", [False, True])
 def test_layer_on_other_streams_than_its_own(qwm, fails, monkeypatch):
     """Built behind work on one stream, stepped on others in turn (after a step that failed on the one, on
