@@ -13,23 +13,16 @@ namespace {
 
 constexpr int kThreads = 256, kRows = kThreads / 16, kReadRows = kThreads / 8;
 
-// The larger magnitude of each half (a NaN stays one); its sign means nothing.
-__device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-
 // Eight bf16 channels of a row (4 words) -> this lane's code bytes (8 bits: c0, c1; 4 bits: c0) and the
 // group's step byte.  Every lane of the warp takes part.
 template <int BITS>
 __device__ __forceinline__ void quantise(const uint32_t (&w)[4], uint32_t &c0, uint32_t &c1, uint32_t &step,
                                          bool &bad) {
   constexpr float kTop = win::code_max(BITS) * (BITS == 8 ? 56.f : 896.f);
-  uint32_t m = max_abs_bf16x2(max_abs_bf16x2(w[0], w[1]), max_abs_bf16x2(w[2], w[3]));
-  m = max_abs_bf16x2(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  m = max_abs_bf16x2(m, __shfl_xor_sync(0xffffffffu, m, 2));
-  m = max_abs_bf16x2(m, m >> 16);
+  uint32_t m = win::max_abs_bf16x2(win::max_abs_bf16x2(w[0], w[1]), win::max_abs_bf16x2(w[2], w[3]));
+  m = win::max_abs_bf16x2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = win::max_abs_bf16x2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  m = win::max_abs_bf16x2(m, m >> 16);
   float amax = __uint_as_float((m & 0x7FFFu) << 16), f[8], s;
 #pragma unroll
   for (int i = 0; i < 4; i++) {

@@ -26,6 +26,13 @@ __device__ __forceinline__ float2 split2(uint64_t v) {
   return f;
 }
 
+// The larger magnitude of each half (a NaN stays one); its sign means nothing.
+__device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
 // ------------------------------------------------------------------ rotary positions
 
 // Cosine and sine of an angle given as pos * turn / 2^64 turns, each as an unevaluated sum hi + lo.
@@ -301,6 +308,20 @@ __device__ __forceinline__ void decode4(uint32_t x, const Step &st, const Bases 
   p[2] = tc::hfma2(place<0x000F000Fu>(y, c.k1024), st.s, st.nl);
   p[3] = tc::hfma2(place<0x00F000F0u>(y, c.k64), st.s, st.n);
 }
+
+// ------------------------------------------------------------------ Queries
+
+// Queries enter the first product in fp16: a bf16 value of 2^-17 to 65504 is exact, smaller ones are rounded to
+// multiples of 2^-24.  A row whose largest magnitude is below 1 is first multiplied by a power of two that
+// brings it to 2^14 .. 2^15 (2^120 at most), which its logits' scale takes back; so what rounding there is
+// stays below 2^-25 of the row's largest element, under the fp32 rounding of its logits.
+// The tests of packed magnitudes m (bf16 without signs, in both halves):
+__device__ __forceinline__ bool any_from_one(uint32_t m) { return ((m + 0x40804080u) & 0x80008000u) != 0u; }       // 1 or more
+__device__ __forceinline__ bool any_beyond_fp16(uint32_t m) { return ((m + 0x38803880u) & 0x80008000u) != 0u; }   // 2^16 or more, or a NaN
+// The power of two that a row of largest magnitude `top` (bf16, below 1) is multiplied by, and 2^k.
+__device__ __forceinline__ uint32_t row_power(uint32_t top) { return 141u - (top >> 7) < 120u ? 141u - (top >> 7) : 120u; }
+__device__ __forceinline__ float power_of_two(int k) { return __uint_as_float((uint32_t)(127 + k) << 23); }
+__device__ __forceinline__ uint32_t larger_half(uint32_t m) { return (m & 0xFFFFu) > (m >> 16) ? m & 0xFFFFu : m >> 16; }
 
 // ------------------------------------------------------------------ weights
 

@@ -2,7 +2,7 @@
 //
 //   l_ij = scale q_i . k_hat_j over the keys row i sees, o_i = softmax(l_i) V_hat, with k_hat and v_hat
 // decoded from the 8- or 4-bit cache inside the kernel.  A cached value is exact in fp16 and so is a
-// bf16 Query in the fp16 range (2^-17 to 65504), so the logits carry only fp32 rounding; the weights
+// bf16 Query, or next to it (see win::row_power), so the logits carry only fp32 rounding; the weights
 // enter the second product in fp16, the largest as 2^7 (win::kTopWeight).
 //
 // Work split: a pair of CTAs (a cluster of two, cta_group::2 MMAs) takes one Key head x 512 Query rows
@@ -53,7 +53,10 @@ constexpr int kBlkH = 64 * 128;            // a [64 rows][64 fp16] swizzled bloc
 constexpr int OFF_Q = 0;                   // 2 Query tiles x 2 blocks (channels 0-63, 64-127)
 constexpr int OFF_K = OFF_Q + NQT * 2 * kBlk;          // stages x 2 blocks [64 keys][64 ch]
 constexpr int OFF_V = OFF_K + kStages * 2 * kBlkH;     // stages x [128 keys][64 ch] (MN-major B)
-constexpr int kSmemBytes = OFF_V + kStages * kBlk;
+// the power of two that each Query row was multiplied by, 32 bits each.  (As a static array, whichever way it was
+// read, a step of the loop took 2,000 cycles instead of 1,260; why is not known.)
+constexpr int OFF_POWER = OFF_V + kStages * kBlk;
+constexpr int kSmemBytes = OFF_POWER + NQT * BM * 4;
 constexpr int kSmemAlloc = kSmemBytes + 1024;
 
 template <bool B>
@@ -75,11 +78,6 @@ __device__ __forceinline__ uint64_t pk64(uint32_t lo, uint32_t hi) {
   return d;
 }
 __device__ __forceinline__ uint64_t pk64(float lo, float hi) { return pk64(__float_as_uint(lo), __float_as_uint(hi)); }
-__device__ __forceinline__ uint32_t max_f16x2(uint32_t a, uint32_t b) {   // a NaN stays one
-  uint32_t d;
-  asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
 // The lowest n bits set (n clamped to 0..32).
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u); }
 
@@ -331,10 +329,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // other step of 64 keys each, and are joined at the end: two chains of MMA and softmax instead of one.
   const bool brief = pair0 + 2 * BM >= rows;
 
+  const uint32_t powers = tc::smem_u32(sm) + OFF_POWER;
   // ---- the Queries, which have arrived by now: bf16 -> fp16 in place, padding rows 0 ----
   if (warp < kSoftmaxWarps) {
+    // this warp's rows: two in each of 16 passes, pass 8 x + k those of tile x from 16 k on
+    tc::sts32(powers + 4u * (uint32_t)((lane >> 1) * 16 + (tid >> 5) * 2 + (lane & 1)), 0u);
     tc::cp_async_wait<0>();
-    uint32_t top = 0u;   // the largest magnitudes, a NaN above all
+    uint32_t top = 0u, small = 0u;   // the largest magnitudes, a NaN above all; passes in which this piece is below 1
 #pragma unroll 1
     for (int x = 0; x < NQT; x++) {
       const int64_t r = row_base + (int64_t)x * 2 * BM + (tid >> 4);
@@ -343,17 +344,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll 4
       for (int k = 0; k < BM / 16; k++) {
         const uint4 v = tc::lds128(at + (uint32_t)k * 2048u);
-        const uint32_t bw[4] = {v.x, v.y, v.z, v.w};
+        const bool live = 16 * k < left;
+        const uint32_t w[4] = {live ? v.x : 0u, live ? v.y : 0u, live ? v.z : 0u, live ? v.w : 0u};
         uint32_t hw[4];
 #pragma unroll
-        for (int u = 0; u < 4; u++) {
-          hw[u] = 16 * k < left ? tc::pack_f16x2(__uint_as_float(bw[u] << 16), __uint_as_float(bw[u] & 0xFFFF0000u)) : 0u;
-          top = max_f16x2(top, hw[u] & 0x7FFF7FFFu);
-        }
+        for (int u = 0; u < 4; u++) hw[u] = tc::pack_f16x2(__uint_as_float(w[u] << 16), __uint_as_float(w[u] & 0xFFFF0000u));
         tc::sts128(at + (uint32_t)k * 2048u, make_uint4(hw[0], hw[1], hw[2], hw[3]));
+        const uint32_t m = win::max_abs_bf16x2(win::max_abs_bf16x2(w[0], w[1]), win::max_abs_bf16x2(w[2], w[3])) & 0x7FFF7FFFu;
+        top = win::max_abs_bf16x2(top, m);
+        small |= win::any_from_one(m) || !live ? 0u : 1u << (8 * x + k);
       }
     }
-    if ((top & 0x7C00u) == 0x7C00u || (top & 0x7C000000u) == 0x7C000000u) qwm_dev_error(a.status, QWM_ERR_RANGE);
+    if (win::any_beyond_fp16(top & 0x7FFF7FFFu)) qwm_dev_error(a.status, QWM_ERR_RANGE);
+#pragma unroll
+    for (int d = 1; d < 16; d <<= 1) small &= __shfl_xor_sync(0xffffffffu, small, d);   // of the whole row
+    __syncwarp();
+    for (uint32_t again = small | __shfl_xor_sync(0xffffffffu, small, 16); again; again &= again - 1u) {   // fetched once more
+      const int pass = __ffs((int)again) - 1, x = pass >> 3, k = pass & 7;
+      const bool mine = (small >> pass) & 1u;
+      const int64_t r = row_base + (int64_t)x * 2 * BM + 16 * k + (tid >> 4), i = win::quotient(r, a.group);
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (mine) v = *(const uint4 *)(a.q + b * a.qs.batch + (kvh * a.group + (r - i * a.group)) * a.qs.head + i * a.qs.token + 8 * (tid & 15));
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      uint32_t m = win::max_abs_bf16x2(win::max_abs_bf16x2(w[0], w[1]), win::max_abs_bf16x2(w[2], w[3])) & 0x7FFF7FFFu;
+      m = win::larger_half(m);
+#pragma unroll
+      for (int d = 1; d < 16; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+      if (!mine) continue;
+      const uint32_t power = win::row_power(m);
+      const float up = win::power_of_two((int)power);
+      uint32_t hw[4];
+#pragma unroll
+      for (int u = 0; u < 4; u++) hw[u] = tc::pack_f16x2(__uint_as_float(w[u] << 16) * up, __uint_as_float(w[u] & 0xFFFF0000u) * up);
+      tc::sts128(q_dst + (uint32_t)x * 2u * kBlk + (uint32_t)k * 2048u, make_uint4(hw[0], hw[1], hw[2], hw[3]));
+      if ((tid & 15) == 0) tc::sts32(powers + 4u * (uint32_t)(pass * 16 + (tid >> 4)), power);
+    }
     tc::fence_proxy_async_smem();
   }
   // (once per role, so that the producers' first codes may be on their way before it)
@@ -370,11 +395,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ======================= softmax (Query tile x, row = TMEM lane) =======================
     const uint32_t tmem = joined();
     if (lane == 0) tc::mbar_arrive_remote(tc::mapa(tc::smem_u32(&bars.q_full), 0));
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * kSoftmaxWarps) : "memory");   // the rows' powers
     const int x = warp / 4, sub = warp % 4;
     const uint32_t lane_addr = (uint32_t)(32 * sub) << 16;
     const uint32_t tS0 = tmem + lane_addr + 128u * x, tO = tmem + lane_addr + 256u + 128u * x;
     const uint32_t p_ready0 = tc::mapa(tc::smem_u32(&bars.p_ready[x][0]), 0);
-    const float sl2 = a.scale_log2 * win::kUnit<BITS>;
+    const int power = (int)tc::lds32(powers + 4u * (uint32_t)((brief ? 0 : x * BM) + 32 * sub + lane));
+    const float sl2 = a.scale_log2 * win::power_of_two(-power) * win::kUnit<BITS>;
     const uint64_t sc2 = pk64(sl2, sl2);
     const int64_t w0 = row_base + (brief ? 0 : (int64_t)x * 2 * BM) + 32 * sub;   // this warp's first row
     const int mine_n = brief ? (steps + 1 - x) >> 1 : steps;   // steps of this tile

@@ -220,18 +220,43 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) window_decode_kerne
 
   win::Everyone every;
   every.init(seq, keys, f0, f1);
-  bool bad = false;
+  // ---- the Queries to fp16; each row's logit scale ----
+  float sl2[NT][2];   // of rows 2 t, 2 t + 1 of every 8
 #pragma unroll
-  for (int nt = 0; nt < NT; nt++)
+  for (int nt = 0; nt < NT; nt++) {
+    const bool live = 8 * nt + g < rows;
+    uint32_t big = 0u;   // largest magnitudes of this thread's quarter of row g
 #pragma unroll
     for (int ks = 0; ks < 8; ks++)
 #pragma unroll
       for (int e = 0; e < 2; e++) {
-        const uint32_t w = 8 * nt + g < rows ? qf[nt][ks][e] : 0u;
-        qf[nt][ks][e] = tc::pack_f16x2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-        bad |= (qf[nt][ks][e] & 0x7C00u) == 0x7C00u || (qf[nt][ks][e] & 0x7C000000u) == 0x7C000000u;
+        qf[nt][ks][e] = live ? qf[nt][ks][e] : 0u;
+        big = win::max_abs_bf16x2(big, qf[nt][ks][e]);
       }
-  if (bad) qwm_dev_error(a.status, QWM_ERR_RANGE);
+    big &= 0x7FFF7FFFu;
+    if (win::any_beyond_fp16(big)) qwm_dev_error(a.status, QWM_ERR_RANGE);
+    uint32_t whole = __ballot_sync(0xffffffffu, !live || win::any_from_one(big));   // four bits a row
+    whole |= whole >> 1;
+    whole |= whole >> 2;
+    int power = 0;
+    if ((whole & 0x11111111u) != 0x11111111u) {   // a row of small Queries
+      uint32_t top = win::larger_half(big);
+#pragma unroll
+      for (int d = 1; d < 4; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+      if (top < 0x3F80u) power = (int)win::row_power(top);
+    }
+    const float up = win::power_of_two(power), back = win::power_of_two(-power);
+#pragma unroll
+    for (int ks = 0; ks < 8; ks++)
+#pragma unroll
+      for (int e = 0; e < 2; e++) {
+        const uint32_t w = qf[nt][ks][e];
+        qf[nt][ks][e] = tc::pack_f16x2(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xFFFF0000u) * up);
+      }
+#pragma unroll
+    for (int e = 0; e < 2; e++)
+      sl2[nt][e] = a.scale_log2 * __shfl_sync(0xffffffffu, back, 4 * (2 * t + e)) * win::kUnit<BITS>;
+  }
 
   float o[NT][8][4], m[NT][2], mneg[NT][2], l[NT][2];
 #pragma unroll
@@ -245,7 +270,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) window_decode_kerne
     l[nt][0] = l[nt][1] = 0.f;
   }
   const int krow = 4 * (g >> 1) + (g & 1);   // the key of MMA row g; row g + 8 is two further on
-  const float sl2 = a.scale_log2 * win::kUnit<BITS>;
   // the step byte of the thread's group, of one row or of two
   const uint32_t ksel = BITS == 8 ? (uint32_t)(t >> 1) * 0x1111u : (uint32_t)t * 0x1111u;
   const uint32_t vsel = (uint32_t)(g >> 1) * 0x1111u + 0x4400u;
@@ -340,8 +364,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) window_decode_kerne
         x0 = tc::max3(x0, s[u16][nt][0], s[u16][nt][2]);
         x1 = tc::max3(x1, s[u16][nt][1], s[u16][nt][3]);
       }
-      x0 = fmaf(x0, sl2, -win::kTopWeight);
-      x1 = fmaf(x1, sl2, -win::kTopWeight);
+      x0 = fmaf(x0, sl2[nt][0], -win::kTopWeight);
+      x1 = fmaf(x1, sl2[nt][1], -win::kTopWeight);
       if (__any_sync(0xffffffffu, x0 > m[nt][0] + kRescale || x1 > m[nt][1] + kRescale)) {
         float n0 = x0, n1 = x1;
 #pragma unroll
@@ -371,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) window_decode_kerne
       for (int u16 = 0; u16 < kSub; u16++) {
         float p[4];
 #pragma unroll
-        for (int e = 0; e < 4; e++) p[e] = tc::ex2_approx(fmaf(s[u16][nt][e], sl2, mneg[nt][e & 1]));
+        for (int e = 0; e < 4; e++) p[e] = tc::ex2_approx(fmaf(s[u16][nt][e], sl2[nt][e & 1], mneg[nt][e & 1]));
         l[nt][0] += p[0] + p[2];
         l[nt][1] += p[1] + p[3];
         pb[u16][nt][0] = transpose8x8(tc::pack_f16x2(p[0], p[1]));

@@ -139,7 +139,8 @@ QWM_API qwm_status qwm_window_read(qwm_ctx *ctx, const qwm_window *win, const in
  *   ws       workspace of qwm_window_attend_workspace bytes (may be NULL when that is 0), free again
  *            when the call's work on the stream is done
  * A row that sees no key gets out = 0 and lse = -inf (merge: stays as it was).  Logits, maxima, sums and
- * the output are accumulated in fp32; the weights enter the second product in fp16: rounded by at most 2^-11 of
+ * the output are accumulated in fp32.  Queries enter the first product off by at most 2^-25 of their row's largest
+ * element, whatever its magnitude; the weights enter the second product in fp16, rounded by at most 2^-11 of
  * their value or 2^-32 of the largest weight, whichever is more. */
 QWM_API qwm_status qwm_window_attend(qwm_ctx *ctx, const qwm_window *win, const uint16_t *q, const qwm_strides *qs,
                                      int64_t nq, const int64_t *q_start, const int64_t *length,

@@ -52,6 +52,28 @@ def test_attend_counts_what_a_sink_dominates(qwm, nq, heads, bits, gap, sink, ot
     assert float((lse.double() - gap - math.log2(1 + share)).abs().max()) <= math.log2(math.e) * n / 64 * 2.0 ** -24 + gap * 2.0 ** -22 + 2.0 ** -20
 
 
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("H,kv,nq,length", [(2, 2, 1, 300), (6, 2, 4, 300), (2, 2, 30, 9000), (2, 1, 40, 300), (2, 2, 300, 200), (1, 1, 600, 300)])
+def test_attend_queries_of_any_magnitude(qwm, H, kv, nq, length, bits):
+    """Rows from 2^-133 to 2^12 beside one another, zero rows and rows with a wide range among them: the
+    logits are those of the bf16 Queries within fp32 rounding."""
+    rng = np.random.default_rng(nq + bits)
+    ctx, win = ctx_of(qwm, H), fill(qwm, ctx_of(qwm, H), rng, bits, kv, 3, length, [length])
+    q = rows(rng, 1, H, nq, "token")
+    power = torch.tensor([0, -22, -30, 12, -1, -60, 3, -126], device="cuda")[torch.arange(H * nq, device="cuda") % 8]
+    q.copy_((q.double() * torch.exp2(power.double()).reshape(1, H, nq, 1)).to(torch.bfloat16))
+    if nq > 3:
+        q[:, :, 2] = 0
+        q[:, :, 3, ::2] *= 2.0 ** -15
+    out = torch.empty(1, H, nq, 128, dtype=torch.float32, device="cuda")
+    lse = torch.empty(1, H, nq, dtype=torch.float32, device="cuda")
+    for scale in (SCALE * 2.0 ** -10, SCALE * 2.0 ** 22):
+        use = q if scale < 1 else (q.double() * torch.where(power >= -1, 2.0 ** -24, 1.0).double().reshape(1, H, nq, 1)).to(torch.bfloat16)
+        qwm.qwm_window_attend(ctx, win, use, ints([length]), ints([length]), 1, length, scale, out, lse=lse)
+        assert qwm.qwm_sync_status(ctx) == 0
+        check_attention(win, use, [length], [length], 1, length, scale, out, lse, out_eps=2.0 ** -22)
+
+
 # ------------------------------------------------------------------ the layer
 
 def tiny_stream(n, steps, heads=2):
