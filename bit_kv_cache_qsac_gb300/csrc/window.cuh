@@ -76,12 +76,22 @@ __device__ __forceinline__ void rope_sincos(int64_t pos, uint64_t turn, float &c
   sl = sgs * (swap ? cr : sr);
 }
 
+// x, but 2^126 of some sign where it is infinite or not a number: the correction of a product with an infinite
+// channel is inf - inf, and added as it is would make the infinite result a NaN.  (One instruction; looking
+// for such channels with a branch took 2 to 8% of the rotating calls' time, this 1%.)
+__device__ __forceinline__ float finite(float x) {
+  float d;
+  asm("min.xorsign.abs.f32 %0, %1, %2;" : "=f"(d) : "f"(x), "f"(0x1p126f));
+  return d;
+}
+
 // p x + q y for two channels at a time, with x = xh + xl and y = yh + yl: the error of the rounded product
 // q yh is carried (ny = -yh), so each result is within a little over half a unit of fp32.
 __device__ __forceinline__ uint64_t rope_pair(uint64_t p, uint64_t q, uint64_t xh, uint64_t xl, uint64_t yh,
                                               uint64_t yl, uint64_t ny) {
   const uint64_t t = tc::mul2(q, yh), e = tc::fma2(q, yh, tc::mul2(q, ny));
-  return tc::add2(tc::fma2(p, xh, t), tc::fma2(p, xl, tc::fma2(q, yl, e)));
+  const float2 c = split2(tc::fma2(p, xl, tc::fma2(q, yl, e)));
+  return tc::add2(tc::fma2(p, xh, t), pair2(finite(c.x), finite(c.y)));
 }
 
 // The coordinate of position p (>= 0) on one axis of the spec's grid.

@@ -67,7 +67,8 @@ QWM_API qwm_status qwm_rope_plan(const int32_t axis_dim[3], const double theta[3
                                  int32_t shared_freq, int32_t grid_h, int32_t grid_w, int32_t inverse,
                                  qwm_rope_spec *out);
 
-/* out = x turned by its positions, rounded to bf16 (nearest-even).
+/* out = x turned by its positions, rounded to bf16 (nearest-even).  An infinite or NaN channel makes its pair
+ * what a c - b s and a s + b c are in IEEE arithmetic (c, s: cosine and sine), and no other channel.
  *   x, out  bf16 [batch][heads][n][128] by xs and os; out may be x itself (same strides)
  *   start   device int64 [batch]: position of token 0 of each sequence
  *   pos     device int32 [batch][n][3] (t, y, x) to use instead of the grid's, or NULL

@@ -74,6 +74,78 @@ def test_attend_queries_of_any_magnitude(qwm, H, kv, nq, length, bits):
         check_attention(win, use, [length], [length], 1, length, scale, out, lse, out_eps=2.0 ** -22)
 
 
+# ------------------------------------------------------------------ rotary positions
+
+BAD = [(np.inf, 1.0), (1.0, np.inf), (-np.inf, 0.5), (np.inf, np.inf), (np.inf, -np.inf), (-np.inf, -np.inf), (np.nan, 1.0), (2.0, np.nan),
+       (np.inf, np.nan), (3.0e38, 3.0e38), (3.0e38, -3.0e38)]
+
+
+def with_bad_pairs(rng, pairing, R, n):
+    """Rows of noise; row i has the pair BAD[i % len(BAD)] at pair i % (R / 2)."""
+    x = ref.bf16(rng.standard_normal((n, 128)))
+    at = []
+    for i in range(n):
+        j = (7 * i) % (R // 2)
+        at.append((2 * j, 2 * j + 1) if pairing == "interleaved" else (j, j + R // 2))
+        x[i, at[i][0]], x[i, at[i][1]] = BAD[i % len(BAD)]
+    return x, at
+
+
+def same_class(got, want):
+    return (np.isnan(got) and np.isnan(want)) or (np.isinf(want) and got == want) or (np.isfinite(want) and np.isfinite(got))
+
+
+@pytest.mark.parametrize("pairing,dims", [("interleaved", (44, 42, 42)), ("interleaved", (2, 4, 30)), ("half", (128, 0, 0)), ("half", (16, 0, 16))])
+@pytest.mark.parametrize("start", [0, 1234])
+def test_rope_infinite_channels(qwm, pairing, dims, start):
+    """An infinite or NaN channel gives its pair what the formula gives (an angle of 0 has a sine of 0, and 0
+    times infinity is NaN), sums beyond the range are infinite, and no other channel is touched."""
+    kw = dict(dims=dims, theta=100.0, pairing=pairing)
+    rng = np.random.default_rng(3)
+    n = 33
+    x, at = with_bad_pairs(rng, pairing, sum(dims), n)
+    t = torch.from_numpy(x.astype(np.float32)).to(torch.bfloat16).cuda()[None, None]
+    clean = t.clone()
+    for i in range(n):
+        clean[0, 0, i, list(at[i])] = 1.0
+    out, base = torch.empty_like(t), torch.empty_like(t)
+    qwm.qwm_rope(ctx_of(qwm, 1), qwm.RopeSpec(**kw), t, ints([start]), out)
+    qwm.qwm_rope(ctx_of(qwm, 1), qwm.RopeSpec(**kw), clean, ints([start]), base)
+    src = f64(t[0, 0])
+    with np.errstate(invalid="ignore", over="ignore"):
+        want = ref.rope(src, *spec_args(kw), ref.grid_positions(start, n, 1, 1))
+    want = np.where(np.abs(want) >= 2.0 ** 128 * (1 - 2.0 ** -9), np.sign(want) * np.inf, want)
+    got = f64(out[0, 0])
+    for i in range(n):
+        for ch in at[i]:
+            assert same_class(got[i, ch], want[i, ch]), (i, ch, src[i, list(at[i])], got[i, ch], want[i, ch])
+        out[0, 0, i, list(at[i])] = base[0, 0, i, list(at[i])]
+    assert torch.equal(out, base)
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("pairing", ["interleaved", "half"])
+def test_write_cuts_infinite_channels_after_turning(qwm, bits, pairing):
+    kw = dict(dims=(128, 0, 0), theta=100.0, pairing=pairing)
+    top = ref.Q[bits] * ref.STEP_TOP[bits]
+    rng = np.random.default_rng(4)
+    n = 2 * len(BAD)
+    x, at = with_bad_pairs(rng, pairing, 128, n)
+    t = torch.from_numpy(x.astype(np.float32)).to(torch.bfloat16).cuda()[None, None]
+    ctx, win = ctx_of(qwm, 1), qwm.Window.empty(bits, 1, 1, 0, n)
+    qwm.qwm_window_write(ctx, win, t, torch.zeros_like(t), ints([50]), rope=qwm.RopeSpec(**kw))
+    assert qwm.qwm_sync_status(ctx) == qwm.QWM_ERR_RANGE
+    kh, vh = torch.empty_like(t), torch.empty_like(t)
+    qwm.qwm_window_read(ctx, win, ints([50]), ints([50 + n]), kh, vh)
+    with np.errstate(invalid="ignore", over="ignore"):
+        want = ref.rope(f64(t[0, 0]), *spec_args(kw), ref.grid_positions(50, n, 1, 1))
+    want = np.where(np.isnan(want), 0.0, np.clip(want, -top, top))
+    got = f64(kh[0, 0])
+    for i in range(n):
+        for ch in at[i]:
+            assert got[i, ch] == want[i, ch] or abs(got[i, ch] - want[i, ch]) <= 2.0 ** -8 * abs(want[i, ch]), (i, ch, got[i, ch], want[i, ch])
+
+
 # ------------------------------------------------------------------ the layer
 
 def tiny_stream(n, steps, heads=2):
