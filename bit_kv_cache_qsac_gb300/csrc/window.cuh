@@ -38,8 +38,9 @@ __device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
 // Cosine and sine of an angle given as pos * turn / 2^64 turns, each as an unevaluated sum hi + lo.
 // The product is taken modulo 2^64, i.e. modulo a whole turn, in integers: no position is too far.
 // The remainder to the nearest quarter turn, |x| <= pi/4, goes through the Taylor series of sine and
-// cosine with the leading terms kept in two floats; hi + lo is within about 2^-27 of the value, so a
-// rotated channel is rounded to bf16 as the exact one is but for one in some 10^5.
+// cosine with the terms up to x^3 / 6 and x^2 / 2 kept in two floats; hi + lo is within 2^-28 of the value (cosine
+// 2^-28.7, sine 2^-30.2 at most in 60 million angles), so a rotated channel is rounded to bf16 as the exact one is but
+// for one in some 10^5.
 __device__ __forceinline__ void rope_sincos(int64_t pos, uint64_t turn, float &ch, float &cl, float &sh, float &sl) {
   const uint64_t a = (uint64_t)pos * turn;
   const uint32_t quarter = (uint32_t)((a + (1ull << 61)) >> 62);
@@ -52,22 +53,24 @@ __device__ __forceinline__ void rope_sincos(int64_t pos, uint64_t turn, float &c
   constexpr float kTauHi = (float)kTau, kTauLo = (float)(kTau - (double)kTauHi);
   const float x = fh * kTauHi;
   const float xl = fmaf(fh, kTauLo, fmaf(fl, kTauHi, fmaf(fh, kTauHi, -x)));
-  const float z = x * x;
-  const float zl = fmaf(2.f * x, xl, fmaf(x, x, -z));
+  const float z = x * x, zz = fmaf(x, x, -z);        // x^2 exactly
+  const float zl = fmaf(2.f * x, xl, zz);            // z + zl: (x + xl)^2
   float pc = fmaf(z, 1.f / 479001600.f, -1.f / 3628800.f);
   pc = fmaf(pc, z, 1.f / 40320.f);
   pc = fmaf(pc, z, -1.f / 720.f);
   pc = fmaf(pc, z, 1.f / 24.f);
-  const float c0 = 1.f - 0.5f * z;
-  const float c1 = fmaf(z * z, pc, fmaf(-0.5f, zl, (1.f - c0) - 0.5f * z));
+  const float h = 0.5f * z, c0 = 1.f - h;            // zl times -1/2 + z / 12, the slope in z of the terms to z^2
+  const float c1 = fmaf(z * z, pc, fmaf(zl, fmaf(z, 1.f / 12.f, -0.5f), (1.f - c0) - h));
   const float c = c0 + c1, cr = c1 - (c - c0);
   float ps = fmaf(z, 1.f / 6227020800.f, -1.f / 39916800.f);
   ps = fmaf(ps, z, 1.f / 362880.f);
   ps = fmaf(ps, z, -1.f / 5040.f);
   ps = fmaf(ps, z, 1.f / 120.f);
-  ps = fmaf(ps, z, -1.f / 6.f);
-  const float s1 = fmaf(xl, c, x * z * ps);
-  const float s = x + s1, sr = s1 - (s - x);
+  constexpr float kSixth = -1.f / 6.f, kSixthLo = (float)(-1.0 / 6.0 - (double)kSixth);
+  const float u = x * kSixth, ul = fmaf(x, kSixthLo, fmaf(x, kSixth, -u));                   // u + ul = -x / 6
+  const float q = u * z, ql = fmaf(ul, z, fmaf(u, zz, fmaf(u, z, -q)));                      // q + ql = -x^3 / 6
+  const float s0 = x + q, s1 = fmaf(x * z * z, ps, fmaf(xl, c, ql)) + (q - (s0 - x));
+  const float s = s0 + s1, sr = s1 - (s - s0);
   const bool swap = quarter & 1u;
   const float sgc = ((quarter + 1u) & 2u) ? -1.f : 1.f, sgs = (quarter & 2u) ? -1.f : 1.f;
   ch = sgc * (swap ? s : c);

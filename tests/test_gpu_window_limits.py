@@ -76,6 +76,43 @@ def test_attend_queries_of_any_magnitude(qwm, H, kv, nq, length, bits):
 
 # ------------------------------------------------------------------ rotary positions
 
+@pytest.mark.parametrize("pairing", ["interleaved", "half"])
+def test_rope_cosine_and_sine(qwm, pairing):
+    """Rows (a, b) that nearly cancel, a cos = b sin to a few parts in 2^16, show the angles' cosine and sine to
+    2^-28: the result's own roundings (2^-8 to bf16, 2^-23 before) are relative to what is left."""
+    spec = qwm.RopeSpec((128, 0, 0), theta=1000.0, pairing=pairing)
+    n, turn = 4096, np.array(spec.turn[:], np.uint64)
+    start = 77_777
+    whole = (np.arange(start, start + n, dtype=np.uint64)[:, None] * turn)   # modulo 2^64
+    ang = whole.astype(np.longdouble) * (2 * np.arctan2(np.longdouble(0), np.longdouble(-1)) / np.longdouble(2) ** 64)
+    c, s = np.cos(ang), np.sin(ang)
+    small, large = np.abs(s).astype(np.float64), np.abs(c).astype(np.float64)
+    left, best = np.full((n, 64), np.inf), np.zeros((2, n, 64))
+    for m in range(128, 256):   # a of 8 bits, b the nearest of 8 bits to a cos / sin
+        b = ref.bf16(m * large / np.maximum(small, 1e-9))
+        d = np.abs(m * large - b * small) / (m + b)
+        pick = d < left
+        left[pick], best[0][pick], best[1][pick] = d[pick], m, b[pick]
+    a, b = best[0] * np.sign(c).astype(np.float64), best[1] * np.sign(s).astype(np.float64)   # a c - b s cancels
+    at = (np.arange(64) * 2, np.arange(64) * 2 + 1) if pairing == "interleaved" else (np.arange(64), np.arange(64) + 64)
+    x = np.zeros((n, 128))
+    x[:, at[0]], x[:, at[1]] = a, b
+    t = torch.from_numpy(x.astype(np.float32)).to(torch.bfloat16).cuda()[None, None]
+    out = torch.empty_like(t)
+    qwm.qwm_rope(ctx_of(qwm, 1), spec, t, ints([start]), out)
+    want = (a * c - b * s).astype(np.float64)
+    got = f64(out[0, 0])[:, at[0]]
+    pair = np.abs(a) + np.abs(b)
+    assert np.median(np.abs(want) / pair) < 2.0 ** -14   # they do cancel
+    assert np.all(np.abs(got - want) <= (2.0 ** -8 + 2.0 ** -22) * np.abs(want) + 2.0 ** -28 * pair)
+    # the other channel of each pair: a s + b c, with b and a exchanged in sign
+    y = np.zeros((n, 128))
+    y[:, at[0]], y[:, at[1]] = -b, a
+    t = torch.from_numpy(y.astype(np.float32)).to(torch.bfloat16).cuda()[None, None]
+    qwm.qwm_rope(ctx_of(qwm, 1), spec, t, ints([start]), out)
+    assert np.all(np.abs(f64(out[0, 0])[:, at[1]] - want) <= (2.0 ** -8 + 2.0 ** -22) * np.abs(want) + 2.0 ** -28 * pair)
+
+
 BAD = [(np.inf, 1.0), (1.0, np.inf), (-np.inf, 0.5), (np.inf, np.inf), (np.inf, -np.inf), (-np.inf, -np.inf), (np.nan, 1.0), (2.0, np.nan),
        (np.inf, np.nan), (3.0e38, 3.0e38), (3.0e38, -3.0e38)]
 
