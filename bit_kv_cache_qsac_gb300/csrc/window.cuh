@@ -36,7 +36,8 @@ __device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
 // ------------------------------------------------------------------ rotary positions
 
 // Cosine and sine of an angle given as pos * turn / 2^64 turns, each as an unevaluated sum hi + lo.
-// The product is taken modulo 2^64, i.e. modulo a whole turn, in integers: no position is too far.
+// The product is taken modulo 2^64, i.e. modulo a whole turn, in integers, so that no position loses more
+// than the rounding of `turn`, 2^-65 turns per unit of position.
 // The remainder to the nearest quarter turn, |x| <= pi/4, goes through the Taylor series of sine and
 // cosine with the terms up to x^3 / 6 and x^2 / 2 kept in two floats; hi + lo is within 2^-28 of the value (cosine
 // 2^-28.7, sine 2^-30.2 at most in 60 million angles), so a rotated channel is rounded to bf16 as the exact one is but

@@ -86,6 +86,28 @@ qwm_status check_window(const qwm_window *w) {
 // Per-sequence arrays: 8-byte (4-byte) elements at their natural alignment.
 bool aligned_to(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
+// theta^(-j / half) / (2 pi) turns in units of 2^-64, rounded once: a double's 53 bits would leave an error of up
+// to 2^8 units, which every unit of position multiplies.  One Newton step from the double r of pow(): the
+// product r^half theta^j is 1 + d, so the root is r (1 - d / half); the product is taken in pairs of doubles
+// (an unevaluated sum hi + lo), each factor in the order that keeps it near 1.
+uint64_t turn_of(double theta, int j, int half) {
+  const double r = pow(theta, -(double)j / half);
+  if (r < 0x1p-64) return 0;   // less than half a unit
+  double hi = 1.0, lo = 0.0;
+  for (int a = half, b = j; a > 0 || b > 0;) {
+    const bool up = b > 0 && (hi < 1.0 || a == 0);
+    const double f = up ? theta : r, p = hi * f, e = fma(hi, f, -p) + lo * f;
+    up ? b-- : a--;
+    hi = p + e;
+    lo = e - (hi - p);
+  }
+  const double rl = -r * ((hi - 1.0) + lo) / half;                                    // the root is r + rl
+  const double kTurn = 0x1.45f306dc9c883p-3, kTurnLo = -0x1.6b01ec5417056p-57;        // 1 / (2 pi)
+  const double t = r * kTurn, tl = fma(r, kTurn, -t) + (r * kTurnLo + rl * kTurn);
+  const double units = t * 0x1p64, whole = floor(units);
+  return (uint64_t)whole + (uint64_t)(int64_t)floor((units - whole) + tl * 0x1p64 + 0.5);
+}
+
 // The most keys a call's rows can see between them.
 int64_t most_keys(const qwm_window &w, int64_t nq, int64_t tpf, int64_t frames) {
   const int64_t span = (nq + tpf - 1) / tpf + 1;   // frames the Queries stand in, at most
@@ -116,9 +138,7 @@ qwm_status qwm_rope_plan(const int32_t axis_dim[3], const double theta[3], int32
   int i = 0;
   for (int a = 0; a < 3; a++)
     for (int j = 0; j < axis_dim[a] / 2; j++, i++) {
-      const double e = shared_freq ? 2.0 * i / r.rot : 2.0 * j / axis_dim[a];
-      const double turns = pow(theta[a], -e) / 6.283185307179586476925286766559;   // at most 1 / (2 pi)
-      const uint64_t t = (uint64_t)(turns * 18446744073709551616.0 + 0.5);
+      const uint64_t t = shared_freq ? turn_of(theta[a], i, r.rot / 2) : turn_of(theta[a], j, axis_dim[a] / 2);
       r.turn[i] = inverse ? 0 - t : t;
       r.axis[i] = (uint8_t)a;
     }

@@ -72,7 +72,8 @@ QWM_API qwm_status qwm_rope_plan(const int32_t axis_dim[3], const double theta[3
  *   x, out  bf16 [batch][heads][n][128] by xs and os; out may be x itself (same strides)
  *   start   device int64 [batch]: position of token 0 of each sequence
  *   pos     device int32 [batch][n][3] (t, y, x) to use instead of the grid's, or NULL
- * Angles are formed exactly as fractions of a turn (64-bit integers), so far positions lose nothing. */
+ * Angles are formed as fractions of a turn in 64-bit integers: beside the rounding of the turns per position,
+ * at most 2^-65 (so p 2^-65 turns at position p, 2^-26 radians up to 2^36), far positions lose nothing. */
 QWM_API qwm_status qwm_rope(qwm_ctx *ctx, const qwm_rope_spec *spec, const uint16_t *x, const qwm_strides *xs,
                             int32_t batch, int32_t heads, int64_t n, const int64_t *start, const int32_t *pos,
                             uint16_t *out, const qwm_strides *os, qwm_stream stream);

@@ -1,6 +1,5 @@
 """The recent window where its arithmetic is tightest: weights far below a dominating sink, Queries of any
 magnitude, infinite channels, far positions; and a layer whose calls are refused or fail half-way."""
-import decimal
 import math
 
 import numpy as np
@@ -75,6 +74,31 @@ def test_attend_queries_of_any_magnitude(qwm, H, kv, nq, length, bits):
 
 
 # ------------------------------------------------------------------ rotary positions
+
+@pytest.mark.parametrize("start", [2 ** 33, 2 ** 40 + 12345, 2 ** 47 - 1])
+@pytest.mark.parametrize("pairing", ["interleaved", "half"])
+def test_rope_far_positions(qwm, pairing, start):
+    """Against angles of 200 bits: beside the rounding, a position's angle is off by at most 2^-65 turns a
+    position (the table's rounding)."""
+    kw = dict(dims=(128, 0, 0), theta=500000.0, pairing=pairing)
+    rng = np.random.default_rng(start % 1000)
+    h, n = 3, 40
+    x = rows(rng, 1, h, n)
+    out = torch.empty(1, h, n, 128, dtype=torch.bfloat16, device="cuda")
+    qwm.qwm_rope(ctx_of(qwm, h), qwm.RopeSpec(**kw), x, ints([start]), out)
+    dims, theta, _, shared = spec_args(kw)
+    turns = ref.exact_turns(dims, theta, shared)
+    part = np.array([[((start + i) * t % 2 ** 200 >> 140) / 2.0 ** 60 for t in turns] for i in range(n)])
+    c, s = np.cos(2 * np.pi * part), np.sin(2 * np.pi * part)
+    at = (np.arange(64) * 2, np.arange(64) * 2 + 1) if pairing == "interleaved" else (np.arange(64), np.arange(64) + 64)
+    for j in range(h):
+        src, want, pair = f64(x[0, j]), np.zeros((n, 128)), np.zeros((n, 128))
+        p, q = src[:, at[0]], src[:, at[1]]
+        want[:, at[0]], want[:, at[1]] = p * c - q * s, p * s + q * c
+        pair[:, at[0]] = pair[:, at[1]] = np.abs(p) + np.abs(q)
+        far = (start + n) * 2.0 ** -65 * 2 * np.pi
+        assert np.all(np.abs(f64(out[0, j]) - want) <= rope_bound(src, want, kw) + far * pair)
+
 
 @pytest.mark.parametrize("pairing", ["interleaved", "half"])
 def test_rope_cosine_and_sine(qwm, pairing):

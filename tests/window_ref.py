@@ -1,6 +1,11 @@
 """Plain 64-bit reference of the recent window (tests only): rotary positions, the window cache and
 windowed attention, written from their definitions on numpy arrays."""
+import decimal
+import functools
+
 import numpy as np
+
+PI = decimal.Decimal("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899863")
 
 D, GROUP = 128, 32
 Q = {8: 127, 4: 7}
@@ -27,6 +32,20 @@ def rope(x, dims, theta, pairing, shared, positions, sign=1.0):
             p, q = x[:, c0], x[:, c1]
             out[:, c0], out[:, c1] = p * np.cos(ang) - q * np.sin(ang), p * np.sin(ang) + q * np.cos(ang)
             i += 1
+    return out
+
+
+@functools.lru_cache(maxsize=None)
+def exact_turns(dims, theta, shared, bits=200):
+    """Every pair's part of a turn per unit of position, from 80 digits, as an integer over 2^bits."""
+    out, i = [], 0
+    with decimal.localcontext() as c:
+        c.prec = 80
+        for a in range(3):
+            for j in range(dims[a] // 2):
+                e = decimal.Decimal(2 * i) / sum(dims) if shared else decimal.Decimal(2 * j) / dims[a]
+                out.append(int(decimal.Decimal(theta[a]) ** -e / (2 * PI) * 2 ** bits))
+                i += 1
     return out
 
 
