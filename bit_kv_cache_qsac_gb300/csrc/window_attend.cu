@@ -303,9 +303,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   win::Keys keys;
   keys.init(seq, frame_of(pair0), frame_of(pair1 - 1));
   const int tiles = (keys.total + BN - 1) / BN;
-  // (tiles < 2^24 and splits <= 64: 32 bits)
-  const int j0 = a.splits == 1 ? 0 : (int)((uint32_t)tiles * (uint32_t)split / (uint32_t)a.splits);
-  const int J = (a.splits == 1 ? tiles : (int)((uint32_t)tiles * (uint32_t)(split + 1) / (uint32_t)a.splits)) - j0;
+  // (tiles < 2^24 and splits <= 2^12: the products can pass 32 bits)
+  const int j0 = a.splits == 1 ? 0 : (int)win::quotient((int64_t)tiles * split, a.splits);
+  const int J = (a.splits == 1 ? tiles : (int)win::quotient((int64_t)tiles * (split + 1), a.splits)) - j0;
   if (J == 0) {   // these rows see no key (in this part): 16 lanes write a row's zeros
     for (int e = tid; e < NQT * BM * 16; e += kThreads) {
       const int64_t r = row_base + (int64_t)(e / 16 / BM) * 2 * BM + e / 16 % BM;
@@ -764,18 +764,21 @@ cudaError_t launch_window_tiles(const WindowAttend &a, cudaStream_t st) {
 // 10,000 for starting and ending, 6,000 more for a second kernel that joins the parts; up to 8 parts may be
 // a cluster's CTAs instead, which fill nine tenths of the slots.  On tensor-memory tiles 20 per key, 20,000
 // and 7,000; calls that fill the SMs are left whole.
+// A part takes 2^18 keys at most, whatever the time: weights below 2^-32 of a part's largest are lost (2^-14 of
+// it between them), and its fp32 sums stay within 2^14 additions of products and 2^12 of weights.
+constexpr int64_t kPartKeys = (int64_t)1 << 18;
 WindowPlan window_plan(int64_t batch, int64_t kv_heads, int64_t rows, int64_t keys, int num_sms) {
   WindowPlan p;
   p.tiles = rows > 32;
   p.splits = 1;
   p.cluster = false;
+  const int64_t least = (keys + kPartKeys - 1) / kPartKeys;
   const int64_t heads = batch * kv_heads, most = keys / 256 < 64 ? keys / 256 : 64;   // 256 keys a part at least
   const int64_t work = p.tiles ? heads * ((rows + kPairRows - 1) / kPairRows) : heads * (rows <= 8 ? 1 : (rows + 15) / 16);
   const int64_t slots = p.tiles ? num_sms / 2 : (rows <= 8 ? 2 : 1) * (int64_t)num_sms;
-  if (work >= slots) return p;
   const int64_t per_key = p.tiles ? 20 : 12, fixed = p.tiles ? 20000 : 10000, join = p.tiles ? 7000 : 6000;
   int64_t best = keys * per_key + fixed;
-  for (int64_t s = 2; s <= most && work * s <= 4 * slots; s++) {
+  for (int64_t s = 2; work < slots && s <= most && work * s <= 4 * slots; s++) {
     const int64_t part = keys * per_key / s + fixed;
     const int64_t joined = (work * s + slots - 1) / slots * part + join;
     if (joined < best) {
@@ -791,6 +794,10 @@ WindowPlan window_plan(int64_t batch, int64_t kv_heads, int64_t rows, int64_t ke
         p.cluster = true;
       }
     }
+  }
+  if (p.splits < least) {
+    p.splits = (int)least;
+    p.cluster = false;
   }
   return p;
 }

@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) window_decode_kerne
   const uint32_t sink = (uint32_t)a.w.sink, ring = (uint32_t)a.w.ring;
   const int64_t head_row = (int64_t)blockIdx.y * (a.w.sink + a.w.ring);
   const int steps_all = (keys.total + kKeys - 1) / kKeys;
-  int j0 = 0, j1 = steps_all;   // (steps_all < 2^28 and splits <= 64: the products can pass 32 bits)
+  int j0 = 0, j1 = steps_all;   // (steps_all < 2^28 and splits <= 2^12: the products can pass 32 bits)
   if (a.splits > 1) {
     const uint32_t q = (uint32_t)steps_all / (uint32_t)a.splits, rem = (uint32_t)steps_all - q * (uint32_t)a.splits, k = blockIdx.x;
     j0 = (int)(k * q + (k < rem ? k : rem));
@@ -622,6 +622,7 @@ cudaError_t launch_window_decode(const WindowAttend &a, cudaStream_t st) {
 // Launched as a dependent of the parts' kernel, so that its start-up overlaps their work.
 cudaError_t launch_window_combine(const WindowAttend &a, cudaStream_t st) {
   const int64_t items = (int64_t)a.w.batch * a.w.kv_heads * a.rows;
+  if ((items + 7) / 8 > INT32_MAX) return cudaErrorInvalidValue;   // (its workspace would be terabytes)
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((items + 7) / 8));
   cfg.blockDim = dim3(256);

@@ -140,10 +140,11 @@ QWM_API qwm_status qwm_window_read(qwm_ctx *ctx, const qwm_window *win, const in
  *            result over both;  0: they are written
  *   ws       workspace of qwm_window_attend_workspace bytes (may be NULL when that is 0), free again
  *            when the call's work on the stream is done
- * A row that sees no key gets out = 0 and lse = -inf (merge: stays as it was).  Logits, maxima, sums and
- * the output are accumulated in fp32.  Queries enter the first product off by at most 2^-25 of their row's largest
- * element, whatever its magnitude; the weights enter the second product in fp16, rounded by at most 2^-11 of
- * their value or 2^-32 of the largest weight, whichever is more. */
+ * A row that sees no key gets out = 0 and lse = -inf (merge: stays as it was).  Queries enter the first product
+ * off by at most 2^-25 of their row's largest element, whatever its magnitude.  Logits, maxima, sums and the
+ * output are accumulated in fp32, over 2^18 keys at most (longer calls are made in parts, which are joined).
+ * The weights enter the second product in fp16, rounded by at most 2^-11 of their value or 2^-32 of the
+ * largest weight of their part, whichever is more. */
 QWM_API qwm_status qwm_window_attend(qwm_ctx *ctx, const qwm_window *win, const uint16_t *q, const qwm_strides *qs,
                                      int64_t nq, const int64_t *q_start, const int64_t *length,
                                      const int32_t *q_count, int64_t tpf, int64_t frames, float softmax_scale,

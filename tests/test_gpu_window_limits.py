@@ -51,6 +51,33 @@ def test_attend_counts_what_a_sink_dominates(qwm, nq, heads, bits, gap, sink, ot
     assert float((lse.double() - gap - math.log2(1 + share)).abs().max()) <= math.log2(math.e) * n / 64 * 2.0 ** -24 + gap * 2.0 ** -22 + 2.0 ** -20
 
 
+def test_attend_long_caches_in_parts(qwm):
+    """A sink above 2^20 equal keys by so much that their weights fall below the fp16 grid: only those of the
+    sink's own part (2^18 keys at most) may.  The others' parts carry them in full."""
+    n, heads, nq, gap = 1 << 20, 76, 40, 32.5
+    ctx, win = ctx_of(qwm, heads), qwm.Window.empty(4, 1, heads, 1, n)
+    win.k_step.fill_(0x78), win.v_step.fill_(0x78)        # steps of 1
+    win.k_codes.fill_(0x88), win.v_codes.fill_(0x99)
+    win.k_codes[:, :, 0], win.v_codes[:, :, 0] = 0x99, 0x88
+    q = torch.ones(1, heads, nq, 128, dtype=torch.bfloat16, device="cuda")
+    out = torch.empty(1, heads, nq, 128, dtype=torch.float32, device="cuda")
+    lse = torch.empty(1, heads, nq, dtype=torch.float32, device="cuda")
+    qwm.qwm_window_attend(ctx, win, q, ints([n + 1]), ints([n + 1]), 1, 2 * n, gap / (128 * math.log2(math.e)), out, lse=lse)
+    assert qwm.qwm_sync_status(ctx) == 0
+    share, part = n * 2.0 ** -gap, 1 << 18
+    want = share / (1 + share)
+    rel = 2.0 ** -11 + 2.0 ** -20 + gap * 2.0 ** -22 + part / 64 * 2.0 ** -24 + part / 16 * 2.0 ** -23
+    assert float((out.double() - want).abs().max()) <= want * rel + part * 2.0 ** -32
+    assert float((lse.double() - gap - math.log2(1 + share)).abs().max()) <= math.log2(math.e) * part / 64 * 2.0 ** -24 + gap * 2.0 ** -22 + 2.0 ** -20
+    # the parts of a call without a sink: Values 1, -1 and 0 on a half, a quarter and the rest of the keys
+    win.k_codes.fill_(0x88), win.v_codes.fill_(0x88)
+    win.v_codes[:, :, 1:1 + n // 2], win.v_codes[:, :, 1 + n // 2:1 + 3 * n // 4] = 0x99, 0x77
+    qwm.qwm_window_attend(ctx, win, q, ints([n + 1]), ints([n + 1]), 1, 2 * n, 1.0, out, lse=lse)
+    want = n / 4 / (n + 1)
+    assert float((out.double() - want).abs().max()) <= 0.75 * (part / 64 * 2.0 ** -24 + part / 16 * 2.0 ** -23) + 2.0 ** -20
+    assert float((lse.double() - math.log2(n + 1)).abs().max()) <= math.log2(math.e) * part / 64 * 2.0 ** -24 + 2.0 ** -19
+
+
 @pytest.mark.parametrize("bits", [8, 4])
 @pytest.mark.parametrize("H,kv,nq,length", [(2, 2, 1, 300), (6, 2, 4, 300), (2, 2, 30, 9000), (2, 1, 40, 300), (2, 2, 300, 200), (1, 1, 600, 300)])
 def test_attend_queries_of_any_magnitude(qwm, H, kv, nq, length, bits):

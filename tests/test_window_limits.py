@@ -1,4 +1,6 @@
 """Host-side limits of the recent window (no GPU)."""
+import ctypes as C
+
 import pytest
 
 import window_ref as ref
@@ -24,3 +26,18 @@ def test_plan_turns_are_rounded_once(qwm, dims, theta, shared, inverse):
     for i, t in enumerate(exact):
         got = spec.turn[i] if not inverse else -spec.turn[i] % 2 ** 64
         assert abs(got * 2 ** 136 - t) <= 2 ** 135 + 2 ** 116, (i, got, t / 2 ** 136)
+
+
+def test_long_calls_are_split(qwm):
+    """No part of a call takes more than 2^18 keys (here without a device: a context of no SMs, which plans no
+    parts for speed)."""
+    ctx = (C.c_char * 4096)()
+    cfg = qwm.qwm_config(8, 128, 256, 64, 4, 8, 2, 10, 0)
+    C.memmove(ctx, C.byref(cfg), C.sizeof(cfg))
+    lib = qwm.raw_library()
+    for sink, ring, nq, frames, parts in ((0, 1 << 18, 1, 1 << 30, 0), (1, 1 << 18, 1, 1 << 30, 2), (0, 1 << 20, 40, 1 << 30, 4),
+                                          (0, (1 << 20) + 1, 600, 1 << 30, 5), (0, 1 << 30, 1, 1 << 30, 4096), (0, 1 << 30, 600, 1 << 30, 4096),
+                                          (0, 1 << 30, 1, 1 << 17, 0), (5, 1 << 30, 600, (1 << 18) - 1024, 0)):
+        w = qwm.qwm_window(4, 2, 4, 0, sink, ring)
+        need = lib.qwm_window_attend_workspace(ctx, w, nq, 1, frames)
+        assert need == 2 * 8 * nq * parts * 129 * 4, (sink, ring, nq, frames, need / (2 * 8 * nq * 129 * 4))
