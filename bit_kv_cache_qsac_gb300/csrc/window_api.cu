@@ -244,7 +244,7 @@ qwm_status qwm_window_attend(qwm_ctx *ctx, const qwm_window *win, const uint16_t
   qwm_status s = check_attend(ctx, win, nq, tpf, frames);
   if (s == QWM_OK) s = check_window(win);
   if (s != QWM_OK) return s;
-  if (!(softmax_scale > 0.f) || !isfinite(softmax_scale)) return QWM_ERR_ARG;
+  if (!(softmax_scale > 0.f) || softmax_scale > 0x1p123f) return QWM_ERR_ARG;   // (times 16 log2(e) it stays finite)
   if ((out_f32 != 0 && out_f32 != 1) || (merge != 0 && merge != 1)) return QWM_ERR_ARG;
   if (merge && (!out_f32 || !lse)) return QWM_ERR_ARG;
   if (nq == 0) return QWM_OK;

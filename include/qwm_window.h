@@ -132,7 +132,7 @@ QWM_API qwm_status qwm_window_read(qwm_ctx *ctx, const qwm_window *win, const in
  *   q        bf16 [batch][H][nq][128] by qs, H = config.heads, a multiple of kv_heads (Query head h reads
  *            Key head h / (H / kv_heads)); an element beyond the fp16 range records QWM_ERR_RANGE
  *   q_start  device int64 [batch];  length  device int64 [batch];  q_count  device int32 [batch] or NULL
- *   softmax_scale  > 0, multiplies the logits
+ *   softmax_scale  > 0, at most 2^123, multiplies the logits
  *   out      [batch][H][nq][128] by os: bf16 (out_f32 == 0) or fp32 (out_f32 == 1)
  *   lse      fp32 [batch][H][nq] dense: log2 of the sum over the keys of 2^(softmax_scale log2(e) l), as
  *            qwm_attend_merge's; or NULL

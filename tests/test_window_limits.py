@@ -41,3 +41,16 @@ def test_long_calls_are_split(qwm):
         w = qwm.qwm_window(4, 2, 4, 0, sink, ring)
         need = lib.qwm_window_attend_workspace(ctx, w, nq, 1, frames)
         assert need == 2 * 8 * nq * parts * 129 * 4, (sink, ring, nq, frames, need / (2 * 8 * nq * 129 * 4))
+
+
+def test_softmax_scale_range(qwm):
+    """A scale whose product with log2(e) and the 4-bit unit is infinite would make 0 logits NaN."""
+    ctx, ok = (C.c_char * 4096)(), 0x7f00000000
+    cfg = qwm.qwm_config(8, 128, 256, 64, 4, 8, 2, 10, 0)
+    C.memmove(ctx, C.byref(cfg), C.sizeof(cfg))
+    st = qwm.qwm_strides(8 * 128 * 4, 128 * 4, 128)
+    for bits in (8, 4):
+        w = qwm.qwm_window(bits, 2, 4, 0, 4, 100, ok, ok, ok, ok)
+        for scale, nq, want in ((2.0 ** 123, 0, qwm.QWM_OK), (2.0 ** 123 * (1 + 2.0 ** -23), 0, qwm.QWM_ERR_ARG), (3.4e38, 0, qwm.QWM_ERR_ARG),
+                                (3.4e38, 4, qwm.QWM_ERR_ARG)):
+            assert qwm.raw_library().qwm_window_attend(ctx, w, ok, st, nq, ok, ok, None, 1, 8, scale, ok, st, 0, None, 0, None, 0, None) == want
