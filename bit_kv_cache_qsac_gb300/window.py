@@ -119,7 +119,8 @@ def _array(ctx, t, name: str, dtype, shape) -> int | None:
     return t.data_ptr()
 
 
-_current_stream = torch._C._cuda_getCurrentRawStream   # the handle itself: a tenth of torch.cuda.current_stream's time
+# the handle itself, at a tenth of torch.cuda.current_stream's time, where this torch has it
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _stream_of(ctx, stream) -> int:

@@ -1,5 +1,8 @@
 """Host-side limits of the recent window (no GPU)."""
 import ctypes as C
+import os
+import subprocess
+import sys
 
 import pytest
 
@@ -54,3 +57,12 @@ def test_softmax_scale_range(qwm):
         for scale, nq, want in ((2.0 ** 123, 0, qwm.QWM_OK), (2.0 ** 123 * (1 + 2.0 ** -23), 0, qwm.QWM_ERR_ARG), (3.4e38, 0, qwm.QWM_ERR_ARG),
                                 (3.4e38, 4, qwm.QWM_ERR_ARG)):
             assert qwm.raw_library().qwm_window_attend(ctx, w, ok, st, nq, ok, ok, None, 1, 8, scale, ok, st, 0, None, 0, None, 0, None) == want
+
+
+def test_import_without_torchs_private_stream_handle(qwm):
+    """The package loads with a torch that lacks the call behind torch.cuda.current_stream."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = ("import torch; torch._C.__dict__.get('_cuda_getCurrentRawStream') and delattr(torch._C, '_cuda_getCurrentRawStream'); "
+            "import bit_kv_cache_qsac_gb300.window as w; assert callable(w._current_stream)")
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-500:]
