@@ -3,7 +3,7 @@
 //
 // Bound: memory (2 bytes read and 2 written per channel); the angles depend on the token alone, so a
 // thread forms those of its 8 channels once and walks over `heads_per_block` heads with them, four heads'
-// loads in flight at a time.  Measured: 40 heads x 10,800 tokens in 35.8 us = 6.2 TB/s (0.92 of a copy);
+// loads in flight at a time.  Measured: 40 heads x 10,800 tokens in 36.7 us = 6.0 TB/s (0.90 of a copy), 37.3 in halves;
 // one token of 16 sequences x 32 heads in 3.4 us (launch, then start -> angle -> product).
 #include <math.h>
 

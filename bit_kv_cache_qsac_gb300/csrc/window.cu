@@ -4,9 +4,10 @@
 // A step has 4 significant bits, so code * s has at most 11 and is exact in fp16, whatever reads it.
 // Bound: memory (write: 512 B of bf16 read and 264 or 136 B written per token and head; read: the
 // reverse).  16 lanes take one row, 8 channels each; four of them share a step, found by two shuffles.
-// Measured, 40 heads x 10,800 tokens at 4 bits: written (Keys turned by three axes) in 64.6 us = 4.3 TB/s,
-// held by instruction issue (74%: two rows are quantised per 512 bytes read); read back in 43 us = 6.5
-// TB/s.  8 bits, 40 heads x 4,680: read back in 24.8 us = 5.8 TB/s.
+// Measured, 40 heads x 10,800 tokens: written at 4 bits in 47 us, with the Keys turned by three axes in 62 (half
+// pairing 68) = 4.5 TB/s; at 8 bits 53, 68 and 72.  Turned and at 4 bits 71% of the issue slots and half of the
+// DRAM rate are in use: what remains is the chain of shuffles, step and reciprocal of each row.  Read back in
+// 44 us = 6.3 TB/s (4 bits) and 51 = 6.6 (8 bits); 40 heads x 4,680 at 8 bits in 24.8 us = 5.9 TB/s.
 #include "window.cuh"
 
 namespace {

@@ -26,11 +26,13 @@
 // and tile 8 MMAs of 256 x 64 x 16 (43 cycles each, bound by reading Q from shared memory) and 4 of
 // 256 x 128 x 16 (64 cycles).  MMAs execute in issue order, so a buffer is written after the PV that
 // read it.
-// Measured (fp16 operands, 2 x 2 x 128 operations per row and visible key): 40 heads x 4,680 rows over 39,000
-// keys at 8 bits in 2.28 ms = 1,639 TFLOP/s, 3,600 rows over 43,200 keys at 4 bits in 1.92 ms = 1,657; the
-// tensor pipe is active in 81% of all cycles, and in 1,200 of about 1,260 per step of the loop.  Around the
-// loop an item spends about 15,000 cycles (first loads 7,000, first logits 2,500, output 4,000), which a
-// prompt under a window of 1,024 keys feels: 2 x 2,111 tokens x 32 heads in 96 us.
+// Measured (device time of calls replayed from a graph; 2 x 2 x 128 operations per row and visible key): 40 heads x
+// 4,680 rows over 39,000 keys at 8 bits in 2.26 ms = 1,653 TFLOP/s, 3,600 rows over 43,200 keys at 4 bits in
+// 1.92 ms = 1,662 (called one after another 2.47 and 2.02 ms = 1,510 and 1,580); the tensor pipe is active in
+// 81% of all cycles, and in 1,200 of about 1,260 per step of the loop.  Around the loop an item spends about
+// 15,000 cycles (first loads 7,000, first logits 2,500, output 4,000), which a prompt under a window of 1,024 keys
+// feels: 2 x 2,111 tokens x 32 heads in 96 us.  With few rows the tiles' padding costs as much as rows: 33 to 256
+// rows of 40 heads over 39,000 keys take 206 to 221 us at 8 bits and 201 to 211 at 4.
 // Every wait is bounded (about one second); on expiry QWM_ERR_DEVICE_TIMEOUT is recorded, every role
 // stops, outstanding MMAs are drained and TMEM is freed.
 #include "window.cuh"
@@ -758,7 +760,7 @@ cudaError_t launch_window_tiles(const WindowAttend &a, cudaStream_t st) {
 }
 
 // Few rows run on warp tiles, which read the cache once per 16 rows; more than 32 on tensor-memory tiles (at
-// 39,000 tokens of 40 heads, 8 bits: 16 rows take 90 us, up to 256 rows on tensor-memory tiles 205).
+// 39,000 tokens of 40 heads, 8 bits: 16 rows take 90 us, 32 take 170, 33 to 256 on tensor-memory tiles 206 to 221).
 // The keys are split into the number of parts for which whole waves of CTAs end soonest, by what a part
 // costs in cycles, as measured: on warp tiles 12 per key (a CTA of 8 warps, whatever the code width) and
 // 10,000 for starting and ending, 6,000 more for a second kernel that joins the parts; up to 8 parts may be

@@ -14,10 +14,13 @@
 // more for V, whose pairs run along the keys).  Every warp keeps its own running maximum and sum; warps
 // meet in shared memory at the end, the parts of a Key head (up to 8) in the shared memory of a
 // thread-block cluster, more parts in a second kernel.
-// Measured: 16 sequences x 32 heads (8 Key heads) x 4,096 keys at 8 bits in 27.2 us = 5.1 TB/s, about 7
+// Measured: 16 sequences x 32 heads (8 Key heads) x 4,096 keys at 8 bits in 27 to 28 us = 5.0 TB/s, about 7
 // us of it before the first keys arrive and in the join; 40 heads x 39,000 keys at 4 bits in 52 us = 4.1
-// TB/s, held by instruction issue (316 warp instructions per 16 keys of a head, 160 of them placing,
-// unbiasing and scaling codes, half of those on the half-rate integer pipe).
+// TB/s (8 bits: 69 us = 6.0).  At 4 bits neither the issue slots (62%: 316 warp instructions per 16 keys of a
+// head, 160 of them placing, unbiasing and scaling codes) nor DRAM (55%) are full: four warps per scheduler
+// run load, product, maximum and product one behind the other, and 280 CTAs stand on 304 places.
+// 9 to 16 rows take 220 to 234 registers a thread, so one CTA per SM (16 rows of 40 heads over 39,000 keys:
+// 90 us at 8 bits, 81 at 4), and 17 to 32 read and decode the cache twice (166 to 170, 140 to 144).
 #include "window.cuh"
 
 namespace {
