@@ -38,7 +38,10 @@ EXPORTED = ("qwm_status_string", "qwm_workspace_bytes", "qwm_create", "qwm_destr
             "qwm_kivi_quantize", "qwm_kivi_dequantize", "qwm_prq_residual", "qwm_prq_dequantize",
             # the recent window (include/qwm_window.h)
             "qwm_rope_plan", "qwm_rope", "qwm_window_bytes", "qwm_window_write", "qwm_window_read", "qwm_window_attend",
-            "qwm_window_attend_workspace")
+            "qwm_window_attend_workspace",
+            # the paged cache (include/qwm_paged.h)
+            "qwm_norm_rope", "qwm_pages_reset", "qwm_pages_update", "qwm_paged_write", "qwm_paged_read", "qwm_paged_attend",
+            "qwm_paged_attend_workspace")
 
 
 class QwmError(RuntimeError):
@@ -167,6 +170,7 @@ class Context:
         self.handle = h
         self.device = torch.device("cuda", torch.cuda.current_device())
         self.window_workspace = {}   # qwm_window_attend: workspace bytes by shape
+        self.paged_workspace = {}    # qwm_paged_attend: the same
 
     @property
     def heads(self):
@@ -587,3 +591,9 @@ def qwm_quantize_kv_full(ctx: Context, k, v, n: int, S, n_seen, u_r, out: Chunk,
 from .window import (QWM_ROPE_HALF, QWM_ROPE_INTERLEAVED, RopeSpec, Window, qwm_rope, qwm_rope_plan,  # noqa: E402
                      qwm_rope_spec, qwm_strides, qwm_window, qwm_window_attend, qwm_window_attend_workspace,
                      qwm_window_bytes, qwm_window_read, qwm_window_write)
+
+
+# ---------------------------------------------------------------- the paged cache (qwm_paged.h)
+
+from .paged import (PagePool, PageTable, qwm_norm_rope, qwm_page_pool, qwm_page_table, qwm_paged_attend,  # noqa: E402
+                    qwm_paged_attend_workspace, qwm_paged_read, qwm_paged_write, qwm_pages_reset, qwm_pages_update)

@@ -1,0 +1,226 @@
+// C ABI of the paged cache (include/qwm_paged.h): argument checks and dispatch.  Nothing here allocates
+// device memory; every check is made before the first CUDA call.
+#include "paged.cuh"
+#include "window_checks.cuh"
+
+namespace {
+
+int log2_of_page(int page) {
+  for (int i = 4; i <= 8; i++)
+    if (page == 1 << i) return i;
+  return -1;
+}
+
+qwm_status check_table(const qwm_page_table *t, bool stack) {
+  if (!t) return QWM_ERR_ARG;
+  if (log2_of_page(t->page) < 0) return QWM_ERR_UNSUPPORTED;
+  if (t->batch < 1 || t->width < 1 || !t->table || !t->length) return QWM_ERR_ARG;
+  if (t->batch > kPagedMaxBatch || (int64_t)t->width * t->page > kPagedMaxTokens) return QWM_ERR_SHAPE;
+  if (!aligned_to(t->table, 4) || !aligned_to(t->length, 8)) return QWM_ERR_ALIGN;
+  if (!stack) return QWM_OK;
+  if (t->pages < 1 || !t->free_list || !t->free_count) return QWM_ERR_ARG;
+  if ((int64_t)t->pages * t->page > ((int64_t)1 << 40)) return QWM_ERR_SHAPE;
+  if (!aligned_to(t->free_list, 4) || !aligned_to(t->free_count, 4)) return QWM_ERR_ALIGN;
+  return QWM_OK;
+}
+
+qwm_status check_pool_shape(const qwm_page_pool *p) {
+  if (!p) return QWM_ERR_ARG;
+  if ((p->bits != 8 && p->bits != 4) || log2_of_page(p->page) < 0) return QWM_ERR_UNSUPPORTED;
+  if (p->pages < 1 || p->kv_heads < 1) return QWM_ERR_ARG;
+  if (p->kv_heads > kMaxGridY || (int64_t)p->pages * p->page > ((int64_t)1 << 40)) return QWM_ERR_SHAPE;
+  return QWM_OK;
+}
+
+qwm_status check_pool(const qwm_page_pool *p) {
+  const qwm_status s = check_pool_shape(p);
+  if (s != QWM_OK) return s;
+  const void *req[] = {p->k_codes, p->v_codes, p->k_step, p->v_step};
+  for (const void *x : req) {
+    if (!x) return QWM_ERR_ARG;
+    if (!aligned16(x)) return QWM_ERR_ALIGN;
+  }
+  return QWM_OK;
+}
+
+// A packed activation: one sequence of n rows.
+qwm_status check_packed(const void *p, const qwm_strides *s, int64_t heads, int64_t n, bool written) {
+  if (!s) return QWM_ERR_ARG;
+  const qwm_strides one = {0, s->head, s->token};
+  return check_rows(p, &one, 1, heads, n, written);
+}
+
+qwm_status check_norm(const float *weight, int32_t per_head, float eps) {
+  if ((per_head != 0 && per_head != 1) || !(eps >= 0.f) || eps > 3.402823466e38f) return QWM_ERR_ARG;
+  return aligned16(weight) ? QWM_OK : QWM_ERR_ALIGN;
+}
+
+constexpr int64_t kMaxRows = (int64_t)1 << 30;   // rows of a Key head in a packed batch
+
+// How a call is run and what workspace it takes.
+struct Plan {
+  int row_tiles;      // warp tiles of 8 (1) or 16 rows (2) an item
+  int shares;
+  size_t bytes;
+};
+
+Plan plan_of(const qwm_ctx *ctx, int group, int64_t max_count) {
+  Plan p;
+  p.row_tiles = max_count * group <= 8 ? 1 : 2;
+  p.shares = paged_decode_shares(p.row_tiles, ctx->num_sms);
+  const size_t rows = (size_t)2 * p.shares * 8 * p.row_tiles;
+  p.bytes = rows * (QWM_D + 1) * sizeof(float) + (size_t)p.shares * sizeof(PagedCut);
+  return p;
+}
+
+qwm_status check_attend(const qwm_ctx *ctx, const qwm_page_pool *pool, int64_t max_count) {
+  if (!ctx || max_count < 0) return QWM_ERR_ARG;
+  const qwm_status s = check_pool_shape(pool);
+  if (s != QWM_OK) return s;
+  if (ctx->cfg.heads % pool->kv_heads != 0 || max_count > kMaxTokens) return QWM_ERR_SHAPE;
+  return QWM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+qwm_status qwm_norm_rope(qwm_ctx *ctx, const qwm_rope_spec *spec, const uint16_t *x, const qwm_strides *xs, int32_t batch,
+                         int32_t heads, int64_t n, const int64_t *start, const int64_t *at, const int32_t *pos,
+                         const float *weight, int32_t per_head, float eps, uint16_t *out, const qwm_strides *os,
+                         qwm_stream stream) {
+  if (!ctx || batch < 0 || heads < 0 || n < 0) return QWM_ERR_ARG;
+  qwm_status s = spec ? check_rope(spec) : QWM_OK;
+  if (s == QWM_OK) s = check_norm(weight, per_head, eps);
+  if (s != QWM_OK) return s;
+  if (batch > kMaxGridY || heads > kMaxGridY || n > kMaxTokens) return QWM_ERR_SHAPE;
+  if ((int64_t)batch * n >= ((int64_t)1 << 34)) return QWM_ERR_SHAPE;
+  if (batch == 0 || heads == 0 || n == 0) return QWM_OK;
+  if ((s = check_rows(x, xs, batch, heads, n, false)) != QWM_OK) return s;
+  if ((s = check_rows(out, os, batch, heads, n, true)) != QWM_OK) return s;
+  if ((start && at) || (spec && !start && !at) || (pos && !spec)) return QWM_ERR_ARG;
+  if (!aligned_to(start, 8) || !aligned_to(at, 8) || !aligned_to(pos, 4)) return QWM_ERR_ALIGN;
+  if (x == out && (xs->batch != os->batch || xs->head != os->head || xs->token != os->token)) return QWM_ERR_ARG;
+  DeviceGuard dev(ctx->device);
+  if (dev.err != cudaSuccess) return QWM_ERR_CUDA;
+  return cuda_status(launch_norm_rope(spec, x, *xs, batch, heads, n, start, at, pos, weight, weight ? per_head : 0, eps, out,
+                                      *os, ctx->num_sms, (cudaStream_t)stream));
+}
+
+qwm_status qwm_pages_reset(qwm_ctx *ctx, const qwm_page_table *tab, qwm_stream stream) {
+  if (!ctx) return QWM_ERR_ARG;
+  const qwm_status s = check_table(tab, true);
+  if (s != QWM_OK) return s;
+  DeviceGuard dev(ctx->device);
+  if (dev.err != cudaSuccess) return QWM_ERR_CUDA;
+  return cuda_status(launch_pages_reset(*tab, ctx->num_sms, (cudaStream_t)stream));
+}
+
+qwm_status qwm_pages_update(qwm_ctx *ctx, const qwm_page_table *tab, const int64_t *keep, const int32_t *count, int64_t n,
+                            int32_t *first, int32_t *granted, int64_t *slot, int64_t *at, qwm_stream stream) {
+  if (!ctx || n < 0) return QWM_ERR_ARG;
+  const qwm_status s = check_table(tab, true);
+  if (s != QWM_OK) return s;
+  if (n > kMaxTokens) return QWM_ERR_SHAPE;
+  if (count ? !first || !granted || (n > 0 && (!slot || !at)) : n > 0) return QWM_ERR_ARG;
+  if (!keep && !count) return QWM_OK;
+  if (!aligned_to(keep, 8) || !aligned_to(count, 4) || !aligned_to(first, 4) || !aligned_to(granted, 4) ||
+      !aligned_to(slot, 8) || !aligned_to(at, 8))
+    return QWM_ERR_ALIGN;
+  DeviceGuard dev(ctx->device);
+  if (dev.err != cudaSuccess) return QWM_ERR_CUDA;
+  return cuda_status(launch_pages_update(*tab, log2_of_page(tab->page), keep, count, n, count ? first : nullptr,
+                                         count ? granted : nullptr, slot, at, ctx->status, (cudaStream_t)stream));
+}
+
+qwm_status qwm_paged_write(qwm_ctx *ctx, const qwm_page_pool *pool, const uint16_t *k, const qwm_strides *ks,
+                           const uint16_t *v, const qwm_strides *vs, int64_t n, const int64_t *slot,
+                           const qwm_rope_spec *rope, const int64_t *at, const int32_t *pos, int32_t norm, const float *weight,
+                           int32_t per_head, float eps, qwm_stream stream) {
+  if (!ctx || n < 0) return QWM_ERR_ARG;
+  qwm_status s = check_pool(pool);
+  if (s == QWM_OK && rope) s = check_rope(rope);
+  if (s != QWM_OK) return s;
+  if (norm != 0 && norm != 1) return QWM_ERR_ARG;
+  if (norm ? (s = check_norm(weight, per_head, eps)) != QWM_OK : weight != nullptr) return norm ? s : QWM_ERR_ARG;
+  if (n > kMaxTokens) return QWM_ERR_SHAPE;
+  if (n == 0) return QWM_OK;
+  if ((s = check_packed(k, ks, pool->kv_heads, n, false)) != QWM_OK) return s;
+  if ((s = check_packed(v, vs, pool->kv_heads, n, false)) != QWM_OK) return s;
+  if (!slot || (rope ? !at : at || pos)) return QWM_ERR_ARG;
+  if (!aligned_to(slot, 8) || !aligned_to(at, 8) || !aligned_to(pos, 4)) return QWM_ERR_ALIGN;
+  DeviceGuard dev(ctx->device);
+  if (dev.err != cudaSuccess) return QWM_ERR_CUDA;
+  return cuda_status(launch_paged_write(*pool, log2_of_page(pool->page), k, *ks, v, *vs, n, slot, rope, at, pos, norm, weight,
+                                        weight ? per_head : 0, eps, ctx->num_sms, ctx->status, (cudaStream_t)stream));
+}
+
+qwm_status qwm_paged_read(qwm_ctx *ctx, const qwm_page_pool *pool, const int64_t *slot, int64_t n, uint16_t *k_hat,
+                          uint16_t *v_hat, qwm_stream stream) {
+  if (!ctx || n < 0) return QWM_ERR_ARG;
+  const qwm_status s = check_pool(pool);
+  if (s != QWM_OK) return s;
+  if (n > kMaxTokens) return QWM_ERR_SHAPE;
+  if (n == 0 || (!k_hat && !v_hat)) return QWM_OK;
+  if (!slot) return QWM_ERR_ARG;
+  if (!aligned_to(slot, 8) || !aligned16(k_hat) || !aligned16(v_hat)) return QWM_ERR_ALIGN;
+  DeviceGuard dev(ctx->device);
+  if (dev.err != cudaSuccess) return QWM_ERR_CUDA;
+  return cuda_status(launch_paged_read(*pool, log2_of_page(pool->page), slot, n, k_hat, v_hat, ctx->num_sms, ctx->status,
+                                       (cudaStream_t)stream));
+}
+
+size_t qwm_paged_attend_workspace(const qwm_ctx *ctx, const qwm_page_pool *pool, int64_t max_count) {
+  if (check_attend(ctx, pool, max_count) != QWM_OK || max_count == 0) return 0;
+  return plan_of(ctx, ctx->cfg.heads / pool->kv_heads, max_count).bytes;
+}
+
+qwm_status qwm_paged_attend(qwm_ctx *ctx, const qwm_page_pool *pool, const qwm_page_table *tab, const uint16_t *q,
+                            const qwm_strides *qs, int64_t n, const int32_t *first, const int32_t *count, int64_t max_count,
+                            int64_t tpf, int64_t frames, int64_t sink, float softmax_scale, void *out, const qwm_strides *os,
+                            int32_t out_f32, float *lse, int32_t merge, void *ws, size_t ws_bytes, qwm_stream stream) {
+  qwm_status s = check_attend(ctx, pool, max_count);
+  if (s == QWM_OK) s = check_pool(pool);
+  if (s == QWM_OK) s = check_table(tab, false);
+  if (s != QWM_OK) return s;
+  if (n < 0 || tab->page != pool->page || tpf < 1 || frames < 1 || sink < 0) return QWM_ERR_ARG;
+  const int H = ctx->cfg.heads, group = H / pool->kv_heads;
+  if (n > kMaxTokens || n * group > kMaxRows || tpf > ((int64_t)1 << 31) || frames > ((int64_t)1 << 31)) return QWM_ERR_SHAPE;
+  if (!(softmax_scale > 0.f) || softmax_scale > 0x1p123f) return QWM_ERR_ARG;   // (times 16 log2(e) it stays finite)
+  if ((out_f32 != 0 && out_f32 != 1) || (merge != 0 && merge != 1)) return QWM_ERR_ARG;
+  if (merge && (!out_f32 || !lse)) return QWM_ERR_ARG;
+  if (n == 0 || max_count == 0) return QWM_OK;
+  if ((s = check_packed(q, qs, H, n, false)) != QWM_OK) return s;
+  if ((s = check_packed(out, os, H, n, true)) != QWM_OK) return s;
+  if (!first || !count) return QWM_ERR_ARG;
+  if (!aligned_to(first, 4) || !aligned_to(count, 4) || !aligned_to(lse, 4)) return QWM_ERR_ALIGN;
+  const Plan p = plan_of(ctx, group, max_count);
+  if (!ws || ws_bytes < p.bytes) return QWM_ERR_ARG;
+  if (!aligned16(ws)) return QWM_ERR_ALIGN;
+  DeviceGuard dev(ctx->device);
+  if (dev.err != cudaSuccess) return QWM_ERR_CUDA;
+  PagedAttend a;
+  a.pool = *pool;
+  a.table = tab->table; a.length = tab->length;
+  a.batch = tab->batch; a.width = tab->width; a.page_log2 = log2_of_page(tab->page);
+  a.q = q; a.qs = *qs; a.n = (int)n;
+  a.first = first; a.count = count; a.max_count = (int)max_count;
+  a.tpf = tpf; a.frames = frames;
+  a.sink = sink < kPagedMaxTokens ? sink : kPagedMaxTokens;   // (no sequence is longer)
+  a.scale_log2 = softmax_scale * 1.4426950408889634f;
+  a.out = out; a.os = *os; a.out_f32 = out_f32; a.merge = merge; a.lse = lse;
+  a.status = ctx->status;
+  a.group = group;
+  a.shares = p.shares;
+  const int part_rows = 8 * p.row_tiles;
+  a.part = (float *)ws;
+  a.part_lse = a.part + (size_t)2 * p.shares * part_rows * QWM_D;
+  a.cuts = (PagedCut *)(a.part_lse + (size_t)2 * p.shares * part_rows);
+  a.bases = win::kBases;
+  const cudaStream_t st = (cudaStream_t)stream;
+  cudaError_t e = launch_paged_decode(a, p.row_tiles, st);
+  if (e == cudaSuccess) e = launch_paged_combine(a, part_rows, st);
+  return cuda_status(e);
+}
+
+}  // extern "C"

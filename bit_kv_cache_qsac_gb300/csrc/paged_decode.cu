@@ -1,0 +1,251 @@
+// Attention over a paged cache on warp tiles, for sequences with few new rows (single tokens, drafted tokens,
+// grouped heads), and the joining of parts.
+//
+// A row r of a Key head is (token r / group, head r % group of the group); an item is one Key head of one
+// sequence with up to 8 NT of its rows.  The work is bound by the cache's bytes and sequences differ in
+// length, so it is shared out by the key: every CTA takes an equal piece of the line of all items
+// (pgd::share_of).  An item that a cut goes through is computed in parts, which a second kernel joins.
+// Inside a CTA an item's keys go to the 8 warps in turn, 16 or 32 at a time, copied to a ring of shared
+// memory of the warp's own two steps ahead (cp.async; no barrier but the warp's) and multiplied on warp
+// MMAs (warp_tile.cuh).  16 keys from a multiple of 16 lie in one page.
+#include "paged.cuh"
+#include "warp_tile.cuh"
+
+namespace {
+
+constexpr int D = win::D;
+using wt::kWarps;
+using wt::Ring;
+constexpr int kThreads = 32 * kWarps;
+template <int BITS>
+constexpr int kBlock = kWarps * wt::step_keys(BITS);   // keys that the 8 warps take at once
+// What an item costs besides its keys, in blocks, and the least piece of an item worth its own start.
+constexpr int kStart = 4, kLeast = 2, kThin = 6;
+
+template <int BITS, int NT>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) paged_decode_kernel(const __grid_constant__ PagedAttend a) {
+  using R = Ring<BITS>;
+  constexpr int kKeys = R::kKeys, kSub = kKeys / 16;   // MMA rows of 16 keys in a step
+  extern __shared__ __align__(16) unsigned char dyn_raw[];
+  // stages start on 128-byte boundaries: permuted addresses are reached by flipping bits
+  unsigned char *dyn = dyn_raw + ((128u - (tc::smem_u32(dyn_raw) & 127u)) & 127u);
+  __shared__ float msm[kWarps][8 * NT], lsm[kWarps][8 * NT];
+  __shared__ PagedCut cut[2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the joining kernel may line up
+  auto load_of = [&](int b) -> pgd::Load {
+    const pgd::Seq q = pgd::sequence(a, b);
+    if (q.rows == 0) return {0, 0};
+    pgd::Keys keys;
+    keys.init(a, q.s, q.frame(a, 0), q.frame(a, q.rows - 1));
+    return {(keys.total + kBlock<BITS> - 1) / kBlock<BITS>, a.pool.kv_heads * ((q.rows + 8 * NT - 1) / (8 * NT))};
+  };
+  pgd::share_of<kThreads>(a.batch, (int)blockIdx.x, a.shares, kStart, kLeast, kThin, load_of, cut);
+  __syncthreads();
+  const PagedCut end = cut[1];
+  int b = cut[0].b, item = cut[0].item, block = cut[0].block;
+  wt::Tile<BITS, NT> tile;
+  tile.place(lane);
+
+  const uint32_t ring0 = tc::smem_u32(dyn) + (uint32_t)(warp * R::kStages * R::kStage);
+  constexpr int kPer = R::kRow / 16, kCopies = kKeys * kPer / 32;   // pieces of a row; copies of a lane and tensor
+  const int srow = lane & 15;
+  const uint32_t kdst = R::k_at(lane / kPer, lane & (kPer - 1));   // k_at(row + 32 / kPer, .) is 512 further on
+  // v_at(row + 32 / kPer, .) is 512 further on but for the permutation: one piece bit flips per 4 rows
+  const uint32_t vdst = R::v_at(lane / kPer, lane & (kPer - 1));
+  auto vdst_of = [&](int i) -> uint32_t { return (vdst ^ (BITS == 8 ? 32u * (i & 3) : 64u * (i & 1))) + 512u * i; };
+
+  bool began = false;   // the share's first cut is written down for the joining kernel
+  while (b < a.batch) {
+    const pgd::Seq q = pgd::sequence(a, b);
+    const int tiles = (q.rows + 8 * NT - 1) / (8 * NT), items = a.pool.kv_heads * tiles;
+    if (item >= items) {   // the next sequence
+      if (b >= end.b) break;
+      b++;
+      item = block = 0;
+      continue;
+    }
+    if (b > end.b || (b == end.b && (item > end.item || (item == end.item && end.block == 0)))) break;
+    const int kvh = item / tiles, row0 = (item - kvh * tiles) * 8 * NT;
+    const int rows = q.rows - row0 < 8 * NT ? q.rows - row0 : 8 * NT;
+    if (!began && threadIdx.x == 0)
+      a.cuts[blockIdx.x] = PagedCut{b, item, block, q.first, kvh, row0, rows};
+    began = true;
+    const int64_t f0 = q.frame(a, 0), f1 = q.frame(a, q.rows - 1);
+    pgd::Keys keys;
+    keys.init(a, q.s, f0, f1);
+    const int blocks = (keys.total + kBlock<BITS> - 1) / kBlock<BITS>;
+    const bool last = b == end.b && item == end.item;
+    const int block1 = last ? end.block : blocks;
+    const int j1 = block1 * kWarps < (keys.total + kKeys - 1) / kKeys ? block1 * kWarps : (keys.total + kKeys - 1) / kKeys;
+
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++) {
+      const int r = row0 + 8 * nt + tile.g, i = (int)((uint32_t)r / (uint32_t)a.group);
+      tile.fetch(nt, a.q + (kvh * a.group + (r - i * a.group)) * a.qs.head + (q.first + i) * a.qs.token, 8 * nt + tile.g < rows);
+    }
+    // ---- copies of step j's keys into a stage of the warp's ring (one group) ----
+    const int32_t *table = a.table + (int64_t)b * a.width;
+    auto copy = [&](int j, int stage) {
+      if (j < j1) {
+        const uint32_t dst = ring0 + (uint32_t)(stage * R::kStage);
+        // each 16 keys (those past the last key repeat its 16): the row of the first, and how many rows follow it
+        int64_t at[kSub];
+        int follow[kSub];
+#pragma unroll
+        for (int u = 0; u < kSub; u++) {
+          const int v = j * kKeys + 16 * u < keys.total ? j * kKeys + 16 * u : (keys.total - 1) & -16;
+          const int p = keys.token(v);
+          at[u] = pgd::page_row(a, pgd::checked(a, table[p >> a.page_log2]), kvh) + (p & ((1 << a.page_log2) - 1));
+          follow[u] = keys.total - 1 - v;
+        }
+#pragma unroll
+        for (int i = 0; i < kCopies; i++) {
+          const int u = kSub == 2 && i >= kCopies / 2 ? 1 : 0, row = (32 * i + lane) / kPer - 16 * u;
+          const int64_t src = (at[u] + (row < follow[u] ? row : follow[u])) * R::kRow + 16 * (lane & (kPer - 1));
+          wt::cp_async16(dst + kdst + 512u * i, a.pool.k_codes + src);
+          wt::cp_async16(dst + vdst_of(i), a.pool.v_codes + src);
+        }
+#pragma unroll
+        for (int u = 0; u < kSub; u++) {   // lanes 0-15: the Keys' step words, 16-31: the Values'
+          const int64_t src = (at[u] + (srow < follow[u] ? srow : follow[u])) * win::kSteps;
+          wt::cp_async4(dst + (lane < 16 ? R::kKS : R::kVS) + 4u * (srow + 16 * u), (lane < 16 ? a.pool.k_step : a.pool.v_step) + src);
+        }
+      }
+      tc::cp_async_commit();
+    };
+    const int j0 = block * kWarps + warp;
+    copy(j0, 0);
+    copy(j0 + kWarps, 1);
+    pgd::Everyone every;
+    every.init(q.s, keys, q.frame(a, row0), q.frame(a, row0 + rows - 1));
+    tile.begin(rows, a.scale_log2, a.status);
+    auto mask_of = [&](int r) {
+      pgd::Row mask;
+      mask.init(q.s, keys, r < rows ? q.frame(a, row0 + r) : -1);
+      return mask;
+    };
+    int stage = 0;
+    for (int j = j0; j < j1; j += kWarps) {
+      tc::cp_async_wait<1>();
+      __syncwarp();   // the step's copies are there, and the stage before it has been read by every lane
+      copy(j + 2 * kWarps, stage == 0 ? 2 : stage - 1);
+      const uint32_t st = ring0 + (uint32_t)(stage * R::kStage);
+      stage = stage == 2 ? 0 : stage + 1;
+      tile.step(st, j * kKeys, every.see(j * kKeys, j * kKeys + kKeys), mask_of, a.bases);
+    }
+    tc::cp_async_wait<0>();
+    __syncthreads();   // the rings are done with: their memory takes the warps' outputs
+
+    // ---- the warps' parts joined in shared memory ----
+    float (*osm)[8][D] = (float (*)[8][D])dyn;
+    tile.sums(msm[warp], lsm[warp]);
+    const bool part = block > 0 || block1 < blocks;
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++) {
+      if (8 * nt >= rows) break;
+      if (nt) __syncthreads();
+      tile.outputs(nt, rows, osm[warp]);
+      __syncthreads();
+      const int r = 8 * nt + warp, ch = 4 * lane;   // warp = row, lane = four channels
+      if (r < rows) {
+        float M, L;
+        float4 acc = wt::join(msm, lsm, r, [&](int w) { return *(const float4 *)&osm[w][warp][ch]; }, M, L);
+        const float inv = L > 0.f ? win::kUnit<BITS> / L : 0.f, lse = L > 0.f ? M + log2f(L) : -INFINITY;
+        acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+        if (!part) {
+          const int i = (row0 + r) / a.group, h = kvh * a.group + (row0 + r - i * a.group);
+          pgd::finish4(a, q.first + i, h, ch, acc, lse);
+          __syncwarp();   // merging lanes have read the earlier log-sum-exp
+          if (lane == 0) pgd::finish_lse(a, q.first + i, h, lse);
+        } else {   // an item's first part in the share's second place, any other in its first
+          const int64_t pr = ((int64_t)blockIdx.x * 2 + (block == 0 ? 1 : 0)) * 8 * NT + r;
+          *(float4 *)(a.part + pr * D + ch) = acc;
+          if (lane == 0) a.part_lse[pr] = lse;
+        }
+      }
+    }
+    __syncthreads();
+    item++;
+    block = 0;
+    if (last) break;
+  }
+  if (!began && threadIdx.x == 0) a.cuts[blockIdx.x] = PagedCut{a.batch, 0, 0, 0, 0, 0, 0};
+}
+
+// Parts of an item joined: the weighted mean of the parts' outputs, each weighted by its share of the
+// exponential sum.  Blocks of 8 warps, one warp per row; blockIdx.x: the share whose beginning cuts the item
+// first, blockIdx.y: 8 of the item's rows.
+__global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constant__ PagedAttend a, int part_rows) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // launched while the parts are computed: wait for them
+  const int s = (int)blockIdx.x + 1, lane = threadIdx.x & 31, r = (int)blockIdx.y * 8 + (threadIdx.x >> 5);
+  const PagedCut c = a.cuts[s];
+  if (c.block == 0 || r >= c.live) return;
+  const PagedCut before = a.cuts[s - 1];
+  if (before.b == c.b && before.item == c.item && before.block > 0) return;   // an earlier cut of the item
+  int last = s;   // the item's last part is this share's first
+  while (last + 1 < a.shares) {
+    const PagedCut d = a.cuts[last + 1];
+    if (d.b != c.b || d.item != c.item || d.block == 0) break;
+    last++;
+  }
+  // parts: the second place of share s - 1, then the first places of shares s .. last
+  auto place = [&](int k) -> int64_t { return ((int64_t)(k < s ? 2 * k + 1 : 2 * k)) * part_rows + r; };
+  float M = -INFINITY;
+  for (int k = s - 1; k <= last; k++) M = fmaxf(M, a.part_lse[place(k)]);
+  float L = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (M > -INFINITY) {
+#pragma unroll 4
+    for (int k = s - 1; k <= last; k++) {
+      const float wt = exp2f(a.part_lse[place(k)] - M);
+      const float4 x = *(const float4 *)(a.part + place(k) * D + 4 * lane);
+      L += wt;
+      acc.x = fmaf(x.x, wt, acc.x);
+      acc.y = fmaf(x.y, wt, acc.y);
+      acc.z = fmaf(x.z, wt, acc.z);
+      acc.w = fmaf(x.w, wt, acc.w);
+    }
+    const float inv = 1.f / L;
+    acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+  }
+  const float lse = L > 0.f ? M + log2f(L) : -INFINITY;
+  const int i = (c.row + r) / a.group, token = c.first + i, h = c.kvh * a.group + (c.row + r - i * a.group);
+  pgd::finish4(a, token, h, 4 * lane, acc, lse);
+  __syncwarp();
+  if (lane == 0) pgd::finish_lse(a, token, h, lse);
+}
+
+template <int BITS, int NT>
+cudaError_t decode_launch(const PagedAttend &a, cudaStream_t st) {
+  auto kernel = paged_decode_kernel<BITS, NT>;
+  static std::atomic<uint64_t> allowed{0};
+  const cudaError_t e = allow_shared(kernel, Ring<BITS>::kBytes, allowed);
+  if (e != cudaSuccess) return e;
+  kernel<<<a.shares, kThreads, Ring<BITS>::kBytes, st>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+// row_tiles: 1 (8 rows an item) or 2 (16).
+int paged_decode_shares(int row_tiles, int num_sms) { return (row_tiles == 1 ? 2 : 1) * num_sms; }
+
+cudaError_t launch_paged_decode(const PagedAttend &a, int row_tiles, cudaStream_t st) {
+  if (row_tiles == 1) return a.pool.bits == 8 ? decode_launch<8, 1>(a, st) : decode_launch<4, 1>(a, st);
+  return a.pool.bits == 8 ? decode_launch<8, 2>(a, st) : decode_launch<4, 2>(a, st);
+}
+
+// Launched as a dependent of the parts' kernel, so that its start-up overlaps their work.
+cudaError_t launch_paged_combine(const PagedAttend &a, int part_rows, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.shares - 1), (unsigned)(part_rows / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_combine_kernel, a, part_rows);
+}

@@ -14,68 +14,6 @@ namespace {
 
 constexpr int kThreads = 256, kRows = kThreads / 16, kReadRows = kThreads / 8;
 
-// Eight bf16 channels of a row (4 words) -> this lane's code bytes (8 bits: c0, c1; 4 bits: c0) and the
-// group's step byte.  Every lane of the warp takes part.
-template <int BITS>
-__device__ __forceinline__ void quantise(const uint32_t (&w)[4], uint32_t &c0, uint32_t &c1, uint32_t &step,
-                                         bool &bad) {
-  constexpr float kTop = win::code_max(BITS) * (BITS == 8 ? 56.f : 896.f);
-  uint32_t m = win::max_abs_bf16x2(win::max_abs_bf16x2(w[0], w[1]), win::max_abs_bf16x2(w[2], w[3]));
-  m = win::max_abs_bf16x2(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  m = win::max_abs_bf16x2(m, __shfl_xor_sync(0xffffffffu, m, 2));
-  m = win::max_abs_bf16x2(m, m >> 16);
-  float amax = __uint_as_float((m & 0x7FFFu) << 16), f[8], s;
-#pragma unroll
-  for (int i = 0; i < 4; i++) {
-    f[2 * i] = __uint_as_float(w[i] << 16);
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
-  step = win::normal_step<BITS>(amax, s);
-  const bool out = !(amax <= kTop);   // out of range or NaN, somewhere in the group
-  if (__any_sync(0xffffffffu, out || win::step_is_small<BITS>(amax))) {
-    if (out) {   // cut to the range, NaN to 0
-      bad = true;
-      amax = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; i++) {
-        f[i] = isnan(f[i]) ? 0.f : fminf(fmaxf(f[i], -kTop), kTop);
-        amax = fmaxf(amax, fabsf(f[i]));
-      }
-    }
-    float a = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    amax = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
-    step = win::step_is_small<BITS>(amax) ? win::small_step<BITS>(amax, s) : win::normal_step<BITS>(amax, s);
-  }
-  float inv;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
-  inv = s > 0.f ? inv : 0.f;
-  const uint64_t inv2 = win::pair2(inv, inv);
-  uint32_t c[8];   // 0x4B400000 + code
-#pragma unroll
-  for (int i = 0; i < 4; i++) {
-    const float2 v = win::split2(win::codes_of(win::pair2(f[2 * i], f[2 * i + 1]), inv2));
-    c[2 * i] = __float_as_uint(v.x);
-    c[2 * i + 1] = __float_as_uint(v.y);
-  }
-  if (BITS == 8) {   // low bytes, biased by 128: the sign bit flips
-    c0 = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410) ^ 0x80808080u;
-    c1 = __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410) ^ 0x80808080u;
-  } else {   // channel 2 k + t in nibble k + 4 t: the sum of (0x4B400000 + code) 16^n, less that of the
-             // constants (modulo 2^32) and with 8 added in every nibble
-    c0 = ((((((c[7] * 16u + c[5]) * 16u + c[3]) * 16u + c[1]) * 16u + c[6]) * 16u + c[4]) * 16u + c[2]) * 16u + c[0] +
-         (0x88888888u - 0x3F400000u);
-    c1 = 0u;
-  }
-}
-
-template <int BITS>
-__device__ __forceinline__ void store_row(uint8_t *codes, uint8_t *steps, int64_t slot_row, int v, uint32_t c0,
-                                          uint32_t c1, uint32_t step) {
-  if (BITS == 8) *(uint2 *)(codes + slot_row * win::D + 8 * v) = make_uint2(c0, c1);
-  else *(uint32_t *)(codes + slot_row * (win::D / 2) + 4 * v) = c0;
-  if ((v & 3) == 0) steps[slot_row * win::kSteps + (v >> 2)] = (uint8_t)step;
-}
-
 // TURN: -1 Keys are stored as they come, else the pairing they are turned by (WHOLE: all channels).
 template <int BITS, int TURN, bool WHOLE>
 __global__ void __launch_bounds__(kThreads)
@@ -123,33 +61,13 @@ __global__ void __launch_bounds__(kThreads)
     }
     if (TURN >= 0) rv.turn(sp, kw);
     uint32_t c0, c1, step;
-    quantise<BITS>(kw, c0, c1, step, bad);
-    if (live) store_row<BITS>(w.k_codes, w.k_step, slot_row, v, c0, c1, step);
-    quantise<BITS>(vw, c0, c1, step, bad);
-    if (live) store_row<BITS>(w.v_codes, w.v_step, slot_row, v, c0, c1, step);
+    win::quantise<BITS>(kw, c0, c1, step, bad);
+    if (live) win::store_row<BITS>(w.k_codes, w.k_step, slot_row, v, c0, c1, step);
+    win::quantise<BITS>(vw, c0, c1, step, bad);
+    if (live) win::store_row<BITS>(w.v_codes, w.v_step, slot_row, v, c0, c1, step);
     slot_row += slots;
   }
   if (bad && live) qwm_dev_error(status, QWM_ERR_RANGE);
-}
-
-// Eight channels of a cached row -> bf16 (4 words).
-template <int BITS>
-__device__ __forceinline__ uint4 restore(uint2 x, uint32_t step, const win::Bases &bases) {
-  uint32_t pr[4], o[4];
-  const win::Step st = win::step_of_byte<BITS>(step);
-  if (BITS == 8) {
-    win::decode8(x.x, st, bases, pr[0], pr[1]);
-    win::decode8(x.y, st, bases, pr[2], pr[3]);
-  } else {
-    win::decode4(x.x, st, bases, pr);
-  }
-#pragma unroll
-  for (int u = 0; u < 4; u++) {
-    if (BITS == 4) pr[u] = win::hmul2(pr[u], 0x4C004C00u);   // times the unit, 16
-    const float2 f = __half22float2(*(const __half2 *)&pr[u]);
-    o[u] = tc::pack_bf16x2(f.x, f.y);
-  }
-  return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 // Eight lanes take a row, vectors v and v + 8 of it each, so that every store instruction writes whole
@@ -197,8 +115,8 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
     for (int t = 0; t < 2; t++) {
       if (!dst[t]) continue;
-      *(uint4 *)dst[t] = restore<BITS>(x[t][0], (st[t] >> (8 * (v >> 2))) & 0xFFu, bases);
-      *(uint4 *)(dst[t] + 64) = restore<BITS>(x[t][1], (st[t] >> (8 * (2 + (v >> 2)))) & 0xFFu, bases);
+      *(uint4 *)dst[t] = win::restore<BITS>(x[t][0], (st[t] >> (8 * (v >> 2))) & 0xFFu, bases);
+      *(uint4 *)(dst[t] + 64) = win::restore<BITS>(x[t][1], (st[t] >> (8 * (2 + (v >> 2)))) & 0xFFu, bases);
       dst[t] += n * win::D;
     }
   }
