@@ -27,7 +27,8 @@ struct PagedAttend {
   float *lse;
   int32_t *status;
   int group;                    // Query heads per Key head; row r of a Key head is (token r / group, head r % group)
-  int shares;                   // shares the work is cut into: CTAs
+  int few;                      // rows of a Key head up to which a sequence goes to the warp tiles
+  int shares;                   // shares the work is cut into: CTAs, or CTA pairs
   struct PagedCut *cuts;        // [shares] where each share begins
   float *part;                  // [2 shares][part_rows][128] outputs of the parts of split items,
   float *part_lse;              // [2 shares][part_rows] their log-sum-exps
@@ -40,9 +41,14 @@ struct PagedCut {
   int b, item, block, first, kvh, row, live;
 };
 
-cudaError_t launch_paged_decode(const PagedAttend &a, int row_tiles, cudaStream_t st);
-cudaError_t launch_paged_combine(const PagedAttend &a, int part_rows, cudaStream_t st);
+// Warp tiles of 8 (row_tiles 1) or 16 rows (2).  beside: the tile kernel was launched just before it.
+cudaError_t launch_paged_decode(const PagedAttend &a, int row_tiles, bool beside, cudaStream_t st);
 int paged_decode_shares(int row_tiles, int num_sms);
+// Tensor-memory tiles: items of kPagedTileRows rows, a CTA pair a share.
+constexpr int kPagedTileRows = 512;
+cudaError_t launch_paged_tiles(const PagedAttend &a, cudaStream_t st);
+// Joins the parts of either kernel's split items, or both's (null: was not launched), part_rows rows each.
+cudaError_t launch_paged_combine(const PagedAttend *few, int part_rows, const PagedAttend *many, cudaStream_t st);
 
 namespace pgd {
 
@@ -175,38 +181,26 @@ __device__ __forceinline__ void finish_lse(const PagedAttend &a, int token, int 
 }  // namespace pgd
 
 // ------------------------------------------------------------------ how the work is shared out
-// All items of the sequences an attention kernel takes stand in one line, by sequence, each as long as its
-// blocks of keys plus `start`, what an item costs besides (in blocks).  Share i begins at i / shares of the
-// line; a cut less than `least` blocks into an item, or less than that from its end, is moved to the item's
-// border.  Every CTA works out its own two cuts in the same way, so nothing is written down beforehand.
+// All items of the sequences an attention kernel takes stand in one line, by sequence, each as long as what its
+// keys and its start and end cost.  Share i begins at i / shares of the line; a cut close to an item's border is
+// moved there.  Every CTA works out its own two cuts in the same way, so nothing is written down beforehand.
 namespace pgd {
 
-struct Load {
-  int blocks, items;   // of a sequence: blocks of keys of an item, and how many items
-};
-
-// Where place x of the line falls in sequence b (x counted from the sequence's first item).
-__device__ __forceinline__ void cut_at(const Load &w, int64_t x, int start, int least, int &item, int &block) {
-  const int64_t cost = w.blocks + start;
-  item = (int)win::quotient(x, cost);
-  block = (int)(x - item * cost) - start;
-  if (block < least) block = 0;
-  else if (w.blocks - block < least) {
-    block = 0;
-    item++;
-  }
+// An item of `blocks` blocks of keys costs start + blocks * each.  Where place x (counted from the item's begin) cuts
+// it: 0, a block at least `least` from both ends, or `blocks` (its end).
+__device__ __forceinline__ int cut_item(int64_t x, int blocks, int start, int each, int least) {
+  const int block = x < start ? 0 : (int)win::quotient(x - start, each);
+  return block < least ? 0 : (blocks - block < least ? blocks : block);
 }
 
-// The cuts of share `share` of `shares` (begin, end), found by the whole block of THREADS threads; `load(b)` is
-// the work of sequence b.  Fewer shares are used when they would fall below `thin` blocks each.  A share
-// without work begins and ends at sequence `batch`.
-template <int THREADS, typename LoadOf>
-__device__ __forceinline__ void share_of(int batch, int share, int shares, int start, int least, int thin, LoadOf load,
-                                         PagedCut (&cut)[2]) {
+// The cuts of share `share` of `shares` (begin, end), found by the whole block of THREADS threads.  work.cost(b) is
+// the length of sequence b's items, work.cut(b, x, item, block) where place x of them falls.  Fewer shares are
+// used when they would be shorter than `thin`.  A share without work begins and ends at sequence `batch`.
+template <int THREADS, typename Work>
+__device__ __forceinline__ void share_of(int batch, int share, int shares, int thin, const Work &work, PagedCut (&cut)[2]) {
   constexpr int kW = THREADS / 32;
   __shared__ int64_t sums[kW + 1];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  auto cost_of = [&](const Load &w) -> int64_t { return (int64_t)w.items * (w.blocks + start); };
   // the running sum of v over the block's threads, and the total
   auto scan = [&](int64_t v, int64_t &total) -> int64_t {
     int64_t s = v;
@@ -229,36 +223,36 @@ __device__ __forceinline__ void share_of(int batch, int share, int shares, int s
     return before + s;
   };
   if (tid < 2) cut[tid] = PagedCut{batch, 0, 0, 0, 0, 0, 0};
-  Load w = tid < batch ? load(tid) : Load{0, 0};
-  int64_t total, upto = scan(cost_of(w), total);
+  int64_t mine = tid < batch ? work.cost(tid) : 0;
+  int64_t total, upto = scan(mine, total);
   int64_t all = total;
   if (batch > THREADS) {
-    int64_t mine = 0;
-    for (int b = THREADS + tid; b < batch; b += THREADS) mine += cost_of(load(b));
-    int64_t rest;
-    scan(mine, rest);
+    int64_t more = 0, rest;
+    for (int b = THREADS + tid; b < batch; b += THREADS) more += work.cost(b);
+    scan(more, rest);
     all += rest;
   }
-  int64_t used = all / thin;
+  int64_t used = win::quotient(all, thin);
   used = used < 1 ? 1 : (used < shares ? used : shares);
-  if (share >= used || all == 0) return;   // (the same for the whole block)
-  const int64_t x0 = all * share / used, x1 = all * (share + 1) / used;
-  int64_t base = 0;
-  for (int b0 = 0; b0 < batch; b0 += THREADS) {
-    if (b0 > 0) {
-      w = b0 + tid < batch ? load(b0 + tid) : Load{0, 0};
-      upto = scan(cost_of(w), total);
-    }
-    const int64_t end = base + upto, begin = end - cost_of(w);
-#pragma unroll
-    for (int e = 0; e < 2; e++) {
-      const int64_t x = e ? x1 : x0;
-      if (x >= begin && x < end) {
-        cut[e].b = b0 + tid;
-        cut_at(w, x - begin, start, least, cut[e].item, cut[e].block);
+  if (share < used && all > 0) {   // (the same for the whole block)
+    const int64_t x0 = all * share / used, x1 = all * (share + 1) / used;
+    int64_t base = 0;
+    for (int b0 = 0; b0 < batch; b0 += THREADS) {
+      if (b0 > 0) {
+        mine = b0 + tid < batch ? work.cost(b0 + tid) : 0;
+        upto = scan(mine, total);
       }
+      const int64_t end = base + upto, begin = end - mine;
+#pragma unroll
+      for (int e = 0; e < 2; e++) {
+        const int64_t x = e ? x1 : x0;
+        if (x >= begin && x < end) {
+          cut[e].b = b0 + tid;
+          work.cut(b0 + tid, x - begin, cut[e].item, cut[e].block);
+        }
+      }
+      base += total;
     }
-    base += total;
   }
   __syncthreads();
 }

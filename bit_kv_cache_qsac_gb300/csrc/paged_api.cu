@@ -57,19 +57,31 @@ qwm_status check_norm(const float *weight, int32_t per_head, float eps) {
 
 constexpr int64_t kMaxRows = (int64_t)1 << 30;   // rows of a Key head in a packed batch
 
-// How a call is run and what workspace it takes.
+// How a call is run and what workspace it takes.  Sequences with up to `few` rows per Key head go to the warp tiles,
+// which read the cache once per 8 or 16 rows, others to the tensor-memory tiles, which pay for 256 or 512.
 struct Plan {
-  int row_tiles;      // warp tiles of 8 (1) or 16 rows (2) an item
-  int shares;
+  bool few_rows, many_rows;
+  int few, row_tiles;         // warp tiles of 8 (1) or 16 rows (2) an item
+  int shares_few, shares_many;
+  size_t part_few, part_many;   // rows of all parts
   size_t bytes;
 };
 
+constexpr int kFew = 32;
+
 Plan plan_of(const qwm_ctx *ctx, int group, int64_t max_count) {
   Plan p;
-  p.row_tiles = max_count * group <= 8 ? 1 : 2;
-  p.shares = paged_decode_shares(p.row_tiles, ctx->num_sms);
-  const size_t rows = (size_t)2 * p.shares * 8 * p.row_tiles;
-  p.bytes = rows * (QWM_D + 1) * sizeof(float) + (size_t)p.shares * sizeof(PagedCut);
+  const int64_t rows = max_count * group;
+  p.many_rows = rows > kFew;
+  p.few_rows = group <= kFew;
+  p.few = kFew;
+  // one tile for all rows of a sequence; beside longer sequences the few rows are mostly those of one token
+  p.row_tiles = (p.many_rows ? group : rows) <= 8 ? 1 : 2;
+  p.shares_few = p.few_rows ? paged_decode_shares(p.row_tiles, ctx->num_sms) : 0;
+  p.shares_many = p.many_rows ? ctx->num_sms / 2 : 0;
+  p.part_few = (size_t)2 * p.shares_few * 8 * p.row_tiles;
+  p.part_many = (size_t)2 * p.shares_many * kPagedTileRows;
+  p.bytes = (p.part_few + p.part_many) * (QWM_D + 1) * sizeof(float) + (size_t)(p.shares_few + p.shares_many) * sizeof(PagedCut);
   return p;
 }
 
@@ -211,15 +223,24 @@ qwm_status qwm_paged_attend(qwm_ctx *ctx, const qwm_page_pool *pool, const qwm_p
   a.out = out; a.os = *os; a.out_f32 = out_f32; a.merge = merge; a.lse = lse;
   a.status = ctx->status;
   a.group = group;
-  a.shares = p.shares;
-  const int part_rows = 8 * p.row_tiles;
-  a.part = (float *)ws;
-  a.part_lse = a.part + (size_t)2 * p.shares * part_rows * QWM_D;
-  a.cuts = (PagedCut *)(a.part_lse + (size_t)2 * p.shares * part_rows);
+  a.few = p.few;
   a.bases = win::kBases;
+  // the parts' outputs, their log-sum-exps, the cuts; the few rows' first
+  float *part = (float *)ws, *part_lse = part + (p.part_few + p.part_many) * QWM_D;
+  PagedCut *cuts = (PagedCut *)(part_lse + p.part_few + p.part_many);
+  a.shares = p.shares_few;
+  a.part = part;
+  a.part_lse = part_lse;
+  a.cuts = cuts;
+  PagedAttend many = a;
+  many.shares = p.shares_many;
+  many.part = part + p.part_few * QWM_D;
+  many.part_lse = part_lse + p.part_few;
+  many.cuts = cuts + p.shares_few;
   const cudaStream_t st = (cudaStream_t)stream;
-  cudaError_t e = launch_paged_decode(a, p.row_tiles, st);
-  if (e == cudaSuccess) e = launch_paged_combine(a, part_rows, st);
+  cudaError_t e = p.many_rows ? launch_paged_tiles(many, st) : cudaSuccess;
+  if (e == cudaSuccess && p.few_rows) e = launch_paged_decode(a, p.row_tiles, p.many_rows, st);
+  if (e == cudaSuccess) e = launch_paged_combine(p.few_rows ? &a : nullptr, 8 * p.row_tiles, p.many_rows ? &many : nullptr, st);
   return cuda_status(e);
 }
 

@@ -1,0 +1,903 @@
+// Attention over a paged cache for sequences with many new rows (chunks of a prompt, frames), on the tensor
+// cores (tcgen05 + TMEM).
+//
+//   l_ij = scale q_i . k_hat_j over the tokens row i sees, o_i = softmax(l_i) V_hat, with k_hat and v_hat
+// decoded from the 8- or 4-bit pages inside the kernel (exact in fp16; see window.cuh for Queries and weights).
+//
+// An item is one Key head of one sequence with 512 of its rows (row r = token r / group, head r % group) and the
+// keys those rows see between them.  All items stand in one line (pgd::share_of) and a CTA pair (a cluster of two,
+// cta_group::2 MMAs) takes an equal piece of it: whole items, and parts of those that a cut goes through.  So
+// sequences of any lengths, causal items of different lengths and calls of a few items fill all SMs alike.
+// CTA c of a pair holds rows 256 x + 128 c .. + 127 of the two Query tiles x = 0, 1.  The B operand of an
+// M = 256 MMA is split by N, so CTA c decodes only keys 32 c .. 32 c + 31 of every 64 for Q K^T and only
+// channels 64 c .. 64 c + 63 for P V: half of everything.
+// Warp roles of each CTA (14 warps):
+//   warps 0-3, 4-7  softmax of Query tile 0 / 1: thread = Query row = TMEM lane, 64 logits at a time; between
+//                   pieces they write the output and fetch the next Queries;
+//   warps 8-11      producers: codes two stages ahead in registers, table entries three, decoded into swizzled
+//                   stages; they run ahead into the next piece while the last one is written;
+//   warp 12         allocates TMEM; in the even CTA it issues every MMA of the pair, in the odd one it
+//                   passes on to the even one that its producers have filled a stage;
+//   warp 13         walks along the share and describes its pieces to the others, two ahead.
+// An item with up to 256 rows gives both tiles those rows and every other 64 keys each, joined at the end.
+// TMEM (512 columns): S_x as two buffers of 64 keys, P_x over them, O_x.  Keys arrive in stages of 128, decoded
+// in 16 rows of one page at a time; step t issues P V of tile x's keys t, then Q K^T of keys t + 2 into the
+// buffer that frees.  Every wait is bounded (about one second); on expiry QWM_ERR_DEVICE_TIMEOUT is
+// recorded, every role stops, outstanding MMAs are drained and TMEM is freed.
+#include "paged.cuh"
+
+namespace {
+
+constexpr int D = win::D;
+constexpr int BM = 128, BN = 128, NQT = 2;  // Query rows of a CTA tile, keys of a stage, CTA tiles
+constexpr int BS = 64;                      // keys of a step
+constexpr int kSoftmaxWarps = 8, kProdWarp0 = 8, kProdWarps = 4, kMmaWarp = 12, kPlanWarp = 13;
+constexpr int kThreads = 32 * 14;
+constexpr uint64_t kWaitNs = 1000000000ull;
+constexpr float kRescaleThreshold = 8.0f;  // log2 units the maximum may lag behind
+constexpr int kStages = 4;                  // (a power of two)
+constexpr int kRows = kPagedTileRows;       // rows of an item: 2 NQT BM
+static_assert(kRows == 2 * NQT * BM, "");
+
+// What pieces of an item cost, in hundreds of cycles: a stage of 128 keys for two tiles of rows, for one, and starting
+// and ending; the least piece (stages) worth its own start, and the shortest share.
+constexpr int kStageCost = 25, kBriefCost = 14, kStartCost = 110, kLeast = 3, kThin = 220;
+
+// shared-memory map of one CTA (bytes from a 1024-aligned base)
+constexpr int kBlk = BM * 128;             // a [128 rows][64 fp16] swizzled block
+constexpr int kBlkH = 64 * 128;            // a [64 rows][64 fp16] swizzled block
+constexpr int OFF_Q = 0;                   // 2 Query tiles x 2 blocks (channels 0-63, 64-127); outputs on their way out
+constexpr int OFF_K = OFF_Q + NQT * 2 * kBlk;          // stages x 2 blocks [64 keys][64 ch]
+constexpr int OFF_V = OFF_K + kStages * 2 * kBlkH;     // stages x [128 keys][64 ch] (MN-major B)
+constexpr int OFF_POWER = OFF_V + kStages * kBlk;      // the power of two each Query row was multiplied by
+constexpr int kSmemAlloc = OFF_POWER + NQT * BM * 4 + 1024;
+
+// A piece of an item: stages j0 .. j0 + J - 1 of it, as the planning warp describes it.
+struct Piece {
+  int b, kvh, first, seq_rows, row0;   // its sequence; packed row of the first token; rows of a Key head; item's first row
+  int place;                           // 0: whole item; else 1 + the place of the part in the share
+  int j0, J, steps;                    // steps of 64 keys
+  int brief;                           // 256 rows at most: both tiles take them
+  int64_t q0, len;
+  pgd::Keys keys;
+  int done;                            // no piece: the share ends
+};
+
+template <bool B>
+struct Flag {
+  static constexpr bool value = B;
+};
+struct Bars {
+  uint64_t full[kStages], empty[kStages];
+  uint64_t s_full[2][2], p_ready[2][2], pv_done[2][2], q_full, o_done, drain;
+  uint64_t told[2], heard[2];   // a piece's description is there; everyone has read it
+};
+
+__device__ __forceinline__ void fail(int *abort_flag, int32_t *status) {
+  *(volatile int *)abort_flag = 1;
+  qwm_dev_error(status, QWM_ERR_DEVICE_TIMEOUT);
+}
+__device__ __forceinline__ uint64_t pk64(uint32_t lo, uint32_t hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
+  return d;
+}
+__device__ __forceinline__ uint64_t pk64(float lo, float hi) { return pk64(__float_as_uint(lo), __float_as_uint(hi)); }
+// The lowest n bits set (n clamped to 0..32).
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u); }
+// All softmax warps meet; true when any of them says so.
+__device__ __forceinline__ bool softmax_meet(bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)p), "n"(32 * kSoftmaxWarps)
+      : "memory");
+  return r != 0;
+}
+
+// The items of a sequence: Key heads by blocks of 512 rows; later blocks may see more keys.
+struct Work {
+  const PagedAttend &a;
+  __device__ __forceinline__ static int blocks_of(const PagedAttend &a, const pgd::Seq &q, int ib, pgd::Keys &keys) {
+    const int r0 = ib * kRows, r1 = r0 + kRows < q.rows ? r0 + kRows : q.rows;
+    keys.init(a, q.s, q.frame(a, r0), q.frame(a, r1 - 1));
+    return (keys.total + BN - 1) / BN;
+  }
+  __device__ __forceinline__ static bool brief(const pgd::Seq &q, int ib) { return ib * kRows + 2 * BM >= q.rows; }
+  __device__ __forceinline__ static int each(const pgd::Seq &q, int ib) { return brief(q, ib) ? kBriefCost : kStageCost; }
+  __device__ __forceinline__ static int count(const PagedAttend &a, const pgd::Seq &q) {   // blocks of rows
+    return q.rows > a.few ? (q.rows + kRows - 1) / kRows : 0;
+  }
+  __device__ __forceinline__ int64_t head_cost(const pgd::Seq &q, int n) const {
+    int64_t c = 0;
+    for (int ib = 0; ib < n; ib++) {
+      pgd::Keys keys;
+      c += kStartCost + (int64_t)blocks_of(a, q, ib, keys) * each(q, ib);
+    }
+    return c;
+  }
+  __device__ __noinline__ int64_t cost(int b) const {
+    const pgd::Seq q = pgd::sequence(a, b);
+    const int n = count(a, q);
+    return n ? head_cost(q, n) * a.pool.kv_heads : 0;
+  }
+  __device__ __noinline__ void cut(int b, int64_t x, int &item, int &block) const {
+    const pgd::Seq q = pgd::sequence(a, b);
+    const int n = count(a, q);
+    const int64_t head = head_cost(q, n);
+    const int kvh = (int)win::quotient(x, head);
+    x -= kvh * head;
+    for (int ib = 0;; ib++) {
+      pgd::Keys keys;
+      const int blocks = blocks_of(a, q, ib, keys);
+      const int64_t c = kStartCost + (int64_t)blocks * each(q, ib);
+      if (x < c || ib + 1 == n) {
+        item = kvh * n + ib;
+        block = pgd::cut_item(x, blocks, kStartCost, each(q, ib), kLeast);
+        if (block == blocks && block > 0) {
+          item++;
+          block = 0;
+        }
+        return;
+      }
+      x -= c;
+    }
+  }
+};
+
+// Where one Query row's result goes (a whole item: out and lse, else the part's workspace).
+struct RowOut {
+  float *f32 = nullptr;
+  uint16_t *bf16 = nullptr;
+  float *lse = nullptr;
+  int merge = 0;
+  __device__ __forceinline__ void init(const PagedAttend &a, const Piece &p, int share, int r) {   // r: row of the item
+    if (p.place) {
+      const int64_t pr = ((int64_t)share * 2 + p.place - 1) * kRows + r;
+      f32 = a.part + pr * D;
+      lse = a.part_lse + pr;
+      return;
+    }
+    const int i = (int)((uint32_t)(p.row0 + r) / (uint32_t)a.group), h = p.kvh * a.group + (p.row0 + r - i * a.group);
+    const int64_t at = h * a.os.head + (int64_t)(p.first + i) * a.os.token;
+    if (a.out_f32) f32 = (float *)a.out + at;
+    else bf16 = (uint16_t *)a.out + at;
+    if (a.lse) lse = a.lse + (int64_t)h * a.n + p.first + i;
+    merge = a.merge;
+  }
+};
+
+// A producer thread's share of a 128-key stage: four pieces of 16 channels.
+template <int BITS>
+struct Codes {
+  uint32_t c[4][BITS / 2];
+  uint32_t step[4];
+};
+
+// One producer thread's side of Keys or Values in CTA cr of a pair.  Keys: rows r = 16 w + 4 i + lane / 4 % 4
+// (i = 0..3) of the CTA's half, key 64 (r / 32) + 32 cr + r % 32, channels 16 (lane % 4 + 4 (lane / 16)): 16
+// neighbours for a warp; Values: key rows 32 w + 8 i + lane / 4, channels 64 cr + 16 (lane % 4): twice 16.  A quarter
+// warp's 16-byte stores take two rows, one of even and one of odd number, so the swizzle puts them into eight
+// bank groups.
+template <int BITS, bool VAL>
+struct Producer {
+  static constexpr int kRowStep = VAL ? 8 : 4, kGroups = VAL ? 2 : 1;
+  static constexpr uint32_t kStage = VAL ? (uint32_t)kBlk : 2u * kBlkH;
+  static constexpr int kRowBytes = D * BITS / 8;
+  const uint8_t *codes, *steps;   // of the pool's row `row0 % 16`, this thread's channels
+  int key0, row0;                 // first key of the warp's 16; this thread's row in them
+  uint32_t dst[2][2];             // shared addresses of the piece's two chunks in even and odd rows i
+
+  __device__ __forceinline__ Producer(const PagedAttend &a, unsigned char *sm, int cr, int w, int lane) {
+    const int row = VAL ? 32 * w + (lane >> 2) : 16 * w + ((lane >> 2) & 3);
+    const int piece = VAL ? (lane & 3) : (lane & 3) + 4 * (lane >> 4);
+    const int ch = VAL ? 64 * cr + 16 * piece : 16 * piece;
+    const int key = VAL ? row : BS * (w >> 1) + 32 * cr + (row & 31);
+    row0 = key & 15;
+    key0 = key - row0;
+    codes = (VAL ? a.pool.v_codes : a.pool.k_codes) + row0 * kRowBytes + ch * BITS / 8;
+    steps = (VAL ? a.pool.v_step : a.pool.k_step) + row0 * win::kSteps + ch / win::kGroup;
+    const uint32_t block = tc::smem_u32(sm + (VAL ? OFF_V : OFF_K)) + (VAL ? 0u : (uint32_t)(piece >> 2) * kBlkH);
+#pragma unroll
+    for (int i = 0; i < 2; i++)
+#pragma unroll
+      for (int h = 0; h < 2; h++) {
+        const uint32_t r = (uint32_t)(row + kRowStep * i), chunk = 2u * (uint32_t)(piece & 3) + h;
+        dst[i][h] = block + r * 128u + ((chunk ^ (r & 7u)) << 4);
+      }
+  }
+  // The table entries of the stage of keys v0 .. v0 + 127.
+  __device__ __forceinline__ void look(const PagedAttend &a, const pgd::Keys &keys, const int32_t *table, int v0,
+                                       int (&entry)[kGroups]) const {
+#pragma unroll
+    for (int g = 0; g < kGroups; g++) {
+      const int v = v0 + key0 + 16 * g;
+      entry[g] = v < keys.total ? __ldg(table + (keys.token(v) >> a.page_log2)) : 0;
+    }
+  }
+  // The codes of that stage; rows past the last key are zeros.
+  __device__ __forceinline__ void load(const PagedAttend &a, const pgd::Keys &keys, int kvh, int v0, const int (&entry)[kGroups],
+                                       Codes<BITS> &p) const {
+#pragma unroll
+    for (int g = 0; g < kGroups; g++) {
+      const int v = v0 + key0 + 16 * g;
+      const int64_t at = pgd::page_row(a, pgd::checked(a, entry[g]), kvh) + (keys.token(v) & ((1 << a.page_log2) - 1));
+      const uint8_t *c = codes + at * kRowBytes, *s = steps + at * win::kSteps;
+#pragma unroll
+      for (int k = 0; k < 4 / kGroups; k++) {
+        const int i = g * (4 / kGroups) + k;
+        p.step[i] = 0u;
+#pragma unroll
+        for (int u = 0; u < BITS / 2; u++) p.c[i][u] = 0u;
+        if (v + row0 + k * kRowStep < keys.total) {
+          if (BITS == 8) {
+            const uint4 x = __ldg((const uint4 *)(c + k * kRowStep * kRowBytes));
+            p.c[i][0] = x.x; p.c[i][1] = x.y; p.c[i][2 % (BITS / 2)] = x.z; p.c[i][3 % (BITS / 2)] = x.w;
+          } else {
+            const uint2 x = __ldg((const uint2 *)(c + k * kRowStep * kRowBytes));
+            p.c[i][0] = x.x; p.c[i][1] = x.y;
+          }
+          p.step[i] = __ldg(s + k * kRowStep * win::kSteps);
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void store(uint32_t stage, const Codes<BITS> &p, const win::Bases &bases) const {
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      uint32_t d[8];
+      const win::Step st = win::step_of_byte<BITS>(p.step[i]);
+      if (BITS == 8) {
+#pragma unroll
+        for (int u = 0; u < 4; u++) win::decode8(p.c[i][u % (BITS / 2)], st, bases, d[2 * u], d[2 * u + 1]);
+      } else {
+        uint32_t q[4];
+        win::decode4(p.c[i][0], st, bases, q);
+        d[0] = q[0]; d[1] = q[1]; d[2] = q[2]; d[3] = q[3];
+        win::decode4(p.c[i][1], st, bases, q);
+        d[4] = q[0]; d[5] = q[1]; d[6] = q[2]; d[7] = q[3];
+      }
+      const uint32_t at = stage * kStage + (uint32_t)(i >> 1) * (2u * kRowStep * 128u);
+      tc::sts128(dst[i & 1][0] + at, make_uint4(d[0], d[1], d[2], d[3]));
+      tc::sts128(dst[i & 1][1] + at, make_uint4(d[4], d[5], d[6], d[7]));
+    }
+  }
+};
+
+template <int BITS>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    paged_attend_kernel(const __grid_constant__ PagedAttend a) {
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  unsigned char *sm = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
+  __shared__ Bars bars;
+  __shared__ PagedCut cut[2];
+  __shared__ Piece pieces[2];
+  __shared__ uint32_t tmem_base_sh;
+  __shared__ int abort_flag;
+  __shared__ float2 half_sums[BM];   // short items: maximum and sum of the second tile's rows
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  const int share = (int)(blockIdx.x >> 1), cr = (int)tc::cluster_ctarank();
+  volatile int *abort_v = &abort_flag;
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the kernels behind this one may line up
+  pgd::share_of<kThreads>(a.batch, share, a.shares, kThin, Work{a}, cut);
+  const PagedCut begin = cut[0], end = cut[1];
+  if (begin.b == a.batch || (begin.b == end.b && begin.item == end.item && begin.block == end.block)) {   // both CTAs
+    if (tid == 0 && cr == 0) a.cuts[share] = PagedCut{a.batch, 0, 0, 0, 0, 0, 0};
+    return;
+  }
+  if (warp == kMmaWarp) {
+    if (lane == 0) {
+      for (int i = 0; i < kStages; i++) {
+        // this CTA's producer warps; in the even CTA also the odd one's last warp, which passes on that its
+        // producers are done (a producer's own arrival in the peer would wait for its loads in flight)
+        tc::mbar_init(&bars.full[i], kProdWarps + 1 - cr);
+        tc::mbar_init(&bars.empty[i], 1);
+      }
+      for (int i = 0; i < 2; i++) {
+        for (int k = 0; k < 2; k++) {
+          tc::mbar_init(&bars.s_full[i][k], 1);
+          tc::mbar_init(&bars.p_ready[i][k], 8);   // both CTAs' 4 softmax warps of tile i
+          tc::mbar_init(&bars.pv_done[i][k], 1);
+        }
+        tc::mbar_init(&bars.told[i], 1);
+        tc::mbar_init(&bars.heard[i], kSoftmaxWarps + kProdWarps + 1);
+      }
+      tc::mbar_init(&bars.q_full, 2 * kSoftmaxWarps);    // both CTAs' softmax warps (even CTA's copy used)
+      tc::mbar_init(&bars.o_done, 1);
+      tc::mbar_init(&bars.drain, 1);
+      abort_flag = 0;
+      tc::fence_mbar_init();
+    }
+    __syncwarp();
+    tc::tmem_alloc2(&tmem_base_sh, 512);
+    tc::tmem_relinquish2();
+    tc::fence_before_sync();
+  }
+  __syncthreads();
+  tc::cluster_sync();   // both CTAs' barriers exist, and their tensor memory
+  tc::fence_after_sync();
+  const uint32_t tmem = tmem_base_sh;
+
+  // The description of the share's piece number i (the whole warp; false: someone gave up).
+  auto hear = [&](int i, Piece &p) -> bool {
+    if (!__all_sync(0xffffffffu, tc::mbar_try_wait(&bars.told[i & 1], (i >> 1) & 1))) {
+      if (!tc::mbar_wait(&bars.told[i & 1], (i >> 1) & 1, kWaitNs)) fail(&abort_flag, a.status);
+      if (__any_sync(0xffffffffu, *abort_v != 0)) return false;
+    }
+    p = pieces[i & 1];
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(&bars.heard[i & 1]);
+    return true;
+  };
+
+  const uint32_t powers = tc::smem_u32(sm) + OFF_POWER;
+  if (warp < kSoftmaxWarps) {
+    // ======================= softmax (Query tile x, row = TMEM lane) =======================
+    const int x = warp / 4, sub = warp % 4;
+    const uint32_t lane_addr = (uint32_t)(32 * sub) << 16;
+    const uint32_t tS0 = tmem + lane_addr + 128u * x, tO = tmem + lane_addr + 256u + 128u * x;
+    const uint32_t p_ready0 = tc::mapa(tc::smem_u32(&bars.p_ready[x][0]), 0);
+    const uint32_t q_full = tc::mapa(tc::smem_u32(&bars.q_full), 0);
+    // this thread's piece of row tid / 16 of tile 0; 16 rows on is 2 KB further, the next tile 2 blocks
+    const uint32_t q_dst = tc::smem_u32(sm) + OFF_Q + (uint32_t)((tid & 15) / 8) * kBlk +
+                           tc::sw128_offset((uint32_t)tid >> 4, 8u * (tid & 7));
+    uint32_t count = 0;   // steps of this tile so far
+    int worked = 0;       // pieces with keys so far
+    for (int pi = 0;; pi++) {
+      Piece p;
+      if (softmax_meet(!hear(pi, p))) break;
+      if (p.done) break;
+      const int rows = p.seq_rows, row_base = p.row0 + cr * BM;   // this CTA's row 0 of tile 0
+      pgd::Seq q;
+      q.q0 = p.q0;
+      q.s = win::Seq{p.len, a.sink, (int64_t)1 << 62, a.tpf, a.frames};
+      if (p.J == 0) {   // these rows see no key: 16 lanes write a row's zeros
+        for (int e = tid; e < NQT * BM * 16; e += 32 * kSoftmaxWarps) {
+          const int r = row_base + e / 16 / BM * 2 * BM + e / 16 % BM;
+          if (r >= rows) continue;
+          RowOut out;
+          out.init(a, p, share, r - p.row0);
+          if (out.merge) continue;
+          const int c = 8 * (e & 15);
+          if (out.bf16) {
+            *(uint4 *)(out.bf16 + c) = make_uint4(0, 0, 0, 0);
+          } else {
+            *(float4 *)(out.f32 + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+            *(float4 *)(out.f32 + c + 4) = make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+          if (out.lse && c == 0) *out.lse = -INFINITY;
+        }
+        continue;
+      }
+      // ---- this CTA's two Query tiles -> shared memory: all rows' copies in flight, then bf16 -> fp16 in
+      // place.  Both tiles' MMAs of the last piece are done and its outputs have left this memory. ----
+      {
+        const int ci = tid & 15, rr0 = tid >> 4;   // 16-byte piece of a row; rows rr0, rr0 + 16, ...
+        const uint16_t *qb = a.q + (int64_t)p.kvh * a.group * a.qs.head + (int64_t)p.first * a.qs.token + 8 * ci;
+        // 16 rows on: 16 / group tokens and 16 % group heads, a token more where the heads run over
+        const int step_i = 16 / a.group, step_h = 16 - step_i * a.group;
+        const int64_t ahead = step_i * a.qs.token + step_h * a.qs.head, wrap = a.qs.token - a.group * a.qs.head;
+#pragma unroll 1
+        for (int y = 0; y < NQT; y++) {
+          const int r = row_base + y * 2 * BM + rr0, i = (int)((uint32_t)r / (uint32_t)a.group);
+          int h = r - i * a.group, left = rows - r < BM ? rows - r : BM;   // (may be negative)
+          const uint16_t *src = qb + h * a.qs.head + i * a.qs.token;
+          uint32_t dst = q_dst + (uint32_t)y * 2u * kBlk;
+#pragma unroll 2
+          for (int k = 0; k < BM / 16; k++) {
+            tc::cp_async16_zfill(dst, left > 0 ? src : qb, left > 0 ? 16u : 0u);
+            dst += 2048u;
+            left -= 16;
+            h += step_h;
+            src += ahead + (h >= a.group ? wrap : 0);
+            h -= h >= a.group ? a.group : 0;
+          }
+        }
+        tc::cp_async_commit();
+      }
+      // what this thread's row sees, while they are on their way
+      const int w0 = row_base + (p.brief ? 0 : x * 2 * BM) + 32 * sub;   // this warp's first row
+      const int r = w0 + lane;
+      pgd::Row mine{0, 0, 0};
+      pgd::Everyone every{INT32_MAX, 0, 0};   // a warp without a row masks nothing (its logits are 0)
+      if (w0 < rows) {
+        mine.init(q.s, p.keys, r < rows ? q.frame(a, r) : -1);
+        every.init(q.s, p.keys, q.frame(a, w0), q.frame(a, w0 + 31 < rows ? w0 + 31 : rows - 1));
+      }
+      {
+        // this warp's rows: two in each of 16 passes, pass 8 y + k those of tile y from 16 k on
+        tc::sts32(powers + 4u * (uint32_t)((lane >> 1) * 16 + warp * 2 + (lane & 1)), 0u);
+        tc::cp_async_wait<0>();
+        uint32_t top = 0u, small = 0u;   // the largest magnitudes, a NaN above all; passes in which this piece is below 1
+#pragma unroll 1
+        for (int y = 0; y < NQT; y++) {
+          const int rr = row_base + y * 2 * BM + (tid >> 4), left = rows - rr < BM ? rows - rr : BM;
+          const uint32_t at = q_dst + (uint32_t)y * 2u * kBlk;
+#pragma unroll 4
+          for (int k = 0; k < BM / 16; k++) {
+            const uint4 v = tc::lds128(at + (uint32_t)k * 2048u);
+            const bool live = 16 * k < left;
+            const uint32_t w[4] = {live ? v.x : 0u, live ? v.y : 0u, live ? v.z : 0u, live ? v.w : 0u};
+            uint32_t hw[4];
+#pragma unroll
+            for (int u = 0; u < 4; u++) hw[u] = tc::pack_f16x2(__uint_as_float(w[u] << 16), __uint_as_float(w[u] & 0xFFFF0000u));
+            tc::sts128(at + (uint32_t)k * 2048u, make_uint4(hw[0], hw[1], hw[2], hw[3]));
+            const uint32_t m = win::max_abs_bf16x2(win::max_abs_bf16x2(w[0], w[1]), win::max_abs_bf16x2(w[2], w[3])) & 0x7FFF7FFFu;
+            top = win::max_abs_bf16x2(top, m);
+            small |= win::any_from_one(m) || !live ? 0u : 1u << (8 * y + k);
+          }
+        }
+        if (win::any_beyond_fp16(top & 0x7FFF7FFFu)) qwm_dev_error(a.status, QWM_ERR_RANGE);
+#pragma unroll
+        for (int d = 1; d < 16; d <<= 1) small &= __shfl_xor_sync(0xffffffffu, small, d);   // of the whole row
+        __syncwarp();
+        for (uint32_t again = small | __shfl_xor_sync(0xffffffffu, small, 16); again; again &= again - 1u) {   // fetched once more
+          const int pass = __ffs((int)again) - 1, y = pass >> 3, k = pass & 7;
+          const bool here = (small >> pass) & 1u;
+          const int rr = row_base + y * 2 * BM + 16 * k + (tid >> 4), i = (int)((uint32_t)rr / (uint32_t)a.group);
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (here) v = *(const uint4 *)(a.q + (p.kvh * a.group + (rr - i * a.group)) * a.qs.head + (int64_t)(p.first + i) * a.qs.token + 8 * (tid & 15));
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          uint32_t m = win::max_abs_bf16x2(win::max_abs_bf16x2(w[0], w[1]), win::max_abs_bf16x2(w[2], w[3])) & 0x7FFF7FFFu;
+          m = win::larger_half(m);
+#pragma unroll
+          for (int d = 1; d < 16; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+          if (!here) continue;
+          const uint32_t power = win::row_power(m);
+          const float up = win::power_of_two((int)power);
+          uint32_t hw[4];
+#pragma unroll
+          for (int u = 0; u < 4; u++) hw[u] = tc::pack_f16x2(__uint_as_float(w[u] << 16) * up, __uint_as_float(w[u] & 0xFFFF0000u) * up);
+          tc::sts128(q_dst + (uint32_t)y * 2u * kBlk + (uint32_t)k * 2048u, make_uint4(hw[0], hw[1], hw[2], hw[3]));
+          if ((tid & 15) == 0) tc::sts32(powers + 4u * (uint32_t)(pass * 16 + (tid >> 4)), power);
+        }
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive_remote(q_full);
+      }
+      softmax_meet(false);   // the rows' powers
+      const int power = (int)tc::lds32(powers + 4u * (uint32_t)((p.brief ? 0 : x * BM) + 32 * sub + lane));
+      const float sl2 = a.scale_log2 * win::power_of_two(-power) * win::kUnit<BITS>;
+      const uint64_t sc2 = pk64(sl2, sl2);
+      const int mine_n = p.brief ? (p.steps + 1 - x) >> 1 : p.steps;   // steps of this tile
+      const int key_of = p.j0 * BN + (p.brief ? x * BS : 0), key_step = p.brief ? 2 * BS : BS;
+      float m_used = -INFINITY;
+      uint64_t acc = 0ull;   // the sum of the weights, each step's added as one: 1 / 64 of the additions to a large sum
+      bool ok = true;
+      for (int t = 0; t < mine_n; t++) {
+        const uint32_t u = count + (uint32_t)t;
+        const int v0 = key_of + t * key_step;
+        const bool full = every.see(v0, v0 + BS);
+        const uint32_t tS = tS0 + (u & 1u) * BS;
+        if (!__all_sync(0xffffffffu, tc::mbar_try_wait(&bars.s_full[x][u & 1u], (u >> 1) & 1u))) {
+          if (!tc::mbar_wait(&bars.s_full[x][u & 1u], (u >> 1) & 1u, kWaitNs)) fail(&abort_flag, a.status);
+          if (__any_sync(0xffffffffu, *abort_v != 0)) { ok = false; break; }   // the whole warp
+        }
+        tc::fence_after_sync();
+        // the step's logits at once: their maximum, then their exponentials relative to m_used, which stands
+        // kTopWeight below the running maximum; when that grows by more than 2^8 (rare after the first step)
+        // the sum and O are rescaled
+        uint32_t s[BS];
+#pragma unroll
+        for (int i = 0; i < BS; i += 16) tc::tmem_ld16(tS + (uint32_t)i, s + i);
+        tc::tmem_ld_wait();
+        if (!full) {
+#pragma unroll
+          for (int h = 0; h < BS / 32; h++) {
+            const int v = v0 + 32 * h;
+            const uint32_t seen = low_bits(mine.c0 - v) | (low_bits(mine.c2 - v) & ~low_bits(mine.c1 - v));
+#pragma unroll
+            for (int i = 0; i < 32; i++)
+              if (!((seen >> i) & 1u)) s[32 * h + i] = 0xFF800000u;  // -inf: weight exactly 0
+          }
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < BS; i += 8)
+#pragma unroll
+          for (int e = 0; e < 4; e++)
+            mx[e] = tc::max3(mx[e], __uint_as_float(s[i + 2 * e]), __uint_as_float(s[i + 2 * e + 1]));
+        const float m_new = fmaxf(m_used, fmaf(tc::max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]), sl2, -win::kTopWeight));
+        if (__any_sync(0xffffffffu, m_new > m_used + kRescaleThreshold)) {
+          const float alpha = m_new == -INFINITY ? 1.f : tc::ex2_approx(m_used - m_new);
+          const uint64_t a2 = pk64(alpha, alpha);
+          acc = tc::fma2(acc, a2, 0ull);
+          if (t > 0) {  // O of the earlier steps, once PV_x(t-1) has been added (PV_x(t) waits for this warp)
+            const uint32_t b = u - 1u;
+            if (!tc::mbar_wait(&bars.pv_done[x][b & 1u], (b >> 1) & 1u, kWaitNs)) fail(&abort_flag, a.status);
+            tc::fence_after_sync();
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+              uint32_t o[16];
+              tc::tmem_ld16(tO + c, o);
+              tc::tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 16; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tc::tmem_st16(tO + c, o);
+            }
+          }
+          m_used = m_new;
+        }
+        const float mneg = m_used == -INFINITY ? 0.f : -m_used;  // a row that has seen no key yet
+        const uint64_t nm2 = pk64(mneg, mneg);
+        uint64_t sum0 = 0ull, sum1 = 0ull;
+#pragma unroll
+        for (int h = 0; h < BS / 32; h++) {
+          uint32_t pw[16];
+#pragma unroll
+          for (int i = 0; i < 16; i++) {  // packed fp32 pairs: S * scale - m, then 2^x
+            const uint64_t x2 = tc::fma2(pk64(s[32 * h + 2 * i], s[32 * h + 2 * i + 1]), sc2, nm2);
+            const float e0 = tc::ex2_approx(tc::f2lo(x2)), e1 = tc::ex2_approx(tc::f2hi(x2));
+            const uint64_t e2 = pk64(e0, e1);
+            if (i & 1) sum1 = h == 0 && i == 1 ? e2 : tc::add2(sum1, e2);
+            else sum0 = h == 0 && i == 0 ? e2 : tc::add2(sum0, e2);
+            pw[i] = tc::pack_f16x2(e0, e1);
+          }
+          tc::tmem_st16(tS + 16u * h, pw);  // P (fp16 pairs) over the logits
+        }
+        acc = tc::add2(acc, tc::add2(sum0, sum1));
+        tc::tmem_st_wait();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive_remote(p_ready0 + 8u * (u & 1u));
+      }
+      count += (uint32_t)mine_n;
+      float l = tc::f2lo(acc) + tc::f2hi(acc), part0 = 1.f, part1 = 0.f;   // what O_0 and O_1 count for
+      if (p.brief) {   // every softmax warp comes here, whatever happened before
+        if (x == 1) half_sums[tid & (BM - 1)] = make_float2(m_used, l);
+        softmax_meet(false);
+        if (x == 0) {
+          const float2 o = half_sums[tid];
+          const float m = fmaxf(m_used, o.x);
+          part0 = m_used == -INFINITY ? 0.f : tc::ex2_approx(m_used - m);
+          part1 = o.x == -INFINITY ? 0.f : tc::ex2_approx(o.x - m);
+          l = fmaf(l, part0, o.y * part1);
+          m_used = m;
+        }
+      }
+      // every MMA of the piece is done: outputs may be read, and the Queries' memory written
+      if (ok && !tc::mbar_wait(&bars.o_done, worked & 1, kWaitNs)) fail(&abort_flag, a.status);
+      worked++;
+      ok = !__any_sync(0xffffffffu, !ok || *abort_v != 0);
+      if (ok && !(p.brief && x == 1)) {
+        tc::fence_after_sync();
+        float inv = l > 0.f ? win::kUnit<BITS> / l : 0.f, keep = 0.f;
+        float L = l > 0.f ? m_used + log2f(l) : -INFINITY;
+        bool write = r < rows;
+        RowOut out;
+        if (write) {
+          out.init(a, p, share, r - p.row0);
+          if (out.merge) {  // out = w_prev out + w_this O / l, the weights the parts' shares of the sum
+            const float Lp = *out.lse, Lm = fmaxf(Lp, L);
+            if (Lm == -INFINITY) {
+              write = false;
+            } else {
+              const float wp = exp2f(Lp - Lm), wt = exp2f(L - Lm), den = wp + wt;
+              keep = wp / den;
+              inv *= wt / den;
+              L = Lm + log2f(den);
+            }
+          }
+          if (write && out.lse) *out.lse = L;
+        }
+        // through the Queries' memory, so that the stores write whole rows: an 8 KB buffer per warp of 256
+        // bytes a row (fp32: two halves), 16-byte pieces permuted by the row's low bits against bank conflicts
+        const uint32_t buf = tc::smem_u32(sm) + OFF_Q + (uint32_t)warp * 8192u, rx = (uint32_t)lane & 7u;
+        const bool half = !p.place && !a.out_f32;   // bf16 rows
+        const float w0_out = part0 * inv, w1_out = part1 * inv;
+        const uint32_t writes = __ballot_sync(0xffffffffu, write);
+        const uint64_t mine_out = half ? (uint64_t)out.bf16 : (uint64_t)out.f32;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          tc::tmem_ld32(tO + c, o);
+          tc::tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * w0_out);
+          if (p.brief && p.steps > 1) {   // (a single step left O_1 unwritten)
+            uint32_t o1[32];
+            tc::tmem_ld32(tO + 128 + c, o1);
+            tc::tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; i++)
+              o[i] = __float_as_uint(fmaf(__uint_as_float(o1[i]), w1_out, __uint_as_float(o[i])));
+          }
+          if (half) {
+#pragma unroll
+            for (int v = 0; v < 4; v++) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; e++)
+                w[e] = tc::pack_bf16x2(__uint_as_float(o[8 * v + 2 * e]), __uint_as_float(o[8 * v + 2 * e + 1]));
+              tc::sts128(buf + (uint32_t)lane * 256u + ((((uint32_t)(c / 8 + v)) ^ rx) << 4), make_uint4(w[0], w[1], w[2], w[3]));
+            }
+          } else {
+#pragma unroll
+            for (int v = 0; v < 8; v++)
+              tc::sts128(buf + (uint32_t)lane * 256u + ((((uint32_t)((c & 32) / 4 + v)) ^ rx) << 4),
+                         make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]));
+            if (c & 32) {   // 64 channels are there
+              __syncwarp();
+#pragma unroll 4
+              for (int i = 0; i < 16; i++) {
+                const int rw = 2 * i + (lane >> 4), e = lane & 15;
+                float *dst = (float *)__shfl_sync(0xffffffffu, mine_out, rw) + (c - 32) + 4 * e;
+                const float k = __shfl_sync(0xffffffffu, keep, rw);
+                const uint4 v = tc::lds128(buf + (uint32_t)rw * 256u + ((uint32_t)(e ^ (rw & 7)) << 4));
+                if ((writes >> rw) & 1u) {
+                  float4 f = make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+                  if (k > 0.f) {
+                    const float4 g = *(const float4 *)dst;
+                    f = make_float4(fmaf(k, g.x, f.x), fmaf(k, g.y, f.y), fmaf(k, g.z, f.z), fmaf(k, g.w, f.w));
+                  }
+                  *(float4 *)dst = f;
+                }
+              }
+              __syncwarp();
+            }
+          }
+        }
+        if (half) {
+          __syncwarp();
+#pragma unroll 8
+          for (int i = 0; i < 16; i++) {
+            const int rw = 2 * i + (lane >> 4), c = lane & 15;
+            uint16_t *dst = (uint16_t *)__shfl_sync(0xffffffffu, mine_out, rw);
+            const uint4 v = tc::lds128(buf + (uint32_t)rw * 256u + ((uint32_t)(c ^ (rw & 7)) << 4));
+            if ((writes >> rw) & 1u) *(uint4 *)(dst + 8 * c) = v;
+          }
+        }
+      }
+      tc::fence_before_sync();
+      if (softmax_meet(!ok)) break;   // (behind it the Queries' memory and both outputs may be written again)
+      tc::fence_after_sync();
+    }
+  } else if (warp == kMmaWarp) {
+    // ======================= the even CTA's issues the pair's MMAs, the odd one's passes on that its CTA's stages
+    // are full =======================
+    // The warp's common answer.  Whether someone gave up is looked at only where there is something to
+    // wait for.
+    auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
+      if (__all_sync(0xffffffffu, tc::mbar_try_wait_cluster(bar, parity))) return true;
+      return __all_sync(0xffffffffu, tc::mbar_wait_cluster(bar, parity, kWaitNs) && !*abort_v);
+    };
+    uint32_t g0 = 0, c0 = 0, c1 = 0;   // stages so far; steps of tiles 0 and 1
+    int worked = 0;
+    bool ok = true;
+    const uint32_t full_even = tc::mapa(tc::smem_u32(&bars.full[0]), 0);
+    constexpr uint32_t idesc = tc::idesc_f16_f32(2 * BM, BS), idesc_pv = tc::idesc_f16_f32_bmn(2 * BM, D);
+    constexpr uint16_t kBoth = 3;
+    // broadcast, so that everything derived from them is the warp's and not a lane's
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), s0 = __shfl_sync(0xffffffffu, tc::smem_u32(sm), 0);
+    const uint64_t dq = tc::desc_sw128(s0 + OFF_Q), dk = tc::desc_sw128(s0 + OFF_K);
+    const uint64_t dv = tc::desc_sw128_mn(s0 + OFF_V, kBlk, 1024);
+    for (int pi = 0; ok; pi++) {
+      Piece p;
+      ok = hear(pi, p);
+      if (!ok || p.done) break;
+      const int J = __shfl_sync(0xffffffffu, p.J, 0), n = __shfl_sync(0xffffffffu, p.steps, 0);
+      const int brief = __shfl_sync(0xffffffffu, p.brief, 0);
+      if (J == 0) continue;
+      if (cr == 1) {
+        for (int j = 0; j < J; j++) {
+          const uint32_t g = g0 + (uint32_t)j;
+          if (!wait(&bars.full[g & (kStages - 1)], (g / kStages) & 1u)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) tc::mbar_arrive_remote(full_even + 8u * (g & (kStages - 1)));
+        }
+        g0 += (uint32_t)J;
+        continue;
+      }
+      // step t of tile x: both tiles take the same 64 keys, or (short items) a half each of stage t.  (The two
+      // forms are compiled apart: chosen at every step they cost a tenth of it.)
+      auto multiply = [&](auto rows_of_two) {
+        constexpr bool two = decltype(rows_of_two)::value;
+        const int T = two ? n : (n + 1) >> 1;   // steps of tile 0
+        auto stage_of = [&](int t) -> uint32_t { return g0 + (uint32_t)(two ? t >> 1 : t); };
+        auto half_of = [&](int x, int t) { return two ? t & 1 : x; };
+        auto begins = [&](int t) { return !two || !(t & 1); };
+        auto ends = [&](int t) { return !two || (t & 1) || t + 1 == n; };
+        auto there = [&](int t) { return two || 2 * t + 1 < n; };   // tile 1 has a step t
+        auto nth = [&](int x, int t) -> uint32_t { return (x ? c1 : c0) + (uint32_t)t; };
+        auto qk = [&](int x, int t) {
+          const uint32_t ko = (stage_of(t) % kStages) * 2 * kBlkH + (uint32_t)half_of(x, t) * 32 * 128, u = nth(x, t);
+          const uint64_t da = dq + (uint64_t)(two ? x * 2 * kBlk / 16 : 0), db = dk + (uint64_t)(ko / 16);
+          const uint32_t d = tm + 128u * x + (u & 1u) * BS;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; kk++)
+            tc::mma2_ss_warp(d, da + (uint64_t)(((kk / 4) * kBlk + 32 * (kk % 4)) / 16),
+                             db + (uint64_t)(((kk / 4) * kBlkH + 32 * (kk % 4)) / 16), idesc, kk > 0);
+          tc::mma2_commit_warp(&bars.s_full[x][u & 1u], kBoth);
+        };
+        auto pv = [&](int x, int t) {
+          const uint32_t vo = (stage_of(t) % kStages) * kBlk + (uint32_t)half_of(x, t) * BS * 128, u = nth(x, t);
+          const uint64_t db = dv + (uint64_t)(vo / 16);
+          const uint32_t pp = tm + 128u * x + (u & 1u) * BS;
+#pragma unroll
+          for (int kk = 0; kk < BS / 16; kk++)
+            tc::mma2_ts_warp(tm + 256u + 128u * x, pp + 8u * kk, db + (uint64_t)(2048 * kk / 16), idesc_pv,
+                             (t > 0 || kk > 0));
+          tc::mma2_commit_warp(&bars.pv_done[x][u & 1u], kBoth);
+        };
+        auto keys_there = [&](int t) {   // the Keys and Values of step t (a stage's first step waits for it)
+          const uint32_t g = stage_of(t);
+          return !begins(t) || wait(&bars.full[g % kStages], (g / kStages) & 1u);
+        };
+        auto weights_there = [&](int x, int t) {
+          const uint32_t u = nth(x, t);
+          return wait(&bars.p_ready[x][u & 1u], (u >> 1) & 1u);
+        };
+        for (int t = 0; ok && t < 2 && t < T; t++) {
+          ok = keys_there(t);
+          if (!ok) break;
+          tc::fence_after_sync();
+          qk(0, t);
+          if (there(t)) qk(1, t);
+        }
+        for (int t = 0; ok && t < T; t++) {
+          ok = weights_there(0, t);
+          if (!ok) break;
+          tc::fence_after_sync();
+          pv(0, t);
+          if (t + 2 < T) {
+            ok = keys_there(t + 2);
+            if (!ok) break;
+            tc::fence_after_sync();
+            qk(0, t + 2);
+          }
+          if (there(t)) {
+            ok = weights_there(1, t);
+            if (!ok) break;
+            tc::fence_after_sync();
+            pv(1, t);
+            if (t + 2 < T && there(t + 2)) qk(1, t + 2);
+          }
+          if (ends(t)) tc::mma2_commit_warp(&bars.empty[stage_of(t) % kStages], kBoth);   // (S precedes P V)
+        }
+        c0 += (uint32_t)T;
+        c1 += (uint32_t)(two ? n : n >> 1);
+      };
+      ok = wait(&bars.q_full, worked & 1);
+      tc::fence_after_sync();
+      if (brief) multiply(Flag<false>{});
+      else multiply(Flag<true>{});
+      g0 += (uint32_t)J;
+      worked++;
+      if (ok) tc::mma2_commit_warp(&bars.o_done, kBoth);
+    }
+    if (!ok) fail(&abort_flag, a.status);
+    if (cr == 0) {
+      tc::mma2_commit_warp(&bars.drain, 1);  // every MMA issued above completes before TMEM is released
+      if (!tc::mbar_wait(&bars.drain, 0, kWaitNs)) qwm_dev_error(a.status, QWM_ERR_DEVICE_TIMEOUT);
+    }
+  } else if (warp == kPlanWarp) {
+    // ======================= the pieces of the share =======================
+    int b = begin.b, item = begin.item, block = begin.block, pi = 0;
+    bool first = true, more = true;
+    while (more) {
+      Piece p;
+      p.done = 1;
+      for (; b < a.batch; b++, item = block = 0) {   // the sequence of the next item
+        const pgd::Seq q = pgd::sequence(a, b);
+        const int n = Work::count(a, q);
+        if (b > end.b || (b == end.b && (item > end.item || (item == end.item && end.block == 0)))) break;
+        if (item >= n * a.pool.kv_heads) continue;
+        const int kvh = item / n, ib = item - kvh * n;
+        const int blocks = Work::blocks_of(a, q, ib, p.keys);
+        const bool last = b == end.b && item == end.item;
+        const int block1 = last ? end.block : blocks;
+        p.b = b;
+        p.kvh = kvh;
+        p.first = q.first;
+        p.seq_rows = q.rows;
+        p.row0 = ib * kRows;
+        p.place = block == 0 ? (block1 == blocks ? 0 : 2) : 1;
+        p.j0 = block;
+        p.J = block1 - block;
+        const int to = p.keys.total < block1 * BN ? p.keys.total : block1 * BN;
+        p.steps = (to - block * BN + BS - 1) / BS;
+        p.brief = Work::brief(q, ib);
+        p.q0 = q.q0;
+        p.len = q.s.len;
+        p.done = 0;
+        if (first && lane == 0 && cr == 0)
+          a.cuts[share] = PagedCut{b, item, block, q.first, kvh, p.row0, q.rows - p.row0 < kRows ? q.rows - p.row0 : kRows};
+        first = false;
+        item = last ? INT32_MAX : item + 1;   // (behind the last one everything lies past the end)
+        block = 0;
+        break;
+      }
+      more = !p.done;
+      if (pi >= 2 && !__all_sync(0xffffffffu, tc::mbar_wait(&bars.heard[pi & 1], ((pi >> 1) - 1) & 1, kWaitNs))) {
+        fail(&abort_flag, a.status);
+        break;
+      }
+      if (lane == 0) pieces[pi & 1] = p;
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&bars.told[pi & 1]);
+      pi++;
+    }
+    if (first && lane == 0 && cr == 0) a.cuts[share] = PagedCut{a.batch, 0, 0, 0, 0, 0, 0};
+  } else {
+    // ======================= producers: Keys, then Values, of every stage =======================
+    const int pw = warp - kProdWarp0;
+    const Producer<BITS, false> pk(a, sm, cr, pw, lane);
+    const Producer<BITS, true> pv(a, sm, cr, pw, lane);
+    Codes<BITS> k0, v0, k1, v1;
+    uint32_t g0 = 0;
+    bool ok = true;
+    for (int pi = 0; ok; pi++) {
+      Piece p;
+      ok = hear(pi, p);
+      if (!ok || p.done) break;
+      const int32_t *table = a.table + (int64_t)p.b * a.width;
+      int ek[1], ev[2];   // table entries of the next stage to be fetched
+      pk.look(a, p.keys, table, p.j0 * BN, ek);
+      pv.look(a, p.keys, table, p.j0 * BN, ev);
+      auto free_again = [&](uint32_t g) -> bool {   // the previous contents of stage g's place are consumed
+        uint64_t *empty = &bars.empty[g & (kStages - 1)];
+        if (g < kStages || __all_sync(0xffffffffu, tc::mbar_try_wait(empty, (g / kStages - 1) & 1u))) return true;
+        if (!tc::mbar_wait(empty, (g / kStages - 1) & 1u, kWaitNs)) fail(&abort_flag, a.status);
+        return !__any_sync(0xffffffffu, *abort_v != 0);         // warp-uniform exit
+      };
+      // stage j is stored and the codes of stage j + 2 fetched in its place; the first round only fetches
+      auto stage = [&](int j, Codes<BITS> &k, Codes<BITS> &v) -> bool {
+        const uint32_t g = g0 + (uint32_t)j, s = g & (kStages - 1);
+        const int next = (p.j0 + j + 2) * BN;
+        const bool store = j >= 0 && j < p.J, load = j + 2 < p.J;
+        if (store) {
+          if (!free_again(g)) return false;
+          pk.store(s, k, a.bases);
+        }
+        if (load) {
+          pk.load(a, p.keys, p.kvh, next, ek, k);
+          pk.look(a, p.keys, table, next + BN, ek);
+        }
+        if (store) {
+          pv.store(s, v, a.bases);
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&bars.full[s]);
+        }
+        if (load) {
+          pv.load(a, p.keys, p.kvh, next, ev, v);
+          pv.look(a, p.keys, table, next + BN, ev);
+        }
+        return true;
+      };
+#pragma unroll 1
+      for (int j = -2; j < p.J; j += 2)
+        if (!stage(j, k0, v0) || !stage(j + 1, k1, v1)) {
+          ok = false;
+          break;
+        }
+      g0 += (uint32_t)p.J;
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::cluster_sync();  // the peer has finished with this CTA's barriers, shared and tensor memory
+  if (warp == kMmaWarp) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc2(tmem_base_sh, 512);
+  }
+}
+
+template <int BITS>
+cudaError_t launch_bits(const PagedAttend &a, cudaStream_t st) {
+  static std::atomic<uint64_t> allowed{0};
+  const cudaError_t e = allow_shared(paged_attend_kernel<BITS>, kSmemAlloc, allowed);
+  if (e != cudaSuccess) return e;
+  paged_attend_kernel<BITS><<<2 * a.shares, kThreads, kSmemAlloc, st>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_paged_tiles(const PagedAttend &a, cudaStream_t st) {
+  return a.pool.bits == 8 ? launch_bits<8>(a, st) : launch_bits<4>(a, st);
+}

@@ -19,8 +19,38 @@ using wt::Ring;
 constexpr int kThreads = 32 * kWarps;
 template <int BITS>
 constexpr int kBlock = kWarps * wt::step_keys(BITS);   // keys that the 8 warps take at once
-// What an item costs besides its keys, in blocks, and the least piece of an item worth its own start.
+// What an item costs besides its keys, in blocks; the least piece of an item, and of the line, worth a start.
 constexpr int kStart = 4, kLeast = 2, kThin = 6;
+
+// The items of a sequence: Key heads by blocks of 8 NT rows, all as long.
+template <int BITS, int NT>
+struct Work {
+  const PagedAttend &a;
+  __device__ __forceinline__ void of(int b, int &blocks, int &items) const {
+    const pgd::Seq q = pgd::sequence(a, b);
+    blocks = items = 0;
+    if (q.rows == 0 || q.rows > a.few) return;
+    pgd::Keys keys;
+    keys.init(a, q.s, q.frame(a, 0), q.frame(a, q.rows - 1));
+    blocks = (keys.total + kBlock<BITS> - 1) / kBlock<BITS>;
+    items = a.pool.kv_heads * ((q.rows + 8 * NT - 1) / (8 * NT));
+  }
+  __device__ __forceinline__ int64_t cost(int b) const {
+    int blocks, items;
+    of(b, blocks, items);
+    return (int64_t)items * (blocks + kStart);
+  }
+  __device__ __forceinline__ void cut(int b, int64_t x, int &item, int &block) const {
+    int blocks, items;
+    of(b, blocks, items);
+    item = (int)win::quotient(x, blocks + kStart);
+    block = pgd::cut_item(x - (int64_t)item * (blocks + kStart), blocks, kStart, 1, kLeast);
+    if (block == blocks && block > 0) {
+      item++;
+      block = 0;
+    }
+  }
+};
 
 template <int BITS, int NT>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) paged_decode_kernel(const __grid_constant__ PagedAttend a) {
@@ -33,15 +63,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) paged_decode_kernel
   __shared__ PagedCut cut[2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the joining kernel may line up
-  auto load_of = [&](int b) -> pgd::Load {
-    const pgd::Seq q = pgd::sequence(a, b);
-    if (q.rows == 0) return {0, 0};
-    pgd::Keys keys;
-    keys.init(a, q.s, q.frame(a, 0), q.frame(a, q.rows - 1));
-    return {(keys.total + kBlock<BITS> - 1) / kBlock<BITS>, a.pool.kv_heads * ((q.rows + 8 * NT - 1) / (8 * NT))};
-  };
-  pgd::share_of<kThreads>(a.batch, (int)blockIdx.x, a.shares, kStart, kLeast, kThin, load_of, cut);
-  __syncthreads();
+  pgd::share_of<kThreads>(a.batch, (int)blockIdx.x, a.shares, kThin, Work<BITS, NT>{a}, cut);
   const PagedCut end = cut[1];
   int b = cut[0].b, item = cut[0].item, block = cut[0].block;
   wt::Tile<BITS, NT> tile;
@@ -58,7 +80,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) paged_decode_kernel
   bool began = false;   // the share's first cut is written down for the joining kernel
   while (b < a.batch) {
     const pgd::Seq q = pgd::sequence(a, b);
-    const int tiles = (q.rows + 8 * NT - 1) / (8 * NT), items = a.pool.kv_heads * tiles;
+    const int tiles = q.rows > a.few ? 0 : (q.rows + 8 * NT - 1) / (8 * NT), items = a.pool.kv_heads * tiles;
     if (item >= items) {   // the next sequence
       if (b >= end.b) break;
       b++;
@@ -171,14 +193,21 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) paged_decode_kernel
     if (last) break;
   }
   if (!began && threadIdx.x == 0) a.cuts[blockIdx.x] = PagedCut{a.batch, 0, 0, 0, 0, 0, 0};
+  // launched beside the tile kernel: who waits for this one waits for both
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // Parts of an item joined: the weighted mean of the parts' outputs, each weighted by its share of the
-// exponential sum.  Blocks of 8 warps, one warp per row; blockIdx.x: the share whose beginning cuts the item
-// first, blockIdx.y: 8 of the item's rows.
-__global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constant__ PagedAttend a, int part_rows) {
+// exponential sum.  Blocks of 8 warps, one warp per row; per share whose beginning cuts an item first, a block for
+// every 8 of the item's rows (few_blocks: the warp tiles' blocks, which come first).
+__global__ void __launch_bounds__(256)
+    paged_combine_kernel(const __grid_constant__ PagedAttend few, const __grid_constant__ PagedAttend many, int few_rows,
+                         int few_blocks) {
   asm volatile("griddepcontrol.wait;" ::: "memory");   // launched while the parts are computed: wait for them
-  const int s = (int)blockIdx.x + 1, lane = threadIdx.x & 31, r = (int)blockIdx.y * 8 + (threadIdx.x >> 5);
+  const bool first = (int)blockIdx.x < few_blocks;
+  const PagedAttend &a = first ? few : many;
+  const int part_rows = first ? few_rows : kPagedTileRows, at = (int)blockIdx.x - (first ? 0 : few_blocks);
+  const int s = at / (part_rows / 8) + 1, lane = threadIdx.x & 31, r = at % (part_rows / 8) * 8 + (threadIdx.x >> 5);
   const PagedCut c = a.cuts[s];
   if (c.block == 0 || r >= c.live) return;
   const PagedCut before = a.cuts[s - 1];
@@ -217,29 +246,39 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constan
 }
 
 template <int BITS, int NT>
-cudaError_t decode_launch(const PagedAttend &a, cudaStream_t st) {
+cudaError_t decode_launch(const PagedAttend &a, bool beside, cudaStream_t st) {
   auto kernel = paged_decode_kernel<BITS, NT>;
   static std::atomic<uint64_t> allowed{0};
   const cudaError_t e = allow_shared(kernel, Ring<BITS>::kBytes, allowed);
   if (e != cudaSuccess) return e;
-  kernel<<<a.shares, kThreads, Ring<BITS>::kBytes, st>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)a.shares);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Ring<BITS>::kBytes;
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = beside ? 1 : 0;   // it needs nothing of the tile kernel: its CTAs follow as SMs come free
+  return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 }  // namespace
 
-// row_tiles: 1 (8 rows an item) or 2 (16).
 int paged_decode_shares(int row_tiles, int num_sms) { return (row_tiles == 1 ? 2 : 1) * num_sms; }
 
-cudaError_t launch_paged_decode(const PagedAttend &a, int row_tiles, cudaStream_t st) {
-  if (row_tiles == 1) return a.pool.bits == 8 ? decode_launch<8, 1>(a, st) : decode_launch<4, 1>(a, st);
-  return a.pool.bits == 8 ? decode_launch<8, 2>(a, st) : decode_launch<4, 2>(a, st);
+cudaError_t launch_paged_decode(const PagedAttend &a, int row_tiles, bool beside, cudaStream_t st) {
+  if (row_tiles == 1) return a.pool.bits == 8 ? decode_launch<8, 1>(a, beside, st) : decode_launch<4, 1>(a, beside, st);
+  return a.pool.bits == 8 ? decode_launch<8, 2>(a, beside, st) : decode_launch<4, 2>(a, beside, st);
 }
 
-// Launched as a dependent of the parts' kernel, so that its start-up overlaps their work.
-cudaError_t launch_paged_combine(const PagedAttend &a, int part_rows, cudaStream_t st) {
+// Launched as a dependent of the parts' kernels, so that its start-up overlaps their work.
+cudaError_t launch_paged_combine(const PagedAttend *few, int part_rows, const PagedAttend *many, cudaStream_t st) {
+  const int few_blocks = few ? (few->shares - 1) * (part_rows / 8) : 0;
+  const int many_blocks = many ? (many->shares - 1) * (kPagedTileRows / 8) : 0;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(a.shares - 1), (unsigned)(part_rows / 8));
+  cfg.gridDim = dim3((unsigned)(few_blocks + many_blocks));
   cfg.blockDim = dim3(256);
   cfg.stream = st;
   cudaLaunchAttribute attr;
@@ -247,5 +286,6 @@ cudaError_t launch_paged_combine(const PagedAttend &a, int part_rows, cudaStream
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_combine_kernel, a, part_rows);
+  return cudaLaunchKernelEx(&cfg, paged_combine_kernel, few ? *few : *many, many ? *many : *few, few ? part_rows : kPagedTileRows,
+                            few_blocks);
 }
