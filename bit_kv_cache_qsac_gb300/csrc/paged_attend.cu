@@ -63,20 +63,20 @@ struct Piece {
   int done;                            // no piece: the share ends
 };
 
-template <bool B>
-struct Flag {
-  static constexpr bool value = B;
-};
 struct Bars {
   uint64_t full[kStages], empty[kStages];
   uint64_t s_full[2][2], p_ready[2][2], pv_done[2][2], q_full, o_done, drain;
   uint64_t told[2], heard[2];   // a piece's description is there; everyone has read it
 };
 
-__device__ __forceinline__ void fail(int *abort_flag, int32_t *status) {
-  *(volatile int *)abort_flag = 1;
+__shared__ Bars bars;
+__shared__ int abort_flag;
+
+__device__ __forceinline__ void fail(int32_t *status) {
+  *(volatile int *)&abort_flag = 1;
   qwm_dev_error(status, QWM_ERR_DEVICE_TIMEOUT);
 }
+__device__ __forceinline__ int aborted() { return *(volatile int *)&abort_flag; }
 __device__ __forceinline__ uint64_t pk64(uint32_t lo, uint32_t hi) {
   uint64_t d;
   asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
@@ -265,20 +265,103 @@ struct Producer {
   }
 };
 
+// The warp's common answer.  Whether someone gave up is looked at only where there is something to wait for.
+__device__ __forceinline__ bool meet(uint64_t *bar, uint32_t parity) {
+  if (__all_sync(0xffffffffu, tc::mbar_try_wait_cluster(bar, parity))) return true;
+  return __all_sync(0xffffffffu, tc::mbar_wait_cluster(bar, parity, kWaitNs) && !aborted());
+}
+
+// The even CTA's MMAs of one piece: n steps, step t of tile x being number c_x + t and in stage g0 + .. of the
+// share.  two: both tiles take the same 64 keys a step; else (short items) a half each of stage t.  (Compiled
+// apart: chosen at every step they cost a tenth of it.)  False: someone gave up.
+template <bool two>
+__device__ __noinline__ bool multiply(uint32_t tmem, uint32_t smem, int steps, uint32_t stage0, uint32_t step0, uint32_t step1) {
+  constexpr uint32_t idesc = tc::idesc_f16_f32(2 * BM, BS), idesc_pv = tc::idesc_f16_f32_bmn(2 * BM, D);
+  constexpr uint16_t kBoth = 3;
+  // broadcast, so that everything derived from them is the warp's and not a lane's
+  const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), s0 = __shfl_sync(0xffffffffu, smem, 0);
+  const uint32_t g0 = __shfl_sync(0xffffffffu, stage0, 0), c0 = __shfl_sync(0xffffffffu, step0, 0), c1 = __shfl_sync(0xffffffffu, step1, 0);
+  const int n = __shfl_sync(0xffffffffu, steps, 0);
+  const uint64_t dq = tc::desc_sw128(s0 + OFF_Q), dk = tc::desc_sw128(s0 + OFF_K);
+  const uint64_t dv = tc::desc_sw128_mn(s0 + OFF_V, kBlk, 1024);
+  bool ok = true;
+  auto wait = [&](uint64_t *bar, uint32_t parity) -> bool { return meet(bar, parity); };
+  const int T = two ? n : (n + 1) >> 1;   // steps of tile 0
+  auto stage_of = [&](int t) -> uint32_t { return g0 + (uint32_t)(two ? t >> 1 : t); };
+  auto half_of = [&](int x, int t) { return two ? t & 1 : x; };
+  auto begins = [&](int t) { return !two || !(t & 1); };
+  auto ends = [&](int t) { return !two || (t & 1) || t + 1 == n; };
+  auto there = [&](int t) { return two || 2 * t + 1 < n; };   // tile 1 has a step t
+  auto nth = [&](int x, int t) -> uint32_t { return (x ? c1 : c0) + (uint32_t)t; };
+  auto qk = [&](int x, int t) {
+    const uint32_t ko = (stage_of(t) % kStages) * 2 * kBlkH + (uint32_t)half_of(x, t) * 32 * 128, u = nth(x, t);
+    const uint64_t da = dq + (uint64_t)(two ? x * 2 * kBlk / 16 : 0), db = dk + (uint64_t)(ko / 16);
+    const uint32_t d = tm + 128u * x + (u & 1u) * BS;
+#pragma unroll
+    for (int kk = 0; kk < D / 16; kk++)
+      tc::mma2_ss_warp(d, da + (uint64_t)(((kk / 4) * kBlk + 32 * (kk % 4)) / 16),
+                       db + (uint64_t)(((kk / 4) * kBlkH + 32 * (kk % 4)) / 16), idesc, kk > 0);
+    tc::mma2_commit_warp(&bars.s_full[x][u & 1u], kBoth);
+  };
+  auto pv = [&](int x, int t) {
+    const uint32_t vo = (stage_of(t) % kStages) * kBlk + (uint32_t)half_of(x, t) * BS * 128, u = nth(x, t);
+    const uint64_t db = dv + (uint64_t)(vo / 16);
+    const uint32_t pp = tm + 128u * x + (u & 1u) * BS;
+#pragma unroll
+    for (int kk = 0; kk < BS / 16; kk++)
+      tc::mma2_ts_warp(tm + 256u + 128u * x, pp + 8u * kk, db + (uint64_t)(2048 * kk / 16), idesc_pv,
+                       (t > 0 || kk > 0));
+    tc::mma2_commit_warp(&bars.pv_done[x][u & 1u], kBoth);
+  };
+  auto keys_there = [&](int t) {   // the Keys and Values of step t (a stage's first step waits for it)
+    const uint32_t g = stage_of(t);
+    return !begins(t) || wait(&bars.full[g % kStages], (g / kStages) & 1u);
+  };
+  auto weights_there = [&](int x, int t) {
+    const uint32_t u = nth(x, t);
+    return wait(&bars.p_ready[x][u & 1u], (u >> 1) & 1u);
+  };
+  for (int t = 0; ok && t < 2 && t < T; t++) {
+    ok = keys_there(t);
+    if (!ok) break;
+    tc::fence_after_sync();
+    qk(0, t);
+    if (there(t)) qk(1, t);
+  }
+  for (int t = 0; ok && t < T; t++) {
+    ok = weights_there(0, t);
+    if (!ok) break;
+    tc::fence_after_sync();
+    pv(0, t);
+    if (t + 2 < T) {
+      ok = keys_there(t + 2);
+      if (!ok) break;
+      tc::fence_after_sync();
+      qk(0, t + 2);
+    }
+    if (there(t)) {
+      ok = weights_there(1, t);
+      if (!ok) break;
+      tc::fence_after_sync();
+      pv(1, t);
+      if (t + 2 < T && there(t + 2)) qk(1, t + 2);
+    }
+    if (ends(t)) tc::mma2_commit_warp(&bars.empty[stage_of(t) % kStages], kBoth);   // (S precedes P V)
+  }
+  return ok;
+}
+
 template <int BITS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     paged_attend_kernel(const __grid_constant__ PagedAttend a) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   unsigned char *sm = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
-  __shared__ Bars bars;
   __shared__ PagedCut cut[2];
   __shared__ Piece pieces[2];
   __shared__ uint32_t tmem_base_sh;
-  __shared__ int abort_flag;
   __shared__ float2 half_sums[BM];   // short items: maximum and sum of the second tile's rows
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int share = (int)(blockIdx.x >> 1), cr = (int)tc::cluster_ctarank();
-  volatile int *abort_v = &abort_flag;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the kernels behind this one may line up
   pgd::share_of<kThreads>(a.batch, share, a.shares, kThin, Work{a}, cut);
@@ -323,8 +406,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // The description of the share's piece number i (the whole warp; false: someone gave up).
   auto hear = [&](int i, Piece &p) -> bool {
     if (!__all_sync(0xffffffffu, tc::mbar_try_wait(&bars.told[i & 1], (i >> 1) & 1))) {
-      if (!tc::mbar_wait(&bars.told[i & 1], (i >> 1) & 1, kWaitNs)) fail(&abort_flag, a.status);
-      if (__any_sync(0xffffffffu, *abort_v != 0)) return false;
+      if (!tc::mbar_wait(&bars.told[i & 1], (i >> 1) & 1, kWaitNs)) fail(a.status);
+      if (__any_sync(0xffffffffu, aborted() != 0)) return false;
     }
     p = pieces[i & 1];
     __syncwarp();
@@ -472,8 +555,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const bool full = every.see(v0, v0 + BS);
         const uint32_t tS = tS0 + (u & 1u) * BS;
         if (!__all_sync(0xffffffffu, tc::mbar_try_wait(&bars.s_full[x][u & 1u], (u >> 1) & 1u))) {
-          if (!tc::mbar_wait(&bars.s_full[x][u & 1u], (u >> 1) & 1u, kWaitNs)) fail(&abort_flag, a.status);
-          if (__any_sync(0xffffffffu, *abort_v != 0)) { ok = false; break; }   // the whole warp
+          if (!tc::mbar_wait(&bars.s_full[x][u & 1u], (u >> 1) & 1u, kWaitNs)) fail(a.status);
+          if (__any_sync(0xffffffffu, aborted() != 0)) { ok = false; break; }   // the whole warp
         }
         tc::fence_after_sync();
         // the step's logits at once: their maximum, then their exponentials relative to m_used, which stands
@@ -506,7 +589,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           acc = tc::fma2(acc, a2, 0ull);
           if (t > 0) {  // O of the earlier steps, once PV_x(t-1) has been added (PV_x(t) waits for this warp)
             const uint32_t b = u - 1u;
-            if (!tc::mbar_wait(&bars.pv_done[x][b & 1u], (b >> 1) & 1u, kWaitNs)) fail(&abort_flag, a.status);
+            if (!tc::mbar_wait(&bars.pv_done[x][b & 1u], (b >> 1) & 1u, kWaitNs)) fail(a.status);
             tc::fence_after_sync();
 #pragma unroll 1
             for (int c = 0; c < D; c += 16) {
@@ -558,9 +641,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
       // every MMA of the piece is done: outputs may be read, and the Queries' memory written
-      if (ok && !tc::mbar_wait(&bars.o_done, worked & 1, kWaitNs)) fail(&abort_flag, a.status);
+      if (ok && !tc::mbar_wait(&bars.o_done, worked & 1, kWaitNs)) fail(a.status);
       worked++;
-      ok = !__any_sync(0xffffffffu, !ok || *abort_v != 0);
+      ok = !__any_sync(0xffffffffu, !ok || aborted() != 0);
       if (ok && !(p.brief && x == 1)) {
         tc::fence_after_sync();
         float inv = l > 0.f ? win::kUnit<BITS> / l : 0.f, keep = 0.f;
@@ -657,123 +740,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp == kMmaWarp) {
     // ======================= the even CTA's issues the pair's MMAs, the odd one's passes on that its CTA's stages
     // are full =======================
-    // The warp's common answer.  Whether someone gave up is looked at only where there is something to
-    // wait for.
-    auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
-      if (__all_sync(0xffffffffu, tc::mbar_try_wait_cluster(bar, parity))) return true;
-      return __all_sync(0xffffffffu, tc::mbar_wait_cluster(bar, parity, kWaitNs) && !*abort_v);
-    };
-    uint32_t g0 = 0, c0 = 0, c1 = 0;   // stages so far; steps of tiles 0 and 1
-    int worked = 0;
+    auto wait = [&](uint64_t *bar, uint32_t parity) -> bool { return meet(bar, parity); };
     bool ok = true;
-    const uint32_t full_even = tc::mapa(tc::smem_u32(&bars.full[0]), 0);
-    constexpr uint32_t idesc = tc::idesc_f16_f32(2 * BM, BS), idesc_pv = tc::idesc_f16_f32_bmn(2 * BM, D);
-    constexpr uint16_t kBoth = 3;
-    // broadcast, so that everything derived from them is the warp's and not a lane's
-    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), s0 = __shfl_sync(0xffffffffu, tc::smem_u32(sm), 0);
-    const uint64_t dq = tc::desc_sw128(s0 + OFF_Q), dk = tc::desc_sw128(s0 + OFF_K);
-    const uint64_t dv = tc::desc_sw128_mn(s0 + OFF_V, kBlk, 1024);
-    for (int pi = 0; ok; pi++) {
+    // The next piece's numbers (false: there is none).  They are broadcast, so that everything derived from them is
+    // the warp's and not a lane's, and each CTA has a loop of its own: a value that two branches meet in would not be.
+    // MMAs whose operands are not in uniform registers take 100 cycles each to issue.
+    int J = 0, n = 0, brief = 0;
+    auto next_piece = [&](int pi) -> bool {
       Piece p;
       ok = hear(pi, p);
-      if (!ok || p.done) break;
-      const int J = __shfl_sync(0xffffffffu, p.J, 0), n = __shfl_sync(0xffffffffu, p.steps, 0);
-      const int brief = __shfl_sync(0xffffffffu, p.brief, 0);
+      J = __shfl_sync(0xffffffffu, p.J, 0);
+      n = __shfl_sync(0xffffffffu, p.steps, 0);
+      brief = __shfl_sync(0xffffffffu, p.brief, 0);
+      return ok && __any_sync(0xffffffffu, !p.done);
+    };
+    if (cr == 1) {
+      const uint32_t full = tc::mapa(tc::smem_u32(&bars.full[0]), 0);
+      uint32_t g = 0;   // stages so far
+      for (int pi = 0; ok && next_piece(pi); pi++)
+        for (int j = 0; ok && j < J; j++, g++) {
+          ok = wait(&bars.full[g & (kStages - 1)], (g / kStages) & 1u);
+          if (ok && lane == 0) tc::mbar_arrive_remote(full + 8u * (g & (kStages - 1)));
+        }
+    } else {
+    int worked = 0;
+    constexpr uint16_t kBoth = 3;
+    uint32_t stages = 0, steps0 = 0, steps1 = 0;   // so far; of tiles 0 and 1
+    for (int pi = 0; ok && next_piece(pi); pi++) {
       if (J == 0) continue;
-      if (cr == 1) {
-        for (int j = 0; j < J; j++) {
-          const uint32_t g = g0 + (uint32_t)j;
-          if (!wait(&bars.full[g & (kStages - 1)], (g / kStages) & 1u)) {
-            ok = false;
-            break;
-          }
-          if (lane == 0) tc::mbar_arrive_remote(full_even + 8u * (g & (kStages - 1)));
-        }
-        g0 += (uint32_t)J;
-        continue;
-      }
-      // step t of tile x: both tiles take the same 64 keys, or (short items) a half each of stage t.  (The two
-      // forms are compiled apart: chosen at every step they cost a tenth of it.)
-      auto multiply = [&](auto rows_of_two) {
-        constexpr bool two = decltype(rows_of_two)::value;
-        const int T = two ? n : (n + 1) >> 1;   // steps of tile 0
-        auto stage_of = [&](int t) -> uint32_t { return g0 + (uint32_t)(two ? t >> 1 : t); };
-        auto half_of = [&](int x, int t) { return two ? t & 1 : x; };
-        auto begins = [&](int t) { return !two || !(t & 1); };
-        auto ends = [&](int t) { return !two || (t & 1) || t + 1 == n; };
-        auto there = [&](int t) { return two || 2 * t + 1 < n; };   // tile 1 has a step t
-        auto nth = [&](int x, int t) -> uint32_t { return (x ? c1 : c0) + (uint32_t)t; };
-        auto qk = [&](int x, int t) {
-          const uint32_t ko = (stage_of(t) % kStages) * 2 * kBlkH + (uint32_t)half_of(x, t) * 32 * 128, u = nth(x, t);
-          const uint64_t da = dq + (uint64_t)(two ? x * 2 * kBlk / 16 : 0), db = dk + (uint64_t)(ko / 16);
-          const uint32_t d = tm + 128u * x + (u & 1u) * BS;
-#pragma unroll
-          for (int kk = 0; kk < D / 16; kk++)
-            tc::mma2_ss_warp(d, da + (uint64_t)(((kk / 4) * kBlk + 32 * (kk % 4)) / 16),
-                             db + (uint64_t)(((kk / 4) * kBlkH + 32 * (kk % 4)) / 16), idesc, kk > 0);
-          tc::mma2_commit_warp(&bars.s_full[x][u & 1u], kBoth);
-        };
-        auto pv = [&](int x, int t) {
-          const uint32_t vo = (stage_of(t) % kStages) * kBlk + (uint32_t)half_of(x, t) * BS * 128, u = nth(x, t);
-          const uint64_t db = dv + (uint64_t)(vo / 16);
-          const uint32_t pp = tm + 128u * x + (u & 1u) * BS;
-#pragma unroll
-          for (int kk = 0; kk < BS / 16; kk++)
-            tc::mma2_ts_warp(tm + 256u + 128u * x, pp + 8u * kk, db + (uint64_t)(2048 * kk / 16), idesc_pv,
-                             (t > 0 || kk > 0));
-          tc::mma2_commit_warp(&bars.pv_done[x][u & 1u], kBoth);
-        };
-        auto keys_there = [&](int t) {   // the Keys and Values of step t (a stage's first step waits for it)
-          const uint32_t g = stage_of(t);
-          return !begins(t) || wait(&bars.full[g % kStages], (g / kStages) & 1u);
-        };
-        auto weights_there = [&](int x, int t) {
-          const uint32_t u = nth(x, t);
-          return wait(&bars.p_ready[x][u & 1u], (u >> 1) & 1u);
-        };
-        for (int t = 0; ok && t < 2 && t < T; t++) {
-          ok = keys_there(t);
-          if (!ok) break;
-          tc::fence_after_sync();
-          qk(0, t);
-          if (there(t)) qk(1, t);
-        }
-        for (int t = 0; ok && t < T; t++) {
-          ok = weights_there(0, t);
-          if (!ok) break;
-          tc::fence_after_sync();
-          pv(0, t);
-          if (t + 2 < T) {
-            ok = keys_there(t + 2);
-            if (!ok) break;
-            tc::fence_after_sync();
-            qk(0, t + 2);
-          }
-          if (there(t)) {
-            ok = weights_there(1, t);
-            if (!ok) break;
-            tc::fence_after_sync();
-            pv(1, t);
-            if (t + 2 < T && there(t + 2)) qk(1, t + 2);
-          }
-          if (ends(t)) tc::mma2_commit_warp(&bars.empty[stage_of(t) % kStages], kBoth);   // (S precedes P V)
-        }
-        c0 += (uint32_t)T;
-        c1 += (uint32_t)(two ? n : n >> 1);
-      };
       ok = wait(&bars.q_full, worked & 1);
       tc::fence_after_sync();
-      if (brief) multiply(Flag<false>{});
-      else multiply(Flag<true>{});
-      g0 += (uint32_t)J;
+      if (ok) ok = brief ? multiply<false>(tmem, tc::smem_u32(sm), n, stages, steps0, steps1)
+                         : multiply<true>(tmem, tc::smem_u32(sm), n, stages, steps0, steps1);
+      steps0 += (uint32_t)(brief ? (n + 1) >> 1 : n);
+      steps1 += (uint32_t)(brief ? n >> 1 : n);
+      stages += (uint32_t)J;
       worked++;
       if (ok) tc::mma2_commit_warp(&bars.o_done, kBoth);
     }
-    if (!ok) fail(&abort_flag, a.status);
-    if (cr == 0) {
-      tc::mma2_commit_warp(&bars.drain, 1);  // every MMA issued above completes before TMEM is released
-      if (!tc::mbar_wait(&bars.drain, 0, kWaitNs)) qwm_dev_error(a.status, QWM_ERR_DEVICE_TIMEOUT);
+    tc::mma2_commit_warp(&bars.drain, 1);  // every MMA issued above completes before TMEM is released
+    if (!tc::mbar_wait(&bars.drain, 0, kWaitNs)) qwm_dev_error(a.status, QWM_ERR_DEVICE_TIMEOUT);
     }
+    if (!ok) fail(a.status);
   } else if (warp == kPlanWarp) {
     // ======================= the pieces of the share =======================
     int b = begin.b, item = begin.item, block = begin.block, pi = 0;
@@ -813,7 +821,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       more = !p.done;
       if (pi >= 2 && !__all_sync(0xffffffffu, tc::mbar_wait(&bars.heard[pi & 1], ((pi >> 1) - 1) & 1, kWaitNs))) {
-        fail(&abort_flag, a.status);
+        fail(a.status);
         break;
       }
       if (lane == 0) pieces[pi & 1] = p;
@@ -841,8 +849,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       auto free_again = [&](uint32_t g) -> bool {   // the previous contents of stage g's place are consumed
         uint64_t *empty = &bars.empty[g & (kStages - 1)];
         if (g < kStages || __all_sync(0xffffffffu, tc::mbar_try_wait(empty, (g / kStages - 1) & 1u))) return true;
-        if (!tc::mbar_wait(empty, (g / kStages - 1) & 1u, kWaitNs)) fail(&abort_flag, a.status);
-        return !__any_sync(0xffffffffu, *abort_v != 0);         // warp-uniform exit
+        if (!tc::mbar_wait(empty, (g / kStages - 1) & 1u, kWaitNs)) fail(a.status);
+        return !__any_sync(0xffffffffu, aborted() != 0);         // warp-uniform exit
       };
       // stage j is stored and the codes of stage j + 2 fetched in its place; the first round only fetches
       auto stage = [&](int j, Codes<BITS> &k, Codes<BITS> &v) -> bool {
