@@ -14,11 +14,12 @@
 // Warp roles of each CTA (14 warps):
 //   warps 0-3, 4-7  softmax of Query tile 0 / 1: thread = Query row = TMEM lane, 64 logits at a time; between
 //                   pieces they write the output and fetch the next Queries;
-//   warps 8-11      producers: codes two stages ahead in registers, table entries three, decoded into swizzled
-//                   stages; they run ahead into the next piece while the last one is written;
-//   warp 12         allocates TMEM; in the even CTA it issues every MMA of the pair, in the odd one it
+//   warp 8          allocates TMEM; in the even CTA it issues every MMA of the pair, in the odd one it
 //                   passes on to the even one that its producers have filled a stage;
-//   warp 13         walks along the share and describes its pieces to the others, two ahead.
+//   warps 9-11, 13  producers: codes two stages ahead in registers, table entries three, decoded into swizzled
+//                   stages; they run ahead into the next piece while the last one is written;
+//   warp 12         walks along the share and describes its pieces to the others, two ahead.
+// (No producer shares a scheduler with warp 8, whose instructions would have to be fetched again and again.)
 // An item with up to 256 rows gives both tiles those rows and every other 64 keys each, joined at the end.
 // TMEM (512 columns): S_x as two buffers of 64 keys, P_x over them, O_x.  Keys arrive in stages of 128, decoded
 // in 16 rows of one page at a time; step t issues P V of tile x's keys t, then Q K^T of keys t + 2 into the
@@ -31,7 +32,7 @@ namespace {
 constexpr int D = win::D;
 constexpr int BM = 128, BN = 128, NQT = 2;  // Query rows of a CTA tile, keys of a stage, CTA tiles
 constexpr int BS = 64;                      // keys of a step
-constexpr int kSoftmaxWarps = 8, kProdWarp0 = 8, kProdWarps = 4, kMmaWarp = 12, kPlanWarp = 13;
+constexpr int kSoftmaxWarps = 8, kProdWarps = 4, kMmaWarp = 8, kPlanWarp = 12;   // producers: 9, 10, 11 and 13
 constexpr int kThreads = 32 * 14;
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units the maximum may lag behind
@@ -265,10 +266,23 @@ struct Producer {
   }
 };
 
-// The warp's common answer.  Whether someone gave up is looked at only where there is something to wait for.
+// A wait of the whole warp with one answer (false: someone gave up): every branch goes by a vote, so that the
+// warp is never seen to part.  Whether someone gave up is looked at only where there is something to wait for.
 __device__ __forceinline__ bool meet(uint64_t *bar, uint32_t parity) {
   if (__all_sync(0xffffffffu, tc::mbar_try_wait_cluster(bar, parity))) return true;
-  return __all_sync(0xffffffffu, tc::mbar_wait_cluster(bar, parity, kWaitNs) && !aborted());
+  const uint64_t t0 = tc::globaltimer_ns();
+  for (;;) {
+    if (__all_sync(0xffffffffu, tc::mbar_try_wait_cluster(bar, parity))) return true;
+    if (__any_sync(0xffffffffu, aborted() != 0 || tc::globaltimer_ns() - t0 > kWaitNs)) return false;
+  }
+}
+// A value that all lanes hold, seen to be the warp's.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __reduce_max_sync(0xffffffffu, v); }
+// One lane's arrival, by predication.
+__device__ __forceinline__ void arrive_one(uint32_t cluster_addr) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t@q mbarrier.arrive.shared::cluster.b64 _, [%0];\n\t}" ::"r"(cluster_addr)
+      : "memory");
 }
 
 // The even CTA's MMAs of one piece: n steps, step t of tile x being number c_x + t and in stage g0 + .. of the
@@ -278,14 +292,11 @@ template <bool two>
 __device__ __noinline__ bool multiply(uint32_t tmem, uint32_t smem, int steps, uint32_t stage0, uint32_t step0, uint32_t step1) {
   constexpr uint32_t idesc = tc::idesc_f16_f32(2 * BM, BS), idesc_pv = tc::idesc_f16_f32_bmn(2 * BM, D);
   constexpr uint16_t kBoth = 3;
-  // broadcast, so that everything derived from them is the warp's and not a lane's
-  const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0), s0 = __shfl_sync(0xffffffffu, smem, 0);
-  const uint32_t g0 = __shfl_sync(0xffffffffu, stage0, 0), c0 = __shfl_sync(0xffffffffu, step0, 0), c1 = __shfl_sync(0xffffffffu, step1, 0);
-  const int n = __shfl_sync(0xffffffffu, steps, 0);
-  const uint64_t dq = tc::desc_sw128(s0 + OFF_Q), dk = tc::desc_sw128(s0 + OFF_K);
-  const uint64_t dv = tc::desc_sw128_mn(s0 + OFF_V, kBlk, 1024);
-  bool ok = true;
-  auto wait = [&](uint64_t *bar, uint32_t parity) -> bool { return meet(bar, parity); };
+  const uint32_t tm = uniform(tmem), s0 = uniform(smem), g0 = uniform(stage0), c0 = uniform(step0), c1 = uniform(step1);
+  const int n = (int)uniform((uint32_t)steps);
+  // descriptors' lower words: K-major ones with 1 in the place of the stride that they do not use
+  const uint32_t dq = ((s0 + OFF_Q) >> 4) | 1u << 16, dk = ((s0 + OFF_K) >> 4) | 1u << 16;
+  const uint32_t dv = ((s0 + OFF_V) >> 4) | (uint32_t)(kBlk >> 4) << 16;
   const int T = two ? n : (n + 1) >> 1;   // steps of tile 0
   auto stage_of = [&](int t) -> uint32_t { return g0 + (uint32_t)(two ? t >> 1 : t); };
   auto half_of = [&](int x, int t) { return two ? t & 1 : x; };
@@ -295,60 +306,56 @@ __device__ __noinline__ bool multiply(uint32_t tmem, uint32_t smem, int steps, u
   auto nth = [&](int x, int t) -> uint32_t { return (x ? c1 : c0) + (uint32_t)t; };
   auto qk = [&](int x, int t) {
     const uint32_t ko = (stage_of(t) % kStages) * 2 * kBlkH + (uint32_t)half_of(x, t) * 32 * 128, u = nth(x, t);
-    const uint64_t da = dq + (uint64_t)(two ? x * 2 * kBlk / 16 : 0), db = dk + (uint64_t)(ko / 16);
+    const uint32_t da = dq + (uint32_t)(two ? x * 2 * kBlk / 16 : 0), db = dk + ko / 16;
     const uint32_t d = tm + 128u * x + (u & 1u) * BS;
 #pragma unroll
     for (int kk = 0; kk < D / 16; kk++)
-      tc::mma2_ss_warp(d, da + (uint64_t)(((kk / 4) * kBlk + 32 * (kk % 4)) / 16),
-                       db + (uint64_t)(((kk / 4) * kBlkH + 32 * (kk % 4)) / 16), idesc, kk > 0);
+      tc::mma2_ss_warp_lo<tc::kDescSw128Hi, tc::kDescSw128Hi>(d, da + (uint32_t)(((kk / 4) * kBlk + 32 * (kk % 4)) / 16),
+                                                              db + (uint32_t)(((kk / 4) * kBlkH + 32 * (kk % 4)) / 16), idesc, kk > 0);
     tc::mma2_commit_warp(&bars.s_full[x][u & 1u], kBoth);
   };
   auto pv = [&](int x, int t) {
     const uint32_t vo = (stage_of(t) % kStages) * kBlk + (uint32_t)half_of(x, t) * BS * 128, u = nth(x, t);
-    const uint64_t db = dv + (uint64_t)(vo / 16);
+    const uint32_t db = dv + vo / 16;
     const uint32_t pp = tm + 128u * x + (u & 1u) * BS;
 #pragma unroll
     for (int kk = 0; kk < BS / 16; kk++)
-      tc::mma2_ts_warp(tm + 256u + 128u * x, pp + 8u * kk, db + (uint64_t)(2048 * kk / 16), idesc_pv,
-                       (t > 0 || kk > 0));
+      tc::mma2_ts_warp_lo<tc::kDescSw128Hi>(tm + 256u + 128u * x, pp + 8u * kk, db + (uint32_t)(2048 * kk / 16), idesc_pv,
+                                            (t > 0 || kk > 0));
     tc::mma2_commit_warp(&bars.pv_done[x][u & 1u], kBoth);
   };
   auto keys_there = [&](int t) {   // the Keys and Values of step t (a stage's first step waits for it)
     const uint32_t g = stage_of(t);
-    return !begins(t) || wait(&bars.full[g % kStages], (g / kStages) & 1u);
+    return !begins(t) || meet(&bars.full[g % kStages], (g / kStages) & 1u);
   };
   auto weights_there = [&](int x, int t) {
     const uint32_t u = nth(x, t);
-    return wait(&bars.p_ready[x][u & 1u], (u >> 1) & 1u);
+    return meet(&bars.p_ready[x][u & 1u], (u >> 1) & 1u);
   };
-  for (int t = 0; ok && t < 2 && t < T; t++) {
-    ok = keys_there(t);
-    if (!ok) break;
+  for (int t = 0; t < 2 && t < T; t++) {
+    if (!keys_there(t)) return false;
     tc::fence_after_sync();
     qk(0, t);
     if (there(t)) qk(1, t);
   }
-  for (int t = 0; ok && t < T; t++) {
-    ok = weights_there(0, t);
-    if (!ok) break;
+  for (int t = 0; t < T; t++) {
+    if (!weights_there(0, t)) return false;
     tc::fence_after_sync();
     pv(0, t);
     if (t + 2 < T) {
-      ok = keys_there(t + 2);
-      if (!ok) break;
+      if (!keys_there(t + 2)) return false;
       tc::fence_after_sync();
       qk(0, t + 2);
     }
     if (there(t)) {
-      ok = weights_there(1, t);
-      if (!ok) break;
+      if (!weights_there(1, t)) return false;
       tc::fence_after_sync();
       pv(1, t);
       if (t + 2 < T && there(t + 2)) qk(1, t + 2);
     }
     if (ends(t)) tc::mma2_commit_warp(&bars.empty[stage_of(t) % kStages], kBoth);   // (S precedes P V)
   }
-  return ok;
+  return true;
 }
 
 template <int BITS>
@@ -740,48 +747,60 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp == kMmaWarp) {
     // ======================= the even CTA's issues the pair's MMAs, the odd one's passes on that its CTA's stages
     // are full =======================
-    auto wait = [&](uint64_t *bar, uint32_t parity) -> bool { return meet(bar, parity); };
-    bool ok = true;
-    // The next piece's numbers (false: there is none).  They are broadcast, so that everything derived from them is
-    // the warp's and not a lane's, and each CTA has a loop of its own: a value that two branches meet in would not be.
-    // MMAs whose operands are not in uniform registers take 100 cycles each to issue.
-    int J = 0, n = 0, brief = 0;
-    auto next_piece = [&](int pi) -> bool {
-      Piece p;
-      ok = hear(pi, p);
-      J = __shfl_sync(0xffffffffu, p.J, 0);
-      n = __shfl_sync(0xffffffffu, p.steps, 0);
-      brief = __shfl_sync(0xffffffffu, p.brief, 0);
-      return ok && __any_sync(0xffffffffu, !p.done);
-    };
+    // Everything that MMAs and loops depend on is reduced over the warp, whose lanes hold the same, and a failed
+    // wait leaves all loops at once: where the compiler cannot see that the warp stays together, operands pass
+    // through a register of each lane, 100 cycles an MMA.
     if (cr == 1) {
       const uint32_t full = tc::mapa(tc::smem_u32(&bars.full[0]), 0);
       uint32_t g = 0;   // stages so far
-      for (int pi = 0; ok && next_piece(pi); pi++)
-        for (int j = 0; ok && j < J; j++, g++) {
-          ok = wait(&bars.full[g & (kStages - 1)], (g / kStages) & 1u);
-          if (ok && lane == 0) tc::mbar_arrive_remote(full + 8u * (g & (kStages - 1)));
+      for (int pi = 0;; pi++) {
+        if (!meet(&bars.told[pi & 1], (uint32_t)(pi >> 1) & 1u)) goto failed;
+        const Piece &p = pieces[pi & 1];
+        const uint32_t done = uniform((uint32_t)p.done);
+        const int J = (int)uniform((uint32_t)p.J);
+        arrive_one(tc::smem_u32(&bars.heard[pi & 1]));
+        if (done) break;
+        for (int j = 0; j < J; j++, g++) {
+          if (!meet(&bars.full[g & (kStages - 1)], (g / kStages) & 1u)) goto failed;
+          arrive_one(full + 8u * (g & (kStages - 1)));
         }
+      }
     } else {
-    int worked = 0;
-    constexpr uint16_t kBoth = 3;
-    uint32_t stages = 0, steps0 = 0, steps1 = 0;   // so far; of tiles 0 and 1
-    for (int pi = 0; ok && next_piece(pi); pi++) {
-      if (J == 0) continue;
-      ok = wait(&bars.q_full, worked & 1);
-      tc::fence_after_sync();
-      if (ok) ok = brief ? multiply<false>(tmem, tc::smem_u32(sm), n, stages, steps0, steps1)
-                         : multiply<true>(tmem, tc::smem_u32(sm), n, stages, steps0, steps1);
-      steps0 += (uint32_t)(brief ? (n + 1) >> 1 : n);
-      steps1 += (uint32_t)(brief ? n >> 1 : n);
-      stages += (uint32_t)J;
-      worked++;
-      if (ok) tc::mma2_commit_warp(&bars.o_done, kBoth);
+      constexpr uint16_t kBoth = 3;
+      const uint32_t tm = uniform(tmem), s0 = uniform(tc::smem_u32(sm));
+      uint32_t stages = 0, steps0 = 0, steps1 = 0, worked = 0;   // so far; of tiles 0 and 1; pieces with keys
+      for (int pi = 0;; pi++) {
+        if (!meet(&bars.told[pi & 1], (uint32_t)(pi >> 1) & 1u)) goto failed;
+        const Piece &p = pieces[pi & 1];
+        const uint32_t J = uniform((uint32_t)p.J), n = uniform((uint32_t)p.steps), brief = uniform((uint32_t)p.brief);
+        const uint32_t done = uniform((uint32_t)p.done);
+        arrive_one(tc::smem_u32(&bars.heard[pi & 1]));
+        if (done) break;
+        if (J == 0) continue;
+        if (!meet(&bars.q_full, worked & 1u)) goto failed;
+        tc::fence_after_sync();
+        if (brief) {
+          if (!multiply<false>(tm, s0, (int)n, stages, steps0, steps1)) goto failed;
+          steps0 += (n + 1) >> 1;
+          steps1 += n >> 1;
+        } else {
+          if (!multiply<true>(tm, s0, (int)n, stages, steps0, steps1)) goto failed;
+          steps0 += n;
+          steps1 += n;
+        }
+        stages += J;
+        worked++;
+        tc::mma2_commit_warp(&bars.o_done, kBoth);
+      }
     }
-    tc::mma2_commit_warp(&bars.drain, 1);  // every MMA issued above completes before TMEM is released
-    if (!tc::mbar_wait(&bars.drain, 0, kWaitNs)) qwm_dev_error(a.status, QWM_ERR_DEVICE_TIMEOUT);
+    if (false) {
+    failed:
+      fail(a.status);
     }
-    if (!ok) fail(a.status);
+    if (cr == 0) {
+      tc::mma2_commit_warp(&bars.drain, 1);  // every MMA issued above completes before TMEM is released
+      if (!tc::mbar_wait(&bars.drain, 0, kWaitNs)) qwm_dev_error(a.status, QWM_ERR_DEVICE_TIMEOUT);
+    }
   } else if (warp == kPlanWarp) {
     // ======================= the pieces of the share =======================
     int b = begin.b, item = begin.item, block = begin.block, pi = 0;
@@ -832,7 +851,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (first && lane == 0 && cr == 0) a.cuts[share] = PagedCut{a.batch, 0, 0, 0, 0, 0, 0};
   } else {
     // ======================= producers: Keys, then Values, of every stage =======================
-    const int pw = warp - kProdWarp0;
+    const int pw = warp == 13 ? 3 : warp - 9;
     const Producer<BITS, false> pk(a, sm, cr, pw, lane);
     const Producer<BITS, true> pv(a, sm, cr, pw, lane);
     Codes<BITS> k0, v0, k1, v1;

@@ -461,3 +461,27 @@ __device__ __forceinline__ void mma2_commit_warp(uint64_t *bar, uint16_t cta_mas
       : "memory");
 }
 }  // namespace tc
+
+// The same with matrix descriptors given by their lower words (an address in units of 16 bytes, and a stride
+// where there is one): the upper word is the same for every operand of a layout, and a literal.
+namespace tc {
+constexpr uint32_t kDescSw128Hi = (1024u >> 4) | (1u << 14) | (2u << 29);   // row groups 1024 bytes apart, version, swizzle
+template <uint32_t A_HI, uint32_t B_HI>
+__device__ __forceinline__ void mma2_ss_warp_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\telect.sync _|q, 0xffffffff;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+      "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "n"(A_HI), "r"(b_lo), "n"(B_HI), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+template <uint32_t B_HI>
+__device__ __forceinline__ void mma2_ts_warp_lo(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\telect.sync _|q, 0xffffffff;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "n"(B_HI), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+}  // namespace tc
