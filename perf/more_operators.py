@@ -453,6 +453,12 @@ def _spec(dims, theta, pairing, gh, gw):
     return qwm.RopeSpec(dims, theta=theta, pairing=pairing, grid=(gh, gw))
 
 
+@functools.lru_cache(maxsize=None)
+def _largest(items):
+    """The largest number of new tokens of a sequence, which a program that plans its batches knows."""
+    return max(_sequences(dict(items))[1])
+
+
 def _spec_of(case):
     return _spec((case["axis_t"], case["axis_y"], case["axis_x"]), case["theta"], case["pairing"], case["gh"], case["gw"])
 
@@ -475,7 +481,7 @@ def _own(s):
         return {"table": tab.table, "length": tab.length, "free": tab.free, "free_count": tab.free_count, "first": s["first"],
                 "granted": s["granted"], "slot": s["slot"], "at": s["at"]}
     qwm.qwm_paged_attend(_context(case["heads"]), qwm.PagePool(case["bits"], **s["pool"]), tab, s["q"], s["first"], s["count"], 1.0 / math.sqrt(D),
-                         s["out"], lse=s["lse"], tpf=case["tpf"], frames=case["frames"], sink=case["sink"], max_count=max(_sequences(case)[1]))
+                         s["out"], lse=s["lse"], tpf=case["tpf"], frames=case["frames"], sink=case["sink"], max_count=_largest(tuple(case.items())))
     return {"out": s["out"], "lse": s["lse"]}
 
 
