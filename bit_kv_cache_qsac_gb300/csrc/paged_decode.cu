@@ -198,51 +198,75 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) paged_decode_kernel
 }
 
 // Parts of an item joined: the weighted mean of the parts' outputs, each weighted by its share of the
-// exponential sum.  Blocks of 8 warps, one warp per row; per share whose beginning cuts an item first, a block for
-// every 8 of the item's rows (few_blocks: the warp tiles' blocks, which come first).
+// exponential sum.  Per share whose beginning cuts an item first, blocks of 8 warps with ROWS rows a warp; the warp
+// tiles' blocks (`few_blocks`) come first.  What depends on one another is three loads: the cuts behind this one and
+// the one before it (a lane each), the parts' log-sum-exps (a lane each), the parts.
+template <int ROWS>
+__device__ __forceinline__ void combine(const PagedAttend &a, int at, int part_rows) {
+  const int blocks = part_rows / (8 * ROWS), s = at / blocks + 1, lane = threadIdx.x & 31;
+  const int r0 = (at % blocks * 8 + (threadIdx.x >> 5)) * ROWS;
+  auto same = [&](const PagedCut &x, const PagedCut &y) { return x.b == y.b && x.item == y.item && x.block > 0; };
+  const PagedCut c = a.cuts[s];
+  const PagedCut near = a.cuts[s - 1 + lane < a.shares ? s - 1 + lane : a.shares - 1];
+  if (c.block == 0 || r0 >= c.live) return;
+  uint32_t inside = __ballot_sync(0xffffffffu, s - 1 + lane < a.shares && same(near, c));
+  if (inside & 1u) return;   // an earlier cut of the item
+  // parts: the second place of share s - 1, then the first places of the shares from s on
+  int n = 1 + __ffs((int)~(inside >> 1)) - 1;
+  if (n == 32)
+    while (s - 1 + n < a.shares && same(a.cuts[s - 1 + n], c)) n++;
+  auto place = [&](int k, int r) -> int64_t { return ((int64_t)(k == 0 ? 2 * (s - 1) + 1 : 2 * (s - 1 + k))) * part_rows + r; };
+  float M[ROWS], mine[ROWS], L[ROWS];
+  float4 acc[ROWS];
+#pragma unroll
+  for (int i = 0; i < ROWS; i++) mine[i] = lane < n && r0 + i < c.live ? a.part_lse[place(lane, r0 + i)] : -INFINITY;
+#pragma unroll
+  for (int i = 0; i < ROWS; i++) {
+    M[i] = mine[i];
+    for (int k = 32 + lane; k < n; k += 32) M[i] = fmaxf(M[i], r0 + i < c.live ? a.part_lse[place(k, r0 + i)] : -INFINITY);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) M[i] = fmaxf(M[i], __shfl_xor_sync(0xffffffffu, M[i], d));
+    mine[i] = mine[i] == -INFINITY ? 0.f : exp2f(mine[i] - M[i]);   // this lane's part's weight
+    L[i] = 0.f;
+    acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+#pragma unroll 4
+  for (int k = 0; k < n; k++) {
+#pragma unroll
+    for (int i = 0; i < ROWS; i++) {
+      if (r0 + i >= c.live) break;
+      float wt = __shfl_sync(0xffffffffu, mine[i], k & 31);
+      if (k >= 32) {
+        const float l = a.part_lse[place(k, r0 + i)];
+        wt = l == -INFINITY ? 0.f : exp2f(l - M[i]);
+      }
+      const float4 x = *(const float4 *)(a.part + place(k, r0 + i) * D + 4 * lane);
+      L[i] += wt;
+      acc[i].x = fmaf(x.x, wt, acc[i].x);
+      acc[i].y = fmaf(x.y, wt, acc[i].y);
+      acc[i].z = fmaf(x.z, wt, acc[i].z);
+      acc[i].w = fmaf(x.w, wt, acc[i].w);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < ROWS; i++) {
+    if (r0 + i >= c.live) break;
+    const float inv = L[i] > 0.f ? 1.f / L[i] : 0.f, lse = L[i] > 0.f ? M[i] + log2f(L[i]) : -INFINITY;
+    const int q = (int)((uint32_t)(c.row + r0 + i) / (uint32_t)a.group), h = c.kvh * a.group + (c.row + r0 + i - q * a.group);
+    pgd::finish4(a, c.first + q, h, 4 * lane, make_float4(acc[i].x * inv, acc[i].y * inv, acc[i].z * inv, acc[i].w * inv), lse);
+    __syncwarp();   // merging lanes have read the earlier log-sum-exp
+    if (lane == 0) pgd::finish_lse(a, c.first + q, h, lse);
+  }
+}
+
+constexpr int kManyRows = 4;   // a warp's rows of the tensor-memory tiles' parts
+
 __global__ void __launch_bounds__(256)
     paged_combine_kernel(const __grid_constant__ PagedAttend few, const __grid_constant__ PagedAttend many, int few_rows,
                          int few_blocks) {
   asm volatile("griddepcontrol.wait;" ::: "memory");   // launched while the parts are computed: wait for them
-  const bool first = (int)blockIdx.x < few_blocks;
-  const PagedAttend &a = first ? few : many;
-  const int part_rows = first ? few_rows : kPagedTileRows, at = (int)blockIdx.x - (first ? 0 : few_blocks);
-  const int s = at / (part_rows / 8) + 1, lane = threadIdx.x & 31, r = at % (part_rows / 8) * 8 + (threadIdx.x >> 5);
-  const PagedCut c = a.cuts[s];
-  if (c.block == 0 || r >= c.live) return;
-  const PagedCut before = a.cuts[s - 1];
-  if (before.b == c.b && before.item == c.item && before.block > 0) return;   // an earlier cut of the item
-  int last = s;   // the item's last part is this share's first
-  while (last + 1 < a.shares) {
-    const PagedCut d = a.cuts[last + 1];
-    if (d.b != c.b || d.item != c.item || d.block == 0) break;
-    last++;
-  }
-  // parts: the second place of share s - 1, then the first places of shares s .. last
-  auto place = [&](int k) -> int64_t { return ((int64_t)(k < s ? 2 * k + 1 : 2 * k)) * part_rows + r; };
-  float M = -INFINITY;
-  for (int k = s - 1; k <= last; k++) M = fmaxf(M, a.part_lse[place(k)]);
-  float L = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (M > -INFINITY) {
-#pragma unroll 4
-    for (int k = s - 1; k <= last; k++) {
-      const float wt = exp2f(a.part_lse[place(k)] - M);
-      const float4 x = *(const float4 *)(a.part + place(k) * D + 4 * lane);
-      L += wt;
-      acc.x = fmaf(x.x, wt, acc.x);
-      acc.y = fmaf(x.y, wt, acc.y);
-      acc.z = fmaf(x.z, wt, acc.z);
-      acc.w = fmaf(x.w, wt, acc.w);
-    }
-    const float inv = 1.f / L;
-    acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-  }
-  const float lse = L > 0.f ? M + log2f(L) : -INFINITY;
-  const int i = (c.row + r) / a.group, token = c.first + i, h = c.kvh * a.group + (c.row + r - i * a.group);
-  pgd::finish4(a, token, h, 4 * lane, acc, lse);
-  __syncwarp();
-  if (lane == 0) pgd::finish_lse(a, token, h, lse);
+  if ((int)blockIdx.x < few_blocks) combine<1>(few, (int)blockIdx.x, few_rows);
+  else combine<kManyRows>(many, (int)blockIdx.x - few_blocks, kPagedTileRows);
 }
 
 template <int BITS, int NT>
@@ -276,7 +300,7 @@ cudaError_t launch_paged_decode(const PagedAttend &a, int row_tiles, bool beside
 // Launched as a dependent of the parts' kernels, so that its start-up overlaps their work.
 cudaError_t launch_paged_combine(const PagedAttend *few, int part_rows, const PagedAttend *many, cudaStream_t st) {
   const int few_blocks = few ? (few->shares - 1) * (part_rows / 8) : 0;
-  const int many_blocks = many ? (many->shares - 1) * (kPagedTileRows / 8) : 0;
+  const int many_blocks = many ? (many->shares - 1) * (kPagedTileRows / (8 * kManyRows)) : 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(few_blocks + many_blocks));
   cfg.blockDim = dim3(256);
@@ -286,6 +310,5 @@ cudaError_t launch_paged_combine(const PagedAttend *few, int part_rows, const Pa
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_combine_kernel, few ? *few : *many, many ? *many : *few, few ? part_rows : kPagedTileRows,
-                            few_blocks);
+  return cudaLaunchKernelEx(&cfg, paged_combine_kernel, few ? *few : *many, many ? *many : *few, part_rows, few_blocks);
 }
