@@ -11,12 +11,12 @@
 // CTA c of a pair holds rows 256 x + 128 c .. + 127 of the two Query tiles x = 0, 1.  The B operand of an
 // M = 256 MMA is split by N, so CTA c decodes only keys 32 c .. 32 c + 31 of every 64 for Q K^T and only
 // channels 64 c .. 64 c + 63 for P V: half of everything.
-// Warp roles of each CTA (14 warps):
+// Warp roles of each CTA (16 warps):
 //   warps 0-3, 4-7  softmax of Query tile 0 / 1: thread = Query row = TMEM lane, 64 logits at a time; between
 //                   pieces they write the output and fetch the next Queries;
 //   warp 8          allocates TMEM; in the even CTA it issues every MMA of the pair, in the odd one it
 //                   passes on to the even one that its producers have filled a stage;
-//   warps 9-11, 13  producers: codes two stages ahead in registers, table entries three, decoded into swizzled
+//   others          producers (9-11: Keys, 13-15: Values): codes two stages ahead in registers, table entries three, decoded into swizzled
 //                   stages; they run ahead into the next piece while the last one is written;
 //   warp 12         walks along the share and describes its pieces to the others, two ahead.
 // (No producer shares a scheduler with warp 8, whose instructions would have to be fetched again and again.)
@@ -32,8 +32,8 @@ namespace {
 constexpr int D = win::D;
 constexpr int BM = 128, BN = 128, NQT = 2;  // Query rows of a CTA tile, keys of a stage, CTA tiles
 constexpr int BS = 64;                      // keys of a step
-constexpr int kSoftmaxWarps = 8, kProdWarps = 4, kMmaWarp = 8, kPlanWarp = 12;   // producers: 9, 10, 11 and 13
-constexpr int kThreads = 32 * 14;
+constexpr int kSoftmaxWarps = 8, kProdWarps = 6, kMmaWarp = 8, kPlanWarp = 12;   // producers: 9-11, 13-15
+constexpr int kThreads = 32 * 16;
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units the maximum may lag behind
 constexpr int kStages = 4;                  // (a power of two)
@@ -153,7 +153,7 @@ struct RowOut {
   uint16_t *bf16 = nullptr;
   float *lse = nullptr;
   int merge = 0;
-  __device__ __forceinline__ void init(const PagedAttend &a, const Piece &p, int share, int r) {   // r: row of the item
+  __device__ __forceinline__ void init(const PagedAttend &a, const volatile Piece &p, int share, int r) {   // r: row of the item
     if (p.place) {
       const int64_t pr = ((int64_t)share * 2 + p.place - 1) * kRows + r;
       f32 = a.part + pr * D;
@@ -169,99 +169,82 @@ struct RowOut {
   }
 };
 
-// A producer thread's share of a 128-key stage: four pieces of 16 channels.
+// A producer's unit of a stage: 16 keys (of one page) by 64 channels of Keys or Values, two rows a thread, 16
+// channels of each: row lane / 4 and the eighth after it, channels 16 (lane % 4).  A quarter warp's 16-byte
+// stores take two rows, one of even and one of odd number, so the swizzle puts them into eight bank groups.
+// Of a CTA's 64 Keys by 128 channels and 128 Values by 64 channels, eight units each, a producer has three (or two).
 template <int BITS>
 struct Codes {
-  uint32_t c[4][BITS / 2];
-  uint32_t step[4];
+  uint32_t c[2][BITS / 2];
+  uint32_t step[2];
 };
-
-// One producer thread's side of Keys or Values in CTA cr of a pair.  Keys: rows r = 16 w + 4 i + lane / 4 % 4
-// (i = 0..3) of the CTA's half, key 64 (r / 32) + 32 cr + r % 32, channels 16 (lane % 4 + 4 (lane / 16)): 16
-// neighbours for a warp; Values: key rows 32 w + 8 i + lane / 4, channels 64 cr + 16 (lane % 4): twice 16.  A quarter
-// warp's 16-byte stores take two rows, one of even and one of odd number, so the swizzle puts them into eight
-// bank groups.
-template <int BITS, bool VAL>
-struct Producer {
-  static constexpr int kRowStep = VAL ? 8 : 4, kGroups = VAL ? 2 : 1;
-  static constexpr uint32_t kStage = VAL ? (uint32_t)kBlk : 2u * kBlkH;
+template <int BITS>
+struct Unit {
   static constexpr int kRowBytes = D * BITS / 8;
-  const uint8_t *codes, *steps;   // of the pool's row `row0 % 16`, this thread's channels
-  int key0, row0;                 // first key of the warp's 16; this thread's row in them
-  uint32_t dst[2][2];             // shared addresses of the piece's two chunks in even and odd rows i
+  static constexpr uint32_t kStage = (uint32_t)kBlk;   // bytes of a stage of either
+  int key0, row;                // first key; this thread's row
+  uint32_t code_at, step_at;    // bytes from the group's first row to this thread's row and channels
+  uint32_t dst[2];              // shared addresses of the row's two chunks
 
-  __device__ __forceinline__ Producer(const PagedAttend &a, unsigned char *sm, int cr, int w, int lane) {
-    const int row = VAL ? 32 * w + (lane >> 2) : 16 * w + ((lane >> 2) & 3);
-    const int piece = VAL ? (lane & 3) : (lane & 3) + 4 * (lane >> 4);
-    const int ch = VAL ? 64 * cr + 16 * piece : 16 * piece;
-    const int key = VAL ? row : BS * (w >> 1) + 32 * cr + (row & 31);
-    row0 = key & 15;
-    key0 = key - row0;
-    codes = (VAL ? a.pool.v_codes : a.pool.k_codes) + row0 * kRowBytes + ch * BITS / 8;
-    steps = (VAL ? a.pool.v_step : a.pool.k_step) + row0 * win::kSteps + ch / win::kGroup;
-    const uint32_t block = tc::smem_u32(sm + (VAL ? OFF_V : OFF_K)) + (VAL ? 0u : (uint32_t)(piece >> 2) * kBlkH);
+  // Unit u (0..7) of the Values (val) or the Keys of CTA cr.
+  __device__ __forceinline__ void place(uint32_t smem, bool val, int u, int cr, int lane) {
+    static_assert(2 * kBlkH == kBlk, "");
+    row = lane >> 2;
+    const int g = val ? u : u >> 1, piece = lane & 3, ch = (val ? 64 * cr : 64 * (u & 1)) + 16 * piece;
+    key0 = val ? 16 * g : BS * (g >> 1) + 32 * cr + 16 * (g & 1);
+    code_at = (uint32_t)(row * kRowBytes + ch * BITS / 8);
+    step_at = (uint32_t)(row * win::kSteps + ch / win::kGroup);
+    const uint32_t at = smem + (val ? OFF_V : OFF_K + (uint32_t)(u & 1) * kBlkH) + (uint32_t)(16 * g + row) * 128u;
 #pragma unroll
-    for (int i = 0; i < 2; i++)
-#pragma unroll
-      for (int h = 0; h < 2; h++) {
-        const uint32_t r = (uint32_t)(row + kRowStep * i), chunk = 2u * (uint32_t)(piece & 3) + h;
-        dst[i][h] = block + r * 128u + ((chunk ^ (r & 7u)) << 4);
-      }
+    for (int h = 0; h < 2; h++) dst[h] = at + (((2u * (uint32_t)piece + h) ^ ((uint32_t)row & 7u)) << 4);
   }
-  // The table entries of the stage of keys v0 .. v0 + 127.
-  __device__ __forceinline__ void look(const PagedAttend &a, const pgd::Keys &keys, const int32_t *table, int v0,
-                                       int (&entry)[kGroups]) const {
-#pragma unroll
-    for (int g = 0; g < kGroups; g++) {
-      const int v = v0 + key0 + 16 * g;
-      entry[g] = v < keys.total ? __ldg(table + (keys.token(v) >> a.page_log2)) : 0;
-    }
+  // The table entry of the stage of keys v0 .. v0 + 127.
+  __device__ __forceinline__ int look(const PagedAttend &a, const pgd::Keys &keys, const int32_t *table, int v0) const {
+    const int v = v0 + key0;
+    return v < keys.total ? __ldg(table + (keys.token(v) >> a.page_log2)) : 0;
   }
-  // The codes of that stage; rows past the last key are zeros.
-  __device__ __forceinline__ void load(const PagedAttend &a, const pgd::Keys &keys, int kvh, int v0, const int (&entry)[kGroups],
-                                       Codes<BITS> &p) const {
+  // The codes of that stage, from page 0's codes and steps of the piece's Key head; rows past the last key get a step
+  // of 0, which makes zeros of whatever codes.
+  __device__ __forceinline__ void load(const PagedAttend &a, const pgd::Keys &keys, const uint8_t *codes, const uint8_t *steps, int v0,
+                                       int entry, Codes<BITS> &p) const {
+    const uint32_t rows = (uint32_t)a.pool.kv_heads << a.page_log2;   // of a page, all heads (at most 2^24)
+    const int v = v0 + key0;
+    const uint32_t page = (uint32_t)pgd::checked(a, entry), place = (uint32_t)keys.token(v) & ((1u << a.page_log2) - 1u);
+    const uint8_t *c = codes + (uint64_t)page * (rows * (uint32_t)kRowBytes) + (place * (uint32_t)kRowBytes + code_at);
+    const uint8_t *s = steps + (uint64_t)page * (rows * (uint32_t)win::kSteps) + (place * (uint32_t)win::kSteps + step_at);
 #pragma unroll
-    for (int g = 0; g < kGroups; g++) {
-      const int v = v0 + key0 + 16 * g;
-      const int64_t at = pgd::page_row(a, pgd::checked(a, entry[g]), kvh) + (keys.token(v) & ((1 << a.page_log2) - 1));
-      const uint8_t *c = codes + at * kRowBytes, *s = steps + at * win::kSteps;
-#pragma unroll
-      for (int k = 0; k < 4 / kGroups; k++) {
-        const int i = g * (4 / kGroups) + k;
-        p.step[i] = 0u;
-#pragma unroll
-        for (int u = 0; u < BITS / 2; u++) p.c[i][u] = 0u;
-        if (v + row0 + k * kRowStep < keys.total) {
-          if (BITS == 8) {
-            const uint4 x = __ldg((const uint4 *)(c + k * kRowStep * kRowBytes));
-            p.c[i][0] = x.x; p.c[i][1] = x.y; p.c[i][2 % (BITS / 2)] = x.z; p.c[i][3 % (BITS / 2)] = x.w;
-          } else {
-            const uint2 x = __ldg((const uint2 *)(c + k * kRowStep * kRowBytes));
-            p.c[i][0] = x.x; p.c[i][1] = x.y;
-          }
-          p.step[i] = __ldg(s + k * kRowStep * win::kSteps);
+    for (int k = 0; k < 2; k++) {
+      p.step[k] = 0u;
+      if (v + row + 8 * k < keys.total) {
+        if (BITS == 8) {
+          const uint4 x = __ldg((const uint4 *)(c + 8 * k * kRowBytes));
+          p.c[k][0] = x.x; p.c[k][1] = x.y; p.c[k][2 % (BITS / 2)] = x.z; p.c[k][3 % (BITS / 2)] = x.w;
+        } else {
+          const uint2 x = __ldg((const uint2 *)(c + 8 * k * kRowBytes));
+          p.c[k][0] = x.x; p.c[k][1] = x.y;
         }
+        p.step[k] = __ldg(s + 8 * k * win::kSteps);
       }
     }
   }
   __device__ __forceinline__ void store(uint32_t stage, const Codes<BITS> &p, const win::Bases &bases) const {
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
+    for (int k = 0; k < 2; k++) {
       uint32_t d[8];
-      const win::Step st = win::step_of_byte<BITS>(p.step[i]);
+      const win::Step st = win::step_of_byte<BITS>(p.step[k]);
       if (BITS == 8) {
 #pragma unroll
-        for (int u = 0; u < 4; u++) win::decode8(p.c[i][u % (BITS / 2)], st, bases, d[2 * u], d[2 * u + 1]);
+        for (int u = 0; u < 4; u++) win::decode8(p.c[k][u % (BITS / 2)], st, bases, d[2 * u], d[2 * u + 1]);
       } else {
         uint32_t q[4];
-        win::decode4(p.c[i][0], st, bases, q);
+        win::decode4(p.c[k][0], st, bases, q);
         d[0] = q[0]; d[1] = q[1]; d[2] = q[2]; d[3] = q[3];
-        win::decode4(p.c[i][1], st, bases, q);
+        win::decode4(p.c[k][1], st, bases, q);
         d[4] = q[0]; d[5] = q[1]; d[6] = q[2]; d[7] = q[3];
       }
-      const uint32_t at = stage * kStage + (uint32_t)(i >> 1) * (2u * kRowStep * 128u);
-      tc::sts128(dst[i & 1][0] + at, make_uint4(d[0], d[1], d[2], d[3]));
-      tc::sts128(dst[i & 1][1] + at, make_uint4(d[4], d[5], d[6], d[7]));
+      const uint32_t at = stage * kStage + (uint32_t)k * 1024u;
+      tc::sts128(dst[0] + at, make_uint4(d[0], d[1], d[2], d[3]));
+      tc::sts128(dst[1] + at, make_uint4(d[4], d[5], d[6], d[7]));
     }
   }
 };
@@ -410,16 +393,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc::fence_after_sync();
   const uint32_t tmem = tmem_base_sh;
 
-  // The description of the share's piece number i (the whole warp; false: someone gave up).
-  auto hear = [&](int i, Piece &p) -> bool {
-    if (!__all_sync(0xffffffffu, tc::mbar_try_wait(&bars.told[i & 1], (i >> 1) & 1))) {
-      if (!tc::mbar_wait(&bars.told[i & 1], (i >> 1) & 1, kWaitNs)) fail(a.status);
-      if (__any_sync(0xffffffffu, aborted() != 0)) return false;
-    }
-    p = pieces[i & 1];
+  // The share's piece number i is described in pieces[i & 1] (the whole warp; false: someone gave up), until this
+  // warp says that it has read all it needs of it.
+  auto hear = [&](int i) -> bool {
+    if (__all_sync(0xffffffffu, tc::mbar_try_wait(&bars.told[i & 1], (i >> 1) & 1))) return true;
+    if (!tc::mbar_wait(&bars.told[i & 1], (i >> 1) & 1, kWaitNs)) fail(a.status);
+    return !__any_sync(0xffffffffu, aborted() != 0);
+  };
+  auto heard = [&](int i) {
     __syncwarp();
     if (lane == 0) tc::mbar_arrive(&bars.heard[i & 1]);
-    return true;
   };
 
   const uint32_t powers = tc::smem_u32(sm) + OFF_POWER;
@@ -436,19 +419,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t count = 0;   // steps of this tile so far
     int worked = 0;       // pieces with keys so far
     for (int pi = 0;; pi++) {
-      Piece p;
-      if (softmax_meet(!hear(pi, p))) break;
+      if (softmax_meet(!hear(pi))) break;
+      // (read where they are needed, so that the steps' registers are the logits')
+      const volatile Piece &p = pieces[pi & 1];
       if (p.done) break;
-      const int rows = p.seq_rows, row_base = p.row0 + cr * BM;   // this CTA's row 0 of tile 0
-      pgd::Seq q;
-      q.q0 = p.q0;
-      q.s = win::Seq{p.len, a.sink, (int64_t)1 << 62, a.tpf, a.frames};
       if (p.J == 0) {   // these rows see no key: 16 lanes write a row's zeros
         for (int e = tid; e < NQT * BM * 16; e += 32 * kSoftmaxWarps) {
-          const int r = row_base + e / 16 / BM * 2 * BM + e / 16 % BM;
-          if (r >= rows) continue;
+          const int r = cr * BM + e / 16 / BM * 2 * BM + e / 16 % BM;
+          if (p.row0 + r >= p.seq_rows) continue;
           RowOut out;
-          out.init(a, p, share, r - p.row0);
+          out.init(a, p, share, r);
           if (out.merge) continue;
           const int c = 8 * (e & 15);
           if (out.bf16) {
@@ -459,70 +439,67 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           if (out.lse && c == 0) *out.lse = -INFINITY;
         }
+        heard(pi);
         continue;
       }
-      // ---- this CTA's two Query tiles -> shared memory: all rows' copies in flight, then bf16 -> fp16 in
-      // place.  Both tiles' MMAs of the last piece are done and its outputs have left this memory. ----
+      const int key_of = p.j0 * BN + (p.brief ? x * BS : 0), key_step = p.brief ? 2 * BS : BS;
+      const int mine_n = p.brief ? (p.steps + 1 - x) >> 1 : p.steps;   // steps of this tile
+      pgd::Row mine{0, 0, 0};
+      pgd::Everyone every{INT32_MAX, 0, 0};   // a warp without a row masks nothing (its logits are 0)
       {
-        const int ci = tid & 15, rr0 = tid >> 4;   // 16-byte piece of a row; rows rr0, rr0 + 16, ...
-        const uint16_t *qb = a.q + (int64_t)p.kvh * a.group * a.qs.head + (int64_t)p.first * a.qs.token + 8 * ci;
+        // ---- this CTA's two Query tiles -> shared memory, bf16 -> fp16: a tile's rows in flight together.  Both tiles'
+        // MMAs of the last piece are done and its outputs have left this memory. ----
+        const int rows = p.seq_rows, row_base = p.row0 + cr * BM;   // this CTA's row 0 of tile 0
+        const int rr0 = tid >> 4;   // 16-byte piece tid % 16 of rows rr0, rr0 + 16, ...
+        const uint16_t *qb = a.q + (int64_t)p.kvh * a.group * a.qs.head + (int64_t)p.first * a.qs.token + 8 * (tid & 15);
         // 16 rows on: 16 / group tokens and 16 % group heads, a token more where the heads run over
         const int step_i = 16 / a.group, step_h = 16 - step_i * a.group;
         const int64_t ahead = step_i * a.qs.token + step_h * a.qs.head, wrap = a.qs.token - a.group * a.qs.head;
+        uint32_t top = 0u, small = 0u;   // the largest magnitudes, a NaN above all; passes in which this piece is below 1
 #pragma unroll 1
         for (int y = 0; y < NQT; y++) {
           const int r = row_base + y * 2 * BM + rr0, i = (int)((uint32_t)r / (uint32_t)a.group);
           int h = r - i * a.group, left = rows - r < BM ? rows - r : BM;   // (may be negative)
           const uint16_t *src = qb + h * a.qs.head + i * a.qs.token;
-          uint32_t dst = q_dst + (uint32_t)y * 2u * kBlk;
-#pragma unroll 2
+          uint4 v[BM / 16];
+#pragma unroll
           for (int k = 0; k < BM / 16; k++) {
-            tc::cp_async16_zfill(dst, left > 0 ? src : qb, left > 0 ? 16u : 0u);
-            dst += 2048u;
-            left -= 16;
+            v[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (16 * k < left) v[k] = *(const uint4 *)src;
             h += step_h;
             src += ahead + (h >= a.group ? wrap : 0);
             h -= h >= a.group ? a.group : 0;
           }
-        }
-        tc::cp_async_commit();
-      }
-      // what this thread's row sees, while they are on their way
-      const int w0 = row_base + (p.brief ? 0 : x * 2 * BM) + 32 * sub;   // this warp's first row
-      const int r = w0 + lane;
-      pgd::Row mine{0, 0, 0};
-      pgd::Everyone every{INT32_MAX, 0, 0};   // a warp without a row masks nothing (its logits are 0)
-      if (w0 < rows) {
-        mine.init(q.s, p.keys, r < rows ? q.frame(a, r) : -1);
-        every.init(q.s, p.keys, q.frame(a, w0), q.frame(a, w0 + 31 < rows ? w0 + 31 : rows - 1));
-      }
-      {
-        // this warp's rows: two in each of 16 passes, pass 8 y + k those of tile y from 16 k on
-        tc::sts32(powers + 4u * (uint32_t)((lane >> 1) * 16 + warp * 2 + (lane & 1)), 0u);
-        tc::cp_async_wait<0>();
-        uint32_t top = 0u, small = 0u;   // the largest magnitudes, a NaN above all; passes in which this piece is below 1
-#pragma unroll 1
-        for (int y = 0; y < NQT; y++) {
-          const int rr = row_base + y * 2 * BM + (tid >> 4), left = rows - rr < BM ? rows - rr : BM;
-          const uint32_t at = q_dst + (uint32_t)y * 2u * kBlk;
-#pragma unroll 4
+          if (y == 0) {   // what this thread's row sees, while they are on their way
+            pgd::Seq q;
+            q.q0 = p.q0;
+            q.s = win::Seq{p.len, a.sink, (int64_t)1 << 62, a.tpf, a.frames};
+            const pgd::Keys keys{p.keys.ns, p.keys.skip, p.keys.total};
+            const int w0 = row_base + (p.brief ? 0 : x * 2 * BM) + 32 * sub, mr = w0 + lane;   // this warp's first row
+            if (w0 < rows) {
+              mine.init(q.s, keys, mr < rows ? q.frame(a, mr) : -1);
+              every.init(q.s, keys, q.frame(a, w0), q.frame(a, w0 + 31 < rows ? w0 + 31 : rows - 1));
+            }
+            // this warp's rows: two in each of 16 passes, pass 8 y + k those of tile y from 16 k on
+            tc::sts32(powers + 4u * (uint32_t)((lane >> 1) * 16 + warp * 2 + (lane & 1)), 0u);
+          }
+#pragma unroll
           for (int k = 0; k < BM / 16; k++) {
-            const uint4 v = tc::lds128(at + (uint32_t)k * 2048u);
-            const bool live = 16 * k < left;
-            const uint32_t w[4] = {live ? v.x : 0u, live ? v.y : 0u, live ? v.z : 0u, live ? v.w : 0u};
+            const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
             uint32_t hw[4];
 #pragma unroll
             for (int u = 0; u < 4; u++) hw[u] = tc::pack_f16x2(__uint_as_float(w[u] << 16), __uint_as_float(w[u] & 0xFFFF0000u));
-            tc::sts128(at + (uint32_t)k * 2048u, make_uint4(hw[0], hw[1], hw[2], hw[3]));
+            tc::sts128(q_dst + (uint32_t)y * 2u * kBlk + (uint32_t)k * 2048u, make_uint4(hw[0], hw[1], hw[2], hw[3]));
             const uint32_t m = win::max_abs_bf16x2(win::max_abs_bf16x2(w[0], w[1]), win::max_abs_bf16x2(w[2], w[3])) & 0x7FFF7FFFu;
             top = win::max_abs_bf16x2(top, m);
-            small |= win::any_from_one(m) || !live ? 0u : 1u << (8 * y + k);
+            small |= win::any_from_one(m) || 16 * k >= left ? 0u : 1u << (8 * y + k);
           }
         }
         if (win::any_beyond_fp16(top & 0x7FFF7FFFu)) qwm_dev_error(a.status, QWM_ERR_RANGE);
 #pragma unroll
         for (int d = 1; d < 16; d <<= 1) small &= __shfl_xor_sync(0xffffffffu, small, d);   // of the whole row
         __syncwarp();
+#pragma unroll 1
         for (uint32_t again = small | __shfl_xor_sync(0xffffffffu, small, 16); again; again &= again - 1u) {   // fetched once more
           const int pass = __ffs((int)again) - 1, y = pass >> 3, k = pass & 7;
           const bool here = (small >> pass) & 1u;
@@ -551,8 +528,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int power = (int)tc::lds32(powers + 4u * (uint32_t)((p.brief ? 0 : x * BM) + 32 * sub + lane));
       const float sl2 = a.scale_log2 * win::power_of_two(-power) * win::kUnit<BITS>;
       const uint64_t sc2 = pk64(sl2, sl2);
-      const int mine_n = p.brief ? (p.steps + 1 - x) >> 1 : p.steps;   // steps of this tile
-      const int key_of = p.j0 * BN + (p.brief ? x * BS : 0), key_step = p.brief ? 2 * BS : BS;
       float m_used = -INFINITY;
       uint64_t acc = 0ull;   // the sum of the weights, each step's added as one: 1 / 64 of the additions to a large sum
       bool ok = true;
@@ -655,10 +630,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc::fence_after_sync();
         float inv = l > 0.f ? win::kUnit<BITS> / l : 0.f, keep = 0.f;
         float L = l > 0.f ? m_used + log2f(l) : -INFINITY;
-        bool write = r < rows;
+        const int r = cr * BM + (p.brief ? 0 : x * 2 * BM) + 32 * sub + lane;   // this thread's row of the item
+        bool write = p.row0 + r < p.seq_rows;
         RowOut out;
         if (write) {
-          out.init(a, p, share, r - p.row0);
+          out.init(a, p, share, r);
           if (out.merge) {  // out = w_prev out + w_this O / l, the weights the parts' shares of the sum
             const float Lp = *out.lse, Lm = fmaxf(Lp, L);
             if (Lm == -INFINITY) {
@@ -741,6 +717,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
       tc::fence_before_sync();
+      heard(pi);
       if (softmax_meet(!ok)) break;   // (behind it the Queries' memory and both outputs may be written again)
       tc::fence_after_sync();
     }
@@ -850,21 +827,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     if (first && lane == 0 && cr == 0) a.cuts[share] = PagedCut{a.batch, 0, 0, 0, 0, 0, 0};
   } else {
-    // ======================= producers: Keys, then Values, of every stage =======================
-    const int pw = warp == 13 ? 3 : warp - 9;
-    const Producer<BITS, false> pk(a, sm, cr, pw, lane);
-    const Producer<BITS, true> pv(a, sm, cr, pw, lane);
-    Codes<BITS> k0, v0, k1, v1;
+    // ======================= producers: three of them Keys, three Values =======================
+    const int pw = warp - (warp > kPlanWarp ? 10 : 9), units = pw % 3 == 2 ? 2 : 3;   // 9, 10, 11, 13, 14, 15
+    Unit<BITS> unit[3];
+#pragma unroll
+    for (int i = 0; i < 3; i++) unit[i].place(tc::smem_u32(sm), pw >= 3, i < units ? 3 * (pw % 3) + i : 0, cr, lane);
+    Codes<BITS> even[3] = {}, odd[3] = {};
     uint32_t g0 = 0;
     bool ok = true;
     for (int pi = 0; ok; pi++) {
-      Piece p;
-      ok = hear(pi, p);
-      if (!ok || p.done) break;
-      const int32_t *table = a.table + (int64_t)p.b * a.width;
-      int ek[1], ev[2];   // table entries of the next stage to be fetched
-      pk.look(a, p.keys, table, p.j0 * BN, ek);
-      pv.look(a, p.keys, table, p.j0 * BN, ev);
+      ok = hear(pi);
+      if (!ok) break;
+      const volatile Piece &vp = pieces[pi & 1];
+      if (vp.done) break;
+      const int32_t *table = a.table + (int64_t)vp.b * a.width;
+      const pgd::Keys keys{vp.keys.ns, vp.keys.skip, vp.keys.total};
+      const int j0 = vp.j0, J = vp.J;
+      const int64_t head_rows = (int64_t)vp.kvh << a.page_log2;
+      const uint8_t *codes = (pw >= 3 ? a.pool.v_codes : a.pool.k_codes) + head_rows * Unit<BITS>::kRowBytes;
+      const uint8_t *steps = (pw >= 3 ? a.pool.v_step : a.pool.k_step) + head_rows * win::kSteps;
+      heard(pi);
+      int entry[3];   // table entries of the next stage to be fetched
+#pragma unroll
+      for (int i = 0; i < 3; i++) entry[i] = unit[i].look(a, keys, table, j0 * BN);
       auto free_again = [&](uint32_t g) -> bool {   // the previous contents of stage g's place are consumed
         uint64_t *empty = &bars.empty[g & (kStages - 1)];
         if (g < kStages || __all_sync(0xffffffffu, tc::mbar_try_wait(empty, (g / kStages - 1) & 1u))) return true;
@@ -872,37 +857,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         return !__any_sync(0xffffffffu, aborted() != 0);         // warp-uniform exit
       };
       // stage j is stored and the codes of stage j + 2 fetched in its place; the first round only fetches
-      auto stage = [&](int j, Codes<BITS> &k, Codes<BITS> &v) -> bool {
+      auto stage = [&](int j, Codes<BITS> (&c)[3]) -> bool {
         const uint32_t g = g0 + (uint32_t)j, s = g & (kStages - 1);
-        const int next = (p.j0 + j + 2) * BN;
-        const bool store = j >= 0 && j < p.J, load = j + 2 < p.J;
-        if (store) {
+        const int next = (j0 + j + 2) * BN;
+        if (j >= 0 && j < J) {
           if (!free_again(g)) return false;
-          pk.store(s, k, a.bases);
-        }
-        if (load) {
-          pk.load(a, p.keys, p.kvh, next, ek, k);
-          pk.look(a, p.keys, table, next + BN, ek);
-        }
-        if (store) {
-          pv.store(s, v, a.bases);
-          tc::fence_proxy_async_smem();
+#pragma unroll
+          for (int i = 0; i < 3; i++)
+            if (i < units) unit[i].store(s, c[i], a.bases);
+          tc::fence_proxy_async_smem();   // (waits for loads in flight, too: they stand behind it)
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(&bars.full[s]);
         }
-        if (load) {
-          pv.load(a, p.keys, p.kvh, next, ev, v);
-          pv.look(a, p.keys, table, next + BN, ev);
+        if (j + 2 < J) {
+#pragma unroll
+          for (int i = 0; i < 3; i++)
+            if (i < units) unit[i].load(a, keys, codes, steps, next, entry[i], c[i]);
+#pragma unroll
+          for (int i = 0; i < 3; i++) entry[i] = unit[i].look(a, keys, table, next + BN);
         }
         return true;
       };
 #pragma unroll 1
-      for (int j = -2; j < p.J; j += 2)
-        if (!stage(j, k0, v0) || !stage(j + 1, k1, v1)) {
+      for (int j = -2; j < J; j += 2)
+        if (!stage(j, even) || !stage(j + 1, odd)) {
           ok = false;
           break;
         }
-      g0 += (uint32_t)p.J;
+      g0 += (uint32_t)J;
     }
   }
   tc::fence_before_sync();
