@@ -97,9 +97,8 @@ __device__ __forceinline__ bool softmax_meet(bool p) {
   return r != 0;
 }
 
-// The items of a sequence: Key heads by blocks of 512 rows; later blocks may see more keys.
+// The items of a sequence: its Key heads by blocks of 512 rows, of which later ones may see more keys.
 struct Work {
-  const PagedAttend &a;
   __device__ __forceinline__ static int blocks_of(const PagedAttend &a, const pgd::Seq &q, int ib, pgd::Keys &keys) {
     const int r0 = ib * kRows, r1 = r0 + kRows < q.rows ? r0 + kRows : q.rows;
     keys.init(a, q.s, q.frame(a, r0), q.frame(a, r1 - 1));
@@ -110,42 +109,145 @@ struct Work {
   __device__ __forceinline__ static int count(const PagedAttend &a, const pgd::Seq &q) {   // blocks of rows
     return q.rows > a.few ? (q.rows + kRows - 1) / kRows : 0;
   }
-  __device__ __forceinline__ int64_t head_cost(const pgd::Seq &q, int n) const {
-    int64_t c = 0;
-    for (int ib = 0; ib < n; ib++) {
-      pgd::Keys keys;
-      c += kStartCost + (int64_t)blocks_of(a, q, ib, keys) * each(q, ib);
+};
+
+// The cuts of share `share` (begin, end) in the line of all items: by sequence, Key head and block of rows.  Found by
+// the whole CTA, each thread taking `per` neighbouring blocks of rows: P, the running sum of the blocks' costs for one
+// Key head, finds first the sequence (whose heads take kv_heads equal pieces of the line), then the head and the
+// block.  starts: shared memory for batch + 1 numbers.  A share without work begins and ends at sequence `batch`.
+__device__ __noinline__ void find_cuts(const PagedAttend &a, int share, int *starts, PagedCut (&cut)[2]) {
+  constexpr int kW = kThreads / 32;
+  __shared__ int64_t sums[kW];
+  __shared__ int64_t edge[2][2];   // P at the begin and the end of the cuts' sequences
+  __shared__ int where[2];         // the cuts' sequences
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  auto scan = [&](int64_t v, int64_t &total) -> int64_t {   // the sum over the threads before, and over all
+    int64_t s = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t o = __shfl_up_sync(0xffffffffu, s, d);
+      if (lane >= d) s += o;
     }
-    return c;
+    __syncthreads();
+    if (lane == 31) sums[warp] = s;
+    __syncthreads();
+    int64_t w = lane < kW ? sums[lane] : 0;
+#pragma unroll
+    for (int d = 1; d < kW; d <<= 1) {
+      const int64_t o = __shfl_up_sync(0xffffffffu, w, d);
+      if (lane >= d) w += o;
+    }
+    total = __shfl_sync(0xffffffffu, w, kW - 1);
+    const int64_t before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
+    return (warp > 0 ? before : 0) + s - v;
+  };
+  if (tid < 2) {
+    cut[tid] = PagedCut{a.batch, 0, 0, 0, 0, 0, 0};
+    where[tid] = -1;
   }
-  __device__ __noinline__ int64_t cost(int b) const {
-    const pgd::Seq q = pgd::sequence(a, b);
-    const int n = count(a, q);
-    return n ? head_cost(q, n) * a.pool.kv_heads : 0;
+  int R = 0;   // blocks of rows so far
+  for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
+    int64_t total;
+    const int n = b0 + tid < a.batch ? Work::count(a, pgd::sequence(a, b0 + tid)) : 0;
+    const int64_t before = scan(n, total);
+    if (b0 + tid < a.batch) starts[b0 + tid] = R + (int)before;
+    R += (int)total;
   }
-  __device__ __noinline__ void cut(int b, int64_t x, int &item, int &block) const {
-    const pgd::Seq q = pgd::sequence(a, b);
-    const int n = count(a, q);
-    const int64_t head = head_cost(q, n);
-    const int kvh = (int)win::quotient(x, head);
-    x -= kvh * head;
-    for (int ib = 0;; ib++) {
+  if (tid == 0) starts[a.batch] = R;
+  __syncthreads();
+  const int per = (R + kThreads - 1) / kThreads, f0 = tid * per < R ? tid * per : R, f1 = f0 + per < R ? f0 + per : R;
+  // visit(f, b, ib, q, blocks, each) for blocks f0 .. f1 - 1 of this thread, until it says so
+  auto walk = [&](auto visit) {
+    if (f0 >= f1) return;
+    int lo = 0, hi = a.batch;   // starts[lo] <= f0 < starts[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (starts[mid] <= f0) lo = mid;
+      else hi = mid;
+    }
+    int b = lo;
+    pgd::Seq q = pgd::sequence(a, b);
+    for (int f = f0; f < f1; f++) {
+      if (f >= starts[b + 1]) {
+        do b++;
+        while (f >= starts[b + 1]);
+        q = pgd::sequence(a, b);
+      }
       pgd::Keys keys;
-      const int blocks = blocks_of(a, q, ib, keys);
-      const int64_t c = kStartCost + (int64_t)blocks * each(q, ib);
-      if (x < c || ib + 1 == n) {
-        item = kvh * n + ib;
-        block = pgd::cut_item(x, blocks, kStartCost, each(q, ib), kLeast);
+      const int ib = f - starts[b], blocks = Work::blocks_of(a, q, ib, keys);
+      if (visit(f, b, ib, blocks, Work::each(q, ib))) return;
+    }
+  };
+  int64_t mine = 0, all;
+  walk([&](int, int, int, int blocks, int each) {
+    mine += kStartCost + (int64_t)blocks * each;
+    return false;
+  });
+  const int64_t before = scan(mine, all);   // P at f0
+  const int kv = a.pool.kv_heads;
+  int64_t used = win::quotient(all * kv, kThin);
+  used = used < 1 ? 1 : (used < a.shares ? used : a.shares);
+  if (share >= used || all == 0) return;   // (the same for the whole CTA)
+  int64_t x[2];
+  x[0] = win::quotient(all * kv * share, used);
+  x[1] = win::quotient(all * kv * (share + 1), used);
+#pragma unroll
+  for (int e = 0; e < 2; e++) {
+    const int64_t X = win::quotient(x[e], kv);
+    if (X >= before && X < before + mine) {
+      int64_t P = before;
+      walk([&](int, int b, int, int blocks, int each) {
+        P += kStartCost + (int64_t)blocks * each;
+        if (X >= P) return false;
+        where[e] = b;
+        return true;
+      });
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < 2; e++) {
+    if (where[e] < 0) continue;   // the line's end
+    const int s0 = starts[where[e]], s1 = starts[where[e] + 1];
+    if ((s0 >= f0 && s0 < f1) || (s1 >= f0 && s1 < f1)) {
+      int64_t P = before;
+      walk([&](int f, int, int, int blocks, int each) {
+        if (f == s0) edge[e][0] = P;
+        if (f == s1) edge[e][1] = P;
+        P += kStartCost + (int64_t)blocks * each;
+        return false;
+      });
+    }
+    if (s1 == R && tid == 0) edge[e][1] = all;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < 2; e++) {
+    const int s = where[e];
+    if (s < 0) continue;
+    const int64_t lo = edge[e][0], each_head = edge[e][1] - lo, y = x[e] - kv * lo;
+    const int kvh = (int)win::quotient(y, each_head);
+    const int64_t z = lo + (y - kvh * each_head);
+    if (z >= before && z < before + mine) {
+      int64_t P = before;
+      walk([&](int f, int b, int ib, int blocks, int each) {
+        const int64_t c = kStartCost + (int64_t)blocks * each;
+        if (z >= P + c) {
+          P += c;
+          return false;
+        }
+        int item = kvh * (starts[b + 1] - starts[b]) + ib, block = pgd::cut_item(z - P, blocks, kStartCost, each, kLeast);
         if (block == blocks && block > 0) {
           item++;
           block = 0;
         }
-        return;
-      }
-      x -= c;
+        cut[e] = PagedCut{b, item, block, 0, 0, 0, 0};
+        return true;
+      });
     }
   }
-};
+  __syncthreads();
+}
 
 // Where one Query row's result goes (a whole item: out and lse, else the part's workspace).
 struct RowOut {
@@ -354,7 +456,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int share = (int)(blockIdx.x >> 1), cr = (int)tc::cluster_ctarank();
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the kernels behind this one may line up
-  pgd::share_of<kThreads>(a.batch, share, a.shares, kThin, Work{a}, cut);
+  find_cuts(a, share, (int *)(sm + OFF_K), cut);
+  __syncthreads();
   const PagedCut begin = cut[0], end = cut[1];
   if (begin.b == a.batch || (begin.b == end.b && begin.item == end.item && begin.block == end.block)) {   // both CTAs
     if (tid == 0 && cr == 0) a.cuts[share] = PagedCut{a.batch, 0, 0, 0, 0, 0, 0};
