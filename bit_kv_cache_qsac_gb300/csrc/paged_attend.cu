@@ -111,11 +111,50 @@ struct Work {
   }
 };
 
+// A block of rows in the line: number f of all, block ib of sequence b, P what the blocks before it cost one Key head.
+struct Place {
+  int f, b, ib, blocks, each;
+  int64_t P;
+  __device__ __forceinline__ int64_t cost() const { return kStartCost + (int64_t)blocks * each; }
+};
+// From block f on, where P stands: the first block that ends behind `target` or has number `index`, or block `end`
+// (of which only f and P are told).  starts: the number of each sequence's first block.  (One copy of the code for
+// all its uses: what a CTA does once is paced by instruction fetches.)
+__device__ __noinline__ Place walk(const PagedAttend &a, const int *starts, int f, int end, int64_t P, int64_t target, int index) {
+  Place p;
+  p.P = P;
+  p.f = f;
+  if (f >= end) return p;
+  int lo = 0, hi = a.batch;   // starts[lo] <= f < starts[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (starts[mid] <= f) lo = mid;
+    else hi = mid;
+  }
+  p.b = lo;
+  pgd::Seq q = pgd::sequence(a, p.b);
+#pragma unroll 1
+  for (; p.f < end; p.f++) {
+    if (p.f >= starts[p.b + 1]) {
+      do p.b++;
+      while (p.f >= starts[p.b + 1]);
+      q = pgd::sequence(a, p.b);
+    }
+    pgd::Keys keys;
+    p.ib = p.f - starts[p.b];
+    p.blocks = Work::blocks_of(a, q, p.ib, keys);
+    p.each = Work::each(q, p.ib);
+    if (p.f == index || p.P + p.cost() > target) break;
+    p.P += p.cost();
+  }
+  return p;
+}
+
 // The cuts of share `share` (begin, end) in the line of all items: by sequence, Key head and block of rows.  Found by
-// the whole CTA, each thread taking `per` neighbouring blocks of rows: P, the running sum of the blocks' costs for one
-// Key head, finds first the sequence (whose heads take kv_heads equal pieces of the line), then the head and the
-// block.  starts: shared memory for batch + 1 numbers.  A share without work begins and ends at sequence `batch`.
-__device__ __noinline__ void find_cuts(const PagedAttend &a, int share, int *starts, PagedCut (&cut)[2]) {
+// the whole CTA, each thread taking neighbouring blocks of rows: P, the running sum of the blocks' costs for one Key
+// head, finds first the sequence (whose heads take kv_heads equal pieces of the line), then the head and the block.
+// starts: shared memory for batch + 1 numbers.  A share without work begins and ends at sequence `batch`.
+__device__ __forceinline__ void find_cuts(const PagedAttend &a, int share, int *starts, PagedCut (&cut)[2]) {
   constexpr int kW = kThreads / 32;
   __shared__ int64_t sums[kW];
   __shared__ int64_t edge[2][2];   // P at the begin and the end of the cuts' sequences
@@ -123,7 +162,7 @@ __device__ __noinline__ void find_cuts(const PagedAttend &a, int share, int *sta
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   auto scan = [&](int64_t v, int64_t &total) -> int64_t {   // the sum over the threads before, and over all
     int64_t s = v;
-#pragma unroll
+#pragma unroll 1
     for (int d = 1; d < 32; d <<= 1) {
       const int64_t o = __shfl_up_sync(0xffffffffu, s, d);
       if (lane >= d) s += o;
@@ -132,7 +171,7 @@ __device__ __noinline__ void find_cuts(const PagedAttend &a, int share, int *sta
     if (lane == 31) sums[warp] = s;
     __syncthreads();
     int64_t w = lane < kW ? sums[lane] : 0;
-#pragma unroll
+#pragma unroll 1
     for (int d = 1; d < kW; d <<= 1) {
       const int64_t o = __shfl_up_sync(0xffffffffu, w, d);
       if (lane >= d) w += o;
@@ -146,6 +185,7 @@ __device__ __noinline__ void find_cuts(const PagedAttend &a, int share, int *sta
     where[tid] = -1;
   }
   int R = 0;   // blocks of rows so far
+#pragma unroll 1
   for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
     int64_t total;
     const int n = b0 + tid < a.batch ? Work::count(a, pgd::sequence(a, b0 + tid)) : 0;
@@ -156,97 +196,45 @@ __device__ __noinline__ void find_cuts(const PagedAttend &a, int share, int *sta
   if (tid == 0) starts[a.batch] = R;
   __syncthreads();
   const int per = (R + kThreads - 1) / kThreads, f0 = tid * per < R ? tid * per : R, f1 = f0 + per < R ? f0 + per : R;
-  // visit(f, b, ib, q, blocks, each) for blocks f0 .. f1 - 1 of this thread, until it says so
-  auto walk = [&](auto visit) {
-    if (f0 >= f1) return;
-    int lo = 0, hi = a.batch;   // starts[lo] <= f0 < starts[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (starts[mid] <= f0) lo = mid;
-      else hi = mid;
-    }
-    int b = lo;
-    pgd::Seq q = pgd::sequence(a, b);
-    for (int f = f0; f < f1; f++) {
-      if (f >= starts[b + 1]) {
-        do b++;
-        while (f >= starts[b + 1]);
-        q = pgd::sequence(a, b);
-      }
-      pgd::Keys keys;
-      const int ib = f - starts[b], blocks = Work::blocks_of(a, q, ib, keys);
-      if (visit(f, b, ib, blocks, Work::each(q, ib))) return;
-    }
-  };
-  int64_t mine = 0, all;
-  walk([&](int, int, int, int blocks, int each) {
-    mine += kStartCost + (int64_t)blocks * each;
-    return false;
-  });
-  const int64_t before = scan(mine, all);   // P at f0
+  int64_t all;
+  const int64_t mine = walk(a, starts, f0, f1, 0, INT64_MAX, -1).P, before = scan(mine, all);
   const int kv = a.pool.kv_heads;
   int64_t used = win::quotient(all * kv, kThin);
   used = used < 1 ? 1 : (used < a.shares ? used : a.shares);
   if (share >= used || all == 0) return;   // (the same for the whole CTA)
   int64_t x[2];
-  x[0] = win::quotient(all * kv * share, used);
-  x[1] = win::quotient(all * kv * (share + 1), used);
-#pragma unroll
+#pragma unroll 1
   for (int e = 0; e < 2; e++) {
+    x[e] = win::quotient(all * kv * (share + e), used);
     const int64_t X = win::quotient(x[e], kv);
-    if (X >= before && X < before + mine) {
-      int64_t P = before;
-      walk([&](int, int b, int, int blocks, int each) {
-        P += kStartCost + (int64_t)blocks * each;
-        if (X >= P) return false;
-        where[e] = b;
-        return true;
-      });
-    }
+    if (X >= before && X < before + mine) where[e] = walk(a, starts, f0, f1, before, X, -1).b;
   }
   __syncthreads();
-#pragma unroll
-  for (int e = 0; e < 2; e++) {
-    if (where[e] < 0) continue;   // the line's end
-    const int s0 = starts[where[e]], s1 = starts[where[e] + 1];
-    if ((s0 >= f0 && s0 < f1) || (s1 >= f0 && s1 < f1)) {
-      int64_t P = before;
-      walk([&](int f, int, int, int blocks, int each) {
-        if (f == s0) edge[e][0] = P;
-        if (f == s1) edge[e][1] = P;
-        P += kStartCost + (int64_t)blocks * each;
-        return false;
-      });
-    }
-    if (s1 == R && tid == 0) edge[e][1] = all;
+#pragma unroll 1
+  for (int e = 0; e < 4; e++) {
+    if (where[e >> 1] < 0) continue;   // the line's end
+    const int s = starts[where[e >> 1] + (e & 1)];
+    if (s >= f0 && s < f1) edge[e >> 1][e & 1] = walk(a, starts, f0, f1, before, INT64_MAX, s).P;
+    if (s == R && tid == 0) edge[e >> 1][e & 1] = all;
   }
   __syncthreads();
-#pragma unroll
+#pragma unroll 1
   for (int e = 0; e < 2; e++) {
-    const int s = where[e];
-    if (s < 0) continue;
-    const int64_t lo = edge[e][0], each_head = edge[e][1] - lo, y = x[e] - kv * lo;
-    const int kvh = (int)win::quotient(y, each_head);
-    const int64_t z = lo + (y - kvh * each_head);
+    if (where[e] < 0) continue;
+    const int64_t lo = edge[e][0], head = edge[e][1] - lo, y = x[e] - kv * lo;
+    const int kvh = (int)win::quotient(y, head);
+    const int64_t z = lo + (y - kvh * head);
     if (z >= before && z < before + mine) {
-      int64_t P = before;
-      walk([&](int f, int b, int ib, int blocks, int each) {
-        const int64_t c = kStartCost + (int64_t)blocks * each;
-        if (z >= P + c) {
-          P += c;
-          return false;
-        }
-        int item = kvh * (starts[b + 1] - starts[b]) + ib, block = pgd::cut_item(z - P, blocks, kStartCost, each, kLeast);
-        if (block == blocks && block > 0) {
-          item++;
-          block = 0;
-        }
-        cut[e] = PagedCut{b, item, block, 0, 0, 0, 0};
-        return true;
-      });
+      const Place p = walk(a, starts, f0, f1, before, z, -1);
+      int item = kvh * (starts[p.b + 1] - starts[p.b]) + p.ib;
+      int block = pgd::cut_item(z - p.P, p.blocks, kStartCost, p.each, kLeast);
+      if (block == p.blocks && block > 0) {
+        item++;
+        block = 0;
+      }
+      cut[e] = PagedCut{p.b, item, block, 0, 0, 0, 0};
     }
   }
-  __syncthreads();
 }
 
 // Where one Query row's result goes (a whole item: out and lse, else the part's workspace).

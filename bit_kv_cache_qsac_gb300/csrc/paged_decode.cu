@@ -26,23 +26,20 @@ constexpr int kStart = 4, kLeast = 2, kThin = 6;
 template <int BITS, int NT>
 struct Work {
   const PagedAttend &a;
-  __device__ __forceinline__ void of(int b, int &blocks, int &items) const {
+  // (one copy of the code: what a CTA does once is paced by instruction fetches)
+  __device__ __noinline__ static int2 of(const PagedAttend &a, int b) {
     const pgd::Seq q = pgd::sequence(a, b);
-    blocks = items = 0;
-    if (q.rows == 0 || q.rows > a.few) return;
+    if (q.rows == 0 || q.rows > a.few) return make_int2(0, 0);
     pgd::Keys keys;
     keys.init(a, q.s, q.frame(a, 0), q.frame(a, q.rows - 1));
-    blocks = (keys.total + kBlock<BITS> - 1) / kBlock<BITS>;
-    items = a.pool.kv_heads * ((q.rows + 8 * NT - 1) / (8 * NT));
+    return make_int2((keys.total + kBlock<BITS> - 1) / kBlock<BITS>, a.pool.kv_heads * ((q.rows + 8 * NT - 1) / (8 * NT)));
   }
   __device__ __forceinline__ int64_t cost(int b) const {
-    int blocks, items;
-    of(b, blocks, items);
-    return (int64_t)items * (blocks + kStart);
+    const int2 w = of(a, b);   // blocks of an item, items
+    return (int64_t)w.y * (w.x + kStart);
   }
   __device__ __forceinline__ void cut(int b, int64_t x, int &item, int &block) const {
-    int blocks, items;
-    of(b, blocks, items);
+    const int blocks = of(a, b).x;
     item = (int)win::quotient(x, blocks + kStart);
     block = pgd::cut_item(x - (int64_t)item * (blocks + kStart), blocks, kStart, 1, kLeast);
     if (block == blocks && block > 0) {
@@ -259,7 +256,7 @@ __device__ __forceinline__ void combine(const PagedAttend &a, int at, int part_r
   }
 }
 
-constexpr int kManyRows = 4;   // a warp's rows of the tensor-memory tiles' parts
+constexpr int kManyRows = 2;   // a warp's rows of the tensor-memory tiles' parts
 
 __global__ void __launch_bounds__(256)
     paged_combine_kernel(const __grid_constant__ PagedAttend few, const __grid_constant__ PagedAttend many, int few_rows,
