@@ -874,7 +874,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int b = begin.b, item = begin.item, block = begin.block, pi = 0;
     bool first = true, more = true;
     while (more) {
-      Piece p;
+      Piece p = {};
       p.done = 1;
       for (; b < a.batch; b++, item = block = 0) {   // the sequence of the next item
         const pgd::Seq q = pgd::sequence(a, b);

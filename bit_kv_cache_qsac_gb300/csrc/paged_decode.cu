@@ -49,6 +49,21 @@ struct Work {
   }
 };
 
+// A piece of an item that the share holds: blocks `block` .. block1 - 1 of its `blocks`.
+struct Piece {
+  int item, block, block1, blocks, kvh, row0, rows;   // rows: live ones from row0; 0: no piece
+  int b, first, seq_rows, q0, len;                    // its sequence
+  pgd::Keys keys;
+  __device__ __forceinline__ pgd::Seq seq(const PagedAttend &a) const {
+    pgd::Seq q;
+    q.first = first;
+    q.rows = seq_rows;
+    q.q0 = q0;
+    q.s = win::Seq{len, a.sink, (int64_t)1 << 62, a.tpf, a.frames};
+    return q;
+  }
+};
+
 template <int BITS, int NT>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) paged_decode_kernel(const __grid_constant__ PagedAttend a) {
   using R = Ring<BITS>;
@@ -58,138 +73,214 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) paged_decode_kernel
   unsigned char *dyn = dyn_raw + ((128u - (tc::smem_u32(dyn_raw) & 127u)) & 127u);
   __shared__ float msm[kWarps][8 * NT], lsm[kWarps][8 * NT];
   __shared__ PagedCut cut[2];
+  __shared__ Piece pieces[3];   // the share's pieces number s - 1 (being replaced), s and s + 1
+  __shared__ int spare[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the joining kernel may line up
   pgd::share_of<kThreads>(a.batch, (int)blockIdx.x, a.shares, kThin, Work<BITS, NT>{a}, cut);
-  const PagedCut end = cut[1];
-  int b = cut[0].b, item = cut[0].item, block = cut[0].block;
+
+  // ---- the share's pieces, described by the last warp (which has the fewest steps) one ahead of their use ----
+  int nb = cut[0].b, nitem = cut[0].item, nblock = cut[0].block;   // where the next one begins
+  auto plan = [&](Piece &to) {
+    Piece p = {};   // (no piece: no rows, and no steps for those who look ahead)
+    const PagedCut end = cut[1];
+    for (; nb < a.batch; nb++, nitem = nblock = 0) {
+      if (nb > end.b || (nb == end.b && (nitem > end.item || (nitem == end.item && end.block == 0)))) break;
+      const pgd::Seq q = pgd::sequence(a, nb);
+      const int tiles = q.rows > a.few ? 0 : (q.rows + 8 * NT - 1) / (8 * NT);
+      if (nitem >= a.pool.kv_heads * tiles) continue;
+      p.kvh = nitem / tiles;
+      p.row0 = (nitem - p.kvh * tiles) * 8 * NT;
+      p.rows = q.rows - p.row0 < 8 * NT ? q.rows - p.row0 : 8 * NT;
+      p.keys.init(a, q.s, q.frame(a, 0), q.frame(a, q.rows - 1));
+      p.blocks = (p.keys.total + kBlock<BITS> - 1) / kBlock<BITS>;
+      p.item = nitem;
+      p.block = nblock;
+      const bool last = nb == end.b && nitem == end.item;
+      p.block1 = last ? end.block : p.blocks;
+      p.b = nb;
+      p.first = q.first;
+      p.seq_rows = q.rows;
+      p.q0 = (int)q.q0;
+      p.len = (int)q.s.len;
+      nitem = last ? INT32_MAX : nitem + 1;   // (behind the last one everything lies past the end)
+      nblock = 0;
+      break;
+    }
+    if (lane == 0) to = p;
+  };
+  if (warp == kWarps - 1) plan(pieces[0]);
+  __syncthreads();
+  if (threadIdx.x == 0) {   // where the share begins, for the joining kernel
+    const Piece &p = pieces[0];
+    a.cuts[blockIdx.x] = p.rows ? PagedCut{p.b, p.item, p.block, p.first, p.kvh, p.row0, p.rows} : PagedCut{a.batch, 0, 0, 0, 0, 0, 0};
+  }
+
   wt::Tile<BITS, NT> tile;
   tile.place(lane);
-
+  auto fetch = [&](const Piece &p) {   // its Queries, bf16 for now
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++) {
+      const int r = p.row0 + 8 * nt + tile.g, i = (int)((uint32_t)r / (uint32_t)a.group);
+      tile.fetch(nt, a.q + (p.kvh * a.group + (r - i * a.group)) * a.qs.head + (p.first + i) * a.qs.token, 8 * nt + tile.g < p.rows);
+    }
+  };
+  // ---- copies into the warp's ring, a step (a group) each, across the pieces' borders: up to two steps on their way,
+  // into the places behind `stage`, the next to be read; the third place is the one read last ----
   const uint32_t ring0 = tc::smem_u32(dyn) + (uint32_t)(warp * R::kStages * R::kStage);
   constexpr int kPer = R::kRow / 16, kCopies = kKeys * kPer / 32;   // pieces of a row; copies of a lane and tensor
-  const int srow = lane & 15;
   const uint32_t kdst = R::k_at(lane / kPer, lane & (kPer - 1));   // k_at(row + 32 / kPer, .) is 512 further on
   // v_at(row + 32 / kPer, .) is 512 further on but for the permutation: one piece bit flips per 4 rows
   const uint32_t vdst = R::v_at(lane / kPer, lane & (kPer - 1));
   auto vdst_of = [&](int i) -> uint32_t { return (vdst ^ (BITS == 8 ? 32u * (i & 3) : 64u * (i & 1))) + 512u * i; };
-
-  bool began = false;   // the share's first cut is written down for the joining kernel
-  while (b < a.batch) {
-    const pgd::Seq q = pgd::sequence(a, b);
-    const int tiles = q.rows > a.few ? 0 : (q.rows + 8 * NT - 1) / (8 * NT), items = a.pool.kv_heads * tiles;
-    if (item >= items) {   // the next sequence
-      if (b >= end.b) break;
-      b++;
-      item = block = 0;
-      continue;
+  auto last_step = [&](const Piece &p) -> int {   // steps of an item that the piece ends with
+    const int all = (p.keys.total + kKeys - 1) / kKeys;
+    return p.block1 * kWarps < all ? p.block1 * kWarps : all;
+  };
+  int cj, cend;        // the next step to be copied of the piece that copies have come to, and its end
+  int ckvh, entry[kSub];   // its Key head; the table's entries for that step
+  pgd::Keys ckeys;
+  const int32_t *ctable;
+  auto look = [&]() {
+    if (cj < cend) {
+#pragma unroll
+      for (int u = 0; u < kSub; u++) {   // each 16 keys; those past the last key repeat its 16
+        const int v = cj * kKeys + 16 * u < ckeys.total ? cj * kKeys + 16 * u : (ckeys.total - 1) & -16;
+        entry[u] = ctable[ckeys.token(v) >> a.page_log2];
+      }
     }
-    if (b > end.b || (b == end.b && (item > end.item || (item == end.item && end.block == 0)))) break;
-    const int kvh = item / tiles, row0 = (item - kvh * tiles) * 8 * NT;
-    const int rows = q.rows - row0 < 8 * NT ? q.rows - row0 : 8 * NT;
-    if (!began && threadIdx.x == 0)
-      a.cuts[blockIdx.x] = PagedCut{b, item, block, q.first, kvh, row0, rows};
-    began = true;
-    const int64_t f0 = q.frame(a, 0), f1 = q.frame(a, q.rows - 1);
-    pgd::Keys keys;
-    keys.init(a, q.s, f0, f1);
-    const int blocks = (keys.total + kBlock<BITS> - 1) / kBlock<BITS>;
-    const bool last = b == end.b && item == end.item;
-    const int block1 = last ? end.block : blocks;
-    const int j1 = block1 * kWarps < (keys.total + kKeys - 1) / kKeys ? block1 * kWarps : (keys.total + kKeys - 1) / kKeys;
-
+  };
+  auto turn_to = [&](const Piece &p) {
+    ckeys.ns = p.keys.ns;
+    ckeys.skip = p.keys.skip;
+    ckeys.total = p.keys.total;
+    ckvh = p.kvh;
+    ctable = a.table + (int64_t)p.b * a.width;
+    cj = p.block * kWarps + warp;
+    cend = p.rows ? last_step(p) : 0;
+    look();
+  };
+  int stage = 0, flying = 0;
+  bool ahead = false;   // copies have come to the piece after the current one
+  auto refill = [&](const Piece *next) {   // next: the piece after the current one, where it may be turned to
+#pragma unroll 1
+    while (flying < 2) {
+      if (cj >= cend) {
+        if (!next || ahead) break;
+        ahead = true;
+        turn_to(*next);
+        if (cj >= cend) break;
+      }
+      const int place = stage + flying >= 3 ? stage + flying - 3 : stage + flying;
+      const uint32_t dst = ring0 + (uint32_t)(place * R::kStage);
+      int64_t at[kSub];   // the row of the first of each 16 keys
+      int follow[kSub];   // and how many rows follow it
 #pragma unroll
-    for (int nt = 0; nt < NT; nt++) {
-      const int r = row0 + 8 * nt + tile.g, i = (int)((uint32_t)r / (uint32_t)a.group);
-      tile.fetch(nt, a.q + (kvh * a.group + (r - i * a.group)) * a.qs.head + (q.first + i) * a.qs.token, 8 * nt + tile.g < rows);
-    }
-    // ---- copies of step j's keys into a stage of the warp's ring (one group) ----
-    const int32_t *table = a.table + (int64_t)b * a.width;
-    auto copy = [&](int j, int stage) {
-      if (j < j1) {
-        const uint32_t dst = ring0 + (uint32_t)(stage * R::kStage);
-        // each 16 keys (those past the last key repeat its 16): the row of the first, and how many rows follow it
-        int64_t at[kSub];
-        int follow[kSub];
+      for (int u = 0; u < kSub; u++) {
+        const int v = cj * kKeys + 16 * u < ckeys.total ? cj * kKeys + 16 * u : (ckeys.total - 1) & -16;
+        at[u] = pgd::page_row(a, pgd::checked(a, entry[u]), ckvh) + (ckeys.token(v) & ((1 << a.page_log2) - 1));
+        follow[u] = ckeys.total - 1 - v;
+      }
 #pragma unroll
-        for (int u = 0; u < kSub; u++) {
-          const int v = j * kKeys + 16 * u < keys.total ? j * kKeys + 16 * u : (keys.total - 1) & -16;
-          const int p = keys.token(v);
-          at[u] = pgd::page_row(a, pgd::checked(a, table[p >> a.page_log2]), kvh) + (p & ((1 << a.page_log2) - 1));
-          follow[u] = keys.total - 1 - v;
-        }
+      for (int i = 0; i < kCopies; i++) {
+        const int u = kSub == 2 && i >= kCopies / 2 ? 1 : 0, row = (32 * i + lane) / kPer - 16 * u;
+        const int64_t src = (at[u] + (row < follow[u] ? row : follow[u])) * R::kRow + 16 * (lane & (kPer - 1));
+        wt::cp_async16(dst + kdst + 512u * i, a.pool.k_codes + src);
+        wt::cp_async16(dst + vdst_of(i), a.pool.v_codes + src);
+      }
+      const int srow = lane & 15;
 #pragma unroll
-        for (int i = 0; i < kCopies; i++) {
-          const int u = kSub == 2 && i >= kCopies / 2 ? 1 : 0, row = (32 * i + lane) / kPer - 16 * u;
-          const int64_t src = (at[u] + (row < follow[u] ? row : follow[u])) * R::kRow + 16 * (lane & (kPer - 1));
-          wt::cp_async16(dst + kdst + 512u * i, a.pool.k_codes + src);
-          wt::cp_async16(dst + vdst_of(i), a.pool.v_codes + src);
-        }
-#pragma unroll
-        for (int u = 0; u < kSub; u++) {   // lanes 0-15: the Keys' step words, 16-31: the Values'
-          const int64_t src = (at[u] + (srow < follow[u] ? srow : follow[u])) * win::kSteps;
-          wt::cp_async4(dst + (lane < 16 ? R::kKS : R::kVS) + 4u * (srow + 16 * u), (lane < 16 ? a.pool.k_step : a.pool.v_step) + src);
-        }
+      for (int u = 0; u < kSub; u++) {   // lanes 0-15: the Keys' step words, 16-31: the Values'
+        const int64_t src = (at[u] + (srow < follow[u] ? srow : follow[u])) * win::kSteps;
+        wt::cp_async4(dst + (lane < 16 ? R::kKS : R::kVS) + 4u * (srow + 16 * u), (lane < 16 ? a.pool.k_step : a.pool.v_step) + src);
       }
       tc::cp_async_commit();
-    };
-    const int j0 = block * kWarps + warp;
-    copy(j0, 0);
-    copy(j0 + kWarps, 1);
+      flying++;
+      cj += kWarps;
+      look();
+    }
+  };
+  fetch(pieces[0]);
+  turn_to(pieces[0]);
+  refill(nullptr);
+  if (warp == kWarps - 1) plan(pieces[1]);
+  __syncthreads();
+
+  int now = 0;   // the current piece's place
+  while (pieces[now].rows) {
+    const int then = now == 2 ? 0 : now + 1;
+    const Piece &p = pieces[now], &next = pieces[then];
+    const int rows = p.rows, row0 = p.row0, jend = last_step(p), jbegin = p.block * kWarps + warp;
+    const pgd::Keys keys{p.keys.ns, p.keys.skip, p.keys.total};
     pgd::Everyone every;
-    every.init(q.s, keys, q.frame(a, row0), q.frame(a, row0 + rows - 1));
+    {
+      const pgd::Seq q = p.seq(a);
+      every.init(q.s, keys, q.frame(a, row0), q.frame(a, row0 + rows - 1));
+    }
     tile.begin(rows, a.scale_log2, a.status);
     auto mask_of = [&](int r) {
+      const pgd::Seq q = pieces[now].seq(a);
       pgd::Row mask;
       mask.init(q.s, keys, r < rows ? q.frame(a, row0 + r) : -1);
       return mask;
     };
-    int stage = 0;
-    for (int j = j0; j < j1; j += kWarps) {
-      tc::cp_async_wait<1>();
+    for (int j = jbegin; j < jend; j += kWarps) {
+      if (flying == 2) tc::cp_async_wait<1>();
+      else tc::cp_async_wait<0>();
       __syncwarp();   // the step's copies are there, and the stage before it has been read by every lane
-      copy(j + 2 * kWarps, stage == 0 ? 2 : stage - 1);
       const uint32_t st = ring0 + (uint32_t)(stage * R::kStage);
       stage = stage == 2 ? 0 : stage + 1;
+      flying--;
+      refill(&next);
       tile.step(st, j * kKeys, every.see(j * kKeys, j * kKeys + kKeys), mask_of, a.bases);
     }
-    tc::cp_async_wait<0>();
-    __syncthreads();   // the rings are done with: their memory takes the warps' outputs
+    refill(&next);            // (a warp without a step in the piece has not turned yet)
+    if (!ahead) turn_to(next);
+    ahead = false;
 
-    // ---- the warps' parts joined in shared memory ----
-    float (*osm)[8][D] = (float (*)[8][D])dyn;
+    // ---- the warps' parts joined: a warp's outputs go through the stage it has read last, the other two are on
+    // their way for the next piece ----
+    __syncwarp();
+    const int mine = stage == 0 ? 2 : stage - 1;
+    float (*osm)[D] = (float (*)[D])(dyn + (size_t)(warp * R::kStages + mine) * R::kStage);
+    if (lane == 0) spare[warp] = mine;
     tile.sums(msm[warp], lsm[warp]);
-    const bool part = block > 0 || block1 < blocks;
+    const bool part = p.block > 0 || p.block1 < p.blocks;
 #pragma unroll
     for (int nt = 0; nt < NT; nt++) {
-      if (8 * nt >= rows) break;
-      if (nt) __syncthreads();
-      tile.outputs(nt, rows, osm[warp]);
-      __syncthreads();
-      const int r = 8 * nt + warp, ch = 4 * lane;   // warp = row, lane = four channels
-      if (r < rows) {
-        float M, L;
-        float4 acc = wt::join(msm, lsm, r, [&](int w) { return *(const float4 *)&osm[w][warp][ch]; }, M, L);
-        const float inv = L > 0.f ? win::kUnit<BITS> / L : 0.f, lse = L > 0.f ? M + log2f(L) : -INFINITY;
-        acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-        if (!part) {
-          const int i = (row0 + r) / a.group, h = kvh * a.group + (row0 + r - i * a.group);
-          pgd::finish4(a, q.first + i, h, ch, acc, lse);
-          __syncwarp();   // merging lanes have read the earlier log-sum-exp
-          if (lane == 0) pgd::finish_lse(a, q.first + i, h, lse);
-        } else {   // an item's first part in the share's second place, any other in its first
-          const int64_t pr = ((int64_t)blockIdx.x * 2 + (block == 0 ? 1 : 0)) * 8 * NT + r;
-          *(float4 *)(a.part + pr * D + ch) = acc;
-          if (lane == 0) a.part_lse[pr] = lse;
+      if (8 * nt < rows) {
+        if (nt) __syncthreads();
+        tile.outputs(nt, rows, osm);
+        if (nt == NT - 1 || 8 * (nt + 1) >= rows) {   // the last of them: the registers take the next Queries
+          fetch(next);
+          if (warp == kWarps - 1) plan(pieces[then == 2 ? 0 : then + 1]);
+        }
+        __syncthreads();
+        const int r = 8 * nt + warp, ch = 4 * lane;   // warp = row, lane = four channels
+        if (r < rows) {
+          float M, L;
+          float4 acc = wt::join(msm, lsm, r, [&](int w) {
+            return *(const float4 *)(dyn + (size_t)(w * R::kStages + spare[w]) * R::kStage + (size_t)(warp * D + ch) * 4);
+          }, M, L);
+          const float inv = L > 0.f ? win::kUnit<BITS> / L : 0.f, lse = L > 0.f ? M + log2f(L) : -INFINITY;
+          acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+          if (!part) {
+            const int i = (row0 + r) / a.group, h = p.kvh * a.group + (row0 + r - i * a.group);
+            pgd::finish4(a, p.first + i, h, ch, acc, lse);
+            __syncwarp();   // merging lanes have read the earlier log-sum-exp
+            if (lane == 0) pgd::finish_lse(a, p.first + i, h, lse);
+          } else {   // an item's first part in the share's second place, any other in its first
+            const int64_t pr = ((int64_t)blockIdx.x * 2 + (p.block == 0 ? 1 : 0)) * 8 * NT + r;
+            *(float4 *)(a.part + pr * D + ch) = acc;
+            if (lane == 0) a.part_lse[pr] = lse;
+          }
         }
       }
     }
     __syncthreads();
-    item++;
-    block = 0;
-    if (last) break;
+    now = then;
   }
-  if (!began && threadIdx.x == 0) a.cuts[blockIdx.x] = PagedCut{a.batch, 0, 0, 0, 0, 0, 0};
+  tc::cp_async_wait<0>();
   // launched beside the tile kernel: who waits for this one waits for both
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
