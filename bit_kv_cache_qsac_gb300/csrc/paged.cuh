@@ -183,7 +183,8 @@ __device__ __forceinline__ void finish_lse(const PagedAttend &a, int token, int 
 // ------------------------------------------------------------------ how the work is shared out
 // All items of the sequences an attention kernel takes stand in one line, by sequence, each as long as what its
 // keys and its start and end cost.  Share i begins at i / shares of the line; a cut close to an item's border is
-// moved there.  Every CTA works out its own two cuts in the same way, so nothing is written down beforehand.
+// moved there.  Every CTA works out its own two cuts in the same way (find_cuts), so nothing is written down
+// beforehand.
 namespace pgd {
 
 // An item of `blocks` blocks of keys costs start + blocks * each.  Where place x (counted from the item's begin) cuts
@@ -191,70 +192,6 @@ namespace pgd {
 __device__ __forceinline__ int cut_item(int64_t x, int blocks, int start, int each, int least) {
   const int block = x < start ? 0 : (int)win::quotient(x - start, each);
   return block < least ? 0 : (blocks - block < least ? blocks : block);
-}
-
-// The cuts of share `share` of `shares` (begin, end), found by the whole block of THREADS threads.  work.cost(b) is
-// the length of sequence b's items, work.cut(b, x, item, block) where place x of them falls.  Fewer shares are
-// used when they would be shorter than `thin`.  A share without work begins and ends at sequence `batch`.
-template <int THREADS, typename Work>
-__device__ __forceinline__ void share_of(int batch, int share, int shares, int thin, const Work &work, PagedCut (&cut)[2]) {
-  constexpr int kW = THREADS / 32;
-  __shared__ int64_t sums[kW + 1];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // the running sum of v over the block's threads, and the total
-  auto scan = [&](int64_t v, int64_t &total) -> int64_t {
-    int64_t s = v;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int64_t o = __shfl_up_sync(0xffffffffu, s, d);
-      if (lane >= d) s += o;
-    }
-    __syncthreads();
-    if (lane == 31) sums[warp] = s;
-    __syncthreads();
-    int64_t before = 0;
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < kW; w++) {
-      const int64_t x = sums[w];
-      before += w < warp ? x : 0;
-      total += x;
-    }
-    return before + s;
-  };
-  if (tid < 2) cut[tid] = PagedCut{batch, 0, 0, 0, 0, 0, 0};
-  int64_t mine = tid < batch ? work.cost(tid) : 0;
-  int64_t total, upto = scan(mine, total);
-  int64_t all = total;
-  if (batch > THREADS) {
-    int64_t more = 0, rest;
-    for (int b = THREADS + tid; b < batch; b += THREADS) more += work.cost(b);
-    scan(more, rest);
-    all += rest;
-  }
-  int64_t used = win::quotient(all, thin);
-  used = used < 1 ? 1 : (used < shares ? used : shares);
-  if (share < used && all > 0) {   // (the same for the whole block)
-    const int64_t x0 = all * share / used, x1 = all * (share + 1) / used;
-    int64_t base = 0;
-    for (int b0 = 0; b0 < batch; b0 += THREADS) {
-      if (b0 > 0) {
-        mine = b0 + tid < batch ? work.cost(b0 + tid) : 0;
-        upto = scan(mine, total);
-      }
-      const int64_t end = base + upto, begin = end - mine;
-#pragma unroll
-      for (int e = 0; e < 2; e++) {
-        const int64_t x = e ? x1 : x0;
-        if (x >= begin && x < end) {
-          cut[e].b = b0 + tid;
-          work.cut(b0 + tid, x - begin, cut[e].item, cut[e].block);
-        }
-      }
-      base += total;
-    }
-  }
-  __syncthreads();
 }
 
 }  // namespace pgd

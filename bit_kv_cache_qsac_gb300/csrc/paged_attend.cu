@@ -5,7 +5,7 @@
 // decoded from the 8- or 4-bit pages inside the kernel (exact in fp16; see window.cuh for Queries and weights).
 //
 // An item is one Key head of one sequence with 512 of its rows (row r = token r / group, head r % group) and the
-// keys those rows see between them.  All items stand in one line (pgd::share_of) and a CTA pair (a cluster of two,
+// keys those rows see between them.  All items stand in one line (find_cuts) and a CTA pair (a cluster of two,
 // cta_group::2 MMAs) takes an equal piece of it: whole items, and parts of those that a cut goes through.  So
 // sequences of any lengths, causal items of different lengths and calls of a few items fill all SMs alike.
 // CTA c of a pair holds rows 256 x + 128 c .. + 127 of the two Query tiles x = 0, 1.  The B operand of an

@@ -4,7 +4,7 @@
 // A row r of a Key head is (token r / group, head r % group of the group); an item is one Key head of one
 // sequence with up to 8 NT of its rows.  The work is bound by the cache's bytes and sequences differ in
 // length, so it is shared out by the key: every CTA takes an equal piece of the line of all items
-// (pgd::share_of).  An item that a cut goes through is computed in parts, which a second kernel joins.
+// (find_cuts).  An item that a cut goes through is computed in parts, which a second kernel joins.
 // Inside a CTA an item's keys go to the 8 warps in turn, 16 or 32 at a time, copied to a ring of shared
 // memory of the warp's own two steps ahead (cp.async; no barrier but the warp's) and multiplied on warp
 // MMAs (warp_tile.cuh).  16 keys from a multiple of 16 lie in one page.
@@ -14,40 +14,91 @@
 namespace {
 
 constexpr int D = win::D;
-using wt::kWarps;
 using wt::Ring;
-constexpr int kThreads = 32 * kWarps;
+constexpr int kWarps = wt::kWarps, kThreads = 32 * kWarps;
 template <int BITS>
 constexpr int kBlock = kWarps * wt::step_keys(BITS);   // keys that the 8 warps take at once
 // What an item costs besides its keys, in blocks; the least piece of an item, and of the line, worth a start.
-constexpr int kStart = 4, kLeast = 2, kThin = 6;
+constexpr int kStart = 4, kLeast = 1, kThin = 4;
 
-// The items of a sequence: Key heads by blocks of 8 NT rows, all as long.
+// The items of sequence b: blocks of keys of each, and how many (Key heads by blocks of 8 NT rows, all as long).
 template <int BITS, int NT>
-struct Work {
-  const PagedAttend &a;
-  // (one copy of the code: what a CTA does once is paced by instruction fetches)
-  __device__ __noinline__ static int2 of(const PagedAttend &a, int b) {
-    const pgd::Seq q = pgd::sequence(a, b);
-    if (q.rows == 0 || q.rows > a.few) return make_int2(0, 0);
-    pgd::Keys keys;
-    keys.init(a, q.s, q.frame(a, 0), q.frame(a, q.rows - 1));
-    return make_int2((keys.total + kBlock<BITS> - 1) / kBlock<BITS>, a.pool.kv_heads * ((q.rows + 8 * NT - 1) / (8 * NT)));
-  }
-  __device__ __forceinline__ int64_t cost(int b) const {
-    const int2 w = of(a, b);   // blocks of an item, items
-    return (int64_t)w.y * (w.x + kStart);
-  }
-  __device__ __forceinline__ void cut(int b, int64_t x, int &item, int &block) const {
-    const int blocks = of(a, b).x;
-    item = (int)win::quotient(x, blocks + kStart);
-    block = pgd::cut_item(x - (int64_t)item * (blocks + kStart), blocks, kStart, 1, kLeast);
-    if (block == blocks && block > 0) {
-      item++;
-      block = 0;
+__device__ __forceinline__ int2 items_of(const PagedAttend &a, int b) {
+  const pgd::Seq q = pgd::sequence(a, b);
+  if (q.rows == 0 || q.rows > a.few) return make_int2(0, 0);
+  pgd::Keys keys;
+  keys.init(a, q.s, q.frame(a, 0), q.frame(a, q.rows - 1));
+  return make_int2((keys.total + kBlock<BITS> - 1) / kBlock<BITS>, a.pool.kv_heads * ((q.rows + 8 * NT - 1) / (8 * NT)));
+}
+
+// The cuts of share `share` (begin, end) in the line of all items, found by the whole CTA.  Fewer shares are used when
+// they would be shorter than kThin.  A share without work begins and ends at sequence `batch`.
+template <int BITS, int NT>
+__device__ __forceinline__ void find_cuts(const PagedAttend &a, int share, PagedCut (&cut)[2]) {
+  __shared__ int64_t sums[kWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid < 2) cut[tid] = PagedCut{a.batch, 0, 0, 0, 0, 0, 0};
+  int64_t x[2] = {INT64_MAX, INT64_MAX};
+  // first the line's length, then the cuts' places; a batch of up to one sequence a thread is looked at once
+  const bool once = a.batch <= kThreads;
+  int2 w;
+  int64_t mine = 0, upto = 0;
+  auto scan = [&]() -> int64_t {   // upto: the sum of `mine` over the threads up to this one; the sum over all
+    upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t o = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += o;
+    }
+    __syncthreads();
+    if (lane == 31) sums[warp] = upto;
+    __syncthreads();
+    int64_t total = 0;
+#pragma unroll
+    for (int k = 0; k < kWarps; k++) {
+      const int64_t v = sums[k];
+      upto += k < warp ? v : 0;
+      total += v;
+    }
+    return total;
+  };
+  int64_t all = 0;
+#pragma unroll 1
+  for (int turn = 0; turn < (once ? 1 : 2); turn++) {
+    int64_t base = 0;
+#pragma unroll 1
+    for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
+      w = make_int2(0, 0);
+      if (b0 + tid < a.batch) w = items_of<BITS, NT>(a, b0 + tid);
+      mine = (int64_t)w.y * (w.x + kStart);
+      const int64_t total = scan();
+      if (once || (turn == 0 && b0 + kThreads >= a.batch)) {   // the length is known
+        all = base + total;
+        int64_t used = win::quotient(all, kThin);
+        used = used < 1 ? 1 : (used < a.shares ? used : a.shares);
+        if (share >= used || all == 0) return;   // (the same for the whole CTA)
+        x[0] = win::quotient(all * share, used);
+        x[1] = win::quotient(all * (share + 1), used);
+      }
+      if (once || turn == 1) {
+        const int64_t end = base + upto, begin = end - mine;
+#pragma unroll 1
+        for (int e = 0; e < 2; e++)
+          if (x[e] >= begin && x[e] < end) {
+            const int64_t y = x[e] - begin;
+            int item = (int)win::quotient(y, w.x + kStart);
+            int block = pgd::cut_item(y - (int64_t)item * (w.x + kStart), w.x, kStart, 1, kLeast);
+            if (block == w.x && block > 0) {
+              item++;
+              block = 0;
+            }
+            cut[e] = PagedCut{b0 + tid, item, block, 0, 0, 0, 0};
+          }
+      }
+      base += total;
     }
   }
-};
+}
 
 // A piece of an item that the share holds: blocks `block` .. block1 - 1 of its `blocks`.
 struct Piece {
@@ -77,7 +128,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) paged_decode_kernel
   __shared__ int spare[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the joining kernel may line up
-  pgd::share_of<kThreads>(a.batch, (int)blockIdx.x, a.shares, kThin, Work<BITS, NT>{a}, cut);
+  find_cuts<BITS, NT>(a, (int)blockIdx.x, cut);
+  __syncthreads();
 
   // ---- the share's pieces, described by the last warp (which has the fewest steps) one ahead of their use ----
   int nb = cut[0].b, nitem = cut[0].item, nblock = cut[0].block;   // where the next one begins
@@ -133,76 +185,85 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) paged_decode_kernel
   // v_at(row + 32 / kPer, .) is 512 further on but for the permutation: one piece bit flips per 4 rows
   const uint32_t vdst = R::v_at(lane / kPer, lane & (kPer - 1));
   auto vdst_of = [&](int i) -> uint32_t { return (vdst ^ (BITS == 8 ? 32u * (i & 3) : 64u * (i & 1))) + 512u * i; };
+  const uint32_t page_rows = 1u << a.page_log2, head_rows = (uint32_t)a.pool.kv_heads << a.page_log2;   // (all heads': 2^24 at most)
   auto last_step = [&](const Piece &p) -> int {   // steps of an item that the piece ends with
     const int all = (p.keys.total + kKeys - 1) / kKeys;
     return p.block1 * kWarps < all ? p.block1 * kWarps : all;
   };
   int cj, cend;        // the next step to be copied of the piece that copies have come to, and its end
-  int ckvh, entry[kSub];   // its Key head; the table's entries for that step
-  pgd::Keys ckeys;
-  const int32_t *ctable;
-  auto look = [&]() {
+  int entry[kSub];     // the table's entries for that step
+  // (what else is needed of the piece is read where it is needed: registers are the products')
+  auto look = [&](const volatile Piece &p) {
     if (cj < cend) {
+      const int total = p.keys.total, ns = p.keys.ns, skip = p.keys.skip;
+      const int32_t *table = a.table + p.b * a.width;   // (4,096 sequences of 2^18 pages at most)
 #pragma unroll
       for (int u = 0; u < kSub; u++) {   // each 16 keys; those past the last key repeat its 16
-        const int v = cj * kKeys + 16 * u < ckeys.total ? cj * kKeys + 16 * u : (ckeys.total - 1) & -16;
-        entry[u] = ctable[ckeys.token(v) >> a.page_log2];
+        const int v = cj * kKeys + 16 * u < total ? cj * kKeys + 16 * u : (total - 1) & -16;
+        entry[u] = table[(v < ns ? v : v + skip) >> a.page_log2];
       }
     }
   };
   auto turn_to = [&](const Piece &p) {
-    ckeys.ns = p.keys.ns;
-    ckeys.skip = p.keys.skip;
-    ckeys.total = p.keys.total;
-    ckvh = p.kvh;
-    ctable = a.table + (int64_t)p.b * a.width;
     cj = p.block * kWarps + warp;
     cend = p.rows ? last_step(p) : 0;
-    look();
+    look(p);
   };
   int stage = 0, flying = 0;
   bool ahead = false;   // copies have come to the piece after the current one
-  auto refill = [&](const Piece *next) {   // next: the piece after the current one, where it may be turned to
+  auto refill = [&](const Piece &now, const Piece &next, bool may_turn) {   // the current piece and the one after it
 #pragma unroll 1
     while (flying < 2) {
       if (cj >= cend) {
-        if (!next || ahead) break;
+        if (!may_turn || ahead) break;
         ahead = true;
-        turn_to(*next);
+        turn_to(next);
         if (cj >= cend) break;
       }
+      const volatile Piece &p = ahead ? next : now;
+      const int total = p.keys.total, ns = p.keys.ns, skip = p.keys.skip;
+      const uint32_t chead = (uint32_t)p.kvh << a.page_log2;   // rows of a page before its Key head's
       const int place = stage + flying >= 3 ? stage + flying - 3 : stage + flying;
       const uint32_t dst = ring0 + (uint32_t)(place * R::kStage);
-      int64_t at[kSub];   // the row of the first of each 16 keys
-      int follow[kSub];   // and how many rows follow it
+      const int v0 = cj * kKeys;
+      const bool whole = v0 + kKeys <= total;
 #pragma unroll
       for (int u = 0; u < kSub; u++) {
-        const int v = cj * kKeys + 16 * u < ckeys.total ? cj * kKeys + 16 * u : (ckeys.total - 1) & -16;
-        at[u] = pgd::page_row(a, pgd::checked(a, entry[u]), ckvh) + (ckeys.token(v) & ((1 << a.page_log2) - 1));
-        follow[u] = ckeys.total - 1 - v;
-      }
+        // each 16 keys (those past the last key repeat its 16): page, and rows before them in it and its earlier heads
+        const int v = whole || v0 + 16 * u < total ? v0 + 16 * u : (total - 1) & -16;
+        const uint32_t page = (uint32_t)pgd::checked(a, entry[u]), row0 = chead + ((uint32_t)(v < ns ? v : v + skip) & (page_rows - 1u));
+        const uint64_t at = (uint64_t)page * (head_rows * (uint32_t)R::kRow) + (row0 * (uint32_t)R::kRow + 16u * lane);
+        const uint64_t step_at = (uint64_t)page * (head_rows * (uint32_t)win::kSteps) + (row0 + (lane & 15u)) * (uint32_t)win::kSteps;
+        const uint8_t *kp = a.pool.k_codes + at, *vp = a.pool.v_codes + at, *sp = (lane < 16 ? a.pool.k_step : a.pool.v_step) + step_at;
+        const uint32_t sdst = dst + (lane < 16 ? R::kKS : R::kVS) + 4u * ((lane & 15) + 16 * u);
+        if (whole) {
 #pragma unroll
-      for (int i = 0; i < kCopies; i++) {
-        const int u = kSub == 2 && i >= kCopies / 2 ? 1 : 0, row = (32 * i + lane) / kPer - 16 * u;
-        const int64_t src = (at[u] + (row < follow[u] ? row : follow[u])) * R::kRow + 16 * (lane & (kPer - 1));
-        wt::cp_async16(dst + kdst + 512u * i, a.pool.k_codes + src);
-        wt::cp_async16(dst + vdst_of(i), a.pool.v_codes + src);
-      }
-      const int srow = lane & 15;
-#pragma unroll
-      for (int u = 0; u < kSub; u++) {   // lanes 0-15: the Keys' step words, 16-31: the Values'
-        const int64_t src = (at[u] + (srow < follow[u] ? srow : follow[u])) * win::kSteps;
-        wt::cp_async4(dst + (lane < 16 ? R::kKS : R::kVS) + 4u * (srow + 16 * u), (lane < 16 ? a.pool.k_step : a.pool.v_step) + src);
+          for (int i = 0; i < kCopies / kSub; i++) {
+            const int c = u * (kCopies / kSub) + i;
+            wt::cp_async16(dst + kdst + 512u * c, kp + 512 * i);
+            wt::cp_async16(dst + vdst_of(c), vp + 512 * i);
+          }
+          wt::cp_async4(sdst, sp);   // lanes 0-15: the Keys' step words, 16-31: the Values'
+        } else {   // rows past the last one repeat it
+          const int follow = total - 1 - v;
+#pragma unroll 1
+          for (int i = 0; i < kCopies / kSub; i++) {
+            const int c = u * (kCopies / kSub) + i, row = (32 * i + lane) / kPer, back = row > follow ? (row - follow) * R::kRow : 0;
+            wt::cp_async16(dst + kdst + 512u * c, kp + 512 * i - back);
+            wt::cp_async16(dst + vdst_of(c), vp + 512 * i - back);
+          }
+          wt::cp_async4(sdst, sp - ((lane & 15) > follow ? ((lane & 15) - follow) * win::kSteps : 0));
+        }
       }
       tc::cp_async_commit();
       flying++;
       cj += kWarps;
-      look();
+      look(p);
     }
   };
   fetch(pieces[0]);
   turn_to(pieces[0]);
-  refill(nullptr);
+  refill(pieces[0], pieces[0], false);
   if (warp == kWarps - 1) plan(pieces[1]);
   __syncthreads();
 
@@ -231,10 +292,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) paged_decode_kernel
       const uint32_t st = ring0 + (uint32_t)(stage * R::kStage);
       stage = stage == 2 ? 0 : stage + 1;
       flying--;
-      refill(&next);
+      refill(p, next, true);
       tile.step(st, j * kKeys, every.see(j * kKeys, j * kKeys + kKeys), mask_of, a.bases);
     }
-    refill(&next);            // (a warp without a step in the piece has not turned yet)
+    refill(p, next, true);    // (a warp without a step in the piece has not turned yet)
     if (!ahead) turn_to(next);
     ahead = false;
 

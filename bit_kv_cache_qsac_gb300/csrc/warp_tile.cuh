@@ -345,16 +345,16 @@ struct Tile {
 };
 
 // Four channels of a row from the warps' parts (unnormalised), its maximum M and sum L; osm_of(w): warp w's.
-template <int ROWS, typename Osm>
-__device__ __forceinline__ float4 join(const float (&msm)[kWarps][ROWS], const float (&lsm)[kWarps][ROWS], int r, Osm osm_of,
+template <int WARPS, int ROWS, typename Osm>
+__device__ __forceinline__ float4 join(const float (&msm)[WARPS][ROWS], const float (&lsm)[WARPS][ROWS], int r, Osm osm_of,
                                        float &M, float &L) {
   M = -INFINITY;
 #pragma unroll
-  for (int w = 0; w < kWarps; w++) M = fmaxf(M, msm[w][r]);
+  for (int w = 0; w < WARPS; w++) M = fmaxf(M, msm[w][r]);
   L = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-  for (int w = 0; w < kWarps; w++) {
+  for (int w = 0; w < WARPS; w++) {
     const float wt = msm[w][r] == -INFINITY ? 0.f : tc::ex2_approx(msm[w][r] - M);
     const float4 x = osm_of(w);
     L = fmaf(lsm[w][r], wt, L);
