@@ -13,67 +13,99 @@
 namespace {
 
 constexpr int kThreads = 256, kRows = kThreads / 16, kReadRows = kThreads / 8;
-constexpr int kUnroll = 4;   // heads whose loads are in flight together
+constexpr int kUnroll = 2;   // heads whose loads are in flight together
 
 __device__ __forceinline__ float low(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float high(uint32_t x) { return __uint_as_float(x & 0xFFFF0000u); }
 
-// What the channels of a row are multiplied by, x s r: 1 / sqrt(mean((x s)^2) + eps s^2).  s is a power of two,
-// 1 but for rows whose squares would leave fp32's range.  w: this lane's 8 channels; all 16 lanes of the row
-// take part.
-__device__ __forceinline__ float row_scale(const uint32_t (&w)[4], float eps, float &s) {
-  auto squares = [&](float f) {
-    uint64_t acc = 0ull;
+__device__ __forceinline__ uint64_t square_sum(const uint32_t (&w)[4], float f) {
+  uint64_t acc = 0ull;
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const uint64_t x = win::pair2(low(w[i]) * f, high(w[i]) * f);
-      acc = tc::fma2(x, x, acc);
-    }
-    float v = win::split2(acc).x + win::split2(acc).y;
+  for (int i = 0; i < 4; i++) {
+    const uint64_t x = f == 1.f ? win::pair2(low(w[i]), high(w[i])) : win::pair2(low(w[i]) * f, high(w[i]) * f);
+    acc = tc::fma2(x, x, acc);
+  }
+  return acc;
+}
+// 1 / sqrt(x): the approximation and a Newton step, which leaves about its own rounding.
+__device__ __forceinline__ float inverse_root(float x) {
+  const float r = rsqrtf(x);
+  const float half = 0.5f * x * r;
+  return x > 0x1p-120f && x < 0x1p120f ? fmaf(r, fmaf(-half, r, 0.5f), r) : r;
+}
+// A mean square beyond 2^120, or so small that squares were lost and eps does not cover them.
+__device__ __forceinline__ bool out_of_range(float v, float eps) { return !(v <= 0x1p120f) || (v < 0x1p-80f && eps < 0x1p-70f); }
+
+// A row whose squares leave fp32's range: the power of two s that brings it back, and r = 1 / sqrt(mean((x s)^2) +
+// eps s^2); r of the row as it is and s = 1 for other rows.  w: this lane's 8 channels; all lanes of the warp take
+// part.
+__device__ __forceinline__ float2 scale_of_odd_row(const uint32_t (&w)[4], float eps) {
+  auto squares = [&](float f) {
+    const float2 a = win::split2(square_sum(w, f));
+    float v = a.x + a.y;
 #pragma unroll
     for (int d = 1; d < 16; d <<= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
     return v;
   };
-  float v = squares(1.f);
-  s = 1.f;
-  // beyond 2^120, or so small that squares were lost and eps does not cover them
-  const bool odd = !(v <= 0x1p120f) || (v < 0x1p-80f && eps < 0x1p-70f);
-  if (__any_sync(0xffffffffu, odd)) {
-    uint32_t m = win::max_abs_bf16x2(win::max_abs_bf16x2(w[0], w[1]), win::max_abs_bf16x2(w[2], w[3])) & 0x7FFF7FFFu;
-    m = win::larger_half(m);
+  float v = squares(1.f), s = 1.f;
+  uint32_t m = win::max_abs_bf16x2(win::max_abs_bf16x2(w[0], w[1]), win::max_abs_bf16x2(w[2], w[3])) & 0x7FFF7FFFu;
+  m = win::larger_half(m);
 #pragma unroll
-    for (int d = 1; d < 16; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
-    // the row's largest channel to about 1 (nothing to be done for infinities, NaN and rows of zeros)
-    int e = 127 - (int)(m >> 7);
-    e = e < -126 ? -126 : (e > 126 ? 126 : e);
-    if (eps > 0.f && e > 50) e = 50;   // (below 2^-50 eps outweighs the squares, or still does)
-    const float f = odd && m < 0x7F80u && m > 0u ? __uint_as_float((uint32_t)(127 + e) << 23) : 1.f;
-    const float u = squares(f);
-    if (f != 1.f) {
-      v = u;
-      s = f;
-    }
+  for (int d = 1; d < 16; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+  // the row's largest channel to about 1 (nothing to be done for infinities, NaN and rows of zeros)
+  int e = 127 - (int)(m >> 7);
+  e = e < -126 ? -126 : (e > 126 ? 126 : e);
+  if (eps > 0.f && e > 50) e = 50;   // (below 2^-50 eps outweighs the squares, or still does)
+  const float f = out_of_range(v, eps) && m < 0x7F80u && m > 0u ? __uint_as_float((uint32_t)(127 + e) << 23) : 1.f;
+  const float u = squares(f);
+  if (f != 1.f) {
+    v = u;
+    s = f;
   }
-  return 1.f / sqrtf(fmaf(v, 1.f / win::D, eps * s * s));
+  return make_float2(1.f / sqrtf(fmaf(v, 1.f / win::D, eps * s * s)), s);
 }
 
-// Eight channels normed (NORM) and turned (TURN >= 0), rounded to bf16.  wt: this lane's weights, HALF: and its
-// partner's behind them.  Every lane of the warp takes part.
-template <bool NORM, int TURN, bool WHOLE, typename Rot>
-__device__ __forceinline__ void norm_turn(uint32_t (&w)[4], const float *wt, float eps, const qwm_rope_spec &sp, const Rot &rv) {
-  if (!NORM) {
-    if (TURN >= 0) rv.turn(sp, w);
-    return;
-  }
-  float s;
-  const float r = row_scale(w, eps, s);
-  uint64_t y[4], z[4];   // this lane's channels, its partner's
-  auto normed = [&](const uint32_t (&x)[4], const float *g, uint64_t (&v)[4]) {
+// What the channels of N rows (1, 2 or 4: heads) of this lane's token are multiplied by; -1 for a row whose squares leave
+// fp32's range, which is left for later (its code beside the others' would take their registers).  The 16 lanes of a
+// token reduce the N sums together, each lane ending with one of them, so that a root is formed once a lane.
+template <int N>
+__device__ __forceinline__ void row_scales(const uint32_t (&w)[N][4], float eps, float (&r)[N]) {
+  const int lane = threadIdx.x & 31;
+  float v[N];
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      v[i] = tc::mul2(win::pair2(low(x[i]), high(x[i])), win::pair2(r, r));
-      v[i] = tc::mul2(v[i], win::pair2(g[2 * i], g[2 * i + 1]));
-    }
+  for (int u = 0; u < N; u++) {
+    const float2 a = win::split2(square_sum(w[u], 1.f));
+    v[u] = a.x + a.y;
+  }
+  const bool up = lane & 8, on = lane & 4;
+  if (N == 4) {   // each lane hands on two sums and keeps two, then one and one
+    const float a = __shfl_xor_sync(0xffffffffu, up ? v[0] : v[2 % N], 8), b = __shfl_xor_sync(0xffffffffu, up ? v[1 % N] : v[3 % N], 8);
+    v[0] = (up ? v[2 % N] : v[0]) + a;
+    v[1 % N] = (up ? v[3 % N] : v[1 % N]) + b;
+    const float c = __shfl_xor_sync(0xffffffffu, on ? v[0] : v[1 % N], 4);
+    v[0] = (on ? v[1 % N] : v[0]) + c;
+  } else {
+    const float a = __shfl_xor_sync(0xffffffffu, N == 2 && !up ? v[1 % N] : v[0], 8);
+    v[0] = (N == 2 && up ? v[1 % N] : v[0]) + a;
+    v[0] += __shfl_xor_sync(0xffffffffu, v[0], 4);
+  }
+  v[0] += __shfl_xor_sync(0xffffffffu, v[0], 2);
+  v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
+  const float mine = out_of_range(v[0], eps) ? -1.f : inverse_root(fmaf(v[0], 1.f / win::D, eps));
+#pragma unroll
+  for (int u = 0; u < N; u++)   // row u's: lanes of bit 3 = u / 2, bit 2 = u % 2 (two rows: bit 3 = u)
+    r[u] = N == 1 ? mine : __shfl_sync(0xffffffffu, mine, (lane & 16) | (N == 4 ? (u >> 1) << 3 | (u & 1) << 2 : u << 3));
+}
+
+// Eight channels times r and the weights, and turned (TURN >= 0), rounded to bf16.  g: this
+// lane's weights, HALF: and its partner's behind them.  Every lane of the warp takes part.
+template <int TURN, bool WHOLE, typename Rot>
+__device__ __forceinline__ void norm_turn(uint32_t (&w)[4], const float *g, float r, const qwm_rope_spec &sp, const Rot &rv) {
+  uint64_t y[4], z[4];   // this lane's channels, its partner's
+  auto normed = [&](const uint32_t (&x)[4], const float *f, uint64_t (&v)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+      v[i] = tc::mul2(tc::mul2(win::pair2(low(x[i]), high(x[i])), win::pair2(r, r)), win::pair2(f[2 * i], f[2 * i + 1]));
   };
   uint32_t p[4] = {0u, 0u, 0u, 0u};
   if (TURN == QWM_ROPE_HALF) {
@@ -81,20 +113,8 @@ __device__ __forceinline__ void norm_turn(uint32_t (&w)[4], const float *wt, flo
 #pragma unroll
     for (int i = 0; i < 4; i++) p[i] = __shfl_sync(0xffffffffu, w[i], from);
   }
-  if (__any_sync(0xffffffffu, s != 1.f)) {   // (a power of two: the products with s are exact, or beyond mattering)
-    uint32_t x[4], q[4];
-    auto scaled = [&](uint32_t v, float f) { return tc::pack_bf16x2(low(v) * f, high(v) * f); };
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      x[i] = scaled(w[i], s);
-      q[i] = scaled(p[i], s);
-    }
-    normed(x, wt, y);
-    if (TURN == QWM_ROPE_HALF) normed(q, wt + 8, z);
-  } else {
-    normed(w, wt, y);
-    if (TURN == QWM_ROPE_HALF) normed(p, wt + 8, z);
-  }
+  normed(w, g, y);
+  if (TURN == QWM_ROPE_HALF) normed(p, g + 8, z);
   if (TURN >= 0) rv.turn_normed(y, z);
 #pragma unroll
   for (int i = 0; i < 4; i++) w[i] = tc::pack_bf16x2(win::split2(y[i]).x, win::split2(y[i]).y);
@@ -126,14 +146,23 @@ struct Rotation : win::RopeVec<PAIRING, WHOLE> {
   }
 };
 
-// This lane's weights of head h (HALF: and its partner's), or ones.
+// The same for a row that row_scales left: its channels times s first (a power of two: exact, or beyond mattering).
+template <int TURN, bool WHOLE, typename Rot>
+__device__ __forceinline__ void norm_turn_odd(uint32_t (&w)[4], const float *g, float eps, const qwm_rope_spec &sp, const Rot &rv) {
+  const float2 f = scale_of_odd_row(w, eps);
+#pragma unroll
+  for (int i = 0; i < 4; i++) w[i] = tc::pack_bf16x2(low(w[i]) * f.y, high(w[i]) * f.y);
+  norm_turn<TURN, WHOLE>(w, g, f.x, sp, rv);
+}
+
+// This lane's weights of a head (HALF: and its partner's), or ones.
 template <int TURN, typename Rot>
 __device__ __forceinline__ void weights_of(const float *weight, int v, const qwm_rope_spec &sp, const Rot &rv, float (&g)[16]) {
 #pragma unroll
   for (int i = 0; i < 16; i++) g[i] = 1.f;
   if (!weight) return;
   auto take = [&](int u, float *to) {
-    const float4 a = __ldg((const float4 *)weight + 2 * u), b = __ldg((const float4 *)weight + 2 * u + 1);
+    const float4 a = ((const float4 *)weight)[2 * u], b = ((const float4 *)weight)[2 * u + 1];
     to[0] = a.x; to[1] = a.y; to[2] = a.z; to[3] = a.w;
     to[4] = b.x; to[5] = b.y; to[6] = b.z; to[7] = b.w;
   };
@@ -141,14 +170,22 @@ __device__ __forceinline__ void weights_of(const float *weight, int v, const qwm
   if (TURN == QWM_ROPE_HALF) take(rv.partner(sp) & 15, g + 8);
 }
 
+// Each head's own weights of a block's heads in shared memory (512 bytes a head): fetched from where they are, every
+// head would wait for its own.  Every thread takes part; a barrier follows.
+__device__ __forceinline__ void keep_weights(float *to, const float *weight, int h0, int h1) {
+  for (int i = threadIdx.x; i < (h1 - h0) * (win::D / 4); i += kThreads)
+    ((float4 *)to)[i] = __ldg((const float4 *)weight + h0 * (win::D / 4) + i);
+}
+
 // TURN: -1 no rotation, else the pairing (WHOLE: all channels).
 template <int TURN, bool WHOLE>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, 4)
     norm_rope_kernel(const __grid_constant__ qwm_rope_spec sp, const uint16_t *x, qwm_strides xs, int batch, int heads,
                      int64_t n, const int64_t *__restrict__ start, const int64_t *__restrict__ at,
                      const int32_t *__restrict__ pos, const float *__restrict__ weight, int per_head, float eps,
                      uint16_t *out, qwm_strides os, int heads_per_block) {
   __shared__ win::RopeTable tab;
+  extern __shared__ __align__(16) float own[];   // per_head: the block's heads' weights
   const int v = threadIdx.x & 15, row = threadIdx.x >> 4;
   const int64_t tok = (int64_t)blockIdx.x * kRows + row;   // over [batch][n]
   const bool in = tok < (int64_t)batch * n;
@@ -164,6 +201,7 @@ __global__ void __launch_bounds__(kThreads, 3)
       r[u] = h + u < h1 ? *(const uint4 *)(src + (int64_t)(h + u) * xs.head) : make_uint4(0, 0, 0, 0);
   };
   load(h0);   // in flight while the angles are formed
+  if (per_head) keep_weights(own, weight, h0, h1);
   int64_t p = 0;
   bool live = in;
   if (at) {
@@ -178,9 +216,12 @@ __global__ void __launch_bounds__(kThreads, 3)
   if (TURN >= 0) {
     tab.fill(sp);
     rv.init(sp, tab, v, live ? p : 0, pos ? pos + (b * n + i) * 3 : nullptr);
+  } else if (per_head) {
+    __syncthreads();
   }
   float g[16];
   weights_of<TURN>(weight, v, sp, rv, g);
+  uint64_t left = 0ull;   // rows of this token left for later (a block walks over 64 heads at most)
   for (int h = h0; h < h1; h += kUnroll) {
     uint32_t w[kUnroll][4];
 #pragma unroll
@@ -188,13 +229,31 @@ __global__ void __launch_bounds__(kThreads, 3)
       w[u][0] = r[u].x; w[u][1] = r[u].y; w[u][2] = r[u].z; w[u][3] = r[u].w;
     }
     if (h + kUnroll < h1) load(h + kUnroll);   // other rows than the ones written below
+    float rs[kUnroll];
+    row_scales(w, eps, rs);
+    bool some = false;
+#pragma unroll
+    for (int u = 0; u < kUnroll; u++) some |= rs[u] < 0.f;
+    if (__any_sync(0xffffffffu, some)) {
+#pragma unroll
+      for (int u = 0; u < kUnroll; u++) left |= rs[u] < 0.f ? 1ull << (h + u - h0) : 0ull;
+    }
 #pragma unroll
     for (int u = 0; u < kUnroll; u++) {
-      if (per_head && h + u < h1) weights_of<TURN>(weight + (int64_t)(h + u) * win::D, v, sp, rv, g);
-      norm_turn<true, TURN, WHOLE>(w[u], g, eps, sp, rv);
-      if (live && h + u < h1)
+      if (per_head && h + u < h1) weights_of<TURN>(own + (h + u - h0) * win::D, v, sp, rv, g);
+      norm_turn<TURN, WHOLE>(w[u], g, rs[u], sp, rv);
+      if (live && h + u < h1 && rs[u] >= 0.f)
         *(uint4 *)(dst + (int64_t)(h + u) * os.head) = make_uint4(w[u][0], w[u][1], w[u][2], w[u][3]);
     }
+  }
+#pragma unroll 1
+  for (int h = h0; h < h1 && __any_sync(0xffffffffu, left != 0ull); h++, left >>= 1) {   // (not overwritten so far)
+    if (!__any_sync(0xffffffffu, left & 1ull)) continue;
+    const uint4 x4 = *(const uint4 *)(src + (int64_t)h * xs.head);
+    uint32_t w[4] = {x4.x, x4.y, x4.z, x4.w};
+    if (per_head) weights_of<TURN>(own + (h - h0) * win::D, v, sp, rv, g);
+    norm_turn_odd<TURN, WHOLE>(w, g, eps, sp, rv);
+    if (live && (left & 1ull)) *(uint4 *)(dst + (int64_t)h * os.head) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
@@ -206,6 +265,7 @@ __global__ void __launch_bounds__(kThreads)
                        const int32_t *__restrict__ pos, const float *__restrict__ weight, int per_head, float eps,
                        int heads_per_block, int32_t *status) {
   __shared__ win::RopeTable tab;
+  extern __shared__ __align__(16) float own[];   // per_head: the block's heads' weights
   const int v = threadIdx.x & 15, row = threadIdx.x >> 4;
   const int64_t tok = (int64_t)blockIdx.x * kRows + row;
   const bool in = tok < n;
@@ -219,10 +279,13 @@ __global__ void __launch_bounds__(kThreads)
   const bool inside = slot < (int64_t)pool.pages << page_log2;
   const bool live = slot >= 0 && inside && (TURN < 0 || win::starts(p));
   if (!inside) qwm_dev_error(status, QWM_ERR_RANGE);
+  if (NORM && per_head) keep_weights(own, weight, h0, h1);
   Rotation<TURN == QWM_ROPE_HALF ? QWM_ROPE_HALF : QWM_ROPE_INTERLEAVED, WHOLE> rv;
   if (TURN >= 0) {
     tab.fill(sp);
     rv.init(sp, tab, v, live ? p : 0, pos ? pos + i * 3 : nullptr);
+  } else if (NORM && per_head) {
+    __syncthreads();
   }
   if (!__any_sync(0xffffffffu, live)) return;
   const bool all = __all_sync(0xffffffffu, live);
@@ -231,6 +294,7 @@ __global__ void __launch_bounds__(kThreads)
   const int64_t page = live ? slot >> page_log2 : 0;
   int64_t slot_row = ((page * pool.kv_heads + h0) << page_log2) + (live ? slot & ((1 << page_log2) - 1) : 0);
   bool bad = false;
+  uint64_t left = 0ull;   // rows of Keys left for later (a block walks over 64 heads at most)
   for (int h = h0; h < h1; h++) {
     uint32_t kw[4] = {a.x, a.y, a.z, a.w}, vw[4] = {c.x, c.y, c.z, c.w};
     if (h + 1 < h1) {   // the next head's rows
@@ -242,14 +306,44 @@ __global__ void __launch_bounds__(kThreads)
     if (!all) {   // padding is not looked at
       if (!live) kw[0] = kw[1] = kw[2] = kw[3] = vw[0] = vw[1] = vw[2] = vw[3] = 0u;
     }
-    if (NORM && per_head) weights_of<TURN>(weight + (int64_t)h * win::D, v, sp, rv, g);
-    norm_turn<NORM, TURN, WHOLE>(kw, g, eps, sp, rv);
+    if (NORM && per_head) weights_of<TURN>(own + (h - h0) * win::D, v, sp, rv, g);
+    bool now = live;
+    if (NORM) {
+      const uint32_t one[1][4] = {{kw[0], kw[1], kw[2], kw[3]}};
+      float r[1];
+      row_scales(one, eps, r);
+      if (__any_sync(0xffffffffu, live && r[0] < 0.f)) {
+        left |= live && r[0] < 0.f ? 1ull << (h - h0) : 0ull;
+        if (r[0] < 0.f) kw[0] = kw[1] = kw[2] = kw[3] = 0u;
+        now = live && r[0] >= 0.f;
+      }
+      norm_turn<TURN, WHOLE>(kw, g, r[0], sp, rv);
+    } else if (TURN >= 0) {
+      rv.turn(sp, kw);
+    }
     uint32_t c0, c1, step;
     win::quantise<BITS>(kw, c0, c1, step, bad);
-    if (live) win::store_row<BITS>(pool.k_codes, pool.k_step, slot_row, v, c0, c1, step);
+    if (now) win::store_row<BITS>(pool.k_codes, pool.k_step, slot_row, v, c0, c1, step);
     win::quantise<BITS>(vw, c0, c1, step, bad);
     if (live) win::store_row<BITS>(pool.v_codes, pool.v_step, slot_row, v, c0, c1, step);
     slot_row += (int64_t)1 << page_log2;
+  }
+  if (NORM) {   // the rows of Keys that were left
+    slot_row -= (int64_t)(h1 - h0) << page_log2;
+    kp = k + i * ks.token + h0 * ks.head + 8 * v;
+#pragma unroll 1
+    for (int h = h0; h < h1 && __any_sync(0xffffffffu, left != 0ull); h++, left >>= 1) {
+      const uint4 x = *(const uint4 *)kp;
+      uint32_t kw[4] = {x.x, x.y, x.z, x.w}, c0, c1, step;
+      if (!(left & 1ull)) kw[0] = kw[1] = kw[2] = kw[3] = 0u;
+      if (per_head) weights_of<TURN>(own + (h - h0) * win::D, v, sp, rv, g);
+      norm_turn_odd<TURN, WHOLE>(kw, g, eps, sp, rv);
+      if (!(left & 1ull)) kw[0] = kw[1] = kw[2] = kw[3] = 0u;   // (no rows of their own: 0 / 0 where eps is 0)
+      win::quantise<BITS>(kw, c0, c1, step, bad);
+      if (left & 1ull) win::store_row<BITS>(pool.k_codes, pool.k_step, slot_row, v, c0, c1, step);
+      kp += ks.head;
+      slot_row += (int64_t)1 << page_log2;
+    }
   }
   if (bad && live) qwm_dev_error(status, QWM_ERR_RANGE);
 }
@@ -310,7 +404,8 @@ cudaError_t write_launch(const qwm_page_pool &pool, int page_log2, const uint16_
                          const int32_t *pos, const float *weight, int per_head, float eps, int num_sms, int32_t *status,
                          cudaStream_t st) {
   const int64_t tiles = (n + kRows - 1) / kRows;
-  const int hpb = heads_per_block(tiles, pool.kv_heads, num_sms, rope ? 9 : 20);
+  int hpb = heads_per_block(tiles, pool.kv_heads, num_sms, rope ? 9 : 20);
+  hpb = hpb < 64 ? hpb : 64;
   const dim3 grid((unsigned)tiles, (unsigned)((pool.kv_heads + hpb - 1) / hpb));
   const qwm_rope_spec none = {};
   auto kernel = paged_write_kernel<BITS, NORM, -1, false>;
@@ -320,7 +415,7 @@ cudaError_t write_launch(const qwm_page_pool &pool, int page_log2, const uint16_
   else if (rope)
     kernel = rope->rot == win::D ? paged_write_kernel<BITS, NORM, QWM_ROPE_HALF, true>
                                  : paged_write_kernel<BITS, NORM, QWM_ROPE_HALF, false>;
-  kernel<<<grid, kThreads, 0, st>>>(rope ? *rope : none, pool, page_log2, k, ks, v, vs, n, slot, at, pos, weight, per_head, eps,
+  kernel<<<grid, kThreads, per_head ? hpb * win::D * sizeof(float) : 0, st>>>(rope ? *rope : none, pool, page_log2, k, ks, v, vs, n, slot, at, pos, weight, per_head, eps,
                                     hpb, status);
   return cudaGetLastError();
 }
@@ -331,7 +426,8 @@ cudaError_t launch_norm_rope(const qwm_rope_spec *spec, const uint16_t *x, const
                              int64_t n, const int64_t *start, const int64_t *at, const int32_t *pos, const float *weight,
                              int per_head, float eps, uint16_t *out, const qwm_strides &os, int num_sms, cudaStream_t st) {
   const int64_t tiles = ((int64_t)batch * n + kRows - 1) / kRows;
-  const int hpb = heads_per_block(tiles, heads, num_sms, 9);
+  int hpb = heads_per_block(tiles, heads, num_sms, 12);
+  hpb = hpb < 64 ? hpb : 64;
   const dim3 grid((unsigned)tiles, (unsigned)((heads + hpb - 1) / hpb));
   const qwm_rope_spec none = {};
   auto kernel = norm_rope_kernel<-1, false>;
@@ -339,7 +435,7 @@ cudaError_t launch_norm_rope(const qwm_rope_spec *spec, const uint16_t *x, const
     kernel = spec->rot == win::D ? norm_rope_kernel<QWM_ROPE_INTERLEAVED, true> : norm_rope_kernel<QWM_ROPE_INTERLEAVED, false>;
   else if (spec)
     kernel = spec->rot == win::D ? norm_rope_kernel<QWM_ROPE_HALF, true> : norm_rope_kernel<QWM_ROPE_HALF, false>;
-  kernel<<<grid, kThreads, 0, st>>>(spec ? *spec : none, x, xs, batch, heads, n, start, at, pos, weight, per_head, eps, out, os,
+  kernel<<<grid, kThreads, per_head ? hpb * win::D * sizeof(float) : 0, st>>>(spec ? *spec : none, x, xs, batch, heads, n, start, at, pos, weight, per_head, eps, out, os,
                                     hpb);
   return cudaGetLastError();
 }

@@ -14,10 +14,10 @@ import math
 
 import torch
 
-from . import (ActiveChunk, Chunk, Context, Window, pack_psac_layout, qwm_attend, qwm_attend_merge, qwm_dequantize,
-               qwm_fit_centroids_kv,
-               qwm_quantize_kv, qwm_quantize_kv_full, qwm_rope, qwm_select_rank, qwm_sync_status,
-               qwm_update_query_stats, qwm_window_attend, qwm_window_read, qwm_window_write)
+from . import (ActiveChunk, Chunk, Context, PagePool, PageTable, Window, pack_psac_layout, qwm_attend, qwm_attend_merge,
+               qwm_dequantize, qwm_fit_centroids_kv, qwm_norm_rope, qwm_paged_attend, qwm_paged_write,
+               qwm_pages_update, qwm_quantize_kv, qwm_quantize_kv_full, qwm_rope, qwm_select_rank,
+               qwm_sync_status, qwm_update_query_stats, qwm_window_attend, qwm_window_read, qwm_window_write)
 from .window import check_rows
 
 _MAX_CHUNKS = 128   # chunks that one call of qwm_attend or qwm_attend_merge takes
@@ -285,3 +285,79 @@ class WindowedLayer:
 
     def nbytes(self) -> int:
         return self.packed.nbytes() + self.window.nbytes()
+
+
+class PagedBatch:
+    """Many sequences of any lengths through the layers of a model, their Keys and Values at 8 or 4 bits in pages
+    that all sequences share.
+
+    A step is begun with what every sequence is shortened to and how many tokens it gets; then each layer is
+    called once with the step's packed Queries, Keys and Values (rows of all sequences one after the other, as
+    `begin` was told).  What a step needs of the device stays on the device, so that a step may be captured in
+    a CUDA graph and replayed with other counts in the same tensors.  Steps are ordered on one stream."""
+
+    def __init__(self, ctx: Context, layers: int, kv_heads: int, batch: int, max_tokens: int, pages: int, rows: int,
+                 page: int = 64, bits: int = 8, rope=None, norm: bool = True, eps: float = 1e-6, tpf: int = 1,
+                 frames: int | None = None, sink: int = 0, device=None):
+        """batch: sequences held at once; max_tokens: of one of them; pages: of the pool, shared; rows: of a step's
+        packed batch; rope: a RopeSpec by which Queries and Keys are turned at their positions, or None; norm:
+        whether they are divided by their rows' root mean square first; tpf, frames, sink: the mask (default:
+        causal)."""
+        self.ctx, self.rope, self.norm, self.eps = ctx, rope, norm, eps
+        self.mask = dict(tpf=tpf, frames=frames, sink=sink)
+        dev = device or torch.device("cuda", torch.cuda.current_device())
+        self.table = PageTable.empty(batch, -(-max_tokens // page), page, pages, dev)
+        self.pools = [PagePool.empty(bits, page, pages, kv_heads, dev) for _ in range(layers)]
+        i32, i64 = dict(dtype=torch.int32, device=dev), dict(dtype=torch.int64, device=dev)
+        self.first, self.granted = torch.zeros(batch, **i32), torch.zeros(batch, **i32)
+        self.slot, self.at = torch.full((rows,), -1, **i64), torch.full((rows,), -1, **i64)
+        self._zero = torch.zeros(1, **i64)
+
+    def begin(self, count: torch.Tensor, keep: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """Shorten every sequence to keep [batch] (int64) tokens, then append count [batch] (int32) new ones: their
+        rows of the packed batch follow one another.  Returns how many each was given: its count, or 0 where the
+        pages do not suffice (its rows are then left out of the step)."""
+        qwm_pages_update(self.ctx, self.table, self.first, self.granted, self.slot, self.at, count=count, keep=keep,
+                         stream=stream)
+        return self.granted
+
+    def _ready(self, q: torch.Tensor, weight, stream) -> torch.Tensor:
+        """The Queries normed and turned, as the Keys are while they are stored."""
+        if not self.norm and self.rope is None:
+            return q
+        h, n, d = q.shape
+        out = torch.empty(n, h, d, dtype=torch.bfloat16, device=q.device).permute(1, 0, 2)
+        if self.norm:
+            qwm_norm_rope(self.ctx, self.rope, q[None], weight, self.eps, out[None],
+                          at=self.at[None] if self.rope is not None else None, stream=stream)
+        else:
+            gh, gw = self.rope.grid_h, self.rope.grid_w
+            t, y, x = self.at // (gh * gw), self.at // gw % gh, self.at % gw
+            qwm_rope(self.ctx, self.rope, q[None], self._zero, out[None], pos=torch.stack([t, y, x], -1)[None].to(torch.int32),
+                     stream=stream)
+        return out
+
+    def layer(self, i: int, q, k, v, q_weight=None, k_weight=None, out=None, lse=None, merge: bool = False,
+              max_count: int | None = None, scale: float | None = None, stream=None) -> torch.Tensor:
+        """Layer i: q [H][rows][d] attends, k and v [kv_heads][rows][d] are stored.  q_weight, k_weight: of the norms
+        (fp32 [d] or one per head, None: ones); out: bf16 (default: a new one, padding rows 0) or fp32; lse and
+        merge as qwm_paged_attend's; max_count: the largest count of the step, where it is known."""
+        if not self.norm and (q_weight is not None or k_weight is not None):
+            raise ValueError("weights of norms that this batch does not form")
+        main = stream if stream is not None else torch.cuda.current_stream(q.device)
+        with torch.cuda.stream(main):
+            qwm_paged_write(self.ctx, self.pools[i], k, v, self.slot, at=self.at if self.rope is not None else None,
+                            rope=self.rope, norm=self.norm, weight=k_weight, eps=self.eps, stream=main)
+            q = self._ready(q, q_weight, main)
+            if out is None:
+                out = torch.zeros_like(q, dtype=torch.bfloat16)
+            qwm_paged_attend(self.ctx, self.pools[i], self.table, q, self.first, self.granted,
+                             1.0 / math.sqrt(q.shape[2]) if scale is None else scale, out, lse=lse, merge=merge,
+                             max_count=max_count, stream=main, **self.mask)
+        return out
+
+    def check(self, stream=None) -> int:
+        return qwm_sync_status(self.ctx, stream)
+
+    def nbytes(self) -> int:
+        return sum(p.nbytes() for p in self.pools)

@@ -16,8 +16,8 @@
  * Conventions as in qwm_window.h, and further:
  *  - A packed batch holds the step's new tokens of all sequences in n rows: Queries, Keys and Values are
  *    [heads][n][128] with the channels contiguous and the other strides given (qwm_strides; `batch` is not
- *    looked at).  Sequence b has rows first[b] .. first[b] + count[b] - 1, sequences in any order; rows of no
- *    sequence are padding and left as they were.
+ *    looked at).  Sequence b has rows first[b] .. first[b] + count[b] - 1, sequences in any order and without
+ *    rows in common; rows of no sequence are padding and left as they were.
  *  - One page table serves the pools of all layers (the same pages of each).
  *  - Everything that changes from step to step is read on the device, so a captured step can be replayed.
  */

@@ -51,7 +51,7 @@ def f64(t):
 
 
 def ints(v, dtype=torch.int64):
-    return torch.tensor(v, dtype=dtype, device="cuda")
+    return v if isinstance(v, torch.Tensor) else torch.tensor(v, dtype=dtype, device="cuda")
 
 
 def status(qwm, ctx):
@@ -424,3 +424,296 @@ def test_attend(qwm, case, known):
         mine[f:f + c] = True
     left = torch.from_numpy(~mine).cuda()
     assert bool((out[:, left] == 5).all()) and bool((lse[:, left] == 5).all())
+
+
+def gpu_check(batch, q, out, lse, first, counts, H, tpf=1, frames=ALL, sink=0, out_eps=2.0 ** -8, parts=0.0):
+    """check() with the reference on the GPU in 64 bits, for larger calls."""
+    kv = batch.pool.kv_heads
+    for b, c in enumerate(counts):
+        n, f = batch.lengths[b], first[b]
+        if c <= 0:
+            continue
+        k, v = (torch.from_numpy(x[b]).cuda().repeat_interleave(H // kv, 0) for x in (batch.k, batch.v))
+        j = torch.arange(n, device="cuda")
+        fq = ((torch.arange(c, device="cuda") + n - c) // tpf)[:, None]
+        see = (j // tpf <= fq) & ((fq - j // tpf < frames) | (j < sink))
+        qq = q[:, f:f + c].double()
+        x = (qq @ k.transpose(1, 2) * (SCALE * math.log2(math.e))).masked_fill(~see, -math.inf)
+        m = x.amax(-1, keepdim=True)
+        w = torch.exp2(x - m)
+        wl = (m + torch.log2(w.sum(-1, keepdim=True)))[..., 0]
+        w = w / w.sum(-1, keepdim=True)
+        want, spread = w @ v, w @ v.abs()
+        mag = (qq.abs() @ k.abs().transpose(1, 2)).amax(-1) * SCALE * math.log2(math.e)
+        eps = (2.0 ** -11 + 2.0 ** -16 * mag + 2.0 ** -20 + parts)[..., None]
+        bound = 2 * eps * spread + n * 2.0 ** -32 * v.abs().max() * 2 + out_eps * want.abs()
+        assert bool(((out[:, f:f + c].double() - want).abs() <= bound).all()), b
+        d = (lse[:, f:f + c].double() - wl).abs()
+        assert bool((d <= 2.0 ** -16 * mag + 2.0 ** -20 + 2.0 ** -22 * wl.abs()).all()), b
+
+
+def attend(qwm, batch, q, first, counts, H, **kw):
+    out = kw.pop("out", None)
+    if out is None:
+        out = torch.zeros(q.shape[1], H, 128, dtype=kw.pop("dtype", torch.bfloat16), device="cuda").permute(1, 0, 2)
+    lse = kw.pop("lse", None)
+    if lse is None:
+        lse = torch.zeros(H, q.shape[1], dtype=torch.float32, device="cuda")
+    qwm.qwm_paged_attend(ctx_of(qwm, H), kw.pop("pool", batch.pool), batch.tab, q, ints(first, torch.int32), ints(counts, torch.int32), SCALE, out, lse=lse,
+                         **kw)
+    return out, lse
+
+
+@pytest.mark.parametrize("bits,page,lengths,counts,H,kv", [
+    (8, 64, [2000, 1300, 700], [2000, 1300, 700], 8, 2), (4, 16, [9000], [1100], 4, 4), (8, 128, [3000], [40], 40, 1), (4, 64, [2500, 30], [1, 2], 40, 1),
+    (8, 16, [150_000], [1], 2, 1), (4, 256, [120_001], [9], 2, 2), (8, 32, [70_000], [65], 4, 2)])
+def test_attend_larger(qwm, bits, page, lengths, counts, H, kv):
+    """Prompts from nothing, few items over long sequences (joined parts), and more heads than the warp tiles take."""
+    rng = np.random.default_rng(H + page)
+    batch = Batch(qwm, rng, bits, page, kv, lengths)
+    first, n = starts(counts)
+    q = rows(rng, H, n)
+    out, lse = attend(qwm, batch, q, first, counts, H, max_count=max(counts))
+    gpu_check(batch, q, out, lse, first, counts, H)
+    for _ in range(2):   # nothing depends on the order in which CTAs run
+        again, lse2 = attend(qwm, batch, q, first, counts, H, max_count=max(counts))
+        assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("batch_size", [257, 600])
+@pytest.mark.parametrize("chunk", [0, 90])
+def test_attend_many_sequences(qwm, batch_size, chunk):
+    rng = np.random.default_rng(batch_size + chunk)
+    lengths = [int(rng.integers(0, 60)) for _ in range(batch_size)]
+    counts = [min(n, int(rng.choice([0, 1, 1, 2]))) for n in lengths]
+    for i in (3, 255, batch_size - 1):
+        lengths[i] = 300
+        counts[i] = chunk or 1
+    b = Batch(qwm, rng, 8, 16, 2, lengths)
+    first, n = starts(counts, gap=1)
+    q = rows(rng, 4, n)
+    out, lse = attend(qwm, b, q, first, counts, 4, max_count=max(counts))
+    gpu_check(b, q, out, lse, first, counts, 4)
+
+
+@pytest.mark.parametrize("counts", [[1, 3], [1, 150]])
+def test_attend_fp32_and_merge(qwm, counts):
+    """A sequence attended in two parts, its first pages and the rest, is the sequence attended at once; rows that see
+    nothing of a part stay as they were, and rows that see nothing at all are 0 and -inf."""
+    rng = np.random.default_rng(5)
+    H, kv, page = 4, 2, 32
+    lengths = [300, 400]
+    b = Batch(qwm, rng, 8, page, kv, lengths)
+    first, n = starts(counts)
+    q = rows(rng, H, n)
+    whole, wl = attend(qwm, b, q, first, counts, H, dtype=torch.float32)
+    gpu_check(b, q, whole, wl, first, counts, H, out_eps=2.0 ** -22)
+    near, nl = attend(qwm, b, q, first, counts, H, dtype=torch.float32, frames=64)
+    far, fl = attend(qwm, b, q, first, counts, H, dtype=torch.float32)
+    # the same Queries over the tokens that the window left out, row by row (64-bit weights of the two parts)
+    back = torch.exp2(nl.double() - wl.double())
+    rest = (whole.double() - near.double() * back[..., None]) / (1 - back)[..., None]
+    rl = wl.double() + torch.log2(1 - back)
+    out, lse = rest.float().contiguous(), rl.float().contiguous()
+    out, lse = attend(qwm, b, q, first, counts, H, out=out, lse=lse, merge=True, frames=64)
+    assert float((out - whole).abs().max()) <= 2.0 ** -9 * float(whole.abs().max())
+    assert float((lse - wl).abs().max()) <= 2.0 ** -14
+    # nothing there yet: merged into (0, -inf) it is the result itself
+    out, lse = attend(qwm, b, q, first, counts, H, out=torch.zeros_like(whole), lse=torch.full_like(wl, -math.inf), merge=True)
+    assert torch.equal(lse, wl) and float((out - whole).abs().max()) <= 2.0 ** -22 * float(whole.abs().max())
+    assert torch.equal(far, whole) and torch.equal(fl, wl)
+
+
+@pytest.mark.parametrize("count", [2, 100])
+def test_attend_growing_logits_and_query_magnitudes(qwm, count):
+    """Keys that grow along the sequence raise the running maximum again and again; Queries of any magnitude, and one
+    beyond the fp16 range, which is recorded."""
+    rng = np.random.default_rng(8)
+    b = Batch(qwm, rng, 8, 64, 1, [600], k_scale=6.0)
+    q = rows(rng, 1, count, outliers=False)
+    for scale in (1.0, 2.0 ** -20, 2.0 ** -100, 0.0):
+        x = (q.double() * scale).to(torch.bfloat16)
+        out, lse = attend(qwm, b, x, [0], [count], 1)
+        assert status(qwm, ctx_of(qwm, 1)) == qwm.QWM_OK
+        gpu_check(b, x, out, lse, [0], [count], 1)
+    x = q.clone()
+    x[0, 1, 5] = 2.0 ** 17
+    attend(qwm, b, x, [0], [count], 1)
+    assert status(qwm, ctx_of(qwm, 1)) == qwm.QWM_ERR_RANGE
+
+
+@pytest.mark.parametrize("most", [4, 70])
+def test_attend_sequences_left_out(qwm, most):
+    """A sequence whose rows begin outside the batch, that has fewer tokens than rows, more rows than was said, or more
+    tokens than its pages hold is left out; rows at the batch's end are cut off."""
+    rng = np.random.default_rng(2)
+    lengths = [100] * 7
+    b = Batch(qwm, rng, 8, 16, 2, lengths)
+    q = rows(rng, 2, 30)
+    want, wl = attend(qwm, b, q, [-1, -1, 4, -1, -1, -1, 28], [0, 0, most // 2, 0, 0, 0, 2], 2, max_count=most)
+    b.tab.length[3] = 2
+    out, lse = attend(qwm, b, q, [-1, 30, 4, 8, 12, 16, 28], [3, 2, most // 2, 3, 0, -7, most // 2], 2, max_count=most)
+    assert status(qwm, ctx_of(qwm, 2)) == qwm.QWM_OK
+    # (the last two rows are claimed by sequence 6 and, of 35 rows, by sequence 2)
+    assert torch.equal(out[:, :28], want[:, :28]) and torch.equal(lse[:, :28], wl[:, :28])
+    for b_, first, counts, err in ((0, 0, most + 1, qwm.QWM_ERR_RANGE), (1, 2, 1, qwm.QWM_ERR_RANGE)):
+        f, c = [0] * 7, [0] * 7
+        f[b_], c[b_] = first, counts
+        if b_ == 1:
+            b.tab.length[1] = b.tab.table.shape[1] * 16 + 1
+        out, lse = attend(qwm, b, q, f, c, 2, max_count=most)
+        assert status(qwm, ctx_of(qwm, 2)) == err
+        assert not out.any() and not lse.any()
+
+
+@pytest.mark.parametrize("counts", [[1, 1], [1, 80]])
+def test_attend_page_outside_the_pool_is_recorded(qwm, counts):
+    rng = np.random.default_rng(3)
+    b = Batch(qwm, rng, 8, 32, 2, [200, 300])
+    first, n = starts(counts)
+    q = rows(rng, 2, n)
+    want, wl = attend(qwm, b, q, first, counts, 2)
+    b.tab.table[0, 2] = b.pool.k_codes.shape[0]
+    b.tab.table[0, 1] = -1
+    out, lse = attend(qwm, b, q, first, counts, 2)
+    assert status(qwm, ctx_of(qwm, 2)) == qwm.QWM_ERR_RANGE
+    assert torch.equal(out[:, first[1]:], want[:, first[1]:]) and torch.equal(lse[:, first[1]:], wl[:, first[1]:])
+
+
+def test_attend_layouts_and_workspace(qwm):
+    rng = np.random.default_rng(4)
+    counts = [40, 1, 3]
+    b = Batch(qwm, rng, 4, 64, 2, [500, 90, 128])
+    first, n = starts(counts)
+    q = rows(rng, 4, n)
+    want, wl = attend(qwm, b, q, first, counts, 4)
+    for layout in ("head", "padded"):
+        x = q.contiguous() if layout == "head" else torch.cat([q, torch.full_like(q[..., :32], 9.0)], -1)[..., :128]
+        out = torch.zeros(4, n, 160, dtype=torch.bfloat16, device="cuda")[..., :128]
+        out, lse = attend(qwm, b, x, first, counts, 4, out=out)
+        assert torch.equal(out, want) and torch.equal(lse, wl)
+    need = qwm.qwm_paged_attend_workspace(ctx_of(qwm, 4), b.pool, 40)
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
+    out, lse = attend(qwm, b, q, first, counts, 4, max_count=40, ws=ws)
+    assert torch.equal(out, want) and torch.equal(lse, wl)
+    with pytest.raises(qwm.QwmError):
+        attend(qwm, b, q, first, counts, 4, max_count=40, ws=ws[:need - 16])
+
+
+@pytest.mark.parametrize("counts", [[1, 2, 1], [1, 100, 33]])
+def test_two_calls_at_once_and_a_replayed_one(qwm, counts):
+    """Calls on two streams, each with its workspace, and one replayed from a graph beside them."""
+    rng = np.random.default_rng(6)
+    b = Batch(qwm, rng, 8, 64, 2, [700, 900, 400])
+    first, n = starts(counts)
+    qs = [rows(rng, 8, n) for _ in range(3)]
+    want = [attend(qwm, b, q, first, counts, 8) for q in qs]
+    outs = [torch.zeros(8, n, 128, dtype=torch.bfloat16, device="cuda") for _ in qs]
+    lses = [torch.zeros(8, n, dtype=torch.float32, device="cuda") for _ in qs]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    g = torch.cuda.CUDAGraph()
+    first, counts = ints(first, torch.int32), ints(counts, torch.int32)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        attend(qwm, b, qs[2], first, counts, 8, out=outs[2], lse=lses[2])
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            attend(qwm, b, qs[i], first, counts, 8, out=outs[i], lse=lses[i], stream=s)
+        g.replay()
+    torch.cuda.synchronize()
+    for (w, wl), o, l in zip(want, outs, lses):
+        assert torch.equal(o, w) and torch.equal(l, wl)
+
+
+# ------------------------------------------------------------------ runs of them together
+
+
+
+
+@pytest.mark.parametrize("norm,rope", [(True, "text"), (True, None), (False, "video"), (False, None)])
+@pytest.mark.parametrize("graph", [False, True])
+def test_paged_batch(qwm, norm, rope, graph):
+    """Sequences that come, grow by prompts, drafts and single tokens, lose drafts and end, through two layers, eager
+    or in one captured step replayed; Keys and Values checked through what the pages stand for, outputs against
+    64 bits."""
+    from bit_kv_cache_qsac_gb300.stream import PagedBatch
+    rng = np.random.default_rng(11)
+    H, kv, B, rows_, page = 4, 2, 5, 96, 16
+    kw = SPECS[rope] if rope else None
+    spec = qwm.RopeSpec(**kw) if kw else None
+    ctx = ctx_of(qwm, H)
+    pb = PagedBatch(ctx, 2, kv, B, 200, 40, rows_, page=page, bits=8, rope=spec, norm=norm)
+    wq, wk = (torch.from_numpy(rng.uniform(0.5, 1.5, (128,)).astype(np.float32)).cuda() if norm else None for _ in range(2))
+    count, keep = ints([0] * B, torch.int32), ints([2 ** 40] * B)
+    q, k, v = ([torch.zeros(h, rows_, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2)] for h in (H, kv, kv))
+    outs = [torch.zeros(H, rows_, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    lses = [torch.zeros(H, rows_, dtype=torch.float32, device="cuda") for _ in range(2)]
+
+    def step():
+        pb.begin(count, keep)
+        for i in range(2):
+            pb.layer(i, q[i], k[i], v[i], wq, wk, out=outs[i], lse=lses[i])
+
+    step()   # (nothing in it yet)
+    if graph:
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step()
+    ref_pages = paged_ref.Pages(B, -(-200 // page), page, 40)
+    stored = [[[] for _ in range(B)] for _ in range(2)]   # per layer and sequence: bf16 (k, v) rows as they came
+    plan = [([40, 0, 17, 1, 0], None), ([1, 30, 3, 1, 0], None), ([1, 2, 1, 40, 40], [None, None, 18, None, None]),
+            ([1, 1, 0, 60, 1], [30, 0, None, None, None]), ([1, 1, 1, 90, 1], [None] * 5)]
+    for counts, keeps in plan:
+        count.copy_(ints(counts, torch.int32))
+        keeps = [2 ** 40 if x is None else x for x in (keeps or [None] * B)]
+        keep.copy_(ints(keeps))
+        for i in range(2):
+            q[i].copy_(rows(rng, H, rows_))
+            k[i].copy_(rows(rng, kv, rows_))
+            v[i].copy_(rows(rng, kv, rows_))
+        g.replay() if graph else step()
+        first, granted, slot, at = ref_pages.update(keeps, counts, rows_)
+        assert pb.granted.tolist() == granted and pb.table.length.tolist() == ref_pages.length
+        assert pb.check() == qwm.QWM_OK
+        for i in range(2):
+            for b in range(B):
+                old = stored[i][b][:max(0, min(len(stored[i][b]), keeps[b]))]
+                new = [(k[i][:, first[b] + t].clone(), v[i][:, first[b] + t].clone()) for t in range(granted[b])]
+                stored[i][b] = old + new
+                n = ref_pages.length[b]
+                assert len(stored[i][b]) == n
+                if n == 0:
+                    continue
+                slots = ints([ref_pages.rows[b][t // page] * page + t % page for t in range(n)])
+                hats = [torch.empty(kv, n, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+                qwm.qwm_paged_read(ctx, pb.pools[i], slots, *hats)
+                # what is stored is the norm and rotation of what came, within half a step of the 8-bit codes
+                for j in range(kv):
+                    x = f64(torch.stack([r[0][j] for r in stored[i][b]]))
+                    y = paged_ref.norm(x, f64(wk), 1e-6) if norm else x
+                    want = turned(y, kw, ref.grid_positions(0, n, *kw.get("grid", (1, 1)))) if kw else y
+                    grp = np.repeat(np.abs(want).reshape(n, 4, 32).max(-1), 32, 1)
+                    # the step is within 1/8 of the largest over 127; bf16 before and after the codes
+                    assert np.all(np.abs(f64(hats[0][j]) - want) <= grp * (1.125 / 127 / 2 + 2.0 ** -8) + 2.0 ** -8 * np.abs(want))
+                c = granted[b]
+                if not c:
+                    continue
+                qq = f64(q[i][:, first[b]:first[b] + c])
+                if norm:
+                    qq = paged_ref.norm(qq, f64(wq), 1e-6)
+                if kw:
+                    pos = ref.grid_positions(n - c, c, *kw.get("grid", (1, 1)))
+                    qq = np.stack([turned(x, kw, pos) for x in qq])
+                pool = {t: getattr(pb.pools[i], t).cpu().numpy() for t in ("k_codes", "k_step", "v_codes", "v_step")}
+                s = slots.cpu().numpy()
+                for h in range(H):
+                    take = lambda t: pool[t][s // page, h // 2, s % page]
+                    kh, vh = (ref.values(take(x + "_codes"), take(x + "_step"), 8) for x in "kv")
+                    want, wl, mag, spread = ref.attend(qq[h], kh, vh, np.arange(n), n - c, 1, ALL, 0, SCALE)
+                    # Queries enter in bf16 (2^-8 of their logits' magnitudes), see check() for the rest
+                    eps = (2.0 ** -11 + (2.0 ** -8 + 2.0 ** -16) * mag + 2.0 ** -20)[:, None]
+                    got = f64(outs[i][h, first[b]:first[b] + c])
+                    assert np.all(np.abs(got - want) <= 2 * eps * spread + 2.0 ** -8 * np.abs(want) + 2.0 ** -20)
+                    d = np.abs(lses[i][h, first[b]:first[b] + c].double().cpu().numpy() - wl)
+                    assert np.all(d <= 2.0 ** -8 * mag + 2.0 ** -16 * mag + 2.0 ** -18)
