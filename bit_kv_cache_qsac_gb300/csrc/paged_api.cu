@@ -55,7 +55,8 @@ qwm_status check_norm(const float *weight, int32_t per_head, float eps) {
   return aligned16(weight) ? QWM_OK : QWM_ERR_ALIGN;
 }
 
-constexpr int64_t kMaxRows = (int64_t)1 << 30;   // rows of a Key head in a packed batch
+constexpr int64_t kMaxRows = (int64_t)1 << 30;      // rows of a Key head in a packed batch
+constexpr int64_t kMaxAllRows = (int64_t)1 << 36;   // of all heads: items are numbered in 32 bits
 
 // How a call is run and what workspace it takes.  Sequences with up to `few` rows per Key head go to the warp tiles,
 // which read the cache once per 8 or 16 rows, others to the tensor-memory tiles, which pay for 256 or 512.
@@ -197,7 +198,7 @@ qwm_status qwm_paged_attend(qwm_ctx *ctx, const qwm_page_pool *pool, const qwm_p
   if (s != QWM_OK) return s;
   if (n < 0 || tab->page != pool->page || tpf < 1 || frames < 1 || sink < 0) return QWM_ERR_ARG;
   const int H = ctx->cfg.heads, group = H / pool->kv_heads;
-  if (n > kMaxTokens || n * group > kMaxRows || tpf > ((int64_t)1 << 31) || frames > ((int64_t)1 << 31)) return QWM_ERR_SHAPE;
+  if (n > kMaxTokens || n * group > kMaxRows || n * H > kMaxAllRows || tpf > ((int64_t)1 << 31) || frames > ((int64_t)1 << 31)) return QWM_ERR_SHAPE;
   if (!(softmax_scale > 0.f) || softmax_scale > 0x1p123f) return QWM_ERR_ARG;   // (times 16 log2(e) it stays finite)
   if ((out_f32 != 0 && out_f32 != 1) || (merge != 0 && merge != 1)) return QWM_ERR_ARG;
   if (merge && (!out_f32 || !lse)) return QWM_ERR_ARG;

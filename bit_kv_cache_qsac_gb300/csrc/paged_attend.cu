@@ -16,9 +16,9 @@
 //                   pieces they write the output and fetch the next Queries;
 //   warp 8          allocates TMEM; in the even CTA it issues every MMA of the pair, in the odd one it
 //                   passes on to the even one that its producers have filled a stage;
-//   others          producers (9-11: Keys, 13-15: Values): codes two stages ahead in registers, table entries three, decoded into swizzled
-//                   stages; they run ahead into the next piece while the last one is written;
-//   warp 12         walks along the share and describes its pieces to the others, two ahead.
+//   warp 12         walks along the share and describes its pieces to the others, one ahead;
+//   others          producers (9-11: Keys, 13-15: Values): codes two stages ahead in registers, table entries three,
+//                   decoded into swizzled stages; they run ahead into the next piece while the last one is written.
 // (No producer shares a scheduler with warp 8, whose instructions would have to be fetched again and again.)
 // An item with up to 256 rows gives both tiles those rows and every other 64 keys each, joined at the end.
 // TMEM (512 columns): S_x as two buffers of 64 keys, P_x over them, O_x.  Keys arrive in stages of 128, decoded

@@ -196,3 +196,10 @@ def test_reference_pages_are_kept_apart():
         assert all(len(r) == -(-n // 16) <= 5 for r, n in zip(ref.rows, ref.length))
         live = [s for s in slot if s >= 0]
         assert len(live) == len(set(live)) == sum(granted)
+
+
+def test_attend_refuses_more_rows_than_items_can_number(qwm):
+    many, pool = _ctx(qwm, heads=1 << 17), _pool(qwm, kv_heads=1 << 15)
+    wide = _st(qwm, token=128 << 17)
+    assert _attend(qwm, ctx=many, pool=pool, qs=wide, os=wide, n=(1 << 19) + 1) == qwm.QWM_ERR_SHAPE
+    assert _attend(qwm, ctx=many, pool=pool, qs=wide, os=wide, n=1 << 19, ws=None) == qwm.QWM_ERR_ARG   # (the next check's)
