@@ -42,7 +42,7 @@ static_assert(kRows == 2 * NQT * BM, "");
 
 // What pieces of an item cost, in hundreds of cycles: a stage of 128 keys for two tiles of rows, for one, and starting
 // and ending; the least piece (stages) worth its own start, and the shortest share.
-constexpr int kStageCost = 25, kBriefCost = 14, kStartCost = 110, kLeast = 3, kThin = 220;
+constexpr int kStageCost = 25, kBriefCost = 14, kStartCost = 110, kLeast = 3, kThin = 100;
 
 // shared-memory map of one CTA (bytes from a 1024-aligned base)
 constexpr int kBlk = BM * 128;             // a [128 rows][64 fp16] swizzled block
@@ -151,11 +151,14 @@ __device__ __noinline__ Place walk(const PagedAttend &a, const int *starts, int 
 }
 
 // The cuts of share `share` (begin, end) in the line of all items: by sequence, Key head and block of rows.  Found by
-// the whole CTA, each thread taking neighbouring blocks of rows: P, the running sum of the blocks' costs for one Key
-// head, finds first the sequence (whose heads take kv_heads equal pieces of the line), then the head and the block.
-// starts: shared memory for batch + 1 numbers.  A share without work begins and ends at sequence `batch`.
-__device__ __forceinline__ void find_cuts(const PagedAttend &a, int share, int *starts, PagedCut (&cut)[2]) {
+// the whole CTA: P, the running sum of the blocks' costs for one Key head, finds first the sequence (whose heads take
+// kv_heads equal pieces of the line), then the head and the block.  Up to 512 blocks of rows are one a thread, with P
+// in shared memory (5,000 cycles less than the walks); more are neighbours of a thread, walked along for each answer.
+// mem: shared memory.  A share without work begins and ends at sequence `batch`.
+__device__ __forceinline__ void find_cuts(const PagedAttend &a, int share, unsigned char *mem, PagedCut (&cut)[2]) {
   constexpr int kW = kThreads / 32;
+  int *starts = (int *)mem;                                                          // [batch + 1]
+  int64_t *sum = (int64_t *)(mem + (kPagedMaxBatch + 2) * (int)sizeof(int));   // [blocks + 1], up to 512 blocks
   __shared__ int64_t sums[kW];
   __shared__ int64_t edge[2][2];   // P at the begin and the end of the cuts' sequences
   __shared__ int where[2];         // the cuts' sequences
@@ -195,17 +198,67 @@ __device__ __forceinline__ void find_cuts(const PagedAttend &a, int share, int *
   }
   if (tid == 0) starts[a.batch] = R;
   __syncthreads();
-  const int per = (R + kThreads - 1) / kThreads, f0 = tid * per < R ? tid * per : R, f1 = f0 + per < R ? f0 + per : R;
-  int64_t all;
-  const int64_t mine = walk(a, starts, f0, f1, 0, INT64_MAX, -1).P, before = scan(mine, all);
   const int kv = a.pool.kv_heads;
-  int64_t used = win::quotient(all * kv, kThin);
-  used = used < 1 ? 1 : (used < a.shares ? used : a.shares);
-  if (share >= used || all == 0) return;   // (the same for the whole CTA)
-  int64_t x[2];
+  int64_t x[2];   // the cuts' places
+  auto places = [&](int64_t all) -> bool {   // false: no work (the same for the whole CTA)
+    int64_t used = win::quotient(all * kv, kThin);
+    used = used < 1 ? 1 : (used < a.shares ? used : a.shares);
+    if (share >= used || all == 0) return false;
+#pragma unroll 1
+    for (int e = 0; e < 2; e++) x[e] = win::quotient(all * kv * (share + e), used);
+    return true;
+  };
+  // cut e, at z of block p's running sums, in Key head kvh
+  auto put = [&](int e, const Place &p, int kvh, int64_t z) {
+    int item = kvh * (starts[p.b + 1] - starts[p.b]) + p.ib;
+    int block = pgd::cut_item(z - p.P, p.blocks, kStartCost, p.each, kLeast);
+    if (block == p.blocks && block > 0) {
+      item++;
+      block = 0;
+    }
+    cut[e] = PagedCut{p.b, item, block, 0, 0, 0, 0};
+  };
+  int64_t all;
+  if (R <= kThreads) {
+    Place p = {};
+    int64_t cost = 0;
+    if (tid < R) {
+      int hi = a.batch;   // starts[p.b] <= tid < starts[hi]
+      while (hi - p.b > 1) {
+        const int mid = (p.b + hi) >> 1;
+        if (starts[mid] <= tid) p.b = mid;
+        else hi = mid;
+      }
+      const pgd::Seq q = pgd::sequence(a, p.b);
+      pgd::Keys keys;
+      p.ib = tid - starts[p.b];
+      p.blocks = Work::blocks_of(a, q, p.ib, keys);
+      p.each = Work::each(q, p.ib);
+      cost = p.cost();
+    }
+    p.P = scan(cost, all);
+    if (!places(all)) return;
+    if (tid < R) sum[tid] = p.P;
+    if (tid == 0) sum[R] = all;
+#pragma unroll 1
+    for (int e = 0; e < 2; e++)
+      if (x[e] >= kv * p.P && x[e] < kv * (p.P + cost)) where[e] = p.b;
+    __syncthreads();
+#pragma unroll 1
+    for (int e = 0; e < 2; e++) {
+      if (where[e] < 0) continue;   // the line's end
+      const int64_t lo = sum[starts[where[e]]], head = sum[starts[where[e] + 1]] - lo, y = x[e] - kv * lo;
+      const int kvh = (int)win::quotient(y, head);
+      const int64_t z = lo + (y - kvh * head);
+      if (z >= p.P && z < p.P + cost) put(e, p, kvh, z);
+    }
+    return;
+  }
+  const int per = (R + kThreads - 1) / kThreads, f0 = tid * per < R ? tid * per : R, f1 = f0 + per < R ? f0 + per : R;
+  const int64_t mine = walk(a, starts, f0, f1, 0, INT64_MAX, -1).P, before = scan(mine, all);
+  if (!places(all)) return;
 #pragma unroll 1
   for (int e = 0; e < 2; e++) {
-    x[e] = win::quotient(all * kv * (share + e), used);
     const int64_t X = win::quotient(x[e], kv);
     if (X >= before && X < before + mine) where[e] = walk(a, starts, f0, f1, before, X, -1).b;
   }
@@ -224,16 +277,7 @@ __device__ __forceinline__ void find_cuts(const PagedAttend &a, int share, int *
     const int64_t lo = edge[e][0], head = edge[e][1] - lo, y = x[e] - kv * lo;
     const int kvh = (int)win::quotient(y, head);
     const int64_t z = lo + (y - kvh * head);
-    if (z >= before && z < before + mine) {
-      const Place p = walk(a, starts, f0, f1, before, z, -1);
-      int item = kvh * (starts[p.b + 1] - starts[p.b]) + p.ib;
-      int block = pgd::cut_item(z - p.P, p.blocks, kStartCost, p.each, kLeast);
-      if (block == p.blocks && block > 0) {
-        item++;
-        block = 0;
-      }
-      cut[e] = PagedCut{p.b, item, block, 0, 0, 0, 0};
-    }
+    if (z >= before && z < before + mine) put(e, walk(a, starts, f0, f1, before, z, -1), kvh, z);
   }
 }
 
@@ -444,7 +488,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int share = (int)(blockIdx.x >> 1), cr = (int)tc::cluster_ctarank();
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the kernels behind this one may line up
-  find_cuts(a, share, (int *)(sm + OFF_K), cut);
+  find_cuts(a, share, sm + OFF_K, cut);
   __syncthreads();
   const PagedCut begin = cut[0], end = cut[1];
   if (begin.b == a.batch || (begin.b == end.b && begin.item == end.item && begin.block == end.block)) {   // both CTAs
@@ -479,9 +523,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc::tmem_relinquish2();
     tc::fence_before_sync();
   }
-  __syncthreads();
-  tc::cluster_sync();   // both CTAs' barriers exist, and their tensor memory
-  tc::fence_after_sync();
+  auto begun = [&]() {   // both CTAs' barriers exist, and their tensor memory (the planning warp has a piece by then)
+    __syncthreads();
+    tc::cluster_sync();
+    tc::fence_after_sync();
+  };
+  if (warp != kPlanWarp) begun();
   const uint32_t tmem = tmem_base_sh;
 
   // The share's piece number i is described in pieces[i & 1] (the whole warp; false: someone gave up), until this
@@ -907,6 +954,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         break;
       }
       more = !p.done;
+      if (pi == 0) begun();
       if (pi >= 2 && !__all_sync(0xffffffffu, tc::mbar_wait(&bars.heard[pi & 1], ((pi >> 1) - 1) & 1, kWaitNs))) {
         fail(a.status);
         break;

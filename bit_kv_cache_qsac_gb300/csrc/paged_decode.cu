@@ -312,16 +312,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) paged_decode_kernel
       if (8 * nt < rows) {
         if (nt) __syncthreads();
         tile.outputs(nt, rows, osm);
-        if (nt == NT - 1 || 8 * (nt + 1) >= rows) {   // the last of them: the registers take the next Queries
-          fetch(next);
-          if (warp == kWarps - 1) plan(pieces[then == 2 ? 0 : then + 1]);
-        }
+        if (nt == NT - 1 || 8 * (nt + 1) >= rows) fetch(next);   // the last of them: the registers take the next Queries
         __syncthreads();
         const int r = 8 * nt + warp, ch = 4 * lane;   // warp = row, lane = four channels
         if (r < rows) {
           float M, L;
           float4 acc = wt::join(msm, lsm, r, [&](int w) {
-            return *(const float4 *)(dyn + (size_t)(w * R::kStages + spare[w]) * R::kStage + (size_t)(warp * D + ch) * 4);
+            return tile.output((const float (*)[D])(dyn + (size_t)(w * R::kStages + spare[w]) * R::kStage), warp, lane);
           }, M, L);
           const float inv = L > 0.f ? win::kUnit<BITS> / L : 0.f, lse = L > 0.f ? M + log2f(L) : -INFINITY;
           acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
@@ -338,6 +335,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) paged_decode_kernel
         }
       }
     }
+    if (warp == kWarps - 1) plan(pieces[then == 2 ? 0 : then + 1]);   // (it has the fewest rows, too)
     __syncthreads();
     now = then;
   }
@@ -366,7 +364,13 @@ __device__ __forceinline__ void combine(const PagedAttend &a, int at, int part_r
     while (s - 1 + n < a.shares && same(a.cuts[s - 1 + n], c)) n++;
   auto place = [&](int k, int r) -> int64_t { return ((int64_t)(k == 0 ? 2 * (s - 1) + 1 : 2 * (s - 1 + k))) * part_rows + r; };
   float M[ROWS], mine[ROWS], L[ROWS];
-  float4 acc[ROWS];
+  float4 acc[ROWS], x[2][ROWS];   // the first two parts (there are no fewer) beside the log-sum-exps
+#pragma unroll
+  for (int k = 0; k < 2; k++) {
+#pragma unroll
+    for (int i = 0; i < ROWS; i++)
+      if (r0 + i < c.live) x[k][i] = __ldcg((const float4 *)(a.part + place(k, r0 + i) * D + 4 * lane));
+  }
 #pragma unroll
   for (int i = 0; i < ROWS; i++) mine[i] = lane < n && r0 + i < c.live ? a.part_lse[place(lane, r0 + i)] : -INFINITY;
 #pragma unroll
@@ -379,8 +383,23 @@ __device__ __forceinline__ void combine(const PagedAttend &a, int at, int part_r
     L[i] = 0.f;
     acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
+  auto add = [&](int i, float wt, const float4 &v) {
+    L[i] += wt;
+    acc[i].x = fmaf(v.x, wt, acc[i].x);
+    acc[i].y = fmaf(v.y, wt, acc[i].y);
+    acc[i].z = fmaf(v.z, wt, acc[i].z);
+    acc[i].w = fmaf(v.w, wt, acc[i].w);
+  };
+#pragma unroll
+  for (int k = 0; k < 2; k++) {
+#pragma unroll
+    for (int i = 0; i < ROWS; i++) {
+      const float wt = __shfl_sync(0xffffffffu, mine[i], k);
+      if (r0 + i < c.live) add(i, wt, x[k][i]);
+    }
+  }
 #pragma unroll 4
-  for (int k = 0; k < n; k++) {
+  for (int k = 2; k < n; k++) {
 #pragma unroll
     for (int i = 0; i < ROWS; i++) {
       if (r0 + i >= c.live) break;
@@ -389,12 +408,7 @@ __device__ __forceinline__ void combine(const PagedAttend &a, int at, int part_r
         const float l = a.part_lse[place(k, r0 + i)];
         wt = l == -INFINITY ? 0.f : exp2f(l - M[i]);
       }
-      const float4 x = *(const float4 *)(a.part + place(k, r0 + i) * D + 4 * lane);
-      L[i] += wt;
-      acc[i].x = fmaf(x.x, wt, acc[i].x);
-      acc[i].y = fmaf(x.y, wt, acc[i].y);
-      acc[i].z = fmaf(x.z, wt, acc[i].z);
-      acc[i].w = fmaf(x.w, wt, acc[i].w);
+      add(i, wt, *(const float4 *)(a.part + place(k, r0 + i) * D + 4 * lane));
     }
   }
 #pragma unroll

@@ -334,13 +334,20 @@ struct Tile {
         }
       }
   }
-  // The outputs of the nt-th eight rows, those of them below `rows`.
+  // The outputs of the nt-th eight rows, those of them below `rows`.  Pairs of channels are permuted by the row and the
+  // quarter of the row, so that a half warp's stores fall into different banks (in their own order 8 of 16 collide).
   __device__ __forceinline__ void outputs(int nt, int rows, float (*osm)[D]) const {
 #pragma unroll
     for (int i = 0; i < 8; i++) {
-      if (8 * nt + 2 * t < rows) *(float2 *)&osm[2 * t][16 * g + 2 * i] = make_float2(o[nt][i][0], o[nt][i][2]);
-      if (8 * nt + 2 * t + 1 < rows) *(float2 *)&osm[2 * t + 1][16 * g + 2 * i] = make_float2(o[nt][i][1], o[nt][i][3]);
+      const int c = 2 * ((8 * g + i) ^ (2 * t | (g >> 1 & 1)));
+      if (8 * nt + 2 * t < rows) *(float2 *)&osm[2 * t][c] = make_float2(o[nt][i][0], o[nt][i][2]);
+      if (8 * nt + 2 * t + 1 < rows) *(float2 *)&osm[2 * t + 1][c] = make_float2(o[nt][i][1], o[nt][i][3]);
     }
+  }
+  // Channels 4 lane .. 4 lane + 3 of row r of eight from there.
+  __device__ static __forceinline__ float4 output(const float (*osm)[D], int r, int lane) {
+    const float4 x = ((const float4 *)osm[r])[lane ^ (r >> 1)];
+    return lane & 8 ? make_float4(x.z, x.w, x.x, x.y) : x;
   }
 };
 

@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) window_decode_kerne
     const int r = 8 * nt + warp, ch = 4 * lane;   // warp = row, lane = four channels
     if (r < rows) {
       float M, L;
-      float4 acc = wt::join(msm, lsm, r, [&](int w) { return *(const float4 *)&osm[w][warp][ch]; }, M, L);
+      float4 acc = wt::join(msm, lsm, r, [&](int w) { return wt::Tile<BITS, NT>::output(osm[w], warp, lane); }, M, L);
       if (CLUSTER) {
         *(float4 *)&part_o[r][ch] = acc;
         if (lane == 0) part_ml[r] = make_float2(M, L);

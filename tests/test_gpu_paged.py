@@ -496,6 +496,21 @@ def test_attend_many_sequences(qwm, batch_size, chunk):
     gpu_check(b, q, out, lse, first, counts, 4)
 
 
+@pytest.mark.parametrize("batch_size", [500, 513, 1100])
+def test_attend_many_prompts(qwm, batch_size):
+    """Up to 512 blocks of rows are looked at in one go, more in turn; some are longer than a block and cut."""
+    rng = np.random.default_rng(batch_size)
+    lengths = [int(rng.integers(17, 80)) for _ in range(batch_size)]
+    counts = [int(rng.choice([17, 17, n])) for n in lengths]
+    for i in (7, batch_size // 2):
+        lengths[i], counts[i] = 900, 600
+    b = Batch(qwm, rng, 4, 16, 2, lengths)
+    first, n = starts(counts)
+    q = rows(rng, 4, n)
+    out, lse = attend(qwm, b, q, first, counts, 4, max_count=max(counts))
+    gpu_check(b, q, out, lse, first, counts, 4)
+
+
 @pytest.mark.parametrize("counts", [[1, 3], [1, 150]])
 def test_attend_fp32_and_merge(qwm, counts):
     """A sequence attended in two parts, its first pages and the rest, is the sequence attended at once; rows that see
