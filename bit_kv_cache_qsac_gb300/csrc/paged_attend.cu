@@ -595,7 +595,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int64_t ahead = step_i * a.qs.token + step_h * a.qs.head, wrap = a.qs.token - a.group * a.qs.head;
         uint32_t top = 0u, small = 0u;   // the largest magnitudes, a NaN above all; passes in which this piece is below 1
 #pragma unroll 1
-        for (int y = 0; y < NQT; y++) {
+        for (int y = 0; y < (p.brief ? 1 : NQT); y++) {   // (short items take tile 0's place alone)
           const int r = row_base + y * 2 * BM + rr0, i = (int)((uint32_t)r / (uint32_t)a.group);
           int h = r - i * a.group, left = rows - r < BM ? rows - r : BM;   // (may be negative)
           const uint16_t *src = qb + h * a.qs.head + i * a.qs.token;
@@ -794,7 +794,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t writes = __ballot_sync(0xffffffffu, write);
         const uint64_t mine_out = half ? (uint64_t)out.bf16 : (uint64_t)out.f32;
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
+        for (int c = 0; c < D && writes; c += 32) {
           uint32_t o[32];
           tc::tmem_ld32(tO + c, o);
           tc::tmem_ld_wait();
@@ -843,7 +843,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
           }
         }
-        if (half) {
+        if (half && writes) {
           __syncwarp();
 #pragma unroll 8
           for (int i = 0; i < 16; i++) {
