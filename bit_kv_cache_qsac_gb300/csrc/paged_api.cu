@@ -68,6 +68,9 @@ struct Plan {
   size_t bytes;
 };
 
+// Both sides of it measured, 40 heads, one sequence, 8 bits (4 bits): 32 rows over 500 / 5,000 / 30,000 tokens take 16 / 36 /
+// 136 us (15 / 33 / 116) on warp tiles and 23 / 47 / 149 (23 / 45 / 146) on the others; 64 rows 22 / 59 / 256 (22 / 52 / 215)
+// and 23 / 47 / 150 (23 / 45 / 146).
 constexpr int kFew = 32;
 
 Plan plan_of(const qwm_ctx *ctx, int group, int64_t max_count) {

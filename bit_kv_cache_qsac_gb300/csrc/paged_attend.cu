@@ -25,6 +25,12 @@
 // in 16 rows of one page at a time; step t issues P V of tile x's keys t, then Q K^T of keys t + 2 into the
 // buffer that frees.  Every wait is bounded (about one second); on expiry QWM_ERR_DEVICE_TIMEOUT is
 // recorded, every role stops, outstanding MMAs are drained and TMEM is freed.
+// Bound: the tensor pipe for long items; what stands around an item's loop for short ones.  Measured: 2,048 tokens over
+// 30,000 before them (8 bits, 32 heads on 8): 583 us = 1,780 TFLOP/s; 4,680 over 40,560 (4 bits, 40 heads): 2.2 ms =
+// 1,700 TFLOP/s (tensor pipe active in 78 and 80% of all cycles).  In cycles: 12,000 until the first piece is described
+// (7,500 for the cuts), 6,000 for its Queries, 3,300 (bf16) to 7,000 (parts) for writing it.  What was live across the
+// steps decided the rest: pieces read from shared memory where they are needed instead of kept in registers gave 751 ->
+// 698 us and 2,557 -> 2,420; multiply() written into the kernel's body instead of apart 785 -> 1,200.
 #include "paged.cuh"
 
 namespace {
@@ -41,7 +47,8 @@ constexpr int kRows = kPagedTileRows;       // rows of an item: 2 NQT BM
 static_assert(kRows == 2 * NQT * BM, "");
 
 // What pieces of an item cost, in hundreds of cycles: a stage of 128 keys for two tiles of rows, for one, and starting
-// and ending; the least piece (stages) worth its own start, and the shortest share.
+// and ending; the least piece (stages) worth its own start, and the shortest share (about an item of one stage: 64 rows
+// over 150 tokens take 21 us and 512 over 512 25; twice as long, so that two such items share a CTA pair, 27 and 35).
 constexpr int kStageCost = 25, kBriefCost = 14, kStartCost = 110, kLeast = 3, kThin = 100;
 
 // shared-memory map of one CTA (bytes from a 1024-aligned base)

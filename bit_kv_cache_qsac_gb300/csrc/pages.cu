@@ -5,7 +5,8 @@
 // follows from the sums, so that nothing depends on the order in which threads run.  Every CTA of a cluster
 // does the scans for itself (4,096 sequences at most, four a thread), and they share the rest: pages pushed,
 // pages popped, rows, with a cluster barrier between.  Bound: latency, each of the three being a search in
-// shared memory and one or two dependent accesses.
+// shared memory and one or two dependent accesses.  Measured: 64 sequences, a token each, 7.5 us; 256 prompts with 64,100
+// rows 11.5 (in one CTA 7.5 and 34).
 #include "paged.cuh"
 
 namespace {
@@ -62,7 +63,7 @@ __global__ void __launch_bounds__(kThreads) pages_update_kernel(const __grid_con
   extern __shared__ __align__(16) unsigned char raw[];
   Shared &sh = *(Shared *)raw;
   const int tid = threadIdx.x, rank = (int)tc::cluster_ctarank(), worker = rank * kThreads + tid;
-  const int workers = (int)gridDim.x * kThreads;
+  const int workers = kCluster * kThreads;
   const int per = (t.batch + kThreads - 1) / kThreads;   // sequences of a thread, neighbours
   const int64_t most = (int64_t)t.width << page_log2;
   auto pages_of = [&](int64_t tokens) -> int { return (int)((tokens + t.page - 1) >> page_log2); };
@@ -196,15 +197,14 @@ cudaError_t launch_pages_update(const qwm_page_table &t, int page_log2, const in
   static std::atomic<uint64_t> allowed{0};
   const cudaError_t e = allow_shared(pages_update_kernel, (int)sizeof(Shared), allowed);
   if (e != cudaSuccess) return e;
-  const unsigned ctas = n <= 2 * kThreads ? 1 : kCluster;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
+  cfg.gridDim = dim3(kCluster);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = sizeof(Shared);
   cfg.stream = st;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = ctas;
+  attr.val.clusterDim.x = kCluster;
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
