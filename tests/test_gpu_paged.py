@@ -496,6 +496,19 @@ def test_attend_many_sequences(qwm, batch_size, chunk):
     gpu_check(b, q, out, lse, first, counts, 4)
 
 
+@pytest.mark.parametrize("bits,page,lengths,counts,H,kv", [
+    (8, 32, [100, 50, 33], [1, 1, 1], 40, 1),      # a token's rows alone are too many for the few rows' kernel
+    (4, 64, [300, 20, 129], [1, 1, 0], 24, 1), (8, 16, [70, 600], [2, 1], 62, 2), (4, 16, [40, 300], [9, 30], 17, 1),
+    (8, 64, [500, 64], [1, 3], 600, 1)])           # ... and go over two blocks of rows
+def test_attend_wide_groups(qwm, bits, page, lengths, counts, H, kv):
+    rng = np.random.default_rng(H + kv)
+    b = Batch(qwm, rng, bits, page, kv, lengths)
+    first, n = starts(counts, gap=1)
+    q = rows(rng, H, n)
+    out, lse = attend(qwm, b, q, first, counts, H, max_count=max(counts))
+    gpu_check(b, q, out, lse, first, counts, H)
+
+
 @pytest.mark.parametrize("batch_size", [500, 513, 1100])
 def test_attend_many_prompts(qwm, batch_size):
     """Up to 512 blocks of rows are looked at in one go, more in turn; some are longer than a block and cut."""
