@@ -265,9 +265,11 @@ def qwm_paged_attend(ctx, pool: PagePool, tab: PageTable, q, first, count, softm
         key = (pool.bits, pool.k_codes.shape[1], most)   # all that the size depends on, beside the context
         need = ctx.paged_workspace.get(key)
         if need is None:
-            if len(ctx.paged_workspace) > 1000:
-                ctx.paged_workspace.clear()
-            need = ctx.paged_workspace[key] = _fast.qwm_paged_attend_workspace(ctx.handle, p, most)
+            need = _fast.qwm_paged_attend_workspace(ctx.handle, p, most)
+            if need:   # (0: a call that will be refused, for what the key does not hold)
+                if len(ctx.paged_workspace) > 1000:
+                    ctx.paged_workspace.clear()
+                ctx.paged_workspace[key] = need
         if stream is None:
             ws = torch.empty(need, dtype=_U8, device=dev)
         else:
