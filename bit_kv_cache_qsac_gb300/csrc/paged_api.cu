@@ -85,7 +85,9 @@ Plan plan_of(const qwm_ctx *ctx, int group, int64_t max_count) {
   p.shares_many = p.many_rows ? ctx->num_sms / 2 : 0;
   p.part_few = (size_t)2 * p.shares_few * 8 * p.row_tiles;
   p.part_many = (size_t)2 * p.shares_many * kPagedTileRows;
-  p.bytes = (p.part_few + p.part_many) * (QWM_D + 1) * sizeof(float) + (size_t)(p.shares_few + p.shares_many) * sizeof(PagedCut);
+  // (a place for the cuts of 8-row tiles in any case: what a count takes, smaller ones do not exceed)
+  const int cuts_few = p.few_rows ? paged_decode_shares(1, ctx->num_sms) : 0;
+  p.bytes = (p.part_few + p.part_many) * (QWM_D + 1) * sizeof(float) + (size_t)(cuts_few + p.shares_many) * sizeof(PagedCut);
   return p;
 }
 

@@ -61,3 +61,13 @@ def test_a_refused_call_leaves_later_ones_as_they_are(qwm, monkeypatch):
     for _ in range(2):
         call(32)
     assert lib.given[0] == 0 and lib.given[1] == lib.given[2] > 0
+
+
+@pytest.mark.parametrize("kv", [1, 2, 8])
+@pytest.mark.parametrize("group", [1, 3, 8, 16, 32, 33])
+def test_workspace_serves_smaller_counts(qwm, kv, group):
+    """The bytes for calls of up to max_count new tokens suffice for each smaller count."""
+    lib, ctx = qwm.raw_library(), _ctx(qwm, kv * group)
+    pool = qwm.qwm_page_pool(8, 64, 40, kv, *[0x7f00000000] * 4)
+    sizes = [lib.qwm_paged_attend_workspace(ctx, pool, c) for c in range(1, 80)] + [lib.qwm_paged_attend_workspace(ctx, pool, 1 << 24)]
+    assert sizes[0] > 0 and sizes == sorted(sizes)
