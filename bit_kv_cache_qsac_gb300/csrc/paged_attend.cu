@@ -671,7 +671,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       softmax_meet(false);   // the rows' powers
       const int power = (int)tc::lds32(powers + 4u * (uint32_t)((p.brief ? 0 : x * BM) + 32 * sub + lane));
-      const float sl2 = a.scale_log2 * win::power_of_two(-power) * win::kUnit<BITS>;
+      const float sl2 = win::logit_scale<BITS>(a.scale_log2, win::power_of_two(-power));
       const uint64_t sc2 = pk64(sl2, sl2);
       float m_used = -INFINITY;
       uint64_t acc = 0ull;   // the sum of the weights, each step's added as one: 1 / 64 of the additions to a large sum

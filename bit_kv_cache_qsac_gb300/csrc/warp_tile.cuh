@@ -136,7 +136,7 @@ struct Tile {
         }
 #pragma unroll
       for (int e = 0; e < 2; e++)
-        sl2[nt][e] = scale_log2 * __shfl_sync(0xffffffffu, back, 4 * (2 * t + e)) * win::kUnit<BITS>;
+        sl2[nt][e] = win::logit_scale<BITS>(scale_log2, __shfl_sync(0xffffffffu, back, 4 * (2 * t + e)));
     }
 
 #pragma unroll

@@ -419,6 +419,10 @@ __device__ __forceinline__ bool any_beyond_fp16(uint32_t m) { return ((m + 0x388
 // The power of two that a row of largest magnitude `top` (bf16, below 1) is multiplied by, and 2^k.
 __device__ __forceinline__ uint32_t row_power(uint32_t top) { return 141u - (top >> 7) < 120u ? 141u - (top >> 7) : 120u; }
 __device__ __forceinline__ float power_of_two(int k) { return __uint_as_float((uint32_t)(127 + k) << 23); }
+// The scale of a row's logits (log2 units), `back` taking its power of two back.  At least 2^-126: as 0 it would make a
+// masked key's -inf a NaN, and a logit, below 2^40 before it, is nothing next to 1 at either.
+template <int BITS>
+__device__ __forceinline__ float logit_scale(float scale_log2, float back) { return fmaxf(scale_log2 * back * kUnit<BITS>, 0x1p-126f); }
 __device__ __forceinline__ uint32_t larger_half(uint32_t m) { return (m & 0xFFFFu) > (m >> 16) ? m & 0xFFFFu : m >> 16; }
 
 // ------------------------------------------------------------------ weights

@@ -403,7 +403,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t tS0 = tmem + lane_addr + 128u * x, tO = tmem + lane_addr + 256u + 128u * x;
     const uint32_t p_ready0 = tc::mapa(tc::smem_u32(&bars.p_ready[x][0]), 0);
     const int power = (int)tc::lds32(powers + 4u * (uint32_t)((brief ? 0 : x * BM) + 32 * sub + lane));
-    const float sl2 = a.scale_log2 * win::power_of_two(-power) * win::kUnit<BITS>;
+    const float sl2 = win::logit_scale<BITS>(a.scale_log2, win::power_of_two(-power));
     const uint64_t sc2 = pk64(sl2, sl2);
     const int64_t w0 = row_base + (brief ? 0 : (int64_t)x * 2 * BM) + 32 * sub;   // this warp's first row
     const int mine_n = brief ? (steps + 1 - x) >> 1 : steps;   // steps of this tile
