@@ -50,6 +50,7 @@ static_assert(kRows == 2 * NQT * BM, "");
 // and ending; the least piece (stages) worth its own start, and the shortest share (about an item of one stage: 64 rows
 // over 150 tokens take 21 us and 512 over 512 25; twice as long, so that two such items share a CTA pair, 27 and 35).
 constexpr int kStageCost = 25, kBriefCost = 14, kStartCost = 110, kLeast = 3, kThin = 100;
+constexpr int kMost = kPagedPieceKeys / BN;   // stages of a piece
 
 // shared-memory map of one CTA (bytes from a 1024-aligned base)
 constexpr int kBlk = BM * 128;             // a [128 rows][64 fp16] swizzled block
@@ -63,7 +64,8 @@ constexpr int kSmemAlloc = OFF_POWER + NQT * BM * 4 + 1024;
 // A piece of an item: stages j0 .. j0 + J - 1 of it, as the planning warp describes it.
 struct Piece {
   int b, kvh, first, seq_rows, row0;   // its sequence; packed row of the first token; rows of a Key head; item's first row
-  int place;                           // 0: whole item; else 1 + the place of the part in the share
+  int place;                           // 0: whole item at once; else 1 + its place in the share
+  int again, whole;                    // joined with the item's pieces before it there; the last piece of a whole item
   int j0, J, steps;                    // steps of 64 keys
   int brief;                           // 256 rows at most: both tiles take them
   int64_t q0, len;
@@ -299,6 +301,7 @@ struct RowOut {
       const int64_t pr = ((int64_t)share * 2 + p.place - 1) * kRows + r;
       f32 = a.part + pr * D;
       lse = a.part_lse + pr;
+      merge = p.again;
       return;
     }
     const int i = (int)((uint32_t)(p.row0 + r) / (uint32_t)a.group), h = p.kvh * a.group + (p.row0 + r - i * a.group);
@@ -309,6 +312,23 @@ struct RowOut {
     merge = a.merge;
   }
 };
+
+// A whole item made in several pieces has its result in its place: the warp's 32 rows from row r0 of the item on, of
+// which `live` exist, go to where they belong.
+__device__ __noinline__ void hand_over(const PagedAttend &a, const volatile Piece &p, int share, int r0, uint32_t live) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();
+#pragma unroll 1
+  for (int k = 0; k < 32; k++) {
+    if (!((live >> k) & 1u)) continue;
+    const int64_t pr = ((int64_t)share * 2 + p.place - 1) * kRows + r0 + k;
+    const int r = p.row0 + r0 + k, i = (int)((uint32_t)r / (uint32_t)a.group), h = p.kvh * a.group + (r - i * a.group);
+    const float L = a.part_lse[pr];
+    pgd::finish4(a, p.first + i, h, 4 * lane, *(const float4 *)(a.part + pr * D + 4 * lane), L);
+    __syncwarp();   // merging lanes have read the earlier log-sum-exp
+    if (lane == 0) pgd::finish_lse(a, p.first + i, h, L);
+  }
+}
 
 // A producer's unit of a stage: 16 keys (of one page) by 64 channels of Keys or Values, two rows a thread, 16
 // channels of each: row lane / 4 and the eighth after it, channels 16 (lane % 4).  A quarter warp's 16-byte
@@ -850,6 +870,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
           }
         }
+        if (p.whole) hand_over(a, p, share, r - lane, __ballot_sync(0xffffffffu, p.row0 + r < p.seq_rows));
         if (half && writes) {
           __syncwarp();
 #pragma unroll 8
@@ -925,12 +946,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kPlanWarp) {
     // ======================= the pieces of the share =======================
-    int b = begin.b, item = begin.item, block = begin.block, pi = 0;
+    int b = begin.b, item = begin.item, from = begin.block, block = from, pi = 0;   // from: the share's first of the item
     bool first = true, more = true;
     while (more) {
       Piece p = {};
       p.done = 1;
-      for (; b < a.batch; b++, item = block = 0) {   // the sequence of the next item
+      for (; b < a.batch; b++, item = from = block = 0) {   // the sequence of the next item
         const pgd::Seq q = pgd::sequence(a, b);
         const int n = Work::count(a, q);
         if (b > end.b || (b == end.b && (item > end.item || (item == end.item && end.block == 0)))) break;
@@ -938,13 +959,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int kvh = item / n, ib = item - kvh * n;
         const int blocks = Work::blocks_of(a, q, ib, p.keys);
         const bool last = b == end.b && item == end.item;
-        const int block1 = last ? end.block : blocks;
+        const int held = last ? end.block : blocks, block1 = held - block > kMost ? block + kMost : held;
+        const bool whole = from == 0 && held == blocks, split = held - from > kMost;
         p.b = b;
         p.kvh = kvh;
         p.first = q.first;
         p.seq_rows = q.rows;
         p.row0 = ib * kRows;
-        p.place = block == 0 ? (block1 == blocks ? 0 : 2) : 1;
+        // (a whole item's pieces meet in the second place: the share's only part there is its last item's)
+        p.place = from > 0 ? 1 : (whole && !split ? 0 : 2);
+        p.again = block > from;
+        p.whole = whole && split && block1 == held;
         p.j0 = block;
         p.J = block1 - block;
         const int to = p.keys.total < block1 * BN ? p.keys.total : block1 * BN;
@@ -956,8 +981,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (first && lane == 0 && cr == 0)
           a.cuts[share] = PagedCut{b, item, block, q.first, kvh, p.row0, q.rows - p.row0 < kRows ? q.rows - p.row0 : kRows};
         first = false;
-        item = last ? INT32_MAX : item + 1;   // (behind the last one everything lies past the end)
-        block = 0;
+        block = block1;
+        if (block1 == held) {
+          item = last ? INT32_MAX : item + 1;   // (behind the last one everything lies past the end)
+          from = block = 0;
+        }
         break;
       }
       more = !p.done;

@@ -25,6 +25,8 @@ template <int BITS>
 constexpr int kBlock = kWarps * wt::step_keys(BITS);   // keys that the 8 warps take at once
 // What an item costs besides its keys, in blocks; the least piece of an item, and of the line, worth a start.
 constexpr int kStart = 4, kLeast = 1, kThin = 4;
+template <int BITS>
+constexpr int kMost = kPagedPieceKeys / kBlock<BITS>;   // blocks of a piece
 
 // The items of sequence b: blocks of keys of each, and how many (Key heads by blocks of 8 NT rows, all as long).
 template <int BITS, int NT>
@@ -105,9 +107,9 @@ __device__ __forceinline__ void find_cuts(const PagedAttend &a, int share, Paged
   }
 }
 
-// A piece of an item that the share holds: blocks `block` .. block1 - 1 of its `blocks`.
+// A piece of an item: blocks `block` .. block1 - 1 of its `blocks`, of which the share holds `from` .. to - 1.
 struct Piece {
-  int item, block, block1, blocks, kvh, row0, rows;   // rows: live ones from row0; 0: no piece
+  int item, from, to, block, block1, blocks, kvh, row0, rows;   // rows: live ones from row0; 0: no piece
   int b, first, seq_rows, q0, len;                    // its sequence
   pgd::Keys keys;
   __device__ __forceinline__ pgd::Seq seq(const PagedAttend &a) const {
@@ -137,11 +139,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) paged_decode_kernel
   __syncthreads();
 
   // ---- the share's pieces, described by the last warp (which has the fewest steps) one ahead of their use ----
-  int nb = cut[0].b, nitem = cut[0].item, nblock = cut[0].block;   // where the next one begins
+  int nb = cut[0].b, nitem = cut[0].item, nfrom = cut[0].block, nblock = nfrom;   // where the next one begins
   auto plan = [&](Piece &to) {
     Piece p = {};   // (no piece: no rows, and no steps for those who look ahead)
     const PagedCut end = cut[1];
-    for (; nb < a.batch; nb++, nitem = nblock = 0) {
+    for (; nb < a.batch; nb++, nitem = nfrom = nblock = 0) {
       if (nb > end.b || (nb == end.b && (nitem > end.item || (nitem == end.item && end.block == 0)))) break;
       const pgd::Seq q = pgd::sequence(a, nb);
       const int tiles = q.rows > a.few ? 0 : (q.rows + 8 * NT - 1) / (8 * NT);
@@ -152,16 +154,21 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) paged_decode_kernel
       p.keys.init(a, q.s, q.frame(a, 0), q.frame(a, q.rows - 1));
       p.blocks = (p.keys.total + kBlock<BITS> - 1) / kBlock<BITS>;
       p.item = nitem;
+      p.from = nfrom;
       p.block = nblock;
       const bool last = nb == end.b && nitem == end.item;
-      p.block1 = last ? end.block : p.blocks;
+      p.to = last ? end.block : p.blocks;
+      p.block1 = p.to - p.block > kMost<BITS> ? p.block + kMost<BITS> : p.to;
       p.b = nb;
       p.first = q.first;
       p.seq_rows = q.rows;
       p.q0 = (int)q.q0;
       p.len = (int)q.s.len;
-      nitem = last ? INT32_MAX : nitem + 1;   // (behind the last one everything lies past the end)
-      nblock = 0;
+      nblock = p.block1;
+      if (p.block1 == p.to) {
+        nitem = last ? INT32_MAX : nitem + 1;   // (behind the last one everything lies past the end)
+        nfrom = nblock = 0;
+      }
       break;
     }
     if (lane == 0) to = p;
@@ -311,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) paged_decode_kernel
     float (*osm)[D] = (float (*)[D])(dyn + (size_t)(warp * R::kStages + mine) * R::kStage);
     if (lane == 0) spare[warp] = mine;
     tile.sums(msm[warp], lsm[warp]);
-    const bool part = p.block > 0 || p.block1 < p.blocks;
+    const bool part = p.from > 0 || p.block1 < p.blocks;
 #pragma unroll
     for (int nt = 0; nt < NT; nt++) {
       if (8 * nt < rows) {
@@ -325,15 +332,27 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) paged_decode_kernel
           float4 acc = wt::join(msm, lsm, r, [&](int w) {
             return tile.output((const float (*)[D])(dyn + (size_t)(w * R::kStages + spare[w]) * R::kStage), warp, lane);
           }, M, L);
-          const float inv = L > 0.f ? win::kUnit<BITS> / L : 0.f, lse = L > 0.f ? M + log2f(L) : -INFINITY;
+          const float inv = L > 0.f ? win::kUnit<BITS> / L : 0.f;
+          float lse = L > 0.f ? M + log2f(L) : -INFINITY;
           acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+          // an item's first part in the share's second place, any other in its first (a whole one in the second until
+          // its last piece: the share's only part there is its last item's)
+          const int64_t pr = ((int64_t)blockIdx.x * 2 + (p.from == 0 ? 1 : 0)) * 8 * NT + r;
+          if (p.block > p.from) {   // joined with the pieces before it (of which this lane wrote these channels)
+            const float Lp = a.part_lse[pr], Lm = fmaxf(Lp, lse);
+            const float wp = Lp == -INFINITY ? 0.f : exp2f(Lp - Lm), wt = lse == -INFINITY ? 0.f : exp2f(lse - Lm), den = wp + wt;
+            const float4 prev = *(const float4 *)(a.part + pr * D + ch);
+            const float up = den > 0.f ? wp / den : 0.f, ut = den > 0.f ? wt / den : 0.f;
+            acc = make_float4(fmaf(prev.x, up, acc.x * ut), fmaf(prev.y, up, acc.y * ut), fmaf(prev.z, up, acc.z * ut), fmaf(prev.w, up, acc.w * ut));
+            lse = den > 0.f ? Lm + log2f(den) : -INFINITY;
+            __syncwarp();   // every lane has read the earlier log-sum-exp
+          }
           if (!part) {
             const int i = (row0 + r) / a.group, h = p.kvh * a.group + (row0 + r - i * a.group);
             pgd::finish4(a, p.first + i, h, ch, acc, lse);
             __syncwarp();   // merging lanes have read the earlier log-sum-exp
             if (lane == 0) pgd::finish_lse(a, p.first + i, h, lse);
-          } else {   // an item's first part in the share's second place, any other in its first
-            const int64_t pr = ((int64_t)blockIdx.x * 2 + (p.block == 0 ? 1 : 0)) * 8 * NT + r;
+          } else {
             *(float4 *)(a.part + pr * D + ch) = acc;
             if (lane == 0) a.part_lse[pr] = lse;
           }

@@ -131,7 +131,10 @@ QWM_API qwm_status qwm_paged_read(qwm_ctx *ctx, const qwm_page_pool *pool, const
  *   lse        fp32 [H][n] dense, or NULL
  *   ws         workspace of qwm_paged_attend_workspace bytes, free again when the call's work on the stream is
  *              done.  Calls (and captured graphs) that may run at the same time need their own.
- * Queries and weights enter the products as in qwm_window_attend. */
+ * Queries and weights enter the products as in qwm_window_attend: Queries off by at most 2^-25 of their row's largest
+ * element, weights in fp16, rounded by at most 2^-11 of their value or 2^-32 of the largest weight of their piece, whichever
+ * is more (with out_f32 the largest error beside the cache's own).  Logits, maxima, sums and the output are accumulated in
+ * fp32, over pieces of 2^18 keys at most, which are joined. */
 QWM_API qwm_status qwm_paged_attend(qwm_ctx *ctx, const qwm_page_pool *pool, const qwm_page_table *tab, const uint16_t *q,
                                     const qwm_strides *qs, int64_t n, const int32_t *first, const int32_t *count,
                                     int64_t max_count, int64_t tpf, int64_t frames, int64_t sink, float softmax_scale,

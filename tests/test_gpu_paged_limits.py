@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 
 import window_ref as ref
-from test_gpu_paged import ALL, Batch, attend, ctx_of, f64, gpu_check, ints, rows, starts, status
+from test_gpu_paged import ALL, SCALE, Batch, ctx_of, ints, rows, status
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -51,3 +51,62 @@ def test_attend_scales_that_underflow(qwm, count, bits, scale):
     for o, l in ((out, lse), (wout[0], wlse[0])):
         assert bool(((o.double() - want).abs() <= 2.0 ** -7 * spread).all())
         assert bool(((l.double() - many).abs() <= 2.0 ** -8).all())
+
+
+# (bits, kv, count, tokens, tpf, frames, sink): whole items in a share and items cut into parts of several pieces, on
+# warp tiles of 8 and of 16 rows and on tiles of 256 and of 512; rows that see nothing of the first or last piece
+LONG = [(8, 304, 1, 1 << 22, 1, ALL, 0), (4, 200, 1, (1 << 22) - 100, 1, ALL, 0), (4, 152, 9, 1 << 22, 1, ALL, 0),
+        (8, 100, 12, (1 << 22) - 77, 1, 1_500_000, 300), (8, 76, 64, 1 << 22, 1, ALL, 0), (4, 50, 40, (1 << 22) - 1, 1, ALL, 0),
+        (4, 76, 300, (1 << 22) - 5, 1, ALL, 0), (8, 50, 600, 3_000_001, 1, 2_900_000, 1000), (8, 76, 300, 3 * (1 << 18) + 150, 1 << 18, 2, 0),
+        (4, 304, 20, 2 * (1 << 18) + 7, 1 << 18, 1, 0)]
+
+
+@pytest.mark.parametrize("mode", ["fp32", "bf16", "merge"])
+@pytest.mark.parametrize("case", LONG)
+def test_attend_long_sequences(qwm, case, mode):
+    """One page of 256 tokens stands in every entry of the table, so that key t is key t % 256 and the definition a
+    weighted softmax over 256.  A piece takes 2^18 keys at most: its products are added 16 keys at a time, each off by
+    2^-23 of the sum where it is truncated (on warp tiles eight warps take an eighth each), its weights 64 at a time (two
+    per lane and 16 keys on warp tiles) by 2^-24; weights are rounded by 2^-11 or 2^-32 of the largest; logits as in
+    check() of the other file, in weights and in their sum; 20 pieces and parts joined, 2^-22 each."""
+    bits, kv, count, n, tpf, frames, sink = case
+    ctx, gen = ctx_of(qwm, kv), torch.Generator(device="cuda").manual_seed(count)
+    pool = qwm.PagePool.empty(bits, 256, 1, kv)
+    k = torch.randn(kv, 256, 128, device="cuda", generator=gen).to(torch.bfloat16)
+    v = (torch.rand(kv, 256, 128, device="cuda", generator=gen) + 0.5).to(torch.bfloat16)
+    qwm.qwm_paged_write(ctx, pool, k, v, torch.arange(256, device="cuda"))
+    kh, vh = (torch.from_numpy(np.stack([ref.values(getattr(pool, x + "_codes")[0, j].cpu().numpy(), getattr(pool, x + "_step")[0, j].cpu().numpy(), bits)
+                                         for j in range(kv)])).cuda() for x in "kv")
+    width = -(-n // 256)
+    tab = qwm.PageTable(256, torch.zeros(1, width, dtype=torch.int32, device="cuda"), ints([n]), ints([0], torch.int32), ints([0], torch.int32))
+    q = torch.randn(kv, count, 128, device="cuda", generator=gen).to(torch.bfloat16)
+    out = torch.zeros(kv, count, 128, device="cuda", dtype=torch.bfloat16 if mode == "bf16" else torch.float32)
+    lse = torch.zeros(kv, count, device="cuda")
+    # how often each row sees each of the 256
+    p, j = torch.arange(n - count, n, device="cuda")[:, None], torch.arange(256, device="cuda")
+    many = lambda lo, hi: ((hi - 1 - j).div(256, rounding_mode="floor") - (lo - 1 - j).div(256, rounding_mode="floor")).clamp(min=0)
+    hi = ((p // tpf + 1) * tpf).clamp(max=n)
+    lo = ((p // tpf + 1 - frames) * tpf).clamp(min=sink)
+    seen = many(torch.zeros_like(hi), hi.clamp(max=sink)) + many(torch.minimum(lo, hi), hi)
+    x = (q.double() @ kh.transpose(1, 2)) * (SCALE * math.log2(math.e)) + torch.log2(seen.double())
+    wl = torch.logsumexp(x * math.log(2), -1) / math.log(2)
+    w = torch.exp2(x - wl[..., None])
+    want, spread = w @ vh, w @ vh.abs()
+    mag = (q.double().abs() @ kh.abs().transpose(1, 2)).amax(-1) * SCALE * math.log2(math.e)
+    few, piece = count <= 32, 1 << 18
+    logits = 2.0 ** -16 * mag + 2.0 ** -20
+    sums = piece / 128 * 2.0 ** -24 if few else piece / 64 * 2.0 ** -24
+    rel = 2.0 ** -11 + 2 * logits + sums + piece / 16 / (8 if few else 1) * 2.0 ** -23 + 20 * 2.0 ** -22
+    far = math.log2(math.e) * sums + logits + 2.0 ** -22 * wl.abs() + 20 * 2.0 ** -22
+    bound = rel[..., None] * spread + piece * 2.0 ** -32 * vh.abs().max()
+    if mode == "merge":   # into a result of the same weight
+        was = torch.randn(kv, count, 128, device="cuda", generator=gen)
+        out.copy_(was), lse.copy_(wl)
+        want, wl = (want + was.double()) / 2, wl + 1
+        bound = bound / 2 + (far[..., None] + 2.0 ** -20) * (spread + was.double().abs())
+    qwm.qwm_paged_attend(ctx, pool, tab, q, ints([0], torch.int32), ints([count], torch.int32), SCALE, out, lse=lse, tpf=tpf, frames=frames, sink=sink,
+                         max_count=count, merge=mode == "merge")
+    assert status(qwm, ctx) == qwm.QWM_OK
+    bound = bound + (2.0 ** -8 if mode == "bf16" else 2.0 ** -22) * want.abs()
+    assert bool(((out.double() - want).abs() <= bound).all()), float(((out.double() - want).abs() / bound).max())
+    assert bool(((lse.double() - wl).abs() <= far + 2.0 ** -22 * wl.abs()).all()), float(((lse.double() - wl).abs() / far).max())
