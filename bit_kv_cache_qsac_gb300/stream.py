@@ -344,7 +344,9 @@ class PagedBatch:
         merge as qwm_paged_attend's; max_count: the largest count of the step, where it is known."""
         if not self.norm and (q_weight is not None or k_weight is not None):
             raise ValueError("weights of norms that this batch does not form")
-        main = stream if stream is not None else torch.cuda.current_stream(q.device)
+        main = torch.cuda.current_stream(q.device) if stream is None else stream
+        if not hasattr(main, "cuda_stream"):   # a handle, as the calls beneath take it too
+            main = torch.cuda.ExternalStream(int(main), q.device)
         with torch.cuda.stream(main):
             qwm_paged_write(self.ctx, self.pools[i], k, v, self.slot, at=self.at if self.rope is not None else None,
                             rope=self.rope, norm=self.norm, weight=k_weight, eps=self.eps, stream=main)
