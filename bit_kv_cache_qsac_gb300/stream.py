@@ -18,7 +18,7 @@ from . import (ActiveChunk, Chunk, Context, PagePool, PageTable, Window, pack_ps
                qwm_dequantize, qwm_fit_centroids_kv, qwm_norm_rope, qwm_paged_attend, qwm_paged_write,
                qwm_pages_update, qwm_quantize_kv, qwm_quantize_kv_full, qwm_rope, qwm_select_rank,
                qwm_sync_status, qwm_update_query_stats, qwm_window_attend, qwm_window_read, qwm_window_write)
-from .window import check_rows
+from .window import _stream_of, check_rows
 
 _MAX_CHUNKS = 128   # chunks that one call of qwm_attend or qwm_attend_merge takes
 
@@ -294,7 +294,8 @@ class PagedBatch:
     A step is begun with what every sequence is shortened to and how many tokens it gets; then each layer is
     called once with the step's packed Queries, Keys and Values (rows of all sequences one after the other, as
     `begin` was told).  What a step needs of the device stays on the device, so that a step may be captured in
-    a CUDA graph and replayed with other counts in the same tensors.  Steps are ordered on one stream."""
+    a CUDA graph and replayed with other counts in the same tensors.  Calls follow one another on whatever streams
+    they are made, but for captured ones, whose replays the caller orders."""
 
     def __init__(self, ctx: Context, layers: int, kv_heads: int, batch: int, max_tokens: int, pages: int, rows: int,
                  page: int = 64, bits: int = 8, rope=None, norm: bool = True, eps: float = 1e-6, tpf: int = 1,
@@ -312,13 +313,50 @@ class PagedBatch:
         self.first, self.granted = torch.zeros(batch, **i32), torch.zeros(batch, **i32)
         self.slot, self.at = torch.full((rows,), -1, **i64), torch.full((rows,), -1, **i64)
         self._zero = torch.zeros(1, **i64)
+        # what the batch owns was filled on this stream; a call on another one waits for the event
+        self._stream = torch.cuda.current_stream(self.at.device)
+        self._done = self._stream.record_event()
+
+    def _turn(self, stream):
+        """The stream of a call (given as an object, a handle or None: the current one), made to follow the last
+        call's."""
+        handle, last = _stream_of(self.ctx, stream), self._stream
+        if handle == last.cuda_stream:
+            return last
+        dev = self.at.device
+        main = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(handle, dev)
+        with torch.cuda.stream(main):
+            if not torch.cuda.is_current_stream_capturing():   # who replays a captured step orders the replays
+                main.wait_event(self._done)
+                for owner in (self, self.table, *self.pools):
+                    for t in vars(owner).values():
+                        if isinstance(t, torch.Tensor):   # not handed out again before `main` is done with it
+                            t.record_stream(main)
+                self._stream = main
+        return main
+
+    def _leave(self, main) -> None:
+        """What a call issued on its stream is what the next one on another stream waits for."""
+        if main is not self._stream:   # captured
+            return
+        if main.cuda_stream == _stream_of(self.ctx, None):
+            eager = not torch.cuda.is_current_stream_capturing()
+        else:
+            with torch.cuda.stream(main):
+                eager = not torch.cuda.is_current_stream_capturing()
+        if eager:
+            self._done.record(main)
 
     def begin(self, count: torch.Tensor, keep: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """Shorten every sequence to keep [batch] (int64) tokens, then append count [batch] (int32) new ones: their
         rows of the packed batch follow one another.  Returns how many each was given: its count, or 0 where the
         pages do not suffice (its rows are then left out of the step)."""
-        qwm_pages_update(self.ctx, self.table, self.first, self.granted, self.slot, self.at, count=count, keep=keep,
-                         stream=stream)
+        main = self._turn(stream)
+        try:
+            qwm_pages_update(self.ctx, self.table, self.first, self.granted, self.slot, self.at, count=count, keep=keep,
+                             stream=main)
+        finally:   # what was issued before an error too is waited for
+            self._leave(main)
         return self.granted
 
     def _ready(self, q: torch.Tensor, weight, stream) -> torch.Tensor:
@@ -344,18 +382,19 @@ class PagedBatch:
         merge as qwm_paged_attend's; max_count: the largest count of the step, where it is known."""
         if not self.norm and (q_weight is not None or k_weight is not None):
             raise ValueError("weights of norms that this batch does not form")
-        main = torch.cuda.current_stream(q.device) if stream is None else stream
-        if not hasattr(main, "cuda_stream"):   # a handle, as the calls beneath take it too
-            main = torch.cuda.ExternalStream(int(main), q.device)
-        with torch.cuda.stream(main):
-            qwm_paged_write(self.ctx, self.pools[i], k, v, self.slot, at=self.at if self.rope is not None else None,
-                            rope=self.rope, norm=self.norm, weight=k_weight, eps=self.eps, stream=main)
-            q = self._ready(q, q_weight, main)
-            if out is None:
-                out = torch.zeros_like(q, dtype=torch.bfloat16)
-            qwm_paged_attend(self.ctx, self.pools[i], self.table, q, self.first, self.granted,
-                             1.0 / math.sqrt(q.shape[2]) if scale is None else scale, out, lse=lse, merge=merge,
-                             max_count=max_count, stream=main, **self.mask)
+        main = self._turn(stream)
+        try:
+            with torch.cuda.stream(main):
+                qwm_paged_write(self.ctx, self.pools[i], k, v, self.slot, at=self.at if self.rope is not None else None,
+                                rope=self.rope, norm=self.norm, weight=k_weight, eps=self.eps, stream=main)
+                q = self._ready(q, q_weight, main)
+                if out is None:
+                    out = torch.zeros_like(q, dtype=torch.bfloat16)
+                qwm_paged_attend(self.ctx, self.pools[i], self.table, q, self.first, self.granted,
+                                 1.0 / math.sqrt(q.shape[2]) if scale is None else scale, out, lse=lse, merge=merge,
+                                 max_count=max_count, stream=main, **self.mask)
+        finally:   # what was issued before an error too is waited for
+            self._leave(main)
         return out
 
     def check(self, stream=None) -> int:
