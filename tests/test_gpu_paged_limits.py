@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 
 import window_ref as ref
-from test_gpu_paged import ALL, SCALE, Batch, ctx_of, ints, rows, status
+from test_gpu_paged import ALL, SCALE, Batch, ctx_of, ints, rows, starts, status
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -110,3 +110,56 @@ def test_attend_long_sequences(qwm, case, mode):
     bound = bound + (2.0 ** -8 if mode == "bf16" else 2.0 ** -22) * want.abs()
     assert bool(((out.double() - want).abs() <= bound).all()), float(((out.double() - want).abs() / bound).max())
     assert bool(((lse.double() - wl).abs() <= far + 2.0 ** -22 * wl.abs()).all()), float(((lse.double() - wl).abs() / far).max())
+
+
+# (bits, lengths, counts, H, kv): whole items and items cut into parts, on warp tiles and on tensor-memory tiles
+MERGED = [(8, [40 + 3 * i for i in range(180)], [1 + i % 2 for i in range(180)], 4, 2), (4, [9000, 31], [2, 1], 8, 2), (4, [90 + i for i in range(50)], [40] * 50, 4, 2),
+          (8, [6000], [300], 2, 2), (8, [700, 5, 300, 2500], [1, 5, 260, 33], 6, 2)]
+
+
+@pytest.mark.parametrize("case", MERGED)
+def test_attend_merged_into_a_result_over_other_keys(qwm, case):
+    """The earlier result is the 64-bit reference's over other keys, rounded to fp32, or made up: nothing seen (-inf,
+    with NaN in the output, which is not to be read), far above this call's sums, far below.  The merged mean is off by
+    what this call's part is (as check() of the other file) and by what its log-sum-exp shifts between the two: ln 2 of the
+    error times the difference."""
+    bits, lengths, counts, H, kv = case
+    rng, gen = np.random.default_rng(sum(counts)), torch.Generator(device="cuda").manual_seed(sum(counts))
+    b = Batch(qwm, rng, bits, 16, kv, lengths)
+    first, n = starts(counts, gap=1)
+    q = rows(rng, H, n)
+    far_k, far_v = (torch.randn(H, 77, 128, device="cuda", generator=gen).double() for _ in range(2))
+    x = q.double() @ far_k.transpose(1, 2) * (SCALE * math.log2(math.e))
+    lse = (torch.logsumexp(x * math.log(2), -1) / math.log(2)).float()
+    out = (torch.softmax(x * math.log(2), -1) @ far_v).float()
+    kind = torch.arange(n, device="cuda")[None] * 3 + torch.arange(H, device="cuda")[:, None]
+    lse[kind % 5 == 1], out[kind % 5 == 1] = -math.inf, math.nan
+    lse[kind % 5 == 2] += 60.0
+    lse[kind % 5 == 3] -= 60.0
+    was, wasl = out.clone(), lse.clone()
+    ctx = ctx_of(qwm, H)
+    for most in (max(counts), None):
+        out.copy_(was), lse.copy_(wasl)
+        qwm.qwm_paged_attend(ctx, b.pool, b.tab, q, ints(first, torch.int32), ints(counts, torch.int32), SCALE, out, lse=lse, merge=True, max_count=most)
+        assert status(qwm, ctx) == qwm.QWM_OK
+        mine = torch.zeros(n, dtype=torch.bool, device="cuda")
+        for i, (c, m) in enumerate(zip(counts, lengths)):
+            f = slice(first[i], first[i] + c)
+            mine[f] = True
+            k, v = (torch.from_numpy(y[i]).cuda().repeat_interleave(H // kv, 0) for y in (b.k, b.v))
+            see = torch.arange(m, device="cuda") <= torch.arange(m - c, m, device="cuda")[:, None]
+            x = (q[:, f].double() @ k.transpose(1, 2) * (SCALE * math.log2(math.e))).masked_fill(~see, -math.inf)
+            wl = torch.logsumexp(x * math.log(2), -1) / math.log(2)
+            w = torch.exp2(x - wl[..., None])
+            part, spread = w @ v, w @ v.abs()
+            mag = (q[:, f].double().abs() @ k.abs().transpose(1, 2)).amax(-1) * SCALE * math.log2(math.e)
+            bound = 2 * (2.0 ** -11 + 2.0 ** -16 * mag + 2.0 ** -20)[..., None] * spread + m * 2.0 ** -31 * v.abs().max()
+            d = 2.0 ** -16 * mag + 2.0 ** -20 + 2.0 ** -22 * wl.abs()
+            lp, prev = wasl[:, f].double(), was[:, f].double().nan_to_num(0.0)
+            want_l = torch.logaddexp2(lp, wl)
+            up, ut = torch.exp2(lp - want_l)[..., None], torch.exp2(wl - want_l)[..., None]
+            want = up * prev + ut * part
+            err = ut * bound + math.log(2) * (d + 2.0 ** -22 * lp.abs().nan_to_num(0, 0, 0))[..., None] * up * ut * (prev - part).abs() + 2.0 ** -20 * (up * prev.abs() + ut * part.abs())
+            assert bool(((out[:, f].double() - want).abs() <= err + 2.0 ** -30).all()), i
+            assert bool(((lse[:, f].double() - want_l).abs() <= d + 2.0 ** -22 * want_l.abs() + 2.0 ** -20).all()), i
+        assert torch.equal(out[:, ~mine].view(torch.int32), was[:, ~mine].view(torch.int32)) and torch.equal(lse[:, ~mine], wasl[:, ~mine])
