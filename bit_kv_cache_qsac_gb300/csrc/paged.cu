@@ -3,8 +3,8 @@
 //
 //   y = x r w, r = 1 / sqrt(mean(x^2) + eps), then each pair (a, b) of channels becomes (a cos - b sin,
 //   a sin + b cos), all in fp32, rounded to bf16 once.
-// Bound: memory.  16 lanes take one row, 8 channels each; two heads' sums of squares are reduced together (five
-// shuffles instead of eight, and one root a lane); the angles depend on the token alone, so a thread forms those of
+// Bound: memory.  16 lanes take one row, 8 channels each; two heads' sums of squares are reduced together (four
+// shuffles and two to hand the roots back instead of eight, and one root a lane instead of two); the angles depend on the token alone, so a thread forms those of
 // its channels once and walks over `heads_per_block` heads with them, the next two heads' rows in flight.
 // Measured, 40 heads x 10,800 tokens, three axes, weights per head: normed and turned in 46 us = 4.8 TB/s of rows read
 // and written (72% of the issue slots: the rotation alone takes 37 us; with four heads in flight 54, with one 57, and
@@ -69,9 +69,9 @@ __device__ __forceinline__ float2 scale_of_odd_row(const uint32_t (&w)[4], float
   return make_float2(1.f / sqrtf(fmaf(v, 1.f / win::D, eps * s * s)), s);
 }
 
-// What the channels of N rows (1, 2 or 4: heads) of this lane's token are multiplied by; -1 for a row whose squares leave
+// What the channels of N rows (1 or 2: heads) of this lane's token are multiplied by; -1 for a row whose squares leave
 // fp32's range, which is left for later (its code beside the others' would take their registers).  The 16 lanes of a
-// token reduce the N sums together, each lane ending with one of them, so that a root is formed once a lane.
+// token reduce two sums together, each lane ending with one of them, so that a root is formed once a lane.
 template <int N>
 __device__ __forceinline__ void row_scales(const uint32_t (&w)[N][4], float eps, float (&r)[N]) {
   const int lane = threadIdx.x & 31;
@@ -81,29 +81,20 @@ __device__ __forceinline__ void row_scales(const uint32_t (&w)[N][4], float eps,
     const float2 a = win::split2(square_sum(w[u], 1.f));
     v[u] = a.x + a.y;
   }
-  const bool up = lane & 8, on = lane & 4;
-  if (N == 4) {   // each lane hands on two sums and keeps two, then one and one
-    const float a = __shfl_xor_sync(0xffffffffu, up ? v[0] : v[2 % N], 8), b = __shfl_xor_sync(0xffffffffu, up ? v[1 % N] : v[3 % N], 8);
-    v[0] = (up ? v[2 % N] : v[0]) + a;
-    v[1 % N] = (up ? v[3 % N] : v[1 % N]) + b;
-    const float c = __shfl_xor_sync(0xffffffffu, on ? v[0] : v[1 % N], 4);
-    v[0] = (on ? v[1 % N] : v[0]) + c;
-  } else {
-    const float a = __shfl_xor_sync(0xffffffffu, N == 2 && !up ? v[1 % N] : v[0], 8);
-    v[0] = (N == 2 && up ? v[1 % N] : v[0]) + a;
-    v[0] += __shfl_xor_sync(0xffffffffu, v[0], 4);
-  }
+  const bool up = lane & 8;   // two rows: each lane hands on one sum and keeps the other
+  const float a = __shfl_xor_sync(0xffffffffu, N == 2 && !up ? v[1 % N] : v[0], 8);
+  v[0] = (N == 2 && up ? v[1 % N] : v[0]) + a;
+  v[0] += __shfl_xor_sync(0xffffffffu, v[0], 4);
   v[0] += __shfl_xor_sync(0xffffffffu, v[0], 2);
   v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
   const float mine = out_of_range(v[0], eps) ? -1.f : inverse_root(fmaf(v[0], 1.f / win::D, eps));
 #pragma unroll
-  for (int u = 0; u < N; u++)   // row u's: lanes of bit 3 = u / 2, bit 2 = u % 2 (two rows: bit 3 = u)
-    r[u] = N == 1 ? mine : __shfl_sync(0xffffffffu, mine, (lane & 16) | (N == 4 ? (u >> 1) << 3 | (u & 1) << 2 : u << 3));
+  for (int u = 0; u < N; u++) r[u] = N == 1 ? mine : __shfl_sync(0xffffffffu, mine, (lane & 16) | u << 3);   // row u's: lanes of bit 3 = u
 }
 
 // Eight channels times r and the weights, and turned (TURN >= 0), rounded to bf16.  g: this
 // lane's weights, HALF: and its partner's behind them.  Every lane of the warp takes part.
-template <int TURN, bool WHOLE, typename Rot>
+template <int TURN, typename Rot>
 __device__ __forceinline__ void norm_turn(uint32_t (&w)[4], const float *g, float r, const qwm_rope_spec &sp, const Rot &rv) {
   uint64_t y[4], z[4];   // this lane's channels, its partner's
   auto normed = [&](const uint32_t (&x)[4], const float *f, uint64_t (&v)[4]) {
@@ -151,12 +142,12 @@ struct Rotation : win::RopeVec<PAIRING, WHOLE> {
 };
 
 // The same for a row that row_scales left: its channels times s first (a power of two: exact, or beyond mattering).
-template <int TURN, bool WHOLE, typename Rot>
+template <int TURN, typename Rot>
 __device__ __forceinline__ void norm_turn_odd(uint32_t (&w)[4], const float *g, float eps, const qwm_rope_spec &sp, const Rot &rv) {
   const float2 f = scale_of_odd_row(w, eps);
 #pragma unroll
   for (int i = 0; i < 4; i++) w[i] = tc::pack_bf16x2(low(w[i]) * f.y, high(w[i]) * f.y);
-  norm_turn<TURN, WHOLE>(w, g, f.x, sp, rv);
+  norm_turn<TURN>(w, g, f.x, sp, rv);
 }
 
 // This lane's weights of a head (HALF: and its partner's), or ones.
@@ -245,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 4)
 #pragma unroll
     for (int u = 0; u < kUnroll; u++) {
       if (per_head && h + u < h1) weights_of<TURN>(own + (h + u - h0) * win::D, v, sp, rv, g);
-      norm_turn<TURN, WHOLE>(w[u], g, rs[u], sp, rv);
+      norm_turn<TURN>(w[u], g, rs[u], sp, rv);
       if (live && h + u < h1 && rs[u] >= 0.f)
         *(uint4 *)(dst + (int64_t)(h + u) * os.head) = make_uint4(w[u][0], w[u][1], w[u][2], w[u][3]);
     }
@@ -256,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 4)
     const uint4 x4 = *(const uint4 *)(src + (int64_t)h * xs.head);
     uint32_t w[4] = {x4.x, x4.y, x4.z, x4.w};
     if (per_head) weights_of<TURN>(own + (h - h0) * win::D, v, sp, rv, g);
-    norm_turn_odd<TURN, WHOLE>(w, g, eps, sp, rv);
+    norm_turn_odd<TURN>(w, g, eps, sp, rv);
     if (live && (left & 1ull)) *(uint4 *)(dst + (int64_t)h * os.head) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
@@ -321,7 +312,7 @@ __global__ void __launch_bounds__(kThreads)
         if (r[0] < 0.f) kw[0] = kw[1] = kw[2] = kw[3] = 0u;
         now = live && r[0] >= 0.f;
       }
-      norm_turn<TURN, WHOLE>(kw, g, r[0], sp, rv);
+      norm_turn<TURN>(kw, g, r[0], sp, rv);
     } else if (TURN >= 0) {
       rv.turn(sp, kw);
     }
@@ -341,7 +332,7 @@ __global__ void __launch_bounds__(kThreads)
       uint32_t kw[4] = {x.x, x.y, x.z, x.w}, c0, c1, step;
       if (!(left & 1ull)) kw[0] = kw[1] = kw[2] = kw[3] = 0u;
       if (per_head) weights_of<TURN>(own + (h - h0) * win::D, v, sp, rv, g);
-      norm_turn_odd<TURN, WHOLE>(kw, g, eps, sp, rv);
+      norm_turn_odd<TURN>(kw, g, eps, sp, rv);
       if (!(left & 1ull)) kw[0] = kw[1] = kw[2] = kw[3] = 0u;   // (no rows of their own: 0 / 0 where eps is 0)
       win::quantise<BITS>(kw, c0, c1, step, bad);
       if (left & 1ull) win::store_row<BITS>(pool.k_codes, pool.k_step, slot_row, v, c0, c1, step);

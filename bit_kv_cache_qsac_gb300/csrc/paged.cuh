@@ -141,10 +141,6 @@ struct Everyone {
   __device__ __forceinline__ bool see(int v0, int v1) const { return v1 <= e0 || (v0 >= e1 && v1 <= e2); }
 };
 
-// The page that holds a token, as a row of the pool's arrays for Key head kvh: the index of its place 0.
-__device__ __forceinline__ int64_t page_row(const PagedAttend &a, int page, int kvh) {
-  return ((int64_t)page * a.pool.kv_heads + kvh) << a.page_log2;
-}
 // A table entry made safe: one outside the pool is read as page 0.
 __device__ __forceinline__ int checked(const PagedAttend &a, int page) {
   if ((uint32_t)page < (uint32_t)a.pool.pages) return page;

@@ -307,8 +307,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) paged_decode_kernel
       refill(p, next, true);
       tile.step(st, j * kKeys, every.see(j * kKeys, j * kKeys + kKeys), mask_of, a.bases);
     }
-    refill(p, next, true);    // (a warp without a step in the piece has not turned yet)
-    if (!ahead) turn_to(next);
+    refill(p, next, true);    // (a warp without a step in the piece has not turned yet; here every one has)
     ahead = false;
 
     // ---- the warps' parts joined: a warp's outputs go through the stage it has read last, the other two are on

@@ -10,11 +10,12 @@ from __future__ import annotations
 import ctypes as C
 import struct
 from dataclasses import dataclass
+from types import SimpleNamespace
 
 import torch
 
 from . import LIB_PATH, _check, _lib
-from .window import _BF16, _R, _S, _array, _refuse, _stream_of, qwm_rope_spec
+from .window import _BF16, _R, _S, _refuse, _stream_of, qwm_rope_spec
 
 _P = C.c_void_p
 _D, _GROUP = 128, 32
@@ -57,23 +58,23 @@ _pack_strides = struct.Struct("qqq").pack                   # qwm_strides
 _U8, _BF = torch.uint8, torch.bfloat16
 
 
+def _wrong(dev, t, name: str, dtypes, shape):
+    _refuse(SimpleNamespace(device=dev), t, name, dtypes, shape)
+
+
 def _dense(dev, t, name: str, dtype, shape):
     """Pointer of a dense device array (or None)."""
     if t is None:
         return None
     if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
-        class At:
-            device = dev
-        _refuse(At, t, name, (dtype,), shape)
+        _wrong(dev, t, name, (dtype,), shape)
     return t.data_ptr()
 
 
 def _packed(dev, t, name: str, shape, dtypes=_BF16):
     """Pointer and strides of a packed activation [heads, rows, 128]."""
     if not isinstance(t, torch.Tensor) or (t.dtype is not _BF and t.dtype not in dtypes) or t.shape != shape or t.device != dev:
-        class At:
-            device = dev
-        _refuse(At, t, name, dtypes, shape)
+        _wrong(dev, t, name, dtypes, shape)
     h, n, one = t.stride()
     if one != 1:
         raise ValueError(f"{name}: channels must be contiguous")
@@ -83,9 +84,7 @@ def _packed(dev, t, name: str, shape, dtypes=_BF16):
 def _rows4(dev, t, name: str, shape):
     """Pointer and strides of an activation [batch, heads, tokens, 128]."""
     if not isinstance(t, torch.Tensor) or (t.dtype is not _BF and t.dtype not in _BF16) or t.shape != shape or t.device != dev:
-        class At:
-            device = dev
-        _refuse(At, t, name, _BF16, shape)
+        _wrong(dev, t, name, _BF16, shape)
     b, h, n, one = t.stride()
     if one != 1:
         raise ValueError(f"{name}: channels must be contiguous")
