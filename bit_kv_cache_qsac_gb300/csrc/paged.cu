@@ -7,9 +7,12 @@
 // shuffles and two to hand the roots back instead of eight, and one root a lane instead of two); the angles depend on the token alone, so a thread forms those of
 // its channels once and walks over `heads_per_block` heads with them, the next two heads' rows in flight.
 // Measured, 40 heads x 10,800 tokens, three axes, weights per head: normed and turned in 46 us = 4.8 TB/s of rows read
-// and written (72% of the issue slots: the rotation alone takes 37 us; with four heads in flight 54, with one 57, and
-// with each head's weights fetched from global memory 55); written at 4 bits 67 us = 4.2 TB/s (78% of the issue slots; its chain per row
-// is the window cache's, and the norm's before it); read back in 43 us = 6.5 TB/s.  32 x 32 heads x 1 token: 4.3 us.
+// and written (72% of the issue slots: the rotation alone takes 37 us, the norm alone 38; with four heads in flight 54, with one
+// 57, and with each head's weights fetched from global memory 55); in halves 54 us with shared weights and 69 with weights per
+// head: each channel is normed twice, for its own lane and its partner's, and 64 registers do not hold both (80 to 96 bytes
+// spilled).  Written at 4 bits 66 us = 4.2 TB/s, at 8 bits 71 (78% of the issue slots; its chain per row is the window cache's,
+// and the norm's before it; in halves 73 and 75, normed only 55 and 61, as it comes 46 and 53); read back in 44 us = 6.3 TB/s
+// (8 bits 52).  32 x 32 heads x 1 token: 4.2 us.
 #include <math.h>
 
 #include "paged.cuh"
@@ -398,6 +401,8 @@ cudaError_t write_launch(const qwm_page_pool &pool, int page_log2, const uint16_
                          const qwm_strides &vs, int64_t n, const int64_t *slot, const qwm_rope_spec *rope, const int64_t *at,
                          const int32_t *pos, const float *weight, int per_head, float eps, int num_sms, int32_t *status,
                          cudaStream_t st) {
+  // (blocks an SM: the chunk above turned, 4 bits, with 5 / 9 / 14 / 20 takes 76 / 68 / 70 / 76 us, in halves 80 / 76 / 80 / 88; not turned
+  // with 10 / 20 / 30 / 40: 61 / 57 / 57 / 59)
   const int64_t tiles = (n + kRows - 1) / kRows;
   int hpb = heads_per_block(tiles, pool.kv_heads, num_sms, rope ? 9 : 20);
   hpb = hpb < 64 ? hpb : 64;
@@ -421,6 +426,7 @@ cudaError_t write_launch(const qwm_page_pool &pool, int page_log2, const uint16_
 cudaError_t launch_norm_rope(const qwm_rope_spec *spec, const uint16_t *x, const qwm_strides &xs, int batch, int heads,
                              int64_t n, const int64_t *start, const int64_t *at, const int32_t *pos, const float *weight,
                              int per_head, float eps, uint16_t *out, const qwm_strides &os, int num_sms, cudaStream_t st) {
+  // (blocks an SM: the chunk above with 6 / 9 / 12 / 20 takes 51 / 47 / 47 / 51 us, in halves 64 / 58 / 57 / 62)
   const int64_t tiles = ((int64_t)batch * n + kRows - 1) / kRows;
   int hpb = heads_per_block(tiles, heads, num_sms, 12);
   hpb = hpb < 64 ? hpb : 64;
@@ -448,6 +454,7 @@ cudaError_t launch_paged_write(const qwm_page_pool &pool, int page_log2, const u
 
 cudaError_t launch_paged_read(const qwm_page_pool &pool, int page_log2, const int64_t *slot, int64_t n, uint16_t *k_hat,
                               uint16_t *v_hat, int num_sms, int32_t *status, cudaStream_t st) {
+  // (blocks an SM: the chunk above, 4 bits, with 10 / 20 / 40 / 80 takes 49 / 48 / 47 / 48 us)
   const int64_t tiles = (n + kReadRows - 1) / kReadRows;
   const int hpb = heads_per_block(tiles, pool.kv_heads, num_sms, 40);
   const dim3 grid((unsigned)tiles, (unsigned)((pool.kv_heads + hpb - 1) / hpb));

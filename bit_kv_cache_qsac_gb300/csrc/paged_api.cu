@@ -79,7 +79,11 @@ Plan plan_of(const qwm_ctx *ctx, int group, int64_t max_count) {
   p.many_rows = rows > kFew;
   p.few_rows = group <= kFew;
   p.few = kFew;
-  // one tile for all rows of a sequence; beside longer sequences the few rows are mostly those of one token
+  // One tile for all rows of a sequence; where longer sequences may stand beside them, for those of one token, which
+  // 16-row tiles (one CTA an SM, half of them empty) slow down more than they help more rows.  24 sequences of up to 8,000
+  // tokens, 8 bits, with 8-row (16-row) tiles: 1 token each of 32 heads on 8: 60 us (69), on 32: 150 (205); 2 tokens of 4 heads
+  // a Key head 54 (71), 5 tokens 117 (118), 8 tokens 149 (139); beside 777 tokens of a prompt 136 (144), 138 (148), 191 (191), 225
+  // (208); 40 heads on 5, 1 and 2 tokens: 41 (57) and 67 (61).
   p.row_tiles = (p.many_rows ? group : rows) <= 8 ? 1 : 2;
   p.shares_few = p.few_rows ? paged_decode_shares(p.row_tiles, ctx->num_sms) : 0;
   p.shares_many = p.many_rows ? ctx->num_sms / 2 : 0;

@@ -8,7 +8,7 @@
 // Inside a CTA an item's keys go to the 8 warps in turn, 16 or 32 at a time, copied to a ring of shared
 // memory of the warp's own two steps ahead (cp.async; no barrier but the warp's) and multiplied on warp
 // MMAs (warp_tile.cuh).  16 keys from a multiple of 16 lie in one page.  The copies run on into the share's next
-// piece while a piece is joined and written.
+// piece while a piece is joined and written.  A share's hold on an item of more than 2^18 keys is several pieces.
 // Measured: a token of each of 64 sequences of 125 to 8,000 (8 bits, 8 Key heads): 94 us in all, 5.9 TB/s of its 550 MB; one
 // token over 39,000 (4 bits, 40 heads): 60 us, where no unit is full (issue 62%, DRAM 47% of nominal).  Around the
 // loops stand 8,000 cycles to the first step (4,000 of them the cuts) and 4,000 to 6,000 a piece (Queries, joining), 9,000 at

@@ -251,8 +251,9 @@ def qwm_paged_attend(ctx, pool: PagePool, tab: PageTable, q, first, count, softm
     """Attention of packed Queries [H, n, 128], rows first[b] .. of sequence b its newest count[b] tokens, over its
     pages: the tokens of the last `frames` frames of `tpf` tokens (None: all) and the first `sink`.  out: bf16 or
     fp32; lse: fp32 [H, n] or None; merge: out (fp32) and lse hold a result over other keys and become the
-    result over both.  max_count: the largest count, or more (None: n).  ws: a uint8 workspace tensor, or None to
-    allocate one (on the call's stream)."""
+    result over both.  max_count: the largest count, or more (None: n): the kernels are chosen by it, and those for long
+    prompts cost a step of single tokens 4 to 9 us and 40 MB of workspace where it says that there may be one.
+    ws: a uint8 workspace tensor, or None to allocate one (on the call's stream)."""
     dev = ctx.device
     p, t = pool.packed(dev), tab.packed(dev)
     n = q.shape[1]

@@ -295,7 +295,11 @@ class PagedBatch:
     called once with the step's packed Queries, Keys and Values (rows of all sequences one after the other, as
     `begin` was told).  What a step needs of the device stays on the device, so that a step may be captured in
     a CUDA graph and replayed with other counts in the same tensors.  Calls follow one another on whatever streams
-    they are made, but for captured ones, whose replays the caller orders."""
+    they are made, but for captured ones, whose replays the caller orders.
+
+    A step's tensors have `rows` rows whatever it was given: those of no sequence are stored and attended nowhere, but
+    the caller brings them, and the Queries' norm and rotation pass over them.  Choose `rows` (or batches of several
+    sizes) near what steps hold."""
 
     def __init__(self, ctx: Context, layers: int, kv_heads: int, batch: int, max_tokens: int, pages: int, rows: int,
                  page: int = 64, bits: int = 8, rope=None, norm: bool = True, eps: float = 1e-6, tpf: int = 1,
@@ -379,7 +383,9 @@ class PagedBatch:
               max_count: int | None = None, scale: float | None = None, stream=None) -> torch.Tensor:
         """Layer i: q [H][rows][d] attends, k and v [kv_heads][rows][d] are stored.  q_weight, k_weight: of the norms
         (fp32 [d] or one per head, None: ones); out: bf16 (default: a new one, padding rows 0) or fp32; lse and
-        merge as qwm_paged_attend's; max_count: the largest count of the step, where it is known."""
+        merge as qwm_paged_attend's; max_count: the largest count of the step, where it is known.  Unknown (None: the
+        batch's rows) it launches the kernels for long prompts, too, which costs a step of single tokens 4 to 9 us a layer and
+        40 MB of workspace.  A rotation without norms turns the Queries in several elementwise launches."""
         if not self.norm and (q_weight is not None or k_weight is not None):
             raise ValueError("weights of norms that this batch does not form")
         main = self._turn(stream)
