@@ -163,3 +163,76 @@ def test_attend_merged_into_a_result_over_other_keys(qwm, case):
             assert bool(((out[:, f].double() - want).abs() <= err + 2.0 ** -30).all()), i
             assert bool(((lse[:, f].double() - want_l).abs() <= d + 2.0 ** -22 * want_l.abs() + 2.0 ** -20).all()), i
         assert torch.equal(out[:, ~mine].view(torch.int32), was[:, ~mine].view(torch.int32)) and torch.equal(lse[:, ~mine], wasl[:, ~mine])
+
+
+# ------------------------------------------------------------------ offsets beyond 32 bits
+
+
+@pytest.mark.parametrize("bits,counts", [(8, [1, 3]), (8, [40, 300]), (4, [5, 2]), (4, [1, 130])])
+def test_pools_beyond_four_gigabytes(qwm, bits, counts):
+    """Pages on both sides of 2^32 bytes of codes (and 2^31 of rows' channels): written, read back and attended they are
+    what the same tokens are in a small pool."""
+    rng, kv, H, page, lengths = np.random.default_rng(bits), 8, 16, 64, [700, 900]
+    pages = 70_000 if bits == 8 else 140_000   # 4.6 GB of codes each
+    need = sum(-(-n // page) for n in lengths)
+    large, small = qwm.PagePool.empty(bits, page, pages, kv), qwm.PagePool.empty(bits, page, need, kv)
+    where = torch.from_numpy(np.concatenate([rng.permutation(need)[:need // 2], pages - 1 - rng.permutation(need)[:need - need // 2]])).cuda()
+    where = where[torch.from_numpy(rng.permutation(need)).cuda()]
+    n = sum(lengths)
+    k, v = rows(rng, kv, n), rows(rng, kv, n)
+    at = torch.cat([torch.arange(m) + off * page for m, off in ((lengths[0], 0), (lengths[1], -(-lengths[0] // page)))]).cuda()
+    first_pages = [-(-m // page) for m in lengths]
+    tabs, ctx = [], ctx_of(qwm, H)
+    hats = []
+    for pool, order in ((large, where), (small, torch.arange(need, device="cuda"))):
+        slot = order[at // page] * page + at % page
+        qwm.qwm_paged_write(ctx, pool, k, v, slot)
+        hats.append([torch.empty(kv, n, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2)])
+        qwm.qwm_paged_read(ctx, pool, slot, *hats[-1])
+        t = torch.full((2, max(first_pages)), -1, dtype=torch.int32, device="cuda")
+        t[0, :first_pages[0]], t[1, :first_pages[1]] = order[:first_pages[0]].int(), order[first_pages[0]:].int()
+        tabs.append(qwm.PageTable(page, t, ints(lengths), torch.zeros(pool.k_codes.shape[0], dtype=torch.int32, device="cuda"), ints([0], torch.int32)))
+    assert int(where.max()) * kv * page * 128 * bits // 8 > 2 ** 32
+    assert all(torch.equal(a, b) and bool(a.any()) for a, b in zip(*hats))
+    first, m = starts(counts)
+    q, got = rows(rng, H, m), []
+    for pool, tab in ((large, tabs[0]), (small, tabs[1])):
+        out, lse = torch.zeros(H, m, 128, dtype=torch.bfloat16, device="cuda"), torch.zeros(H, m, device="cuda")
+        qwm.qwm_paged_attend(ctx, pool, tab, q, ints(first, torch.int32), ints(counts, torch.int32), SCALE, out, lse=lse, max_count=max(counts))
+        got.append((out, lse))
+    assert status(qwm, ctx) == qwm.QWM_OK
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1]) and bool(got[0][0].any())
+
+
+@pytest.mark.parametrize("head_major", [False, True])
+def test_packed_batches_beyond_32_bits(qwm, head_major):
+    """The last rows of a batch whose activations pass 2^31 elements (and 2^32 bytes): normed, turned, stored and attended they
+    are what the same rows are in a small batch."""
+    rng, H, n, counts, lengths = np.random.default_rng(3), 40, 440_000, [2, 60], [300, 400]
+    ctx, spec, live = ctx_of(qwm, H), qwm.RopeSpec((128, 0, 0), theta=1e6, pairing="half"), sum(counts)
+    lot = lambda dtype=torch.bfloat16: (torch.zeros(H, n, 128, dtype=dtype, device="cuda") if head_major
+                                        else torch.zeros(n, H, 128, dtype=dtype, device="cuda").permute(1, 0, 2))
+    x, ready, out = lot(), lot(), lot()
+    some = rows(rng, H, live)
+    x[:, -live:] = some
+    at = torch.full((n,), -1, dtype=torch.int64, device="cuda")
+    at[-live:] = torch.arange(live, device="cuda") + 7
+    w = torch.from_numpy(rng.uniform(0.5, 1.5, (H, 128)).astype(np.float32)).cuda()
+    qwm.qwm_norm_rope(ctx, spec, x[None], w, 1e-6, ready[None], at=at[None])
+    want = torch.empty(1, H, live, 128, dtype=torch.bfloat16, device="cuda")
+    qwm.qwm_norm_rope(ctx, spec, some[None], w, 1e-6, want, at=at[None, -live:].contiguous())
+    assert torch.equal(ready[:, -live:], want[0]) and not ready[:, :-live].any()
+    b = Batch(qwm, rng, 8, 32, H, lengths)
+    pools = [qwm.PagePool.empty(8, 32, 4, H) for _ in range(2)]
+    slot = torch.full((n,), -1, dtype=torch.int64, device="cuda")
+    slot[-live:] = torch.arange(live, device="cuda") * 2
+    qwm.qwm_paged_write(ctx, pools[0], x, x, slot, at=at, rope=spec, weight=w)
+    qwm.qwm_paged_write(ctx, pools[1], some, some, slot[-live:].contiguous(), at=at[-live:].contiguous(), rope=spec, weight=w)
+    assert all(torch.equal(getattr(pools[0], t), getattr(pools[1], t)) for t in ("k_codes", "k_step", "v_codes", "v_step")) and pools[0].k_codes.any()
+    small, lse = torch.zeros(H, live, 128, dtype=torch.bfloat16, device="cuda"), [torch.zeros(H, m, device="cuda") for m in (n, live)]
+    qwm.qwm_paged_attend(ctx, b.pool, b.tab, ready, ints([n - live, n - live + counts[0]], torch.int32), ints(counts, torch.int32), SCALE, out, lse=lse[0],
+                         max_count=max(counts))
+    qwm.qwm_paged_attend(ctx, b.pool, b.tab, want[0], ints([0, counts[0]], torch.int32), ints(counts, torch.int32), SCALE, small, lse=lse[1], max_count=max(counts))
+    assert status(qwm, ctx) == qwm.QWM_OK
+    assert torch.equal(out[:, -live:], small) and torch.equal(lse[0][:, -live:], lse[1]) and bool(small.any())
+    assert not out[:, :-live].any() and not lse[0][:, :-live].any()
