@@ -51,7 +51,7 @@ qwm_status check_packed(const void *p, const qwm_strides *s, int64_t heads, int6
 }
 
 qwm_status check_norm(const float *weight, int32_t per_head, float eps) {
-  if ((per_head != 0 && per_head != 1) || !(eps >= 0.f) || eps > 3.402823466e38f) return QWM_ERR_ARG;
+  if ((per_head != 0 && per_head != 1) || !(eps >= 0.f) || eps > 0x1p100f) return QWM_ERR_ARG;   // (beside a mean square it stays finite)
   return aligned16(weight) ? QWM_OK : QWM_ERR_ALIGN;
 }
 

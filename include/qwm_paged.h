@@ -41,7 +41,7 @@ extern "C" {
  *           are left as they were.  One of the two is given, or neither without a rotation.
  *   pos     device int32 [batch][n][3] (t, y, x) to turn by instead of the grid's, or NULL
  *   weight  fp32 [128], or [heads][128] (per_head == 1), or NULL for ones
- *   eps     >= 0, finite
+ *   eps     >= 0, at most 2^100
  * A row with an infinite or NaN channel becomes what the formula gives in IEEE arithmetic. */
 QWM_API qwm_status qwm_norm_rope(qwm_ctx *ctx, const qwm_rope_spec *spec, const uint16_t *x, const qwm_strides *xs,
                                  int32_t batch, int32_t heads, int64_t n, const int64_t *start, const int64_t *at,

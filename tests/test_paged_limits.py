@@ -71,3 +71,14 @@ def test_workspace_serves_smaller_counts(qwm, kv, group):
     pool = qwm.qwm_page_pool(8, 64, 40, kv, *[0x7f00000000] * 4)
     sizes = [lib.qwm_paged_attend_workspace(ctx, pool, c) for c in range(1, 80)] + [lib.qwm_paged_attend_workspace(ctx, pool, 1 << 24)]
     assert sizes[0] > 0 and sizes == sorted(sizes)
+
+
+def test_eps_range(qwm):
+    """A mean square of up to 2^113 beside an eps of fp32's largest numbers would be infinite in their sum, and the row 0
+    where the formula gives numbers (2^60 / sqrt(2^128) = 2^-4): eps is 2^100 at most."""
+    lib, ctx, ok = qwm.raw_library(), _ctx(qwm, 8), 0x7f00000000
+    s = qwm.qwm_strides(1 << 14, 128, 1024)
+    pool = qwm.qwm_page_pool(8, 64, 40, 8, *[ok] * 4)
+    for eps, n, want in ((2.0 ** 100, 0, qwm.QWM_OK), (2.0 ** 100 * (1 + 2.0 ** -23), 0, qwm.QWM_ERR_ARG), (3.4e38, 3, qwm.QWM_ERR_ARG)):
+        assert lib.qwm_norm_rope(ctx, None, ok, s, 1, 8, n, None, None, None, None, 0, eps, ok + 4096, s, None) == want
+        assert lib.qwm_paged_write(ctx, pool, ok, s, ok, s, n, ok, None, None, None, 1, None, 0, eps, None) == want
