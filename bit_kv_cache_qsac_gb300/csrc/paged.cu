@@ -4,8 +4,9 @@
 //   y = x r w, r = 1 / sqrt(mean(x^2) + eps), then each pair (a, b) of channels becomes (a cos - b sin,
 //   a sin + b cos), all in fp32, rounded to bf16 once.
 // Bound: memory.  16 lanes take one row, 8 channels each; two heads' sums of squares are reduced together (four
-// shuffles and two to hand the roots back instead of eight, and one root a lane instead of two); the angles depend on the token alone, so a thread forms those of
-// its channels once and walks over `heads_per_block` heads with them, the next two heads' rows in flight.
+// shuffles and two to hand the roots back instead of eight, and one root a lane instead of two); the angles depend on
+// the token alone, so a thread forms those of its channels once and walks over `heads_per_block` heads with them, the
+// next two heads' rows in flight.
 // Measured, 40 heads x 10,800 tokens, three axes, weights per head: normed and turned in 46 us = 4.8 TB/s of rows read
 // and written (72% of the issue slots: the rotation alone takes 37 us, the norm alone 38; with four heads in flight 54, with one
 // 57, and with each head's weights fetched from global memory 55); in halves 54 us with shared weights and 69 with weights per
@@ -401,8 +402,8 @@ cudaError_t write_launch(const qwm_page_pool &pool, int page_log2, const uint16_
                          const qwm_strides &vs, int64_t n, const int64_t *slot, const qwm_rope_spec *rope, const int64_t *at,
                          const int32_t *pos, const float *weight, int per_head, float eps, int num_sms, int32_t *status,
                          cudaStream_t st) {
-  // (blocks an SM: the chunk above turned, 4 bits, with 5 / 9 / 14 / 20 takes 76 / 68 / 70 / 76 us, in halves 80 / 76 / 80 / 88; not turned
-  // with 10 / 20 / 30 / 40: 61 / 57 / 57 / 59)
+  // (blocks an SM: the chunk above turned, 4 bits, with 5 / 9 / 14 / 20 takes 76 / 68 / 70 / 76 us, in halves 80 / 76 / 80 /
+  // 88; not turned with 10 / 20 / 30 / 40: 61 / 57 / 57 / 59)
   const int64_t tiles = (n + kRows - 1) / kRows;
   int hpb = heads_per_block(tiles, pool.kv_heads, num_sms, rope ? 9 : 20);
   hpb = hpb < 64 ? hpb : 64;

@@ -28,9 +28,10 @@
 // Bound: the tensor pipe for long items; what stands around an item's loop for short ones.  Measured: 2,048 tokens over
 // 30,000 before them (8 bits, 32 heads on 8): 579 us = 1,795 TFLOP/s; 4,680 over 40,560 (4 bits, 40 heads): 2.17 ms =
 // 1,730 TFLOP/s (tensor pipe active in 78.7 and 79.5% of all cycles; under the power cap, after some 50 ms
-// of them, 7 to 10% less).  In cycles: 12,000 until the first piece is described (7,500 for the cuts), 6,000 for its Queries, 3,300 (bf16) to 7,000 (parts) for writing it.  What was live across the
-// steps decided the rest: pieces read from shared memory where they are needed instead of kept in registers gave 751 ->
-// 698 us and 2,557 -> 2,420; multiply() written into the kernel's body instead of apart 785 -> 1,200.
+// of them, 7 to 10% less).  In cycles: 12,000 until the first piece is described (7,500 for the cuts), 6,000 for its
+// Queries, 3,300 (bf16) to 7,000 (parts) for writing it.  What was live across the steps decided the rest: pieces read
+// from shared memory where they are needed instead of kept in registers gave 751 -> 698 us and 2,557 -> 2,420;
+// multiply() written into the kernel's body instead of apart 785 -> 1,200.
 #include "paged.cuh"
 
 namespace {
